@@ -17,7 +17,14 @@
  *                         prefill chunks in the same batch ("Scheduler": V1
  *                         mixes prefill and decode in one step; "Chunked
  *                         prefill"), with prefix-cached requests sharing
- *                         physical blocks ("Prefix Caching").
+ *                         physical blocks ("Prefix Caching");
+ *   paged_build_tables  - a step's block tables, lengths, positions and
+ *                         slots from its requests' lengths ("Scheduler",
+ *                         allocate_slots; "Run forward pass", step 2);
+ *   paged_qk_norm_rope  - norms of the q and k heads, their rotation by the
+ *                         tokens' positions and the KV write, in one pass;
+ *   pkv_prompt_attention - causal attention of whole prompts from their
+ *                         contiguous q, k and v, without the pool.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -77,6 +84,8 @@ extern "C" {
 #define PKV_DEV_BAD_SLOT 0x8     /* a slot_mapping entry lies at or beyond 16 * num_blocks */
 #define PKV_DEV_TIMEOUT 0x10     /* an internal pipeline wait gave up (never expected) */
 #define PKV_DEV_OVERFLOW 0x20    /* internal work list overflow (never expected) */
+#define PKV_DEV_BAD_POS 0x40     /* a position at or beyond the rotation table's num_positions */
+#define PKV_DEV_NO_BLOCKS 0x80   /* a request needs more blocks than free_blocks has left */
 
 typedef struct {
     int32_t num_blocks;    /* blocks in the pool */
@@ -301,6 +310,135 @@ int paged_attention_static(const void *q, int32_t num_tokens, int32_t num_q_head
                            const int32_t *block_table, int32_t num_reqs, int32_t max_blocks_per_req,
                            const int32_t *seq_lens, const int32_t *query_start_loc,
                            float scale, void *out, void *stream);
+
+/*
+ * A step's metadata from its requests' lengths ("Scheduler", allocate_slots:
+ * each request gets the blocks its new tokens need; "Run forward pass", step
+ * 2). Request r has L0 = context_lens[r] tokens in the pool and brings
+ * n = query_lens[r] new ones, L1 = L0 + n. In request order, each takes
+ * ceil(L1 / 16) - ceil(L0 / 16) ids from free_blocks, starting at the
+ * cursor, into its block_table row behind the entries it has. Then
+ *     seq_lens[r] = L1                 query_start_loc[r + 1] = n_0 + ... + n_r
+ *     positions[t] = L0 + i            slot_mapping[t] = block * 16 + position % 16
+ * for token t, token i of request r: what paged_kv_write, paged_attention
+ * and paged_qk_norm_rope take.
+ *
+ *  query_lens       int32 [num_reqs]; 0 is allowed
+ *  context_lens     int32 [num_reqs]
+ *  free_blocks      int32 [num_free], ids nobody holds (may be NULL if num_free is 0)
+ *  free_cursor      int32, the first unused entry of free_blocks; NULL: 0
+ *  block_table      int32 [num_reqs][max_blocks_per_req], extended in place;
+ *                   the entry of a partly filled last block is read
+ *  seq_lens         int32 [num_reqs] (output; may be context_lens: updated in place)
+ *  query_start_loc  int32 [num_reqs + 1] (output)
+ *  positions        int32 [num_tokens] (output; may be NULL)
+ *  slot_mapping     int32 [num_tokens] (output)
+ *  free_cursor_out  int32, the cursor behind the ids handed out (output; may
+ *                   be free_cursor: updated in place, or NULL)
+ *  status           optional device int32, PKV_DEV_* bits OR-ed in
+ *
+ * num_tokens rows are written whatever the lengths add up to: rows behind
+ * the last request's (a batch padded to a captured size) get position -1 and
+ * slot -1. Other outputs must not overlap the inputs.
+ *
+ * A request is refused - its rows get position -1 and slot -1, its length and
+ * table stay, it takes no block - when its lengths are negative or past 16 *
+ * max_blocks_per_req (PKV_DEV_BAD_LEN), when its rows end beyond num_tokens
+ * (PKV_DEV_BAD_QSL; query_start_loc stops at num_tokens), or when the ids
+ * left do not cover it (PKV_DEV_NO_BLOCKS; requests behind it that need
+ * blocks are then refused too). A negative query length counts as 0 and
+ * raises PKV_DEV_BAD_QSL. An id outside [0, num_blocks) that is handed out
+ * or read gives its tokens slot -1 (handed out: table entry -1) and raises
+ * PKV_DEV_BAD_BLOCK.
+ *
+ * Ordering: nothing is read before every earlier kernel on the stream has
+ * completed, and kernels launched behind it on the stream start only when it
+ * has: the tables may go straight to paged_attention and
+ * paged_kv_write_slots.
+ */
+int paged_build_tables(const int32_t *query_lens, const int32_t *context_lens, int32_t num_reqs,
+                       const int32_t *free_blocks, int32_t num_free, const int32_t *free_cursor, int32_t num_tokens,
+                       int32_t num_blocks, int32_t *block_table, int32_t max_blocks_per_req, int32_t *seq_lens,
+                       int32_t *query_start_loc, int32_t *positions, int32_t *slot_mapping,
+                       int32_t *free_cursor_out, int32_t *status, void *stream);
+
+/*
+ * What a layer does to its projections before attention: a root-mean-square
+ * norm of every q and k head, the rotation of the head's first rotary_dim
+ * columns by the token's position, and the KV write, in one pass. For a head
+ * x of D = head_size columns:
+ *     y = x / sqrt(mean(x^2) + eps) * weight      (weight NULL: y = x)
+ *     (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)     for every pair f
+ * Pair f in [0, rotary_dim / 2) has the columns (f, f + rotary_dim / 2), or
+ * (2f, 2f + 1) when interleaved. c = cos_sin[p][f] and s =
+ * cos_sin[p][rotary_dim / 2 + f], p the token's position on the axis that f
+ * belongs to: with num_axes axes (time, height, width of an image or video
+ * token) the first axis_pairs[0] pairs follow axis 0, the next axis_pairs[1]
+ * axis 1, and so on. Computed in 32 bits, rounded to bf16 once.
+ *
+ * q goes to q_out; k to k_out (if given) and to the pool (if given), v to the
+ * pool, by slot_mapping as in paged_kv_write (negative: not written to the
+ * pool; at or beyond 16 * num_blocks: not written, PKV_DEV_BAD_SLOT). One of
+ * k_out and kv_cache has to be given. A token with a negative position on any
+ * axis is padding: nothing of it is written. A position at or beyond
+ * num_positions raises PKV_DEV_BAD_POS and is treated the same way.
+ *
+ *  desc       strides are elements from token to token (a multiple of 8, at
+ *             least heads * head_size for more than one token); heads of a
+ *             token lie next to each other, so q, k and v may be slices of
+ *             one projection's rows. head_size: a multiple of 16 up to 256;
+ *             rotary_dim: a multiple of 16 in [16, head_size].
+ *  q, k, v    bf16; v is read only with kv_cache
+ *  weights    bf16 [head_size] or NULL
+ *  positions  int32 [num_axes][num_tokens]
+ *  cos_sin    float [num_positions][rotary_dim], cosines then sines
+ *  q_out      may be q (same stride), k_out may be k: in place. No other overlap.
+ */
+#define PKV_MAX_ROPE_AXES 4
+typedef struct {
+    int32_t num_q_heads, num_kv_heads, head_size, rotary_dim;
+    int32_t interleaved;                    /* 0: columns f and f + rotary_dim / 2 pair up; else 2f and 2f + 1 */
+    int32_t num_axes;                       /* 1 .. PKV_MAX_ROPE_AXES */
+    int32_t axis_pairs[PKV_MAX_ROPE_AXES];  /* pairs of each axis, together rotary_dim / 2 (one axis: not read) */
+    int32_t num_positions;                  /* rows of cos_sin */
+    float eps;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+} pkv_rope_desc;
+
+int paged_qk_norm_rope(const pkv_rope_desc *desc, const void *q, const void *k, const void *v, int32_t num_tokens,
+                       const void *q_weight, const void *k_weight, const int32_t *positions, const float *cos_sin,
+                       void *q_out, void *k_out, const int32_t *slot_mapping, void *kv_cache, int32_t num_blocks,
+                       int32_t *status, void *stream);
+
+/*
+ * Causal attention of whole prompts (a prompt's first step, or a model used
+ * without a pool): sequences packed behind one another, each token attending
+ * to its own sequence up to itself. For token i of sequence r, row t =
+ * query_start_loc[r] + i, and query head hq, kv head h = hq / (num_q_heads /
+ * num_kv_heads):
+ *
+ *   out[t][hq][:] = sum_{j=0..i} softmax_j(scale * q[t][hq] . k[t-i+j][h]) v[t-i+j][h]
+ *
+ *  q, k, v    bf16; strides are elements from token to token (a multiple of
+ *             8, at least heads * head_size), heads of a token next to each
+ *             other; head_size 64 or 128, at most 128 q heads per kv head
+ *  query_start_loc  int32 [num_reqs + 1]. A sequence may be empty. One with
+ *             bounds that descend or leave [0, num_tokens] is skipped and
+ *             raises PKV_DEV_BAD_QSL. Rows outside every sequence are left
+ *             as they were.
+ *  scale      finite and greater than 0
+ *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the inputs
+ *  status     optional device int32, PKV_DEV_* bits OR-ed in
+ *
+ * A value that is not finite reaches the rows that may see its token and no
+ * other (rows whose tile holds such a value are summed again one by one:
+ * correct, but slow). Needs no workspace; calls may overlap. As with
+ * paged_attention, make the first call on a device before any capture.
+ */
+int pkv_prompt_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_size, const int32_t *query_start_loc, int32_t num_reqs, float scale, void *out,
+                         int32_t *status, void *stream);
 
 /*
  * Host-buffer step pipeline: steps whose inputs come from, and whose output

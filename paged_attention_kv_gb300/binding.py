@@ -36,12 +36,15 @@ PKV_DEV_BAD_BLOCK = 0x4
 PKV_DEV_BAD_SLOT = 0x8
 PKV_DEV_TIMEOUT = 0x10
 PKV_DEV_OVERFLOW = 0x20
+PKV_DEV_BAD_POS = 0x40
+PKV_DEV_NO_BLOCKS = 0x80
 
 EXPORTED = ("pkv_kv_cache_bytes", "paged_slot_mapping", "paged_kv_write", "paged_kv_write_slots",
             "paged_kv_gather_blocks",
             "paged_kv_scatter_blocks", "paged_attention_workspace_bytes",
             "paged_attention_min_workspace_bytes", "paged_attention", "paged_attention_timed",
-            "paged_attention_bounded", "paged_attention_static", "pkv_pipeline_create", "pkv_pipeline_next",
+            "paged_attention_bounded", "paged_attention_static", "paged_build_tables", "paged_qk_norm_rope",
+            "pkv_prompt_attention", "pkv_pipeline_create", "pkv_pipeline_next",
             "pkv_pipeline_submit", "pkv_pipeline_sync", "pkv_pipeline_destroy", "pkv_read_status", "pkv_selftest_bounded_wait", "pkv_status_string")
 
 
@@ -54,6 +57,18 @@ class PagedKVError(RuntimeError):
 class CacheDesc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_size", ctypes.c_int32)]
+
+
+MAX_ROPE_AXES = 4
+
+
+class RopeDesc(ctypes.Structure):
+    """pkv_rope_desc of include/pagedkv.h."""
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_size", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("axis_pairs", ctypes.c_int32 * MAX_ROPE_AXES), ("num_positions", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
 
 
 PIPELINE_MAX_DEPTH = 4
@@ -93,6 +108,12 @@ def _load():
     lib.paged_attention_bounded.argtypes = [vp, i32, i32, vp, desc_p, vp, i32, i32, vp, vp, i32, ctypes.c_float, vp,
                                             vp, sz, vp, ctypes.POINTER(vp)]
     lib.paged_attention_static.argtypes = [vp, i32, i32, vp, desc_p, vp, i32, i32, vp, vp, ctypes.c_float, vp, vp]
+    i64 = ctypes.c_int64
+    lib.paged_build_tables.argtypes = [vp, vp, i32, vp, i32, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.paged_qk_norm_rope.argtypes = [ctypes.POINTER(RopeDesc), vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32,
+                                       vp, vp]
+    lib.pkv_prompt_attention.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, vp, i32, ctypes.c_float, vp,
+                                         vp, vp]
     lib.pkv_selftest_bounded_wait.argtypes = [vp, ctypes.c_uint32, vp]
     lib.pkv_pipeline_create.argtypes = [ctypes.POINTER(PipelineDesc), ctypes.POINTER(vp)]
     lib.pkv_pipeline_next.argtypes = [vp, ctypes.POINTER(i32)]
@@ -316,6 +337,220 @@ def paged_attention_static(q, kv_cache, block_table, seq_lens, query_start_loc, 
                                       seq_lens.shape[0], block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc),
                                       float(scale), _ptr(out), _stream(stream)), "paged_attention_static")
     return out
+
+
+class PreparedCall:
+    """One of the library's calls with its arguments checked and converted
+    once. Calling the object enqueues it on the given (or the current) stream
+    of the tensors' device and returns ``outputs``; the buffers it was made
+    with are read and written each time, and kept alive."""
+
+    def __init__(self, name: str, args: tuple, device, outputs, keep: tuple):
+        self.name, self.args, self.device, self.outputs, self._keep = name, args, device, outputs, keep
+        self._fn = getattr(LIB, name)
+
+    def __call__(self, stream=None):
+        if torch.cuda.current_device() == self.device.index:
+            rc = self._fn(*self.args, _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                rc = self._fn(*self.args, _stream(stream))
+        if rc != PKV_OK:
+            raise PagedKVError(rc, self.name)
+        return self.outputs
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _want_rows(t, name: str) -> tuple[int, int, int, int]:
+    """A bf16 [tokens][heads][head_size] tensor whose tokens' heads lie next
+    to each other; returns (tokens, heads, head_size, token stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][head_size], got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    n, h, d = t.shape
+    if n and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"the heads of a token of {name} must be contiguous, got strides {t.stride()}")
+    return n, h, d, t.stride(0) if n > 1 else h * d
+
+
+def prepare_build_tables(query_lens, context_lens, free_blocks, block_table, num_tokens: int, num_blocks: int, *,
+                         cursor=None, cursor_out=None, seq_lens=None, query_start_loc=None, positions=None,
+                         slot_mapping=None, status=None) -> PreparedCall:
+    """The checked call of ``paged_build_tables``, to be called every step."""
+    for t, nd, name in ((query_lens, 1, "query_lens"), (context_lens, 1, "context_lens"),
+                        (free_blocks, 1, "free_blocks"), (block_table, 2, "block_table")):
+        _want(t, torch.int32, nd, name)
+    dev, r = block_table.device, query_lens.shape[0]
+    if context_lens.shape[0] != r or block_table.shape[0] != r:
+        raise ValueError("query_lens, context_lens and block_table disagree on the number of requests")
+
+    def buf(t, n, name):
+        if t is None:
+            return torch.empty(n, dtype=torch.int32, device=dev)
+        _want(t, torch.int32, 1, name)
+        if t.shape[0] < n:
+            raise ValueError(f"{name} has {t.shape[0]} entries, {n} are written")
+        return t
+
+    if num_tokens < 0:
+        raise ValueError("num_tokens is negative")
+    if cursor is not None:
+        buf(cursor, 1, "cursor")
+    cursor_out = buf(cursor_out, 1, "cursor_out")
+    seq_lens = buf(seq_lens, r, "seq_lens")
+    query_start_loc = buf(query_start_loc, r + 1, "query_start_loc")
+    positions = buf(positions, num_tokens, "positions")
+    slot_mapping = buf(slot_mapping, num_tokens, "slot_mapping")
+    if status is not None:
+        buf(status, 1, "status")
+    _same_device(dev, query_lens=query_lens, context_lens=context_lens, free_blocks=free_blocks, cursor=cursor,
+                 cursor_out=cursor_out, seq_lens=seq_lens, query_start_loc=query_start_loc, positions=positions,
+                 slot_mapping=slot_mapping, status=status)
+    i32 = ctypes.c_int32
+    args = (_ptr(query_lens), _ptr(context_lens), i32(r), _ptr(free_blocks), i32(free_blocks.shape[0]), _ptr(cursor),
+            i32(num_tokens), i32(num_blocks), _ptr(block_table), i32(block_table.shape[1]), _ptr(seq_lens),
+            _ptr(query_start_loc), _ptr(positions), _ptr(slot_mapping), _ptr(cursor_out), _ptr(status))
+    keep = (query_lens, context_lens, free_blocks, block_table, cursor, cursor_out, status)
+    return PreparedCall("paged_build_tables", args, dev,
+                        (seq_lens, query_start_loc, positions, slot_mapping, cursor_out), keep)
+
+
+def paged_build_tables(query_lens, context_lens, free_blocks, block_table, num_tokens: int, num_blocks: int, *,
+                       cursor=None, cursor_out=None, seq_lens=None, query_start_loc=None, positions=None,
+                       slot_mapping=None, status=None, stream=None):
+    """Hands each request the blocks its new tokens need (``free_blocks`` from
+    ``cursor`` on, in request order), extends ``block_table`` in place and
+    returns ``(seq_lens, query_start_loc, positions, slot_mapping, cursor)``
+    of the step. Pass ``seq_lens=context_lens`` and ``cursor_out=cursor`` to
+    update them in place."""
+    return prepare_build_tables(query_lens, context_lens, free_blocks, block_table, num_tokens, num_blocks,
+                                cursor=cursor, cursor_out=cursor_out, seq_lens=seq_lens,
+                                query_start_loc=query_start_loc, positions=positions, slot_mapping=slot_mapping,
+                                status=status)(stream)
+
+
+def prepare_qk_norm_rope(q, k, positions, cos_sin, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                         interleaved: bool = False, axis_sections=None, v=None, slot_mapping=None, kv_cache=None,
+                         q_out=None, k_out=None, status=None) -> PreparedCall:
+    """The checked call of ``paged_qk_norm_rope``, to be called every step."""
+    t, hq, d, q_stride = _want_rows(q, "q")
+    tk, hkv, dk, k_stride = _want_rows(k, "k")
+    if (tk, dk) != (t, d):
+        raise ValueError("q and k disagree on tokens or head_size")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    _want(positions, torch.int32, positions.dim() if positions.dim() in (1, 2) else 1, "positions")
+    if positions.shape[-1] != t:
+        raise ValueError("positions must be [tokens] or [axes][tokens]")
+    _want(cos_sin, torch.float32, 2, "cos_sin")
+    rotary = cos_sin.shape[1]
+    if not 1 <= axes <= MAX_ROPE_AXES:
+        raise ValueError(f"positions has {axes} axes, 1 to {MAX_ROPE_AXES} are supported")
+    sections = [rotary // 2] if axes == 1 and axis_sections is None else list(axis_sections or ())
+    if len(sections) != axes or sum(sections) != rotary // 2 or min(sections) < 0:
+        raise ValueError("axis_sections must give each axis its pairs, together half of cos_sin's columns")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _want(w, torch.bfloat16, 1, name)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must have head_size entries")
+    v_stride, nb = 0, 0
+    if kv_cache is not None:
+        _want(kv_cache, torch.bfloat16, 5, "kv_cache")
+        desc = cache_desc(kv_cache)
+        if (desc.num_kv_heads, desc.head_size) != (hkv, d):
+            raise ValueError("k differs from kv_cache in heads or head_size")
+        if desc.block_size != BLOCK_SIZE:
+            raise PagedKVError(PKV_E_BLOCK_SIZE, "paged_qk_norm_rope")
+        if v is None or slot_mapping is None:
+            raise ValueError("kv_cache needs v and slot_mapping")
+        tv, hv, dv, v_stride = _want_rows(v, "v")
+        if (tv, hv, dv) != (t, hkv, d):
+            raise ValueError("v must have k's shape")
+        _want(slot_mapping, torch.int32, 1, "slot_mapping")
+        if slot_mapping.shape[0] < t:
+            raise ValueError("slot_mapping is shorter than q")
+        nb = desc.num_blocks
+    if q_out is None:
+        q_out = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
+    if k_out is None and kv_cache is None:
+        k_out = torch.empty((t, hkv, d), dtype=k.dtype, device=k.device)
+    to, ho, do, qo_stride = _want_rows(q_out, "q_out")
+    if (to, ho, do) != (t, hq, d):
+        raise ValueError("q_out must have q's shape")
+    ko_stride = 0
+    if k_out is not None:
+        to, ho, do, ko_stride = _want_rows(k_out, "k_out")
+        if (to, ho, do) != (t, hkv, d):
+            raise ValueError("k_out must have k's shape")
+    if status is not None:
+        _want(status, torch.int32, 1, "status")
+    _same_device(q.device, k=k, v=v, positions=positions, cos_sin=cos_sin, q_weight=q_weight, k_weight=k_weight,
+                 slot_mapping=slot_mapping, kv_cache=kv_cache, q_out=q_out, k_out=k_out, status=status)
+    rd = RopeDesc(hq, hkv, d, rotary, int(bool(interleaved)), axes, (ctypes.c_int32 * MAX_ROPE_AXES)(*sections),
+                  cos_sin.shape[0], float(eps), q_stride, k_stride, v_stride, qo_stride, ko_stride)
+    i32 = ctypes.c_int32
+    args = (ctypes.byref(rd), _ptr(q), _ptr(k), _ptr(v if kv_cache is not None else None), i32(t), _ptr(q_weight),
+            _ptr(k_weight), _ptr(positions), _ptr(cos_sin), _ptr(q_out), _ptr(k_out),
+            _ptr(slot_mapping if kv_cache is not None else None), _ptr(kv_cache), i32(nb), _ptr(status))
+    return PreparedCall("paged_qk_norm_rope", args, q.device, (q_out, k_out),
+                        (rd, q, k, v, q_weight, k_weight, positions, cos_sin, slot_mapping, kv_cache, status))
+
+
+def paged_qk_norm_rope(q, k, positions, cos_sin, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                       interleaved: bool = False, axis_sections=None, v=None, slot_mapping=None, kv_cache=None,
+                       q_out=None, k_out=None, status=None, stream=None):
+    """Norms (where a weight is given) and rotates the heads of q and k by
+    ``cos_sin`` (float32 [num_positions][rotary_dim]) at ``positions`` ([T],
+    or [axes][T] with ``axis_sections``), and with ``kv_cache`` writes k and v
+    to its slots. Returns ``(q_out, k_out)``; ``k_out`` is None when only the
+    pool was asked for."""
+    return prepare_qk_norm_rope(q, k, positions, cos_sin, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                interleaved=interleaved, axis_sections=axis_sections, v=v, slot_mapping=slot_mapping,
+                                kv_cache=kv_cache, q_out=q_out, k_out=k_out, status=status)(stream)
+
+
+def prepare_prompt_attention(q, k, v, query_start_loc, scale: float, *, out=None, status=None) -> PreparedCall:
+    """The checked call of ``pkv_prompt_attention``, to be called every step."""
+    t, hq, d, q_stride = _want_rows(q, "q")
+    tk, hkv, dk, k_stride = _want_rows(k, "k")
+    tv, hv, dv, v_stride = _want_rows(v, "v")
+    if (tk, dk) != (t, d) or (tv, hv, dv) != (tk, hkv, dk):
+        raise ValueError("q, k and v disagree on tokens, kv heads or head_size")
+    _want(query_start_loc, torch.int32, 1, "query_start_loc")
+    if query_start_loc.shape[0] < 1:
+        raise ValueError("query_start_loc must have num_reqs + 1 entries")
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
+    _want(out, torch.bfloat16, 3, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if status is not None:
+        _want(status, torch.int32, 1, "status")
+    _same_device(q.device, k=k, v=v, query_start_loc=query_start_loc, out=out, status=status)
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    args = (_ptr(q), i64(q_stride), _ptr(k), i64(k_stride), _ptr(v), i64(v_stride), i32(t), i32(hq), i32(hkv), i32(d),
+            _ptr(query_start_loc), i32(query_start_loc.shape[0] - 1), ctypes.c_float(scale), _ptr(out), _ptr(status))
+    return PreparedCall("pkv_prompt_attention", args, q.device, out, (q, k, v, query_start_loc, status))
+
+
+def pkv_prompt_attention(q, k, v, query_start_loc, scale: float, *, out=None, status=None,
+                         stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts: row ``query_start_loc[r] + i`` of q
+    sees rows ``query_start_loc[r] .. query_start_loc[r] + i`` of k and v
+    (grouped heads). q, k and v may be slices of one projection's rows. Rows
+    outside every sequence are left as they were (in a fresh ``out``:
+    undefined)."""
+    return prepare_prompt_attention(q, k, v, query_start_loc, scale, out=out, status=status)(stream)
 
 
 def _event_handle(ev, stream) -> int:

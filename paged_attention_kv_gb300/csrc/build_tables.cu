@@ -1,0 +1,241 @@
+// A step's metadata from its requests' lengths: new blocks handed out in
+// request order, block-table rows extended, sequence lengths, query starts,
+// positions and slots ("Inside vLLM", page 1, "Scheduler": allocate_slots
+// gives each request the blocks of 16 that its new tokens need; "Run forward
+// pass", step 2, builds the tables and the slot mapping).
+//
+// Request r with L0 tokens of context and n new ones ends at L1 = L0 + n and
+// takes ceil(L1 / 16) - ceil(L0 / 16) new blocks; both prefix sums (tokens,
+// blocks) come from one scan. Every CTA of the cluster scans all requests
+// (a kilobyte or two from L2), which costs less than handing the result on,
+// and then fills its share of the tokens; the new token at a block's first
+// position also writes the block-table entry, so no entry is written twice.
+// The lengths and the cursor may be updated in place: they are written by
+// rank 0 once the whole cluster has read them (a cluster barrier per
+// kThreads requests).
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+
+namespace pkv {
+namespace {
+
+struct TableArgs {
+    const int32_t *query_lens, *context_lens, *free_blocks, *cursor;
+    int num_reqs, max_blocks_per_req, num_free, num_tokens, num_blocks;
+    int32_t *block_table, *seq_lens, *qsl, *positions, *slots, *cursor_out, *status;
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Tokens and blocks summed together (64 bits each: the lengths are the
+// caller's, their sums may pass 32).
+struct Sums {
+    long long tok, blk;
+};
+
+__device__ __forceinline__ Sums warp_inclusive(Sums v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, v.tok, d);
+        const long long b = __shfl_up_sync(0xffffffffu, v.blk, d);
+        if (lane >= d) {
+            v.tok += t;
+            v.blk += b;
+        }
+    }
+    return v;
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs a) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ Sums s_warp[kWarps];
+    __shared__ long long s_taken[kWarps];
+    __shared__ int s_start[kThreads + 1];  // first token of each request of the pass, at most num_tokens
+    __shared__ int s_len[kThreads];        // context before the step; -1: the request is refused
+    __shared__ int s_base[kThreads];       // its first new block in free_blocks
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    const int T = a.num_tokens;
+    // No early trigger: kernels of this library that read the tables ahead
+    // of their own wait must not start before this one has finished.
+    pdl_wait();
+    const int cur = a.cursor ? *a.cursor : 0;
+    const long long avail = cur >= 0 && cur <= a.num_free ? a.num_free - cur : 0;
+    Sums carry{0, 0};
+    long long taken = 0;  // blocks handed out so far
+    int bits = 0;
+    for (int r0 = 0; r0 == 0 || r0 < a.num_reqs; r0 += kThreads) {
+        const int r = r0 + tid;
+        const bool in = r < a.num_reqs;
+        int n = in ? __ldg(a.query_lens + r) : 0;
+        const int L0 = in ? a.context_lens[r] : 0;  // may be written below: not through the read-only path
+        if (n < 0) {
+            n = 0;
+            bits |= PKV_DEV_BAD_QSL;
+        }
+        const long long L1 = (long long)L0 + n;
+        bool refused = L0 < 0 || L1 > (long long)a.max_blocks_per_req * PKV_BLOCK_SIZE;
+        if (refused) bits |= PKV_DEV_BAD_LEN;
+        Sums v{n, refused ? 0 : (L1 + 15) / 16 - (L0 + 15LL) / 16};
+        const long long need = v.blk;
+        v = warp_inclusive(v, lane);
+        if (lane == 31) s_warp[warp] = v;
+        __syncthreads();
+        Sums before = carry;
+        for (int w = 0; w < kWarps; ++w) {
+            const Sums s = s_warp[w];
+            if (w < warp) {
+                before.tok += s.tok;
+                before.blk += s.blk;
+            }
+            carry.tok += s.tok;
+            carry.blk += s.blk;
+        }
+        const long long end = before.tok + v.tok, first = before.blk + v.blk - need;
+        // Requests whose tokens do not fit the step, or whose blocks are not
+        // there, get nothing. Both sums only grow, so a refusal never changes
+        // what the requests before it got.
+        if (end > T && n > 0) {
+            refused = true;
+            bits |= PKV_DEV_BAD_QSL;
+        }
+        if (need > 0 && first + need > avail) {
+            refused = true;
+            bits |= PKV_DEV_NO_BLOCKS;
+        }
+        s_start[tid] = (int)min(end - n, (long long)T);
+        s_len[tid] = refused ? -1 : L0;
+        s_base[tid] = refused ? 0 : (int)(cur + first);
+        if (tid == kThreads - 1) s_start[kThreads] = (int)min(end, (long long)T);
+        long long got = refused ? 0 : need;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) got += __shfl_xor_sync(0xffffffffu, got, d);
+        if (lane == 0) s_taken[warp] = got;
+        __syncthreads();
+        cluster_arrive();  // this CTA has read the pass's lengths (and the cursor)
+        for (int w = 0; w < kWarps; ++w) taken += s_taken[w];
+
+        const int t0 = s_start[0], t1 = s_start[kThreads];
+        for (int g = (t0 >> 2) + (int)rank * kThreads + tid; g < ((t1 + 3) >> 2);
+             g += (int)(gridDim.x * kThreads)) {
+            int pos[4], slot[4];
+            int j = -1, nxt = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * g + e;
+                pos[e] = slot[e] = -1;
+                if (t < t0 || t >= t1) continue;
+                if (j < 0 || t >= nxt) {  // last request of the pass that starts at or before t
+                    int lo = 0, hi = kThreads;
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) >> 1;
+                        if (s_start[mid] <= t) lo = mid; else hi = mid;
+                    }
+                    j = lo;
+                    nxt = s_start[j + 1];
+                }
+                const int len = s_len[j];
+                if (len < 0) continue;
+                const int p = len + (t - s_start[j]);
+                const int b = p / PKV_BLOCK_SIZE, fresh = b - (len + 15) / 16;
+                int32_t *entry = a.block_table + (long long)(r0 + j) * a.max_blocks_per_req + b;
+                int id = fresh >= 0 ? __ldg(a.free_blocks + s_base[j] + fresh) : *entry;
+                if (id < 0 || id >= a.num_blocks) {
+                    bits |= PKV_DEV_BAD_BLOCK;
+                    id = -1;
+                }
+                if (p % PKV_BLOCK_SIZE == 0) *entry = id;
+                pos[e] = p;
+                slot[e] = id < 0 ? -1 : id * PKV_BLOCK_SIZE + p % PKV_BLOCK_SIZE;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * g + e;
+                if (t < t0 || t >= t1) continue;
+                a.slots[t] = slot[e];
+                if (a.positions) a.positions[t] = pos[e];
+            }
+        }
+        __syncwarp();
+        cluster_wait();
+        if (rank == 0 && in) {
+            a.seq_lens[r] = refused ? L0 : (int)L1;
+            a.qsl[r + 1] = (int)min(end, (long long)T);
+        }
+        __syncthreads();
+    }
+    // rows behind the last request
+    for (long long t = min(carry.tok, (long long)T) + (long long)rank * kThreads + tid; t < T;
+         t += gridDim.x * kThreads) {
+        a.slots[t] = -1;
+        if (a.positions) a.positions[t] = -1;
+    }
+    if (rank == 0 && tid == 0) {
+        a.qsl[0] = 0;
+        if (a.cursor_out) *a.cursor_out = (int)(cur + taken);
+    }
+    if (bits) raise_status(a.status, bits);
+    __threadfence();
+}
+
+template <int kThreads>
+cudaError_t launch(const TableArgs &a, int ctas, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, build_tables_kernel<kThreads>, a);
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" PKV_API int paged_build_tables(const int32_t *query_lens, const int32_t *context_lens, int32_t num_reqs,
+                                          const int32_t *free_blocks, int32_t num_free, const int32_t *free_cursor,
+                                          int32_t num_tokens, int32_t num_blocks, int32_t *block_table,
+                                          int32_t max_blocks_per_req, int32_t *seq_lens, int32_t *query_start_loc,
+                                          int32_t *positions, int32_t *slot_mapping, int32_t *free_cursor_out,
+                                          int32_t *status, void *stream) {
+    if (num_reqs < 0 || num_tokens < 0 || num_free < 0 || max_blocks_per_req < 0 || num_blocks <= 0)
+        return PKV_E_DIMS;
+    if (num_blocks > INT32_MAX / PKV_BLOCK_SIZE || max_blocks_per_req > INT32_MAX / PKV_BLOCK_SIZE ||
+        num_tokens > INT32_MAX - 65536 || num_reqs > INT32_MAX - 65536)
+        return PKV_E_DIMS;
+    if (!query_start_loc || (num_tokens > 0 && !slot_mapping) || (num_free > 0 && !free_blocks)) return PKV_E_NULL;
+    if (num_reqs > 0 && (!query_lens || !context_lens || !seq_lens || (max_blocks_per_req > 0 && !block_table)))
+        return PKV_E_NULL;
+    if (!aligned(query_lens, 4) || !aligned(context_lens, 4) || !aligned(free_blocks, 4) || !aligned(free_cursor, 4) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(positions, 4) ||
+        !aligned(slot_mapping, 4) || !aligned(free_cursor_out, 4) || !aligned(status, 4))
+        return PKV_E_ALIGN;
+    const TableArgs a{query_lens,  context_lens, free_blocks, free_cursor,  num_reqs, max_blocks_per_req, num_free,
+                      num_tokens,  num_blocks,   block_table, seq_lens,     query_start_loc, positions, slot_mapping,
+                      free_cursor_out, status};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t err = num_tokens <= 4096 ? launch<1024>(a, 1, st) : launch<1024>(a, 8, st);
+    return err == cudaSuccess ? PKV_OK : PKV_E_CUDA;
+}

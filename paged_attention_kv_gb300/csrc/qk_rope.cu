@@ -1,0 +1,335 @@
+// What a layer does to its projections before attention, in one pass: a
+// root-mean-square norm of each q and k head, the rotation of the head's
+// first columns by the token's position, and the KV write ("Inside vLLM",
+// page 1, "Run forward pass": the forward pass computes q, k and v of the
+// new tokens and populates their KVs in paged memory).
+//
+//   y = x * rsqrt(mean(x^2) + eps) * w          (no weight: y = x)
+//   (a, b) -> (a cos - b sin, b cos + a sin)    pair f of the rotary columns,
+//                                               angle at the token's position
+//                                               on the axis that f belongs to
+//
+// All of it in 32 bits from the bf16 inputs, rounded to bf16 once. HBM-bound
+// for many tokens: q and k are read and written once, v goes straight to the
+// pool. A head is held by kLanes lanes, each with two 16-byte chunks that are
+// half the rotary columns apart, so that either pairing of the columns stays
+// within a lane; a warp stays with one token, so that cosines, sines and
+// weights are read once for all the heads it takes.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+
+namespace pkv {
+namespace {
+
+struct RopeArgs {
+    const __nv_bfloat16 *q, *k, *v, *q_weight, *k_weight;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements from token to token
+    __nv_bfloat16 *q_out, *k_out, *cache;
+    const int32_t *positions, *slots;
+    const float *cos_sin;
+    long long num_slots;
+    int num_tokens, num_q_heads, num_kv_heads, head_size, rotary, num_axes, num_positions;
+    int section_end[PKV_MAX_ROPE_AXES];  // axis a has the pairs [section_end[a - 1], section_end[a])
+    int parts;                           // warps that share a token's heads
+    float eps;
+    int32_t *status;
+};
+
+__device__ __forceinline__ int axis_of(const RopeArgs &a, int f) {
+    int x = 0;
+#pragma unroll
+    for (int i = 0; i < PKV_MAX_ROPE_AXES - 1; ++i) x += i < a.num_axes - 1 && f >= a.section_end[i];
+    return x;
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+}
+
+template <int kLanes, bool kInterleaved>
+__global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs a) {
+    constexpr int kHeads = 32 / kLanes;  // heads a warp holds at once
+    constexpr int kUnroll = 2;           // times that in flight
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, j = lane % kLanes;
+    const long long unit = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const long long t = unit / a.parts;
+    const int part = (int)(unit % a.parts);
+    pdl_wait();
+    if (t >= a.num_tokens) return;
+    const int D = a.head_size, half = a.rotary / 2;
+    const bool active = j < D / 16, turned = j < a.rotary / 16;
+    // this lane's two chunks of every head
+    const int c0 = turned ? j : a.rotary / 8 + 2 * (j - a.rotary / 16);
+    const int c1 = turned ? j + a.rotary / 16 : c0 + 1;
+
+    // The token's positions; a negative one is padding, one past the table
+    // is reported. Either way the token's rows are left as they are.
+    int pos[PKV_MAX_ROPE_AXES];
+    bool pad = false, bad = false;
+#pragma unroll
+    for (int x = 0; x < PKV_MAX_ROPE_AXES; ++x) {
+        pos[x] = x < a.num_axes ? __ldg(a.positions + (long long)x * a.num_tokens + t) : 0;
+        pad |= pos[x] < 0;
+        bad |= pos[x] >= a.num_positions;
+    }
+    if (pad || bad) {
+        if (!pad && part == 0 && lane == 0) raise_status(a.status, PKV_DEV_BAD_POS);
+        return;
+    }
+    long long slot = -1;
+    if (a.cache) {
+        slot = __ldg(a.slots + t);
+        if (slot >= a.num_slots) {
+            if (part == 0 && lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
+            slot = -1;
+        }
+    }
+    // Cosines and sines of this lane's eight pairs: pairs f0 .. f0 + 3 and
+    // f1 .. f1 + 3.
+    float cs[8], sn[8];
+    if (turned) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int f = kInterleaved ? (h ? c1 : c0) * 4 : j * 8 + h * 4;
+            const int x0 = axis_of(a, f);
+            if (axis_of(a, f + 3) == x0) {
+                int p = pos[0];
+#pragma unroll
+                for (int x = 1; x < PKV_MAX_ROPE_AXES; ++x) p = x == x0 ? pos[x] : p;
+                const float *row = a.cos_sin + (long long)p * a.rotary + f;
+                const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
+                const float4 s = __ldg(reinterpret_cast<const float4 *>(row + half));
+                cs[4 * h] = c.x; cs[4 * h + 1] = c.y; cs[4 * h + 2] = c.z; cs[4 * h + 3] = c.w;
+                sn[4 * h] = s.x; sn[4 * h + 1] = s.y; sn[4 * h + 2] = s.z; sn[4 * h + 3] = s.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int xe = axis_of(a, f + e);
+                    int p = pos[0];
+#pragma unroll
+                    for (int x = 1; x < PKV_MAX_ROPE_AXES; ++x) p = x == xe ? pos[x] : p;
+                    const float *row = a.cos_sin + (long long)p * a.rotary + f + e;
+                    cs[4 * h + e] = __ldg(row);
+                    sn[4 * h + e] = __ldg(row + half);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            cs[e] = 1.f;
+            sn[e] = 0.f;
+        }
+    }
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 wq[2] = {zero, zero}, wk[2] = {zero, zero};
+    if (active && a.q_weight) {
+        wq[0] = __ldg(reinterpret_cast<const uint4 *>(a.q_weight) + c0);
+        wq[1] = __ldg(reinterpret_cast<const uint4 *>(a.q_weight) + c1);
+    }
+    if (active && a.k_weight) {
+        wk[0] = __ldg(reinterpret_cast<const uint4 *>(a.k_weight) + c0);
+        wk[1] = __ldg(reinterpret_cast<const uint4 *>(a.k_weight) + c1);
+    }
+
+    const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;
+    const int heads = Hq + Hkv + (slot >= 0 ? Hkv : 0);
+    const uint4 *qs = reinterpret_cast<const uint4 *>(a.q + t * a.q_stride);
+    const uint4 *ks = reinterpret_cast<const uint4 *>(a.k + t * a.k_stride);
+    const uint4 *vs = reinterpret_cast<const uint4 *>(a.v + t * a.v_stride);
+    const int row = D / 8;  // 16-byte chunks of a head
+    const long long tile = (long long)PKV_BLOCK_SIZE * row;
+    uint4 *kv_row = reinterpret_cast<uint4 *>(a.cache) +
+                    (slot >= 0 ? slot / PKV_BLOCK_SIZE * 2 * Hkv * tile + slot % PKV_BLOCK_SIZE * row : 0);
+    for (int base = part * kHeads * kUnroll; base < heads; base += a.parts * kHeads * kUnroll) {
+        uint4 in[kUnroll][2];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int h = base + u * kHeads + lane / kLanes;
+            in[u][0] = in[u][1] = zero;
+            if (active && h < heads) {
+                const uint4 *src = h < Hq ? qs + h * row : h < Hq + Hkv ? ks + (h - Hq) * row : vs + (h - Hq - Hkv) * row;
+                in[u][0] = src[c0];  // not through the read-only path: the outputs may be the inputs
+                in[u][1] = src[c1];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int h = base + u * kHeads + lane / kLanes;
+            const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
+            float x0[8], x1[8];
+            unpack8(in[u][0], x0);
+            unpack8(in[u][1], x1);
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
+#pragma unroll
+            for (int d = kLanes / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+            if (is_v) {
+                if (active && h < heads) {
+                    uint4 *dst = kv_row + (long long)(Hkv + h - Hq - Hkv) * tile;
+                    dst[c0] = in[u][0];
+                    dst[c1] = in[u][1];
+                }
+                continue;
+            }
+            if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+                const float rs = rsqrtf(ss / (float)D + a.eps);
+                float w0[8], w1[8];
+                unpack8(is_q ? wq[0] : wk[0], w0);
+                unpack8(is_q ? wq[1] : wk[1], w1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x0[e] = x0[e] * rs * w0[e];
+                    x1[e] = x1[e] * rs * w1[e];
+                }
+            }
+            if (turned) {
+                if (kInterleaved) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a0 = x0[2 * e], b0 = x0[2 * e + 1], a1 = x1[2 * e], b1 = x1[2 * e + 1];
+                        x0[2 * e] = a0 * cs[e] - b0 * sn[e];
+                        x0[2 * e + 1] = b0 * cs[e] + a0 * sn[e];
+                        x1[2 * e] = a1 * cs[4 + e] - b1 * sn[4 + e];
+                        x1[2 * e + 1] = b1 * cs[4 + e] + a1 * sn[4 + e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float p = x0[e], r = x1[e];
+                        x0[e] = p * cs[e] - r * sn[e];
+                        x1[e] = r * cs[e] + p * sn[e];
+                    }
+                }
+            }
+            if (!active || h >= heads) continue;
+            const uint4 y0 = pack8(x0), y1 = pack8(x1);
+            if (is_q) {
+                uint4 *dst = reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride) + h * row;
+                dst[c0] = y0;
+                dst[c1] = y1;
+            } else {
+                if (a.k_out) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride) + (h - Hq) * row;
+                    dst[c0] = y0;
+                    dst[c1] = y1;
+                }
+                if (slot >= 0) {
+                    uint4 *dst = kv_row + (long long)(h - Hq) * tile;
+                    dst[c0] = y0;
+                    dst[c1] = y1;
+                }
+            }
+        }
+    }
+}
+
+template <int kLanes>
+cudaError_t launch(const RopeArgs &a, bool interleaved, cudaStream_t st) {
+    const long long units = (long long)a.num_tokens * a.parts;
+    const dim3 grid((unsigned)((units + 7) / 8));
+    return interleaved ? launch_pdl(qk_rope_kernel<kLanes, true>, grid, dim3(256), 0, st, a)
+                       : launch_pdl(qk_rope_kernel<kLanes, false>, grid, dim3(256), 0, st, a);
+}
+
+bool stride_ok(long long stride, long long width, int tokens) {
+    return stride % 8 == 0 && (tokens <= 1 || stride >= width) && stride < (1LL << 32);
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" PKV_API int paged_qk_norm_rope(const pkv_rope_desc *d, const void *q, const void *k, const void *v,
+                                          int32_t num_tokens, const void *q_weight, const void *k_weight,
+                                          const int32_t *positions, const float *cos_sin, void *q_out, void *k_out,
+                                          const int32_t *slot_mapping, void *kv_cache, int32_t num_blocks,
+                                          int32_t *status, void *stream) {
+    if (!d) return PKV_E_NULL;
+    if (d->head_size <= 0 || d->head_size % 16 != 0 || d->head_size > 256) return PKV_E_HEAD_SIZE;
+    if (num_tokens < 0 || d->num_q_heads <= 0 || d->num_kv_heads <= 0 || d->num_q_heads > 4096 ||
+        d->num_kv_heads > 4096)
+        return PKV_E_DIMS;
+    if (d->rotary_dim < 16 || d->rotary_dim % 16 != 0 || d->rotary_dim > d->head_size || d->num_positions <= 0)
+        return PKV_E_DIMS;
+    if (d->num_axes < 1 || d->num_axes > PKV_MAX_ROPE_AXES || !(d->eps >= 0.f)) return PKV_E_DIMS;
+    RopeArgs a{};
+    int end = 0;
+    for (int x = 0; x < d->num_axes; ++x) {
+        const int n = d->num_axes == 1 ? d->rotary_dim / 2 : d->axis_pairs[x];
+        if (n < 0 || n > d->rotary_dim / 2) return PKV_E_DIMS;
+        end += n;
+        a.section_end[x] = end;
+    }
+    if (end != d->rotary_dim / 2) return PKV_E_DIMS;
+    const long long wq = (long long)d->num_q_heads * d->head_size, wkv = (long long)d->num_kv_heads * d->head_size;
+    if (!stride_ok(d->q_stride, wq, num_tokens) || !stride_ok(d->k_stride, wkv, num_tokens) ||
+        !stride_ok(d->q_out_stride, wq, num_tokens) || (k_out && !stride_ok(d->k_out_stride, wkv, num_tokens)) ||
+        (kv_cache && !stride_ok(d->v_stride, wkv, num_tokens)))
+        return PKV_E_DIMS;
+    if (kv_cache && (num_blocks <= 0 || num_blocks > INT32_MAX / PKV_BLOCK_SIZE)) return PKV_E_DIMS;
+    if (num_tokens == 0) return PKV_OK;
+    if (!q || !k || !positions || !cos_sin || !q_out || (kv_cache && (!v || !slot_mapping))) return PKV_E_NULL;
+    if (!k_out && !kv_cache) return PKV_E_NULL;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+        !aligned(cos_sin, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(kv_cache, 16) ||
+        !aligned(positions, 4) || !aligned(slot_mapping, 4) || !aligned(status, 4))
+        return PKV_E_ALIGN;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.q_weight = static_cast<const __nv_bfloat16 *>(q_weight);
+    a.k_weight = static_cast<const __nv_bfloat16 *>(k_weight);
+    a.q_stride = d->q_stride;
+    a.k_stride = d->k_stride;
+    a.v_stride = d->v_stride;
+    a.q_out_stride = d->q_out_stride;
+    a.k_out_stride = d->k_out_stride;
+    a.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    a.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    a.cache = static_cast<__nv_bfloat16 *>(kv_cache);
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.cos_sin = cos_sin;
+    a.num_slots = (long long)num_blocks * PKV_BLOCK_SIZE;
+    a.num_tokens = num_tokens;
+    a.num_q_heads = d->num_q_heads;
+    a.num_kv_heads = d->num_kv_heads;
+    a.head_size = d->head_size;
+    a.rotary = d->rotary_dim;
+    a.num_axes = d->num_axes;
+    a.num_positions = d->num_positions;
+    a.eps = d->eps;
+    a.status = status;
+    const int lanes = d->head_size <= 64 ? 4 : d->head_size <= 128 ? 8 : 16;
+    const int steps = (d->num_q_heads + 2 * d->num_kv_heads + 64 / lanes - 1) / (64 / lanes);
+    // A token's heads are shared out over more warps while the tokens alone
+    // do not fill the GPU.
+    a.parts = 1;
+    while (a.parts < steps && (long long)num_tokens * a.parts < 8192) ++a.parts;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t err = lanes == 4 ? launch<4>(a, d->interleaved != 0, st)
+                            : lanes == 8 ? launch<8>(a, d->interleaved != 0, st)
+                                         : launch<16>(a, d->interleaved != 0, st);
+    return err == cudaSuccess ? PKV_OK : PKV_E_CUDA;
+}
