@@ -39,22 +39,31 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-// Tokens and blocks summed together (64 bits each: the lengths are the
-// caller's, their sums may pass 32).
+// Tokens and blocks summed side by side, each clamped to its cap: one more
+// than the step's rows, one more than the ids left. A sum at its cap refuses
+// its request whatever its exact value, and clamped sums of counts are still
+// associative, so 32 bits do for any lengths.
 struct Sums {
-    long long tok, blk;
+    uint32_t tok, blk;
 };
 
-__device__ __forceinline__ Sums warp_inclusive(Sums v, int lane) {
+__device__ __forceinline__ Sums add(Sums a, Sums b, Sums cap) {
+    return {min(a.tok + b.tok, cap.tok), min(a.blk + b.blk, cap.blk)};
+}
+
+__device__ __forceinline__ Sums shift(Sums v, int d) {
+    return {__shfl_up_sync(0xffffffffu, v.tok, d), __shfl_up_sync(0xffffffffu, v.blk, d)};
+}
+
+// Inclusive sums over the warp; *before: the exclusive ones.
+__device__ __forceinline__ Sums warp_scan(Sums v, Sums cap, int lane, Sums *before) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, v.tok, d);
-        const long long b = __shfl_up_sync(0xffffffffu, v.blk, d);
-        if (lane >= d) {
-            v.tok += t;
-            v.blk += b;
-        }
+        const Sums o = shift(v, d);
+        if (lane >= d) v = add(v, o, cap);
     }
+    *before = shift(v, 1);
+    if (lane == 0) *before = {0, 0};
     return v;
 }
 
@@ -62,20 +71,21 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs a) {
     constexpr int kWarps = kThreads / 32;
     __shared__ Sums s_warp[kWarps];
-    __shared__ long long s_taken[kWarps];
-    __shared__ int s_start[kThreads + 1];  // first token of each request of the pass, at most num_tokens
+    __shared__ int s_start[kThreads + 1];  // first row of each request of the pass, at most num_tokens
     __shared__ int s_len[kThreads];        // context before the step; -1: the request is refused
-    __shared__ int s_base[kThreads];       // its first new block in free_blocks
+    __shared__ int s_base[kThreads];       // its first new id in free_blocks
+    __shared__ uint32_t s_taken;           // ids handed out so far
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int T = a.num_tokens;
+    if (tid == 0) s_taken = 0;
     // No early trigger: kernels of this library that read the tables ahead
     // of their own wait must not start before this one has finished.
     pdl_wait();
     const int cur = a.cursor ? *a.cursor : 0;
-    const long long avail = cur >= 0 && cur <= a.num_free ? a.num_free - cur : 0;
+    const uint32_t avail = cur >= 0 && cur <= a.num_free ? a.num_free - cur : 0;
+    const Sums cap{(uint32_t)T + 1, avail + 1};
     Sums carry{0, 0};
-    long long taken = 0;  // blocks handed out so far
     int bits = 0;
     for (int r0 = 0; r0 == 0 || r0 < a.num_reqs; r0 += kThreads) {
         const int r = r0 + tid;
@@ -89,46 +99,40 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs 
         const long long L1 = (long long)L0 + n;
         bool refused = L0 < 0 || L1 > (long long)a.max_blocks_per_req * PKV_BLOCK_SIZE;
         if (refused) bits |= PKV_DEV_BAD_LEN;
-        Sums v{n, refused ? 0 : (L1 + 15) / 16 - (L0 + 15LL) / 16};
-        const long long need = v.blk;
-        v = warp_inclusive(v, lane);
+        const uint32_t need = refused ? 0 : (uint32_t)((L1 + 15) / 16 - (L0 + 15LL) / 16);
+        Sums before;
+        const Sums v = warp_scan({min((uint32_t)n, cap.tok), min(need, cap.blk)}, cap, lane, &before);
         if (lane == 31) s_warp[warp] = v;
         __syncthreads();
-        Sums before = carry;
-        for (int w = 0; w < kWarps; ++w) {
-            const Sums s = s_warp[w];
-            if (w < warp) {
-                before.tok += s.tok;
-                before.blk += s.blk;
-            }
-            carry.tok += s.tok;
-            carry.blk += s.blk;
-        }
-        const long long end = before.tok + v.tok, first = before.blk + v.blk - need;
-        // Requests whose tokens do not fit the step, or whose blocks are not
-        // there, get nothing. Both sums only grow, so a refusal never changes
+        // every warp adds up the warps before it, each lane one warp's sums
+        Sums base;
+        const Sums upto = warp_scan(lane < kWarps ? s_warp[lane] : Sums{0, 0}, cap, lane, &base);
+        base = {__shfl_sync(0xffffffffu, base.tok, warp), __shfl_sync(0xffffffffu, base.blk, warp)};
+        base = add(carry, base, cap);
+        const Sums first = add(base, before, cap), end = add(base, v, cap);
+        carry = add(carry, {__shfl_sync(0xffffffffu, upto.tok, 31), __shfl_sync(0xffffffffu, upto.blk, 31)}, cap);
+        // Requests whose rows do not fit the step, or whose blocks are not
+        // there, get nothing. The sums only grow, so a refusal never changes
         // what the requests before it got.
-        if (end > T && n > 0) {
+        if (n > 0 && end.tok > (uint32_t)T) {
             refused = true;
             bits |= PKV_DEV_BAD_QSL;
         }
-        if (need > 0 && first + need > avail) {
+        if (need > 0 && end.blk > avail) {
             refused = true;
             bits |= PKV_DEV_NO_BLOCKS;
         }
-        s_start[tid] = (int)min(end - n, (long long)T);
+        s_start[tid] = (int)min(first.tok, (uint32_t)T);
         s_len[tid] = refused ? -1 : L0;
-        s_base[tid] = refused ? 0 : (int)(cur + first);
-        if (tid == kThreads - 1) s_start[kThreads] = (int)min(end, (long long)T);
-        long long got = refused ? 0 : need;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) got += __shfl_xor_sync(0xffffffffu, got, d);
-        if (lane == 0) s_taken[warp] = got;
+        s_base[tid] = refused ? 0 : cur + (int)first.blk;
+        if (tid == kThreads - 1) s_start[kThreads] = (int)min(end.tok, (uint32_t)T);
+        const uint32_t got = __reduce_max_sync(0xffffffffu, refused || need == 0 ? 0u : end.blk);
+        if (lane == 0 && got) atomicMax(&s_taken, got);
         __syncthreads();
         cluster_arrive();  // this CTA has read the pass's lengths (and the cursor)
-        for (int w = 0; w < kWarps; ++w) taken += s_taken[w];
 
         const int t0 = s_start[0], t1 = s_start[kThreads];
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
         for (int g = (t0 >> 2) + (int)rank * kThreads + tid; g < ((t1 + 3) >> 2);
              g += (int)(gridDim.x * kThreads)) {
             int pos[4], slot[4];
@@ -138,11 +142,16 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs 
                 const int t = 4 * g + e;
                 pos[e] = slot[e] = -1;
                 if (t < t0 || t >= t1) continue;
-                if (j < 0 || t >= nxt) {  // last request of the pass that starts at or before t
-                    int lo = 0, hi = kThreads;
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) >> 1;
-                        if (s_start[mid] <= t) lo = mid; else hi = mid;
+                if (j < 0 || t >= nxt) {
+                    // the last request of the pass that starts at or before t
+                    int lo = j < 0 ? 0 : j, hi = kThreads;
+                    if (j >= 0 && (j + 2 >= kThreads || s_start[j + 2] > t)) {
+                        lo = j + 1;  // the next one, as among decode requests
+                    } else {
+                        while (hi - lo > 1) {
+                            const int mid = (lo + hi) >> 1;
+                            if (s_start[mid] <= t) lo = mid; else hi = mid;
+                        }
                     }
                     j = lo;
                     nxt = s_start[j + 1];
@@ -161,6 +170,12 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs 
                 pos[e] = p;
                 slot[e] = id < 0 ? -1 : id * PKV_BLOCK_SIZE + p % PKV_BLOCK_SIZE;
             }
+            if (wide && 4 * g >= t0 && 4 * g + 3 < t1) {
+                *reinterpret_cast<int4 *>(a.slots + 4 * g) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                if (a.positions)
+                    *reinterpret_cast<int4 *>(a.positions + 4 * g) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+                continue;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = 4 * g + e;
@@ -173,19 +188,19 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs 
         cluster_wait();
         if (rank == 0 && in) {
             a.seq_lens[r] = refused ? L0 : (int)L1;
-            a.qsl[r + 1] = (int)min(end, (long long)T);
+            a.qsl[r + 1] = (int)min(end.tok, (uint32_t)T);
         }
         __syncthreads();
     }
     // rows behind the last request
-    for (long long t = min(carry.tok, (long long)T) + (long long)rank * kThreads + tid; t < T;
+    for (long long t = (long long)min(carry.tok, (uint32_t)T) + (long long)rank * kThreads + tid; t < T;
          t += gridDim.x * kThreads) {
         a.slots[t] = -1;
         if (a.positions) a.positions[t] = -1;
     }
     if (rank == 0 && tid == 0) {
         a.qsl[0] = 0;
-        if (a.cursor_out) *a.cursor_out = (int)(cur + taken);
+        if (a.cursor_out) *a.cursor_out = cur + (int)s_taken;
     }
     if (bits) raise_status(a.status, bits);
     __threadfence();
@@ -223,7 +238,7 @@ extern "C" PKV_API int paged_build_tables(const int32_t *query_lens, const int32
     if (num_reqs < 0 || num_tokens < 0 || num_free < 0 || max_blocks_per_req < 0 || num_blocks <= 0)
         return PKV_E_DIMS;
     if (num_blocks > INT32_MAX / PKV_BLOCK_SIZE || max_blocks_per_req > INT32_MAX / PKV_BLOCK_SIZE ||
-        num_tokens > INT32_MAX - 65536 || num_reqs > INT32_MAX - 65536)
+        num_tokens > INT32_MAX - 65536 || num_reqs > INT32_MAX - 65536 || num_free > INT32_MAX - 65536)
         return PKV_E_DIMS;
     if (!query_start_loc || (num_tokens > 0 && !slot_mapping) || (num_free > 0 && !free_blocks)) return PKV_E_NULL;
     if (num_reqs > 0 && (!query_lens || !context_lens || !seq_lens || (max_blocks_per_req > 0 && !block_table)))
@@ -236,6 +251,8 @@ extern "C" PKV_API int paged_build_tables(const int32_t *query_lens, const int32
                       num_tokens,  num_blocks,   block_table, seq_lens,     query_start_loc, positions, slot_mapping,
                       free_cursor_out, status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t err = num_tokens <= 4096 ? launch<1024>(a, 1, st) : launch<1024>(a, 8, st);
+    const cudaError_t err = num_tokens <= 1024 && num_reqs <= 256 ? launch<256>(a, 1, st)
+                            : num_tokens <= 4096                  ? launch<1024>(a, 1, st)
+                                                                  : launch<1024>(a, 8, st);
     return err == cudaSuccess ? PKV_OK : PKV_E_CUDA;
 }

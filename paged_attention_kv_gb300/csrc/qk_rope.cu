@@ -13,8 +13,10 @@
 // for many tokens: q and k are read and written once, v goes straight to the
 // pool. A head is held by kLanes lanes, each with two 16-byte chunks that are
 // half the rotary columns apart, so that either pairing of the columns stays
-// within a lane; a warp stays with one token, so that cosines, sines and
-// weights are read once for all the heads it takes.
+// within a lane; a warp stays with one token, so that positions, cosines and
+// sines are read once for all the heads it takes. Two steps of heads are in
+// flight ahead of the one at work; the arithmetic is on packed pairs (the
+// scalar form was bound by instruction issue: 158 against 147 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,17 +30,26 @@
 namespace pkv {
 namespace {
 
+// Three blocks of 8 warps an SM: 80 registers hold a warp's two heads in
+// flight without much spilling (32768 tokens of 32/8 heads x 128 columns: 147
+// us; two blocks 168, four blocks, at 64 registers, 169).
+constexpr int kBlocksPerSm = 3;
+// Warps wanted before a token's heads stay with one warp: as many as run at
+// once. More warps repeat the token's look-ups for nothing (2240 tokens: 10.3
+// us at 4,864; 19,456 or one step a warp, 1.3 times that; one warp a token, 1.9).
+constexpr int kWarpsWanted = 4864;
+
 struct RopeArgs {
     const __nv_bfloat16 *q, *k, *v, *q_weight, *k_weight;
     long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements from token to token
     __nv_bfloat16 *q_out, *k_out, *cache;
     const int32_t *positions, *slots;
     const float *cos_sin;
-    long long num_slots;
+    int num_slots;
     int num_tokens, num_q_heads, num_kv_heads, head_size, rotary, num_axes, num_positions;
     int section_end[PKV_MAX_ROPE_AXES];  // axis a has the pairs [section_end[a - 1], section_end[a])
     int parts;                           // warps that share a token's heads
-    float eps;
+    float eps, inv_d;
     int32_t *status;
 };
 
@@ -49,36 +60,58 @@ __device__ __forceinline__ int axis_of(const RopeArgs &a, int f) {
     return x;
 }
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+// Eight bf16 values as four pairs of floats, and back.
+__device__ __forceinline__ void unpack8(uint4 v, float2 (&x)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+    return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                      pack_bf16x2(x[3].x, x[3].y));
 }
 
 template <int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(256, kBlocksPerSm) qk_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int kHeads = 32 / kLanes;  // heads a warp holds at once
-    constexpr int kUnroll = 2;           // times that in flight
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, j = lane % kLanes;
     const long long unit = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const long long t = unit / a.parts;
-    const int part = (int)(unit % a.parts);
-    pdl_wait();
+    const int part = (int)(unit - t * a.parts);
     if (t >= a.num_tokens) return;
     const int D = a.head_size, half = a.rotary / 2;
     const bool active = j < D / 16, turned = j < a.rotary / 16;
     // this lane's two chunks of every head
     const int c0 = turned ? j : a.rotary / 8 + 2 * (j - a.rotary / 16);
     const int c1 = turned ? j + a.rotary / 16 : c0 + 1;
+    const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;
+    const int heads = Hq + Hkv + (a.cache ? Hkv : 0);
+    const int row = D / 8;  // 16-byte chunks of a head
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    struct Head {
+        uint4 x0, x1;
+    };
+    // Not through the read-only path: the outputs may be the inputs. (A warp
+    // reads a head before it writes it, and no other warp touches it.)
+    const __nv_bfloat16 *qt = a.q + t * a.q_stride, *kt = a.k + t * a.k_stride - Hq * D,
+                        *vt = a.v + t * a.v_stride - (Hq + Hkv) * D;
+    auto load = [&](int h) {
+        Head r{zero, zero};
+        if (active && h < heads) {
+            const uint4 *src = reinterpret_cast<const uint4 *>((h < Hq ? qt : h < Hq + Hkv ? kt : vt) + h * D);
+            r.x0 = src[c0];
+            r.x1 = src[c1];
+        }
+        return r;
+    };
+    pdl_wait();
+    // The first heads are on their way before the position and what hangs on
+    // it are looked up.
+    const int step = a.parts * kHeads;
+    int h = part * kHeads + lane / kLanes;
+    Head cur = load(h), next = load(h + step);
 
     // The token's positions; a negative one is padding, one past the table
     // is reported. Either way the token's rows are left as they are.
@@ -90,35 +123,36 @@ __global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs a) {
         pad |= pos[x] < 0;
         bad |= pos[x] >= a.num_positions;
     }
+    int slot = a.cache ? __ldg(a.slots + t) : -1;
     if (pad || bad) {
         if (!pad && part == 0 && lane == 0) raise_status(a.status, PKV_DEV_BAD_POS);
         return;
     }
-    long long slot = -1;
-    if (a.cache) {
-        slot = __ldg(a.slots + t);
-        if (slot >= a.num_slots) {
-            if (part == 0 && lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
-            slot = -1;
-        }
+    if (slot >= a.num_slots) {
+        if (part == 0 && lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
+        slot = -1;
     }
-    // Cosines and sines of this lane's eight pairs: pairs f0 .. f0 + 3 and
-    // f1 .. f1 + 3.
+    // Cosines and sines of this lane's eight pairs, f0 .. f0 + 3 and f1 .. f1 + 3.
     float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+    }
     if (turned) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int f = kInterleaved ? (h ? c1 : c0) * 4 : j * 8 + h * 4;
+        for (int g = 0; g < 2; ++g) {
+            const int f = kInterleaved ? (g ? c1 : c0) * 4 : j * 8 + g * 4;
             const int x0 = axis_of(a, f);
             if (axis_of(a, f + 3) == x0) {
                 int p = pos[0];
 #pragma unroll
                 for (int x = 1; x < PKV_MAX_ROPE_AXES; ++x) p = x == x0 ? pos[x] : p;
-                const float *row = a.cos_sin + (long long)p * a.rotary + f;
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
-                const float4 s = __ldg(reinterpret_cast<const float4 *>(row + half));
-                cs[4 * h] = c.x; cs[4 * h + 1] = c.y; cs[4 * h + 2] = c.z; cs[4 * h + 3] = c.w;
-                sn[4 * h] = s.x; sn[4 * h + 1] = s.y; sn[4 * h + 2] = s.z; sn[4 * h + 3] = s.w;
+                const float *at = a.cos_sin + (long long)p * a.rotary + f;
+                const float4 c = __ldg(reinterpret_cast<const float4 *>(at));
+                const float4 s = __ldg(reinterpret_cast<const float4 *>(at + half));
+                cs[4 * g] = c.x; cs[4 * g + 1] = c.y; cs[4 * g + 2] = c.z; cs[4 * g + 3] = c.w;
+                sn[4 * g] = s.x; sn[4 * g + 1] = s.y; sn[4 * g + 2] = s.z; sn[4 * g + 3] = s.w;
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -126,118 +160,84 @@ __global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs a) {
                     int p = pos[0];
 #pragma unroll
                     for (int x = 1; x < PKV_MAX_ROPE_AXES; ++x) p = x == xe ? pos[x] : p;
-                    const float *row = a.cos_sin + (long long)p * a.rotary + f + e;
-                    cs[4 * h + e] = __ldg(row);
-                    sn[4 * h + e] = __ldg(row + half);
+                    const float *at = a.cos_sin + (long long)p * a.rotary + f + e;
+                    cs[4 * g + e] = __ldg(at);
+                    sn[4 * g + e] = __ldg(at + half);
                 }
             }
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cs[e] = 1.f;
-            sn[e] = 0.f;
-        }
     }
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 wq[2] = {zero, zero}, wk[2] = {zero, zero};
-    if (active && a.q_weight) {
-        wq[0] = __ldg(reinterpret_cast<const uint4 *>(a.q_weight) + c0);
-        wq[1] = __ldg(reinterpret_cast<const uint4 *>(a.q_weight) + c1);
-    }
-    if (active && a.k_weight) {
-        wk[0] = __ldg(reinterpret_cast<const uint4 *>(a.k_weight) + c0);
-        wk[1] = __ldg(reinterpret_cast<const uint4 *>(a.k_weight) + c1);
-    }
-
-    const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;
-    const int heads = Hq + Hkv + (slot >= 0 ? Hkv : 0);
-    const uint4 *qs = reinterpret_cast<const uint4 *>(a.q + t * a.q_stride);
-    const uint4 *ks = reinterpret_cast<const uint4 *>(a.k + t * a.k_stride);
-    const uint4 *vs = reinterpret_cast<const uint4 *>(a.v + t * a.v_stride);
-    const int row = D / 8;  // 16-byte chunks of a head
     const long long tile = (long long)PKV_BLOCK_SIZE * row;
     uint4 *kv_row = reinterpret_cast<uint4 *>(a.cache) +
-                    (slot >= 0 ? slot / PKV_BLOCK_SIZE * 2 * Hkv * tile + slot % PKV_BLOCK_SIZE * row : 0);
-    for (int base = part * kHeads * kUnroll; base < heads; base += a.parts * kHeads * kUnroll) {
-        uint4 in[kUnroll][2];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = base + u * kHeads + lane / kLanes;
-            in[u][0] = in[u][1] = zero;
-            if (active && h < heads) {
-                const uint4 *src = h < Hq ? qs + h * row : h < Hq + Hkv ? ks + (h - Hq) * row : vs + (h - Hq - Hkv) * row;
-                in[u][0] = src[c0];  // not through the read-only path: the outputs may be the inputs
-                in[u][1] = src[c1];
+                    (slot >= 0 ? (long long)(slot / PKV_BLOCK_SIZE) * 2 * Hkv * tile + slot % PKV_BLOCK_SIZE * row : 0);
+    // The warp's heads: all lanes go round equally often (the norms' sums
+    // cross lanes), those past the last head with zeros.
+    for (int base = part * kHeads; base < heads; base += step, h += step) {
+        const Head in = cur;
+        cur = next;
+        next = load(h + 2 * step);
+        const bool live = active && h < heads;
+        if (h >= Hq + Hkv) {
+            if (live && slot >= 0) {
+                uint4 *dst = kv_row + (h - Hq) * tile;  // V's heads lie behind K's
+                dst[c0] = in.x0;
+                dst[c1] = in.x1;
             }
         }
+        float2 x0[4], x1[4];
+        unpack8(in.x0, x0);
+        unpack8(in.x1, x1);
+        if (a.q_weight || a.k_weight) {
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int h = base + u * kHeads + lane / kLanes;
-            const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
-            float x0[8], x1[8];
-            unpack8(in[u][0], x0);
-            unpack8(in[u][1], x1);
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
+            for (int e = 0; e < 4; ++e) s2 = ffma2(x0[e], x0[e], ffma2(x1[e], x1[e], s2));
+            float ss = s2.x + s2.y;
 #pragma unroll
             for (int d = kLanes / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            if (is_v) {
-                if (active && h < heads) {
-                    uint4 *dst = kv_row + (long long)(Hkv + h - Hq - Hkv) * tile;
-                    dst[c0] = in[u][0];
-                    dst[c1] = in[u][1];
-                }
-                continue;
-            }
-            if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-                const float rs = rsqrtf(ss / (float)D + a.eps);
-                float w0[8], w1[8];
-                unpack8(is_q ? wq[0] : wk[0], w0);
-                unpack8(is_q ? wq[1] : wk[1], w1);
+            const __nv_bfloat16 *w = h < Hq ? a.q_weight : a.k_weight;
+            if (w && active) {
+                const float rs = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+                const float2 rs2 = make_float2(rs, rs);
+                float2 w0[4], w1[4];
+                unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + c0), w0);
+                unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + c1), w1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x0[e] = x0[e] * rs * w0[e];
-                    x1[e] = x1[e] * rs * w1[e];
+                for (int e = 0; e < 4; ++e) {
+                    x0[e] = fmul2(fmul2(x0[e], rs2), w0[e]);
+                    x1[e] = fmul2(fmul2(x1[e], rs2), w1[e]);
                 }
             }
-            if (turned) {
-                if (kInterleaved) {
+        }
+        if (!live || h >= Hq + Hkv) continue;
+        if (turned) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a0 = x0[2 * e], b0 = x0[2 * e + 1], a1 = x1[2 * e], b1 = x1[2 * e + 1];
-                        x0[2 * e] = a0 * cs[e] - b0 * sn[e];
-                        x0[2 * e + 1] = b0 * cs[e] + a0 * sn[e];
-                        x1[2 * e] = a1 * cs[4 + e] - b1 * sn[4 + e];
-                        x1[2 * e + 1] = b1 * cs[4 + e] + a1 * sn[4 + e];
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float p = x0[e], r = x1[e];
-                        x0[e] = p * cs[e] - r * sn[e];
-                        x1[e] = r * cs[e] + p * sn[e];
-                    }
+            for (int e = 0; e < 4; ++e) {
+                const float2 p = x0[e], r = x1[e];
+                if (kInterleaved) {  // columns 2e and 2e + 1 of a chunk
+                    x0[e] = make_float2(p.x * cs[e] - p.y * sn[e], p.y * cs[e] + p.x * sn[e]);
+                    x1[e] = make_float2(r.x * cs[4 + e] - r.y * sn[4 + e], r.y * cs[4 + e] + r.x * sn[4 + e]);
+                } else {             // the same column of both chunks
+                    const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]), s = make_float2(sn[2 * e], sn[2 * e + 1]);
+                    x0[e] = ffma2(r, make_float2(-s.x, -s.y), fmul2(p, c));
+                    x1[e] = ffma2(p, s, fmul2(r, c));
                 }
             }
-            if (!active || h >= heads) continue;
-            const uint4 y0 = pack8(x0), y1 = pack8(x1);
-            if (is_q) {
-                uint4 *dst = reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride) + h * row;
+        }
+        const uint4 y0 = pack8(x0), y1 = pack8(x1);
+        if (h < Hq) {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride) + h * row;
+            dst[c0] = y0;
+            dst[c1] = y1;
+        } else {
+            if (a.k_out) {
+                uint4 *dst = reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride) + (h - Hq) * row;
                 dst[c0] = y0;
                 dst[c1] = y1;
-            } else {
-                if (a.k_out) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.k_out + t * a.k_out_stride) + (h - Hq) * row;
-                    dst[c0] = y0;
-                    dst[c1] = y1;
-                }
-                if (slot >= 0) {
-                    uint4 *dst = kv_row + (long long)(h - Hq) * tile;
-                    dst[c0] = y0;
-                    dst[c1] = y1;
-                }
+            }
+            if (slot >= 0) {
+                uint4 *dst = kv_row + (h - Hq) * tile;
+                dst[c0] = y0;
+                dst[c1] = y1;
             }
         }
     }
@@ -311,7 +311,7 @@ extern "C" PKV_API int paged_qk_norm_rope(const pkv_rope_desc *d, const void *q,
     a.positions = positions;
     a.slots = slot_mapping;
     a.cos_sin = cos_sin;
-    a.num_slots = (long long)num_blocks * PKV_BLOCK_SIZE;
+    a.num_slots = num_blocks * PKV_BLOCK_SIZE;
     a.num_tokens = num_tokens;
     a.num_q_heads = d->num_q_heads;
     a.num_kv_heads = d->num_kv_heads;
@@ -320,13 +320,14 @@ extern "C" PKV_API int paged_qk_norm_rope(const pkv_rope_desc *d, const void *q,
     a.num_axes = d->num_axes;
     a.num_positions = d->num_positions;
     a.eps = d->eps;
+    a.inv_d = 1.f / (float)d->head_size;
     a.status = status;
     const int lanes = d->head_size <= 64 ? 4 : d->head_size <= 128 ? 8 : 16;
-    const int steps = (d->num_q_heads + 2 * d->num_kv_heads + 64 / lanes - 1) / (64 / lanes);
+    const int steps = (d->num_q_heads + 2 * d->num_kv_heads + 32 / lanes - 1) / (32 / lanes);
     // A token's heads are shared out over more warps while the tokens alone
     // do not fill the GPU.
     a.parts = 1;
-    while (a.parts < steps && (long long)num_tokens * a.parts < 8192) ++a.parts;
+    while (a.parts < steps && (long long)num_tokens * a.parts < kWarpsWanted) ++a.parts;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t err = lanes == 4 ? launch<4>(a, d->interleaved != 0, st)
                             : lanes == 8 ? launch<8>(a, d->interleaved != 0, st)
