@@ -51,8 +51,11 @@ namespace pkv {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kMmaWarp = 8, kCopyWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kMmaWarp = 0, kCopyWarp = 1, kSoftmaxWarp = 4, kOutWarp = 12;  // softmax 4-11, output 12-15
+constexpr int kThreads = 512;
+// Registers a thread: the softmax holds a row of 128 scores and 32 words of P.
+// Four warpgroups of 128 at launch: 2 * (64 + 192) = 4 * 128.
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;           // S_A 0, S_B 128, O_A 256, O_B 256 + D
 constexpr float kRescaleThreshold = 8.f;  // log2 units: P stays <= 2^8
@@ -77,7 +80,7 @@ struct Item {
 
 struct Bars {
     static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6 /* [tile][half] */, kPvDone = 10, kDFull = 12,
-                         kDEmpty = 14, kDrain = 16, kKvFull = 17;
+                         kDEmpty = 14, kOFull = 16, kLFull = 18, kOFree = 20, kDrain = 22, kKvFull = 23;
 };
 
 template <int D>
@@ -90,15 +93,67 @@ struct Smem {
     static constexpr int kOffItem = kOffKv + kStages * kTile;
     static constexpr int kOffBar = kOffItem + 2 * (int)sizeof(Item);
     static constexpr int kBars = Bars::kKvFull + 2 * kStages;
-    static constexpr int kOffSeq = kOffBar + kBars * 8;
+    static constexpr int kOffSum = kOffBar + kBars * 8;  // float [tile][row]: sums of p
+    static constexpr int kOffSeq = kOffSum + 2 * kRows * 4;
     static constexpr int kBytes = kOffSeq + kSeqCache * 4;
     static constexpr int kAlloc = kBytes + 1024;
 };
 static_assert(Smem<128>::kAlloc <= 232448 - 1024, "prompt kernel shared memory");
 static_assert(Smem<64>::kAlloc <= 232448 - 1024, "prompt kernel shared memory");
 
+// A bounded wait that the whole warp leaves with one answer. No call in it:
+// values that live across a call are kept out of uniform registers, where the
+// MMA instructions want them (60 to 90 cycles an MMA instead of 15, more than
+// the tensor core's 64), and a role's registers must not pass through one.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort));
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = global_timer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (n % 32 == 0) {
+            const bool late = global_timer_ns() - t0 > kWaitTimeoutNs;
+            if (late) {
+                raise_status(status, PKV_DEV_TIMEOUT);
+                *abort = 1;
+            }
+            if (__any_sync(0xffffffffu, late || *abort)) return false;
+        }
+    }
+}
+
+// A value that all lanes hold, as the compiler can know it too.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+
+// Shared-memory matrix descriptors (128-byte swizzle) as their two words: the
+// low one holds the address and the leading offset, the high one is the same
+// for every operand here (8-row groups 1024 bytes apart).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+    return ((addr & 0x3FFFF) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi));
+}
+
+// Ties the values to this place among the volatile instructions: what is
+// computed from them cannot move ahead of it.
+__device__ __forceinline__ void keep(float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                          "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
 // Item tiles of sequence r; 0 for an empty or a bad one (bad: reported).
@@ -138,7 +193,9 @@ __device__ __noinline__ void exact_row(const PromptArgs &a, int q0, int i, int h
         for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
         return s * a.scale;
     };
+#pragma unroll 1
     for (int j = 0; j <= i; ++j) m = fmaxf(m, score(j));
+#pragma unroll 1
     for (int j = 0; j <= i; ++j) {
         const float p = exp2f((score(j) - m) * kLog2e);
         const __nv_bfloat16 *vj = v + j * a.v_stride;
@@ -165,13 +222,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + M::kOffBar);
     uint64_t *q_full = bar + Bars::kQFull, *q_empty = bar + Bars::kQEmpty, *s_full = bar + Bars::kSFull;
     uint64_t *p_full = bar + Bars::kPFull, *pv_done = bar + Bars::kPvDone, *d_full = bar + Bars::kDFull;
-    uint64_t *d_empty = bar + Bars::kDEmpty, *drain = bar + Bars::kDrain;
+    uint64_t *d_empty = bar + Bars::kDEmpty, *o_full = bar + Bars::kOFull, *l_full = bar + Bars::kLFull;
+    uint64_t *o_free = bar + Bars::kOFree, *drain = bar + Bars::kDrain;
+    float *row_sum = reinterpret_cast<float *>(smem + M::kOffSum);
     uint64_t *kv_full = bar + Bars::kKvFull, *kv_empty = kv_full + kStages;
     Item *items = reinterpret_cast<Item *>(smem + M::kOffItem);
     int *seq = reinterpret_cast<int *>(smem + M::kOffSeq);
     volatile int *abort = &s_abort;
     int32_t *status = a.status;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // broadcast: the compiler then knows that a role's branch is the whole warp's (see uniform())
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         s_abort = 0;
@@ -185,7 +245,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&pv_done[i], 1);
             mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], 9);  // the MMA warp and the softmax warps
+            mbar_init(&d_empty[i], 13);  // the MMA, softmax and output warps
+            mbar_init(&o_full[i], 1);
+            mbar_init(&l_full[i], 4);
+            mbar_init(&o_free[i], 4);
         }
         mbar_init(drain, 1);
         for (int i = 0; i < kStages; ++i) {
@@ -216,9 +279,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     __syncthreads();
     tmem_fence_after_sync();
     const uint32_t tm = s_tmem;
-
     if (warp == kCopyWarp) {
         // ------------------------ items, Q, K and V ------------------------
+        setmaxnreg_dec<kOtherRegs>();
         if (lane == 0) {
             tma_prefetch_desc(&q_map);
             tma_prefetch_desc(&k_map);
@@ -239,7 +302,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         int hi = s_levels;        // items_from(hi) <= every item still to come
         long long above = 0;      // items_from(hi)
         uint32_t x = 0;           // K and V tiles issued
-        uint32_t q_used[2] = {0, 0};
+        uint32_t q_used = 0, q_any = 0;  // bit t: parity of Q_t's tiles copied; any copied
         bool ok = true;
         for (int k = 0; ok; ++k) {
             const long long it = (long long)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -287,116 +350,114 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             }
             __syncwarp();
             if (!w.valid) break;
-            auto load_q = [&](int t) {
-                if (!w.n_keys[t]) return true;
-                if (!warp_wait(&q_empty[t], (q_used[t] & 1) ^ 1, status, abort)) return false;
-                ++q_used[t];
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[t], a.tile_tokens * a.group * D * 2);
+            // Q_A, K(0), Q_B, V(0), K(1), V(1), ...
+            const int nt = max(w.n_keys[0], w.n_keys[1]);
+#pragma unroll 1
+            for (int i = 0; i < 2 * nt && ok; ++i, ++x) {
+                if (i < 2 && w.n_keys[i]) {
+                    if (!warp_wait(&q_empty[i], ((q_used >> i) & 1) ^ 1, status, abort)) { ok = false; break; }
+                    q_used ^= 1u << i;
+                    q_any |= 1u << i;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&q_full[i], a.tile_tokens * a.group * D * 2);
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b)
-                        tma_load_3d(smem + M::kOffQ + t * M::kTile + b * M::kHalf, &q_map, b * 64, w.h * a.group,
-                                    w.q0 + w.i0 + t * a.tile_tokens, &q_full[t]);
+                        for (int b = 0; b < D / 64; ++b)
+                            tma_load_3d(smem + M::kOffQ + i * M::kTile + b * M::kHalf, &q_map, b * 64, w.h * a.group,
+                                        w.q0 + w.i0 + i * a.tile_tokens, &q_full[i]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                return true;
-            };
-            auto load_kv = [&](const CUtensorMap *map, int j) {
                 const int st = x % kStages;
-                if (!warp_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, status, abort)) return false;
+                if (!warp_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, status, abort)) { ok = false; break; }
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&kv_full[st], kKeys * D * 2);
-                    tma_load_4d(smem + M::kOffKv + st * M::kTile, map, 0, w.q0 + j * kKeys, 0, w.h, &kv_full[st]);
+                    tma_load_4d(smem + M::kOffKv + st * M::kTile, i & 1 ? &v_map : &k_map, 0, w.q0 + (i >> 1) * kKeys, 0,
+                                w.h, &kv_full[st]);
                 }
                 __syncwarp();
-                ++x;
-                return true;
-            };
-            const int nt = max(w.n_keys[0], w.n_keys[1]);
-            ok = load_q(0) && load_kv(&k_map, 0) && load_q(1) && load_kv(&v_map, 0);
-            for (int j = 1; j < nt && ok; ++j) ok = load_kv(&k_map, j) && load_kv(&v_map, j);
+            }
         }
         if (!ok && lane == 0) {
             // let copies already issued land before the CTA can leave
             for (uint32_t y = x > (uint32_t)kStages ? x - kStages : 0; y < x; ++y)
                 mbar_drain(&kv_full[y % kStages], (y / kStages) & 1, status, nullptr, 0);
             for (int t = 0; t < 2; ++t)
-                if (q_used[t]) mbar_drain(&q_full[t], (q_used[t] - 1) & 1, status, nullptr, 0);
+                if (q_any >> t & 1) mbar_drain(&q_full[t], ((q_used >> t) & 1) ^ 1, status, nullptr, 0);
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------- MMA issue ----------------------------
+        setmaxnreg_dec<kOtherRegs>();
         constexpr uint32_t kIdS = umma_idesc_bf16(kRows, kKeys, 0, 0);
         constexpr uint32_t kIdPV = umma_idesc_bf16(kRows, D, 0, 1);
-        const uint32_t q_s = smem_u32(smem + M::kOffQ), kv_s = smem_u32(smem + M::kOffKv);
-        uint32_t x = 0;                                    // K and V tiles of the items so far
-        uint32_t q_used[2] = {0, 0}, pv[2] = {0, 0};       // Q tiles taken, PV products issued
+        const uint32_t tmu = uniform(tm);
+        const uint32_t q_lo = desc_lo(smem_u32(smem + M::kOffQ), 16);
+        const uint32_t k_lo = desc_lo(smem_u32(smem + M::kOffKv), 16);          // as K: K-major
+        const uint32_t v_lo = desc_lo(smem_u32(smem + M::kOffKv), M::kHalf);    // as V: MN-major
+        uint32_t x = 0;      // K and V tiles of the items so far
+        uint32_t q_used = 0, pv0 = 0, pv1 = 0;  // q_used: parity bits of Q tiles taken; pv: PV products issued
+        uint32_t o_used = 0;                    // parity bits of the outputs written
         bool ok = true;
         auto kv_wait = [&](uint32_t y) {
             return warp_wait(&kv_full[y % kStages], (y / kStages) & 1, status, abort);
-        };
-        // S_t = Q_t K into S's columns, which hold the P of t's previous
-        // product: that one has to be over first.
-        auto issue_s = [&](int t, uint32_t y) {
-            if (pv[t] > 0 && !warp_wait(&pv_done[t], (pv[t] - 1) & 1, status, abort)) return false;
-            tmem_fence_after_sync();
-            const uint32_t ks = kv_s + (y % kStages) * M::kTile;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                umma_bf16_warp(tm + t * kKeys,
-                               umma_desc_sw128(q_s + t * M::kTile + (kk / 4) * M::kHalf + (kk % 4) * 32, 16, 1024),
-                               umma_desc_sw128(ks + (kk / 4) * M::kHalf + (kk % 4) * 32, 16, 1024), kIdS,
-                               kk > 0 ? 1u : 0u);
-            umma_commit_warp(&s_full[t]);
-            return true;
         };
         for (int k = 0; ok; ++k) {
             if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) { ok = false; break; }
             const Item w = items[k & 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[k & 1]);
-            if (!w.valid) break;
-            const int nA = w.n_keys[0], nB = w.n_keys[1], nt = max(nA, nB);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int n_t = t ? nB : nA;
-                if (!ok || n_t == 0) continue;
-                ok = warp_wait(&q_full[t], q_used[t] & 1, status, abort);
-                ++q_used[t];
-                if (ok && t == 0) ok = kv_wait(x);
-                if (ok) ok = issue_s(t, x);
-                if (ok && n_t == 1) umma_commit_warp(&q_empty[t]);
-            }
-            if (!ok) break;
-            umma_commit_warp(&kv_empty[x % kStages]);
-            for (int j = 0; j < nt && ok; ++j) {
+            if (!uniform(w.valid)) break;
+            const int nA = uniform(w.n_keys[0]), nB = uniform(w.n_keys[1]), nt = max(nA, nB);
+            // Step j: O_t += P_t(j) V(j), then S_t(j + 1), for A, then for B.
+#pragma unroll 1
+            for (int j = -1; j < nt && ok; ++j) {
                 const uint32_t yv = x + 2 * j + 1, yk = yv + 1;  // V(j), K(j + 1)
-                const uint32_t vs = kv_s + (yv % kStages) * M::kTile;
-#pragma unroll
+#pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
                     const int n_t = t ? nB : nA;
-                    if (!ok || j >= n_t) continue;
-                    // A sees no more key tiles than B, unless B is empty.
-                    const bool last_v = t == 1 || j >= nB;
+                    const uint32_t pv = t ? pv1 : pv0;
+                    if (j >= 0 && j < n_t) {
+                        const uint32_t b_lo = v_lo + (yv % kStages) * (M::kTile >> 4);
+                        if (t == 0 || j >= nA) ok = kv_wait(yv);
+                        if (ok && j == 0) {  // the previous item's O has been read
+                            ok = warp_wait(&o_free[t], ((o_used >> t) & 1) ^ 1, status, abort);
+                            o_used ^= 1u << t;
+                        }
+#pragma unroll 1
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            ok = warp_wait(&p_full[2 * t + half], pv & 1, status, abort);
+                            if (!ok) break;
+                            tmem_fence_after_sync();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (ok) ok = warp_wait(&p_full[2 * t + half], pv[t] & 1, status, abort);
-                        if (ok && half == 0 && (t == 0 || j >= nA)) ok = kv_wait(yv);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ts(tmu + kColO + t * D, tmu + t * kKeys + half * 32 + kk * 8,
+                                       b_lo + (half * 4 + kk) * (2048 >> 4), kIdPV, (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        if (!ok) break;
+                        umma_commit_warp(&pv_done[t]);
+                        if (t) ++pv1; else ++pv0;
+                        if (j + 1 == n_t) umma_commit_warp(&o_full[t]);
+                        // A sees no more key tiles than B, unless B is empty.
+                        if (t == 1 || j >= nB) umma_commit_warp(&kv_empty[yv % kStages]);
+                    }
+                    if (j + 1 < n_t) {
+                        if (j < 0) {
+                            ok = warp_wait(&q_full[t], (q_used >> t) & 1, status, abort);
+                            q_used ^= 1u << t;
+                        }
+                        if (ok && (t == 0 || j + 1 >= nA)) ok = kv_wait(yk);
+                        // S_t goes into columns that hold the P of t's
+                        // previous product: that one has to be over first.
+                        const uint32_t done = t ? pv1 : pv0;
+                        if (ok && done > 0) ok = warp_wait(&pv_done[t], (done - 1) & 1, status, abort);
                         if (!ok) break;
                         tmem_fence_after_sync();
+                        const uint32_t a_lo = q_lo + t * (M::kTile >> 4);
+                        const uint32_t b_lo = k_lo + (yk % kStages) * (M::kTile >> 4);
 #pragma unroll
-                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            umma_bf16_tmem_a_warp(tm + kColO + t * D, tm + t * kKeys + kk * 8,
-                                                  umma_desc_sw128(vs + kk * 2048, M::kHalf, 1024), kIdPV,
-                                                  (j > 0 || kk > 0) ? 1u : 0u);
-                    }
-                    if (!ok) break;
-                    umma_commit_warp(&pv_done[t]);
-                    ++pv[t];
-                    if (last_v) umma_commit_warp(&kv_empty[yv % kStages]);
-                    if (j + 1 < n_t) {
-                        if (t == 0 || j + 1 >= nA) ok = kv_wait(yk);
-                        if (ok) ok = issue_s(t, yk);
-                        if (!ok) break;
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_ss(tmu + t * kKeys, a_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2,
+                                   b_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2, kIdS, kk > 0 ? 1u : 0u);
+                        umma_commit_warp(&s_full[t]);
                         if (t == 1 || j + 1 >= nB) umma_commit_warp(&kv_empty[yk % kStages]);
                         if (j + 2 == n_t) umma_commit_warp(&q_empty[t]);
                     }
@@ -408,16 +469,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         umma_commit_warp(drain);
         if (lane == 0) mbar_drain(drain, 0, status, nullptr, 0);
         __syncwarp();
-    } else {
-        // ------------------------ softmax and output ------------------------
-        const int t = warp >> 2;                  // query tile A or B
+    } else if (warp >= kSoftmaxWarp && warp < kOutWarp) {
+        // ----------------------------- softmax -----------------------------
+        setmaxnreg_inc<kSoftmaxRegs>();
+        const int t = (warp - kSoftmaxWarp) >> 2;  // query tile A or B
         const int row = (warp & 3) * 32 + lane;   // its row = TMEM lane
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tm + lane_off + t * kKeys, o_col = tm + lane_off + kColO + t * D;
         const float scale_log2 = a.scale * kLog2e;
         const int g = a.group;
         uint32_t x = 0;   // K and V tiles of the items so far
-        uint32_t n = 0;   // key tiles this query tile has been through
+        uint32_t n = 0, n_out = 0;  // key tiles and items this query tile has been through
         for (int k = 0;; ++k) {
             if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) break;
             const Item w = items[k & 1];
@@ -461,26 +523,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], s[c][e], s[c][e + 1]);
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
-                if (j == 0) {
-                    m = top;  // key 0 is visible to every row
-                } else {
-                    const bool moves = top > m + kRescaleThreshold;
-                    if (__any_sync(0xffffffffu, moves)) {
-                        // PV(j - 1) was over before S(j) was issued: O is at rest.
-                        const float alpha = moves ? fast_exp2(m - top) : 1.f;
-                        if (moves) m = top;
-                        l *= alpha;
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            float o[16];
-                            tmem_ld16(o_col + c * 16, o);
-                            tmem_wait_ld_regs(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                            tmem_st16(o_col + c * 16, o);
-                        }
-                    }
-                }
                 // V rows past the sequence belong to the next one, or to
                 // nobody: their P is 0, but 0 times NaN is not. The first
                 // query tile that takes this V tile clears them.
@@ -489,72 +531,138 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     if (!warp_wait(&kv_full[y % kStages], (y / kStages) & 1, status, abort)) { ok = false; break; }
                     uint8_t *vt = smem + M::kOffKv + (y % kStages) * M::kTile;
                     const int first = w.n - j * kKeys, words = (kKeys - first) * 8;
-#pragma unroll
+#pragma unroll 1
                     for (int b = 0; b < D / 64; ++b)
+#pragma unroll 1
                         for (int c = row; c < words; c += kRows)
                             *reinterpret_cast<uint4 *>(vt + b * M::kHalf + first * 128 + c * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                const float2 sc2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m, -m);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[32];
+                // P of the first 64 keys against the reference as it stands, so
+                // that the exponentials need not wait for the maximum; where a
+                // row of the warp moves its reference (always on the first tile)
+                // they are made again.
+                const float2 sc2 = make_float2(scale_log2, scale_log2);
+                auto exps = [&](const float (&v0)[32], const float (&v1)[32], uint32_t (&p)[32]) {
+                    const float2 nm2 = make_float2(-m, -m);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float *v = &s[2 * half + e / 16][2 * (e % 16)];
+                        const float *v = e < 16 ? &v0[2 * e] : &v1[2 * e - 32];
                         const float2 z = ffma2(make_float2(v[0], v[1]), sc2, nm2);
                         const float2 pe = make_float2(fast_exp2(z.x), fast_exp2(z.y));
                         sum[e & 1] = fadd2(sum[e & 1], pe);
                         p[e] = pack_bf16x2(pe.x, pe.y);
                     }
+                    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                };
+                uint32_t p[32];
+                float sum;
+                bool first = j == 0;
+                while (true) {
+                    sum = exps(s[0], s[1], p);
+                    const bool moves = first || top > m + kRescaleThreshold;
+                    if (!__any_sync(0xffffffffu, moves)) break;
+                    first = false;
+                    const float alpha = moves ? fast_exp2(m - top) : 1.f;
+                    if (moves) m = top;
+                    if (j == 0) continue;
+                    // PV(j - 1) was over before S(j) was issued: O is at rest.
+                    l *= alpha;
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        tmem_ld16(o_col + c * 16, o);
+                        tmem_wait_ld_regs(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                        tmem_st16(o_col + c * 16, o);
+                    }
+                }
+                auto hand_on = [&](int half) {
                     tmem_st32u(s_col + half * 32, p);
                     tmem_wait_st();
                     tmem_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
-                }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                };
+                hand_on(0);
+                // not ahead of the first half's hand-over
+                keep(s[2]);
+                keep(s[3]);
+                l += sum;
+                l += exps(s[2], s[3], p);
+                hand_on(1);
             }
             x += 2 * nt;
-            if (!ok) break;
-            if (!warp_wait(&pv_done[t], (n - 1) & 1, status, abort)) break;
-            tmem_fence_after_sync();
-            const float inv = 1.f / l;
-            const int head = w.h * g + row % g;
-            __nv_bfloat16 *dst = a.out + (((long long)w.q0 + i) * a.num_q_heads + head) * D;
-            float odd = 0.f;  // NaN once an output is not finite
+            if (!ok || !warp_wait(&o_free[t], (n_out & 1) ^ 1, status, abort)) break;
+            ++n_out;
+            row_sum[t * kRows + row] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&l_full[t]);
+        }
+    } else if (warp >= kOutWarp) {
+        // ------------------------------ output ------------------------------
+        setmaxnreg_dec<kOtherRegs>();
+        // O / l to memory while the softmax and the tensor core are at the
+        // next item; O is theirs again once it has been read.
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t o_col = tm + ((uint32_t)((warp & 3) * 32) << 16) + kColO;
+        const int g = a.group;
+        uint32_t used = 0;  // parity bits of the outputs so far
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) break;
+            const Item w = items[k & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_empty[k & 1]);
+            if (!w.valid) break;
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                if (!w.n_keys[t]) continue;
+                const uint32_t par = (used >> t) & 1;
+                used ^= 1u << t;
+                ok = warp_wait(&l_full[t], par, status, abort) && warp_wait(&o_full[t], par, status, abort);
+                if (!ok) break;
+                tmem_fence_after_sync();
+                const int i = w.i0 + t * a.tile_tokens + row / g;
+                const bool valid = row < a.tile_tokens * g && i < w.n;
+                const float inv = 1.f / row_sum[t * kRows + row];
+                const int head = w.h * g + row % g;
+                __nv_bfloat16 *dst = a.out + (((long long)w.q0 + i) * a.num_q_heads + head) * D;
+                float odd = 0.f;  // NaN once an output is not finite
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    tmem_ld16(o_col + t * D + c, o);
+                    tmem_wait_ld_regs(o);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tmem_ld32(o_col + c * 32, o);
-                tmem_wait_ld_regs(o);
+                    for (int e = 0; e < 16; ++e) {
+                        o[e] *= inv;
+                        odd = fmaf(o[e], 0.f, odd);
+                    }
+                    if (valid) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    o[e] *= inv;
-                    odd = fmaf(o[e], 0.f, odd);
-                }
-                if (valid) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 pk;
-                        pk.x = pack_bf16x2(o[e], o[e + 1]);
-                        pk.y = pack_bf16x2(o[e + 2], o[e + 3]);
-                        pk.z = pack_bf16x2(o[e + 4], o[e + 5]);
-                        pk.w = pack_bf16x2(o[e + 6], o[e + 7]);
-                        *reinterpret_cast<uint4 *>(dst + c * 32 + e) = pk;
+                        for (int e = 0; e < 16; e += 8)
+                            *reinterpret_cast<uint4 *>(dst + c + e) =
+                                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
                     }
                 }
-            }
-            tmem_fence_before_sync();
-            unsigned redo = __ballot_sync(0xffffffffu, valid && odd != 0.f);
-            while (redo) {
-                const int src = __ffs(redo) - 1;
-                redo &= redo - 1;
+                tmem_fence_before_sync();
                 __syncwarp();
-                exact_row<D>(a, w.q0, __shfl_sync(0xffffffffu, i, src), __shfl_sync(0xffffffffu, head, src), lane);
+                if (lane == 0) mbar_arrive(&o_free[t]);
+                unsigned redo = __ballot_sync(0xffffffffu, valid && odd != 0.f);
+                while (redo) {
+                    const int src = __ffs(redo) - 1;
+                    redo &= redo - 1;
+                    __syncwarp();
+                    exact_row<D>(a, w.q0, __shfl_sync(0xffffffffu, i, src), __shfl_sync(0xffffffffu, head, src), lane);
+                }
             }
         }
+    } else {
+        setmaxnreg_dec<kOtherRegs>();  // warps 2 and 3: a warpgroup gives up registers together
     }
 
     tmem_fence_before_sync();
