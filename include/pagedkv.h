@@ -431,8 +431,7 @@ int paged_qk_norm_rope(const pkv_rope_desc *desc, const void *q, const void *k, 
  *  status     optional device int32, PKV_DEV_* bits OR-ed in
  *
  * A value that is not finite reaches the rows that may see its token and no
- * other (rows whose tile holds such a value are summed again one by one:
- * correct, but slow). Needs no workspace; calls may overlap. As with
+ * other. Needs no workspace; calls may overlap. As with
  * paged_attention, make the first call on a device before any capture.
  */
 int pkv_prompt_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,

@@ -17,15 +17,15 @@
 //                     maximum, exponentials against a running reference that
 //                     moves (O rescaled) only when the maximum outgrows it by
 //                     2^8; bf16 pairs over S's own columns in TMEM, handed on
-//                     in two halves so that the product of the first half of
-//                     the keys runs during the second half's exponentials;
+//                     in two parts so that the product of the first keys runs
+//                     during the exponentials of the last;
 //   O_t += P_t V      tcgen05.mma, A = P_t from TMEM, B = V as it lies.
 // The softmax of A runs while the tensor core works for B and the other way
 // round. The sums l are of the unrounded p; rounding P to bf16 (2^-9 of each
 // term) is what the tensor core takes.
 //
-// Warps: 0-3 softmax and output of A, 4-7 of B, 8 MMA issue and TMEM, 9
-// copies and the item list. The grid is persistent. The host does not know
+// Warps: 0 MMA issue and TMEM, 1 copies and the item list, 2-3 guard of V, 4-7
+// softmax of A, 8-11 of B, 12-15 output. The grid is persistent. The host does not know
 // the lengths, and no workspace is needed: items are numbered by tile level
 // (longest keys first) over all sequences, every CTA counts the tiles once,
 // and its copy warp finds its next item by a binary search over levels while
@@ -51,14 +51,20 @@ namespace pkv {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kMmaWarp = 0, kCopyWarp = 1, kSoftmaxWarp = 4, kOutWarp = 12;  // softmax 4-11, output 12-15
+constexpr int kMmaWarp = 0, kCopyWarp = 1, kGuardWarp = 2, kSoftmaxWarp = 4, kOutWarp = 12;
 constexpr int kThreads = 512;
 // Registers a thread: the softmax holds a row of 128 scores and 32 words of P.
-// Four warpgroups of 128 at launch: 2 * (64 + 192) = 4 * 128.
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
+// Four warpgroups of 128 at launch: 2 * (72 + 184) = 4 * 128.
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;           // S_A 0, S_B 128, O_A 256, O_B 256 + D
+// P is handed on in two parts of 96 and 32 keys: the product of the first (six
+// MMAs, 384 cycles) runs while the second is made, and little is left to do
+// once the second is there.
+constexpr int kFirstKeys = 96;
 constexpr float kRescaleThreshold = 8.f;  // log2 units: P stays <= 2^8
+constexpr int kNoGuard = INT_MAX;
+constexpr int kGuardTiles = 3;            // an item's at most 256 tokens touch at most three key tiles
 constexpr int kSeqCache = 4096;           // sequences whose tile counts are kept in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -73,15 +79,22 @@ struct PromptArgs {
 };
 
 // One work item: tokens [i0, i0 + 2 tile_tokens) of the sequence of n tokens
-// that starts at token q0; n_keys[t]: key tiles that query tile t sees.
+// that starts at token q0; n_keys[t]: key tiles that query tile t sees; guard:
+// kNoGuard, or the first key tile that some row sees only in part, when the
+// item is done again because an output was not finite.
 struct Item {
-    int valid, q0, n, i0, h, n_keys[2], pad;
+    int valid, q0, n, i0, h, n_keys[2], guard;
 };
 
 struct Bars {
     static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6 /* [tile][half] */, kPvDone = 10, kDFull = 12,
-                         kDEmpty = 14, kOFull = 16, kLFull = 18, kOFree = 20, kDrain = 22, kKvFull = 23;
+                         kDEmpty = 14, kOFull = 16, kLFull = 18, kOFree = 20, kBadFull = 22, kDrain = 24, kKvFull = 25;
 };
+
+__device__ __forceinline__ Item guarded(Item w) {
+    w.guard = w.i0 / kKeys;
+    return w;
+}
 
 template <int D>
 struct Smem {
@@ -92,9 +105,11 @@ struct Smem {
     static constexpr int kOffKv = 2 * kTile;
     static constexpr int kOffItem = kOffKv + kStages * kTile;
     static constexpr int kOffBar = kOffItem + 2 * (int)sizeof(Item);
-    static constexpr int kBars = Bars::kKvFull + 2 * kStages;
+    static constexpr int kBars = Bars::kKvFull + 2 * kStages + kStages / 2;
     static constexpr int kOffSum = kOffBar + kBars * 8;  // float [tile][row]: sums of p
-    static constexpr int kOffSeq = kOffSum + 2 * kRows * 4;
+    static constexpr int kOffBad = kOffSum + 2 * kRows * 4;  // bits [item & 1][guarded tile][key]
+    static constexpr int kOffRedo = kOffBad + 2 * kGuardTiles * (kKeys / 8);  // int [item & 1]
+    static constexpr int kOffSeq = kOffRedo + 8;
     static constexpr int kBytes = kOffSeq + kSeqCache * 4;
     static constexpr int kAlloc = kBytes + 1024;
 };
@@ -105,11 +120,20 @@ static_assert(Smem<64>::kAlloc <= 232448 - 1024, "prompt kernel shared memory");
 // values that live across a call are kept out of uniform registers, where the
 // MMA instructions want them (60 to 90 cycles an MMA instead of 15, more than
 // the tensor core's 64), and a role's registers must not pass through one.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t *status, volatile int *abort) {
+    if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
     const unsigned long long t0 = global_timer_ns();
     for (uint32_t n = 1;; ++n) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
         if (n % 32 == 0) {
             const bool late = global_timer_ns() - t0 > kWaitTimeoutNs;
             if (late) {
@@ -119,6 +143,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_
             if (__any_sync(0xffffffffu, late || *abort)) return false;
         }
     }
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort) {
+    return warp_wait(smem_u32(bar), parity, status, abort);
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 // A value that all lanes hold, as the compiler can know it too.
@@ -156,6 +189,41 @@ __device__ __forceinline__ void keep(float (&v)[32]) {
                           "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
+// P = 2^(s * scale - m) of 32 keys as bf16 pairs, and the sums of the unrounded
+// values. One exponential a value on the MUFU (8 lanes a cycle per SM quarter),
+// everything else on packed pairs.
+__device__ __forceinline__ void exps(const float (&s)[32], float scale_log2, float m, float2 (&sum)[2], uint32_t *p) {
+    const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m, -m);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 z = ffma2(make_float2(s[2 * e], s[2 * e + 1]), sc, nm);
+        const float2 v = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+        sum[e & 1] = fadd2(sum[e & 1], v);
+        p[e] = pack_bf16x2(v.x, v.y);
+    }
+}
+
+__device__ __forceinline__ float row_max(const float (&s)[4][32]) {
+    float mx[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        mx[c] = fmaxf(s[c][0], s[c][1]);
+#pragma unroll
+        for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], s[c][e], s[c][e + 1]);
+    }
+    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+__device__ __forceinline__ void store_p(uint32_t col, const uint32_t (&p)[48]) {
+    uint32_t a[32], b[16];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) a[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = p[32 + i];
+    tmem_st32u(col, a);
+    tmem_st16u(col + 32, b);
+}
+
 // Item tiles of sequence r; 0 for an empty or a bad one (bad: reported).
 __device__ __forceinline__ int seq_tiles(const PromptArgs &a, int r, bool report) {
     const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1);
@@ -167,45 +235,39 @@ __device__ __forceinline__ int seq_tiles(const PromptArgs &a, int r, bool report
     return (int)(((long long)q1 - q0 + per - 1) / per);
 }
 
-// One output row by the definition, by a whole warp: for rows whose tile
-// product met an infinity or NaN. The product multiplies masked values by a
-// probability of 0, which is exact unless the value is not finite; here a
-// token's sum takes its visible keys only.
+__device__ __forceinline__ __nv_bfloat162 pair_of(uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); }
+// Whether one of a word's two bf16 values is infinite or NaN (all exponent
+// bits set): their complements' exponent fields have a zero half.
+__device__ __forceinline__ bool odd_pair(uint32_t w) {
+    const uint32_t x = ~w & 0x7f807f80u;
+    return ((x - 0x00010001u) & ~x & 0x80008000u) != 0;
+}
+__device__ __forceinline__ bool odd_value(uint32_t bf16_bits) { return (bf16_bits & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ uint32_t clean_pair(uint32_t w) {
+    return (odd_value(w) ? 0u : w & 0xffffu) | (odd_value(w >> 16) ? 0u : w & 0xffff0000u);
+}
+
+// The noted keys' values that are not finite, into columns [c, c + 16) of the
+// output row of token i, for the keys it sees: their probability is above 0,
+// whatever it is.
 template <int D>
-__device__ __noinline__ void exact_row(const PromptArgs &a, int q0, int i, int head, int lane) {
-    constexpr int kE = D / 32;
-    const int h = head / a.group;
-    const __nv_bfloat16 *q = a.q + ((long long)q0 + i) * a.q_stride + head * D + lane * kE;
-    const __nv_bfloat16 *k = a.k + (long long)q0 * a.k_stride + h * D + lane * kE;
-    const __nv_bfloat16 *v = a.v + (long long)q0 * a.v_stride + h * D + lane * kE;
-    float qv[kE], acc[kE], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-        qv[e] = __bfloat162float(q[e]);
-        acc[e] = 0.f;
-    }
-    auto score = [&](int j) {
-        const __nv_bfloat16 *kj = k + j * a.k_stride;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) s = fmaf(qv[e], __bfloat162float(kj[e]), s);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        return s * a.scale;
-    };
+__device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, const uint32_t *bad, int i, int c,
+                                        float (&o)[16]) {
 #pragma unroll 1
-    for (int j = 0; j <= i; ++j) m = fmaxf(m, score(j));
-#pragma unroll 1
-    for (int j = 0; j <= i; ++j) {
-        const float p = exp2f((score(j) - m) * kLog2e);
-        const __nv_bfloat16 *vj = v + j * a.v_stride;
-        l += p;
+    for (int b = 0; b < kGuardTiles * (kKeys / 32); ++b) {
+        uint32_t bits = bad[b];
+        while (bits) {
+            const int key = w.guard * kKeys + b * 32 + __ffs(bits) - 1;
+            bits &= bits - 1;
+            const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v + ((long long)w.q0 + key) * a.v_stride + w.h * D + c);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] = fmaf(p, __bfloat162float(vj[e]), acc[e]);
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t x = __ldg(v + e);
+                if (key <= i && odd_value(x)) o[2 * e] += __uint_as_float(x << 16);
+                if (key <= i && odd_value(x >> 16)) o[2 * e + 1] += __uint_as_float(x & 0xffff0000u);
+            }
+        }
     }
-    __nv_bfloat16 *o = a.out + (((long long)q0 + i) * a.num_q_heads + head) * D + lane * kE;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = __float2bfloat16(acc[e] / l);
 }
 
 template <int D>
@@ -225,7 +287,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     uint64_t *d_empty = bar + Bars::kDEmpty, *o_full = bar + Bars::kOFull, *l_full = bar + Bars::kLFull;
     uint64_t *o_free = bar + Bars::kOFree, *drain = bar + Bars::kDrain;
     float *row_sum = reinterpret_cast<float *>(smem + M::kOffSum);
-    uint64_t *kv_full = bar + Bars::kKvFull, *kv_empty = kv_full + kStages;
+    uint64_t *bad_full = bar + Bars::kBadFull;
+    uint64_t *kv_full = bar + Bars::kKvFull, *kv_empty = kv_full + kStages, *v_safe = kv_empty + kStages;
+    uint32_t *bad_keys = reinterpret_cast<uint32_t *>(smem + M::kOffBad);
+    volatile int *redo = reinterpret_cast<volatile int *>(smem + M::kOffRedo);
     Item *items = reinterpret_cast<Item *>(smem + M::kOffItem);
     int *seq = reinterpret_cast<int *>(smem + M::kOffSeq);
     volatile int *abort = &s_abort;
@@ -237,6 +302,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         s_abort = 0;
         s_levels = 0;
         s_tiles = 0;
+        redo[0] = redo[1] = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -245,7 +311,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&pv_done[i], 1);
             mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], 13);  // the MMA, softmax and output warps
+            mbar_init(&d_empty[i], 15);  // the MMA, guard, softmax and output warps
+            mbar_init(&bad_full[i], 2);
             mbar_init(&o_full[i], 1);
             mbar_init(&l_full[i], 4);
             mbar_init(&o_free[i], 4);
@@ -254,11 +321,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
+            if (i % 2) mbar_init(&v_safe[i / 2], 2);
         }
         mbar_fence_init();
     }
+    if (warp == kCopyWarp && lane == 0) {
+        tma_prefetch_desc(&q_map);
+        tma_prefetch_desc(&k_map);
+        tma_prefetch_desc(&v_map);
+    }
     pdl_launch_dependents();
     pdl_wait();
+    if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
     __syncthreads();
     {
         int most = 0;
@@ -274,7 +348,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             atomicAdd(&s_tiles, sum);
         }
     }
-    if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
@@ -282,11 +355,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     if (warp == kCopyWarp) {
         // ------------------------ items, Q, K and V ------------------------
         setmaxnreg_dec<kOtherRegs>();
-        if (lane == 0) {
-            tma_prefetch_desc(&q_map);
-            tma_prefetch_desc(&k_map);
-            tma_prefetch_desc(&v_map);
-        }
         const int Hkv = a.num_kv_heads, R = a.num_reqs;
         const long long total = (long long)s_tiles * Hkv;
         auto tiles_of = [&](int r) { return r < kSeqCache ? seq[r] : seq_tiles(a, r, false); };
@@ -304,7 +372,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t x = 0;           // K and V tiles issued
         uint32_t q_used = 0, q_any = 0;  // bit t: parity of Q_t's tiles copied; any copied
         bool ok = true;
-        for (int k = 0; ok; ++k) {
+        // The CTA's k-th item.
+        auto find = [&](int k) {
             const long long it = (long long)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             Item w{};
             if (it < total) {
@@ -337,44 +406,64 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 w.q0 = __ldg(a.qsl + r);
                 w.n = __ldg(a.qsl + r + 1) - w.q0;
                 w.i0 = lo * 2 * a.tile_tokens;
+                w.guard = kNoGuard;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int last = min(w.n, w.i0 + (t + 1) * a.tile_tokens);  // past the tile's last token
                     w.n_keys[t] = last > w.i0 + t * a.tile_tokens ? (last + kKeys - 1) / kKeys : 0;
                 }
             }
-            if (!warp_wait(&d_empty[k & 1], ((k >> 1) & 1) ^ 1, status, abort)) { ok = false; break; }
+            return w;
+        };
+        Item ahead = find(0);
+        int found = 1;  // items looked up
+        for (int k = 0; ok; ++k) {
+            // The item that had this slot is through, output and all: it, or a
+            // new one, comes next. With nothing new the other slot's item may
+            // still have to be done again.
+            int slot = k & 1;
+            if (!warp_wait(&d_empty[slot], ((k >> 1) & 1) ^ 1, status, abort)) { ok = false; break; }
+            if (!redo[slot] && !ahead.valid) {
+                slot ^= 1;
+                if (!warp_wait(&d_empty[slot], (((k + 1) >> 1) & 1) ^ 1, status, abort)) { ok = false; break; }
+            }
+            const bool again = redo[slot];
+            const Item w = again ? guarded(items[slot]) : ahead;
+            __syncwarp();
             if (lane == 0) {
+                redo[slot] = 0;
                 items[k & 1] = w;
                 mbar_arrive(&d_full[k & 1]);
             }
             __syncwarp();
             if (!w.valid) break;
-            // Q_A, K(0), Q_B, V(0), K(1), V(1), ...
-            const int nt = max(w.n_keys[0], w.n_keys[1]);
+            // Q_A, K(0), Q_B, V(0), K(1), V(1), ... by one lane; the next item
+            // is looked up once the ring is full.
+            const int all = 2 * max(w.n_keys[0], w.n_keys[1]);
 #pragma unroll 1
-            for (int i = 0; i < 2 * nt && ok; ++i, ++x) {
-                if (i < 2 && w.n_keys[i]) {
-                    if (!warp_wait(&q_empty[i], ((q_used >> i) & 1) ^ 1, status, abort)) { ok = false; break; }
-                    q_used ^= 1u << i;
-                    q_any |= 1u << i;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&q_full[i], a.tile_tokens * a.group * D * 2);
-#pragma unroll
-                        for (int b = 0; b < D / 64; ++b)
-                            tma_load_3d(smem + M::kOffQ + i * M::kTile + b * M::kHalf, &q_map, b * 64, w.h * a.group,
-                                        w.q0 + w.i0 + i * a.tile_tokens, &q_full[i]);
-                    }
-                    __syncwarp();
-                }
-                const int st = x % kStages;
-                if (!warp_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, status, abort)) { ok = false; break; }
+            for (int i0 = 0, i1 = min(all, kStages); i0 < all && ok; i0 = i1, i1 = all) {
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&kv_full[st], kKeys * D * 2);
-                    tma_load_4d(smem + M::kOffKv + st * M::kTile, i & 1 ? &v_map : &k_map, 0, w.q0 + (i >> 1) * kKeys, 0,
-                                w.h, &kv_full[st]);
+#pragma unroll 1
+                    for (int i = i0; i < i1; ++i, ++x) {
+                        if (i < 2 && w.n_keys[i]) {
+                            if (!mbar_wait(&q_empty[i], ((q_used >> i) & 1) ^ 1, status, abort)) { ok = false; break; }
+                            q_used ^= 1u << i;
+                            q_any |= 1u << i;
+                            mbar_arrive_expect_tx(&q_full[i], a.tile_tokens * a.group * D * 2);
+#pragma unroll
+                            for (int b = 0; b < D / 64; ++b)
+                                tma_load_3d(smem + M::kOffQ + i * M::kTile + b * M::kHalf, &q_map, b * 64,
+                                            w.h * a.group, w.q0 + w.i0 + i * a.tile_tokens, &q_full[i]);
+                        }
+                        const int st = x % kStages;
+                        if (!mbar_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, status, abort)) { ok = false; break; }
+                        mbar_arrive_expect_tx(&kv_full[st], kKeys * D * 2);
+                        tma_load_4d(smem + M::kOffKv + st * M::kTile, i & 1 ? &v_map : &k_map, 0,
+                                    w.q0 + (i >> 1) * kKeys, 0, w.h, &kv_full[st]);
+                    }
                 }
-                __syncwarp();
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok && i0 == 0 && !again) ahead = find(found++);
             }
         }
         if (!ok && lane == 0) {
@@ -393,76 +482,108 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const uint32_t q_lo = desc_lo(smem_u32(smem + M::kOffQ), 16);
         const uint32_t k_lo = desc_lo(smem_u32(smem + M::kOffKv), 16);          // as K: K-major
         const uint32_t v_lo = desc_lo(smem_u32(smem + M::kOffKv), M::kHalf);    // as V: MN-major
-        uint32_t x = 0;      // K and V tiles of the items so far
-        uint32_t q_used = 0, pv0 = 0, pv1 = 0;  // q_used: parity bits of Q tiles taken; pv: PV products issued
-        uint32_t o_used = 0;                    // parity bits of the outputs written
-        bool ok = true;
-        auto kv_wait = [&](uint32_t y) {
-            return warp_wait(&kv_full[y % kStages], (y / kStages) & 1, status, abort);
+        const uint32_t bars = smem_u32(bar);
+        auto at = [&](int i) { return bars + 8 * i; };
+        auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, status, abort); };
+        auto kv_wait = [&](uint32_t y) { return wait(at(Bars::kKvFull + y % kStages), (y / kStages) & 1); };
+        auto kv_release = [&](uint32_t y) { commit(at(Bars::kKvFull + kStages + y % kStages)); };
+        auto pv_part = [&](int t, int part, uint32_t y, uint32_t fresh) {
+            const uint32_t b_lo = v_lo + (y % kStages) * (M::kTile >> 4);
+#pragma unroll
+            for (int kk = part * (kFirstKeys / 16); kk < (part ? kKeys : kFirstKeys) / 16; ++kk)
+                mma_ts(tmu + kColO + t * D, tmu + t * kKeys + kk * 8, b_lo + kk * (2048 >> 4), kIdPV,
+                       kk > 0 ? 1u : 1u - fresh);
         };
+        auto s_product = [&](int t, uint32_t y) {
+            const uint32_t a_lo = q_lo + t * (M::kTile >> 4), b_lo = k_lo + (y % kStages) * (M::kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tmu + t * kKeys, a_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2,
+                       b_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2, kIdS, kk > 0 ? 1u : 0u);
+        };
+        uint32_t x = 0;                   // K and V tiles of the items so far
+        uint32_t pv0 = 0, pv1 = 0;        // PV products issued for A, B
+        uint32_t q_used = 0, o_used = 0;  // parity bits by query tile: Q tiles taken, outputs written
+        uint32_t v_used = 0;              // by V slot: guarded tiles
+        bool ok = true;
         for (int k = 0; ok; ++k) {
-            if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) { ok = false; break; }
+            if (!wait(at(Bars::kDFull + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
             const Item w = items[k & 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[k & 1]);
             if (!uniform(w.valid)) break;
-            const int nA = uniform(w.n_keys[0]), nB = uniform(w.n_keys[1]), nt = max(nA, nB);
-            // Step j: O_t += P_t(j) V(j), then S_t(j + 1), for A, then for B.
+            const int nA = uniform(w.n_keys[0]), nB = uniform(w.n_keys[1]), nt = max(nA, nB), guard = uniform(w.guard);
+            // S_A(0), S_B(0); then step j: O_t += P_t(j) V(j) and S_t(j + 1),
+            // for A, then for B. A sees no more key tiles than B, unless B is
+            // empty. What can be asked for ahead (the next tiles) is, while
+            // the tensor core is at a product.
+            if (!kv_wait(x)) { ok = false; break; }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int n_t = t ? nB : nA;
+                const uint32_t done = t ? pv1 : pv0;
+                if (n_t == 0) continue;
+                ok = wait(at(Bars::kQFull + t), (q_used >> t) & 1);
+                q_used ^= 1u << t;
+                // S_t goes into columns that hold the P of t's previous
+                // product: that one has to be over first.
+                if (ok && done > 0) ok = wait(at(Bars::kPvDone + t), (done - 1) & 1);
+                if (!ok) break;
+                tmem_fence_after_sync();
+                s_product(t, x);
+                commit(at(Bars::kSFull + t));
+                if (n_t == 1) commit(at(Bars::kQEmpty + t));
+            }
+            if (!ok) break;
+            kv_release(x);
 #pragma unroll 1
-            for (int j = -1; j < nt && ok; ++j) {
+            for (int j = 0; j < nt; ++j) {
                 const uint32_t yv = x + 2 * j + 1, yk = yv + 1;  // V(j), K(j + 1)
-#pragma unroll 1
-                for (int t = 0; t < 2; ++t) {
-                    const int n_t = t ? nB : nA;
-                    const uint32_t pv = t ? pv1 : pv0;
-                    if (j >= 0 && j < n_t) {
-                        const uint32_t b_lo = v_lo + (yv % kStages) * (M::kTile >> 4);
-                        if (t == 0 || j >= nA) ok = kv_wait(yv);
-                        if (ok && j == 0) {  // the previous item's O has been read
-                            ok = warp_wait(&o_free[t], ((o_used >> t) & 1) ^ 1, status, abort);
-                            o_used ^= 1u << t;
-                        }
-#pragma unroll 1
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            ok = warp_wait(&p_full[2 * t + half], pv & 1, status, abort);
-                            if (!ok) break;
-                            tmem_fence_after_sync();
+                if (j < guard) {
+                    ok = kv_wait(yv);
+                } else {
+                    const uint32_t v = yv / 2 % (kStages / 2);
+                    ok = wait(at(Bars::kKvFull + 2 * kStages + v), (v_used >> v) & 1);
+                    v_used ^= 1u << v;
+                }
+                if (ok && j == 0) {  // the previous item's O has been read
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_ts(tmu + kColO + t * D, tmu + t * kKeys + half * 32 + kk * 8,
-                                       b_lo + (half * 4 + kk) * (2048 >> 4), kIdPV, (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
-                        }
-                        if (!ok) break;
-                        umma_commit_warp(&pv_done[t]);
-                        if (t) ++pv1; else ++pv0;
-                        if (j + 1 == n_t) umma_commit_warp(&o_full[t]);
-                        // A sees no more key tiles than B, unless B is empty.
-                        if (t == 1 || j >= nB) umma_commit_warp(&kv_empty[yv % kStages]);
-                    }
-                    if (j + 1 < n_t) {
-                        if (j < 0) {
-                            ok = warp_wait(&q_full[t], (q_used >> t) & 1, status, abort);
-                            q_used ^= 1u << t;
-                        }
-                        if (ok && (t == 0 || j + 1 >= nA)) ok = kv_wait(yk);
-                        // S_t goes into columns that hold the P of t's
-                        // previous product: that one has to be over first.
-                        const uint32_t done = t ? pv1 : pv0;
-                        if (ok && done > 0) ok = warp_wait(&pv_done[t], (done - 1) & 1, status, abort);
-                        if (!ok) break;
-                        tmem_fence_after_sync();
-                        const uint32_t a_lo = q_lo + t * (M::kTile >> 4);
-                        const uint32_t b_lo = k_lo + (yk % kStages) * (M::kTile >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            mma_ss(tmu + t * kKeys, a_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2,
-                                   b_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2, kIdS, kk > 0 ? 1u : 0u);
-                        umma_commit_warp(&s_full[t]);
-                        if (t == 1 || j + 1 >= nB) umma_commit_warp(&kv_empty[yk % kStages]);
-                        if (j + 2 == n_t) umma_commit_warp(&q_empty[t]);
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || !(t ? nB : nA)) continue;
+                        ok = wait(at(Bars::kOFree + t), ((o_used >> t) & 1) ^ 1);
+                        o_used ^= 1u << t;
                     }
                 }
+                if (!ok) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int n_t = t ? nB : nA;
+                    if (j >= n_t) continue;
+                    const uint32_t par = (t ? pv1 : pv0) & 1;
+                    if (!wait(at(Bars::kPFull + 2 * t), par)) { ok = false; break; }
+                    tmem_fence_after_sync();
+                    pv_part(t, 0, yv, j == 0);
+                    if (!wait(at(Bars::kPFull + 2 * t + 1), par)) { ok = false; break; }
+                    tmem_fence_after_sync();
+                    pv_part(t, 1, yv, 0);
+                    commit(at(Bars::kPvDone + t));
+                    if (t) ++pv1; else ++pv0;
+                    if (t == 1 || j >= nB) kv_release(yv);
+                    if (j + 1 == n_t) {
+                        commit(at(Bars::kOFull + t));
+                        continue;
+                    }
+                    if ((t == 0 || j + 1 >= nA) && !kv_wait(yk)) { ok = false; break; }
+                    if (!wait(at(Bars::kPvDone + t), par)) { ok = false; break; }
+                    tmem_fence_after_sync();
+                    s_product(t, yk);
+                    commit(at(Bars::kSFull + t));
+                    if (t == 1 || j + 1 >= nB) kv_release(yk);
+                    if (j + 2 == n_t) commit(at(Bars::kQEmpty + t));
+                }
+                if (!ok) break;
             }
+            if (!ok) break;
             x += 2 * nt;
         }
         // no MMA may still be writing TMEM when it is freed
@@ -504,71 +625,39 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 if (!warp_wait(&s_full[t], n & 1, status, abort)) { ok = false; break; }
                 tmem_fence_after_sync();
                 float s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
-                if ((j + 1) * kKeys - 1 > first_limit) {
-                    const int lim = limit - j * kKeys;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[c][e] = c * 32 + e <= lim ? s[c][e] : -INFINITY;
-                }
-                float mx[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mx[c] = fmaxf(s[c][0], s[c][1]);
-#pragma unroll
-                    for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], s[c][e], s[c][e + 1]);
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
-                // V rows past the sequence belong to the next one, or to
-                // nobody: their P is 0, but 0 times NaN is not. The first
-                // query tile that takes this V tile clears them.
-                if ((j + 1) * kKeys > w.n && (t == 0 || j >= w.n_keys[0])) {
-                    const uint32_t y = x + 2 * j + 1;
-                    if (!warp_wait(&kv_full[y % kStages], (y / kStages) & 1, status, abort)) { ok = false; break; }
-                    uint8_t *vt = smem + M::kOffKv + (y % kStages) * M::kTile;
-                    const int first = w.n - j * kKeys, words = (kKeys - first) * 8;
-#pragma unroll 1
-                    for (int b = 0; b < D / 64; ++b)
-#pragma unroll 1
-                        for (int c = row; c < words; c += kRows)
-                            *reinterpret_cast<uint4 *>(vt + b * M::kHalf + first * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                }
-                // P of the first 64 keys against the reference as it stands, so
-                // that the exponentials need not wait for the maximum; where a
-                // row of the warp moves its reference (always on the first tile)
-                // they are made again.
-                const float2 sc2 = make_float2(scale_log2, scale_log2);
-                auto exps = [&](const float (&v0)[32], const float (&v1)[32], uint32_t (&p)[32]) {
-                    const float2 nm2 = make_float2(-m, -m);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float *v = e < 16 ? &v0[2 * e] : &v1[2 * e - 32];
-                        const float2 z = ffma2(make_float2(v[0], v[1]), sc2, nm2);
-                        const float2 pe = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                        sum[e & 1] = fadd2(sum[e & 1], pe);
-                        p[e] = pack_bf16x2(pe.x, pe.y);
-                    }
-                    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                };
-                uint32_t p[32];
+                uint32_t p[kFirstKeys / 2];
                 float sum;
-                bool first = j == 0;
+                // P of the first kFirstKeys keys, against the reference as it
+                // stands: the exponentials need not wait for the row's maximum,
+                // which is taken beside them. Where a row of the warp outgrows
+                // its reference (rare), O follows and the tile is done again; S
+                // is still there.
                 while (true) {
-                    sum = exps(s[0], s[1], p);
-                    const bool moves = first || top > m + kRescaleThreshold;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
+                    if ((j + 1) * kKeys - 1 > first_limit) {
+                        const int lim = limit - j * kKeys, sure = first_limit - j * kKeys;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c * 32 + 31 <= sure) continue;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[c][e] = c * 32 + e <= lim ? s[c][e] : -INFINITY;
+                        }
+                    }
+                    if (j == 0) m = row_max(s) * scale_log2;  // key 0 is visible to every row
+                    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < kFirstKeys / 32; ++c) exps(s[c], scale_log2, m, part, p + 16 * c);
+                    const float top = row_max(s) * scale_log2;
+                    sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                    const bool moves = j > 0 && top > m + kRescaleThreshold;
                     if (!__any_sync(0xffffffffu, moves)) break;
-                    first = false;
                     const float alpha = moves ? fast_exp2(m - top) : 1.f;
                     if (moves) m = top;
-                    if (j == 0) continue;
-                    // PV(j - 1) was over before S(j) was issued: O is at rest.
                     l *= alpha;
+                    // PV(j - 1) was over before S(j) was issued: O is at rest.
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         float o[16];
@@ -579,20 +668,23 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         tmem_st16(o_col + c * 16, o);
                     }
                 }
-                auto hand_on = [&](int half) {
-                    tmem_st32u(s_col + half * 32, p);
+                auto hand_on = [&](int part) {
                     tmem_wait_st();
                     tmem_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+                    if (lane == 0) mbar_arrive(&p_full[2 * t + part]);
                 };
+                store_p(s_col, p);
                 hand_on(0);
-                // not ahead of the first half's hand-over
-                keep(s[2]);
-                keep(s[3]);
-                l += sum;
-                l += exps(s[2], s[3], p);
-                hand_on(1);
+                keep(s[3]);  // its exponentials not ahead of the first part's hand-over
+                {
+                    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t q[16];
+                    exps(s[3], scale_log2, m, part, q);
+                    tmem_st16u(s_col + kFirstKeys / 2, q);
+                    hand_on(1);
+                    l += sum + ((part[0].x + part[0].y) + (part[1].x + part[1].y));
+                }
             }
             x += 2 * nt;
             if (!ok || !warp_wait(&o_free[t], (n_out & 1) ^ 1, status, abort)) break;
@@ -614,9 +706,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         for (int k = 0; ok; ++k) {
             if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) break;
             const Item w = items[k & 1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[k & 1]);
             if (!w.valid) break;
+            if (!warp_wait(&bad_full[k & 1], (k >> 1) & 1, status, abort)) break;
+            const uint32_t *bad = bad_keys + (k & 1) * kGuardTiles * (kKeys / 32);
+            float odd = 0.f;  // NaN once an output of this thread is not finite
+            const bool any_bad = __any_sync(0xffffffffu, lane < kGuardTiles * (kKeys / 32) && bad[lane]);
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
                 if (!w.n_keys[t]) continue;
@@ -630,7 +724,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 const float inv = 1.f / row_sum[t * kRows + row];
                 const int head = w.h * g + row % g;
                 __nv_bfloat16 *dst = a.out + (((long long)w.q0 + i) * a.num_q_heads + head) * D;
-                float odd = 0.f;  // NaN once an output is not finite
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
                     float o[16];
@@ -641,6 +734,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         o[e] *= inv;
                         odd = fmaf(o[e], 0.f, odd);
                     }
+                    if (any_bad) add_bad<D>(a, w, bad, i, c, o);
                     if (valid) {
 #pragma unroll
                         for (int e = 0; e < 16; e += 8)
@@ -652,17 +746,85 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_free[t]);
-                unsigned redo = __ballot_sync(0xffffffffu, valid && odd != 0.f);
-                while (redo) {
-                    const int src = __ffs(redo) - 1;
-                    redo &= redo - 1;
-                    __syncwarp();
-                    exact_row<D>(a, w.q0, __shfl_sync(0xffffffffu, i, src), __shfl_sync(0xffffffffu, head, src), lane);
-                }
             }
+            if (__any_sync(0xffffffffu, odd != 0.f) && w.guard == kNoGuard && lane == 0) redo[k & 1] = 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_empty[k & 1]);
         }
     } else {
-        setmaxnreg_dec<kOtherRegs>();  // warps 2 and 3: a warpgroup gives up registers together
+        // --------------------------- guard of V ---------------------------
+        // The tensor core multiplies masked values by a probability of 0,
+        // which leaves nothing of them unless they are infinite or NaN. Where
+        // an item's output is not finite, the item is done again with its
+        // last key tiles, the only ones with masked keys, looked over first:
+        // rows past the sequence are cleared, other values that are not finite
+        // too, and those keys noted; the output warps add them to the rows
+        // that see them. (Looking over every item's tiles cost 3 to 5 %.)
+        setmaxnreg_dec<kOtherRegs>();
+        const int row0 = (warp - kGuardWarp) * (kKeys / 2);  // each warp has half of a tile's keys
+        uint32_t x = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) break;
+            const Item w = items[k & 1];
+            if (!w.valid) break;
+            const int nt = max(w.n_keys[0], w.n_keys[1]);
+            uint32_t *bad = bad_keys + (k & 1) * kGuardTiles * (kKeys / 32);
+            if (lane < 2 * kGuardTiles) bad[lane / 2 * (kKeys / 32) + row0 / 32 + lane % 2] = 0;
+            __syncwarp();
+            for (int j = 0; j < nt; ++j) {
+                // waited for in turn: a phase's parity tells it from the one
+                // before only
+                const uint32_t y = x + 2 * j + 1;
+                if (!warp_wait(&kv_full[y % kStages], (y / kStages) & 1, status, abort)) { ok = false; break; }
+                if (j < w.guard) continue;
+                uint4 *vt = reinterpret_cast<uint4 *>(smem + M::kOffKv + (y % kStages) * M::kTile);
+                const int rows = min(kKeys, w.n - j * kKeys);
+                // A value times 0 is NaN unless it is finite: one packed
+                // multiply-add for two values, over this warp's half tile.
+                __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);
+                const __nv_bfloat162 zero = odd;
+#pragma unroll 1
+                for (int b = 0; b < D / 64; ++b) {
+                    const uint4 *half = vt + (b * kKeys + row0) * 8 + lane;
+#pragma unroll
+                    for (int c = 0; c < kKeys / 2 * 8 / 32; ++c) {
+                        const uint4 v = half[c * 32];
+                        odd = __hfma2(pair_of(v.x), zero, odd);
+                        odd = __hfma2(pair_of(v.y), zero, odd);
+                        odd = __hfma2(pair_of(v.z), zero, odd);
+                        odd = __hfma2(pair_of(v.w), zero, odd);
+                    }
+                }
+                const float2 found = __bfloat1622float2(odd);
+                if (__any_sync(0xffffffffu, found.x != 0.f || found.y != 0.f) || row0 + kKeys / 2 > rows) {
+#pragma unroll 1
+                    for (int b = 0; b < D / 64; ++b) {
+                        uint4 *half = vt + (b * kKeys + row0) * 8;
+#pragma unroll 1
+                        for (int c = lane; c < kKeys / 2 * 8; c += 32) {  // the swizzle keeps a row's chunks in the row
+                            const int r = row0 + c / 8;
+                            const uint4 v = half[c];
+                            if (r >= rows) {
+                                half[c] = make_uint4(0, 0, 0, 0);
+                            } else if (odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w)) {
+                                half[c] = make_uint4(clean_pair(v.x), clean_pair(v.y), clean_pair(v.z), clean_pair(v.w));
+                                atomicOr(&bad[(j - w.guard) * (kKeys / 32) + r / 32], 1u << (r % 32));
+                            }
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_safe[y / 2 % (kStages / 2)]);
+            }
+            x += 2 * nt;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bad_full[k & 1]);
+                mbar_arrive(&d_empty[k & 1]);
+            }
+        }
     }
 
     tmem_fence_before_sync();
