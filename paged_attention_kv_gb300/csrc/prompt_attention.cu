@@ -63,6 +63,7 @@ constexpr uint32_t kColO = 256;           // S_A 0, S_B 128, O_A 256, O_B 256 + 
 // once the second is there.
 constexpr int kFirstKeys = 96;
 constexpr float kRescaleThreshold = 8.f;  // log2 units: P stays <= 2^8
+constexpr int kSlots = 4;                 // items between the copy warp and the output
 constexpr int kNoGuard = INT_MAX;
 constexpr int kGuardTiles = 3;            // an item's at most 256 tokens touch at most three key tiles
 constexpr int kSeqCache = 4096;           // sequences whose tile counts are kept in shared memory
@@ -75,6 +76,7 @@ struct PromptArgs {
     const int32_t *qsl;
     int num_tokens, num_reqs, num_q_heads, num_kv_heads, group, tile_tokens;  // tile_tokens = 128 / group
     float scale;
+    int wide_out;  // out is on a 32-byte boundary
     int32_t *status;
 };
 
@@ -87,8 +89,9 @@ struct Item {
 };
 
 struct Bars {
-    static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6 /* [tile][half] */, kPvDone = 10, kDFull = 12,
-                         kDEmpty = 14, kOFull = 16, kLFull = 18, kOFree = 20, kBadFull = 22, kDrain = 24, kKvFull = 25;
+    static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6 /* [tile][part] */, kPvDone = 10, kOFull = 12,
+                         kLFull = 14, kOFree = 16, kDrain = 18, kDFull = 19, kDEmpty = kDFull + kSlots,
+                         kBadFull = kDEmpty + kSlots, kKvFull = kBadFull + kSlots;
 };
 
 __device__ __forceinline__ Item guarded(Item w) {
@@ -104,22 +107,26 @@ struct Smem {
     static constexpr int kOffQ = 0;
     static constexpr int kOffKv = 2 * kTile;
     static constexpr int kOffItem = kOffKv + kStages * kTile;
-    static constexpr int kOffBar = kOffItem + 2 * (int)sizeof(Item);
+    static constexpr int kOffBar = kOffItem + kSlots * (int)sizeof(Item);
     static constexpr int kBars = Bars::kKvFull + 2 * kStages + kStages / 2;
     static constexpr int kOffSum = kOffBar + kBars * 8;  // float [tile][row]: sums of p
-    static constexpr int kOffBad = kOffSum + 2 * kRows * 4;  // bits [item & 1][guarded tile][key]
-    static constexpr int kOffRedo = kOffBad + 2 * kGuardTiles * (kKeys / 8);  // int [item & 1]
-    static constexpr int kOffSeq = kOffRedo + 8;
+    static constexpr int kOffBad = kOffSum + 2 * kRows * 4;  // bits [slot][guarded tile][key]
+    static constexpr int kOffRedo = kOffBad + kSlots * kGuardTiles * (kKeys / 8);  // int [slot]
+    static constexpr int kOffSeq = kOffRedo + kSlots * 4;
     static constexpr int kBytes = kOffSeq + kSeqCache * 4;
     static constexpr int kAlloc = kBytes + 1024;
 };
 static_assert(Smem<128>::kAlloc <= 232448 - 1024, "prompt kernel shared memory");
 static_assert(Smem<64>::kAlloc <= 232448 - 1024, "prompt kernel shared memory");
 
-// A bounded wait that the whole warp leaves with one answer. No call in it:
-// values that live across a call are kept out of uniform registers, where the
-// MMA instructions want them (60 to 90 cycles an MMA instead of 15, more than
-// the tensor core's 64), and a role's registers must not pass through one.
+// Bounded waits: after kWaitTimeoutNs, or once another wait has given up, they
+// set *abort and return false; the CTA reports PKV_DEV_TIMEOUT when it ends.
+// They are short, since each is in the code many times and all roles share the
+// instruction cache (at 108 KB of code short prompts ran a fifth slower than
+// at 78 KB); and there is no call in them: values that live across a call are
+// kept out of uniform registers, where the MMA instructions want them (60 to 90
+// cycles an MMA instead of 15, more than the tensor core's 64), and a role's
+// larger share of registers would not pass through one.
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -129,23 +136,36 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t *status, volatile int *abort) {
+__device__ __forceinline__ uint32_t timer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+// By a whole warp, which leaves it with one answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
-    const unsigned long long t0 = global_timer_ns();
-    for (uint32_t n = 1;; ++n) {
-        if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
-        if (n % 32 == 0) {
-            const bool late = global_timer_ns() - t0 > kWaitTimeoutNs;
-            if (late) {
-                raise_status(status, PKV_DEV_TIMEOUT);
-                *abort = 1;
-            }
-            if (__any_sync(0xffffffffu, late || *abort)) return false;
+    const uint32_t t0 = timer_lo();
+    while (!__all_sync(0xffffffffu, try_wait(bar, parity))) {
+        if (__any_sync(0xffffffffu, timer_lo() - t0 > (uint32_t)kWaitTimeoutNs || *abort)) {
+            *abort = 1;
+            return false;
         }
     }
+    return true;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort) {
-    return warp_wait(smem_u32(bar), parity, status, abort);
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return warp_wait(smem_u32(bar), parity, abort);
+}
+// By one thread.
+__device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t b = smem_u32(bar), t0 = timer_lo();
+    while (!try_wait(b, parity)) {
+        if (timer_lo() - t0 > (uint32_t)kWaitTimeoutNs || *abort) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile(
@@ -270,6 +290,31 @@ __device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, cons
     }
 }
 
+// Columns [c, c + 16) of an output row: O / l, rounded, in one 32-byte store
+// (16-byte stores, a sector half filled, held the output warps twice as long).
+template <int D>
+__device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, const uint32_t *bad, bool any_bad, bool valid,
+                                        int i, int c, float inv, float (&o)[16], float &odd, __nv_bfloat16 *dst) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        o[e] *= inv;
+        odd = fmaf(o[e], 0.f, odd);
+    }
+    if (any_bad) add_bad<D>(a, w, bad, i, c, o);
+    if (!valid) return;
+    uint32_t p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+    if (a.wide_out) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c), "r"(p[0]), "r"(p[1]),
+                     "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]), "r"(p[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(p[0], p[1], p[2], p[3]);
+        *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -302,7 +347,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         s_abort = 0;
         s_levels = 0;
         s_tiles = 0;
-        redo[0] = redo[1] = 0;
+        for (int i = 0; i < kSlots; ++i) {
+            redo[i] = 0;
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], 15);  // the MMA, guard, softmax and output warps
+            mbar_init(&bad_full[i], 2);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -310,9 +360,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             mbar_init(&p_full[2 * i], 4);
             mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&pv_done[i], 1);
-            mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], 15);  // the MMA, guard, softmax and output warps
-            mbar_init(&bad_full[i], 2);
             mbar_init(&o_full[i], 1);
             mbar_init(&l_full[i], 4);
             mbar_init(&o_free[i], 4);
@@ -337,6 +384,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     {
         int most = 0;
         unsigned long long sum = 0;
+#pragma unroll 1
         for (int r = threadIdx.x; r < a.num_reqs; r += kThreads) {
             const int n = seq_tiles(a, r, blockIdx.x == 0);
             if (r < kSeqCache) seq[r] = n;
@@ -362,6 +410,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         // tiles, so m grows with the keys seen).
         auto items_from = [&](int m) {
             long long c = 0;
+#pragma unroll 1
             for (int r = lane; r < R; r += 32) c += max(0, tiles_of(r) - m);
 #pragma unroll
             for (int d = 16; d; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
@@ -393,11 +442,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 long long want = idx / Hkv;  // the want-th sequence with more than lo tiles
                 w.h = (int)(idx % Hkv);
                 int r = 0;
+#pragma unroll 1
                 for (int r0 = 0; r0 < R; r0 += 32) {
                     const unsigned has = __ballot_sync(0xffffffffu, r0 + lane < R && tiles_of(r0 + lane) > lo);
                     const int c = __popc(has);
-                    if (want < c) {
-                        r = r0 + (int)__fns(has, 0, (int)want + 1);
+                    if (want < c) {  // the lane with want set bits below its own
+                        const unsigned at = __ballot_sync(
+                            0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == (int)want);
+                        r = r0 + __ffs(at) - 1;
                         break;
                     }
                     want -= c;
@@ -415,38 +467,23 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             }
             return w;
         };
-        Item ahead = find(0);
-        int found = 1;  // items looked up
-        for (int k = 0; ok; ++k) {
-            // The item that had this slot is through, output and all: it, or a
-            // new one, comes next. With nothing new the other slot's item may
-            // still have to be done again.
-            int slot = k & 1;
-            if (!warp_wait(&d_empty[slot], ((k >> 1) & 1) ^ 1, status, abort)) { ok = false; break; }
-            if (!redo[slot] && !ahead.valid) {
-                slot ^= 1;
-                if (!warp_wait(&d_empty[slot], (((k + 1) >> 1) & 1) ^ 1, status, abort)) { ok = false; break; }
-            }
-            const bool again = redo[slot];
-            const Item w = again ? guarded(items[slot]) : ahead;
-            __syncwarp();
-            if (lane == 0) {
-                redo[slot] = 0;
-                items[k & 1] = w;
-                mbar_arrive(&d_full[k & 1]);
-            }
-            __syncwarp();
-            if (!w.valid) break;
-            // Q_A, K(0), Q_B, V(0), K(1), V(1), ... by one lane; the next item
-            // is looked up once the ring is full.
-            const int all = 2 * max(w.n_keys[0], w.n_keys[1]);
+        Item w{}, ahead{};
+        int found = 0;        // items looked up
+        bool again = false;
 #pragma unroll 1
-            for (int i0 = 0, i1 = min(all, kStages); i0 < all && ok; i0 = i1, i1 = all) {
+        for (int k = -1; ok; ++k) {
+            // Q_A, K(0), Q_B, V(0), K(1), V(1), ... of item k, by one lane; the
+            // next item is looked up once the ring is full.
+            const int all = 2 * max(w.n_keys[0], w.n_keys[1]);
+            int i = 0;
+#pragma unroll 1
+            for (int round = 0; round < 2 && ok; ++round) {
+                const int stop = round ? all : min(all, kStages);
                 if (lane == 0) {
 #pragma unroll 1
-                    for (int i = i0; i < i1; ++i, ++x) {
+                    for (; i < stop; ++i, ++x) {
                         if (i < 2 && w.n_keys[i]) {
-                            if (!mbar_wait(&q_empty[i], ((q_used >> i) & 1) ^ 1, status, abort)) { ok = false; break; }
+                            if (!lane_wait(&q_empty[i], ((q_used >> i) & 1) ^ 1, abort)) { ok = false; break; }
                             q_used ^= 1u << i;
                             q_any |= 1u << i;
                             mbar_arrive_expect_tx(&q_full[i], a.tile_tokens * a.group * D * 2);
@@ -456,15 +493,37 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                                             w.h * a.group, w.q0 + w.i0 + i * a.tile_tokens, &q_full[i]);
                         }
                         const int st = x % kStages;
-                        if (!mbar_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, status, abort)) { ok = false; break; }
+                        if (!lane_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, abort)) { ok = false; break; }
                         mbar_arrive_expect_tx(&kv_full[st], kKeys * D * 2);
                         tma_load_4d(smem + M::kOffKv + st * M::kTile, i & 1 ? &v_map : &k_map, 0,
                                     w.q0 + (i >> 1) * kKeys, 0, w.h, &kv_full[st]);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (ok && i0 == 0 && !again) ahead = find(found++);
+                if (ok && round == 0 && !again) ahead = find(found++);
             }
+            if (!ok) break;
+            // The item that had the next slot is through, output and all: it,
+            // or a new one, comes next. With nothing new the other slots' items
+            // may still have to be done again.
+            int slot = 0;
+            again = false;
+            for (int e = 1; e <= kSlots && !again && (e == 1 || !ahead.valid); ++e) {
+                slot = (k + e) % kSlots;
+                ok = warp_wait(&d_empty[slot], (((k + e) / kSlots) & 1) ^ 1, abort);
+                if (!ok) break;
+                again = redo[slot];
+            }
+            if (!ok) break;
+            w = again ? guarded(items[slot]) : ahead;
+            __syncwarp();
+            if (lane == 0) {
+                redo[slot] = 0;
+                items[(k + 1) % kSlots] = w;
+                mbar_arrive(&d_full[(k + 1) % kSlots]);
+            }
+            __syncwarp();
+            if (!w.valid) break;
         }
         if (!ok && lane == 0) {
             // let copies already issued land before the CTA can leave
@@ -484,7 +543,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const uint32_t v_lo = desc_lo(smem_u32(smem + M::kOffKv), M::kHalf);    // as V: MN-major
         const uint32_t bars = smem_u32(bar);
         auto at = [&](int i) { return bars + 8 * i; };
-        auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, status, abort); };
+        auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, abort); };
         auto kv_wait = [&](uint32_t y) { return wait(at(Bars::kKvFull + y % kStages), (y / kStages) & 1); };
         auto kv_release = [&](uint32_t y) { commit(at(Bars::kKvFull + kStages + y % kStages)); };
         auto pv_part = [&](int t, int part, uint32_t y, uint32_t fresh) {
@@ -507,10 +566,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t v_used = 0;              // by V slot: guarded tiles
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            if (!wait(at(Bars::kDFull + (k & 1)), (k >> 1) & 1)) { ok = false; break; }
-            const Item w = items[k & 1];
+            if (!wait(at(Bars::kDFull + k % kSlots), (k / kSlots) & 1)) { ok = false; break; }
+            const Item w = items[k % kSlots];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[k & 1]);
+            if (lane == 0) mbar_arrive(&d_empty[k % kSlots]);
             if (!uniform(w.valid)) break;
             const int nA = uniform(w.n_keys[0]), nB = uniform(w.n_keys[1]), nt = max(nA, nB), guard = uniform(w.guard);
             // S_A(0), S_B(0); then step j: O_t += P_t(j) V(j) and S_t(j + 1),
@@ -602,10 +661,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t x = 0;   // K and V tiles of the items so far
         uint32_t n = 0, n_out = 0;  // key tiles and items this query tile has been through
         for (int k = 0;; ++k) {
-            if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) break;
-            const Item w = items[k & 1];
+            if (!warp_wait(&d_full[k % kSlots], (k / kSlots) & 1, abort)) break;
+            const Item w = items[k % kSlots];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[k & 1]);
+            if (lane == 0) mbar_arrive(&d_empty[k % kSlots]);
             if (!w.valid) break;
             const int n_t = w.n_keys[t], nt = max(w.n_keys[0], w.n_keys[1]);
             if (n_t == 0) {
@@ -622,7 +681,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             float m = 0.f, l = 0.f;
             bool ok = true;
             for (int j = 0; j < n_t; ++j, ++n) {
-                if (!warp_wait(&s_full[t], n & 1, status, abort)) { ok = false; break; }
+                if (!warp_wait(&s_full[t], n & 1, abort)) { ok = false; break; }
                 tmem_fence_after_sync();
                 float s[4][32];
                 uint32_t p[kFirstKeys / 2];
@@ -687,7 +746,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 }
             }
             x += 2 * nt;
-            if (!ok || !warp_wait(&o_free[t], (n_out & 1) ^ 1, status, abort)) break;
+            if (!ok || !warp_wait(&o_free[t], (n_out & 1) ^ 1, abort)) break;
             ++n_out;
             row_sum[t * kRows + row] = l;
             __syncwarp();
@@ -704,11 +763,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t used = 0;  // parity bits of the outputs so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) break;
-            const Item w = items[k & 1];
+            if (!warp_wait(&d_full[k % kSlots], (k / kSlots) & 1, abort)) break;
+            const Item w = items[k % kSlots];
             if (!w.valid) break;
-            if (!warp_wait(&bad_full[k & 1], (k >> 1) & 1, status, abort)) break;
-            const uint32_t *bad = bad_keys + (k & 1) * kGuardTiles * (kKeys / 32);
+            if (!warp_wait(&bad_full[k % kSlots], (k / kSlots) & 1, abort)) break;
+            const uint32_t *bad = bad_keys + (k % kSlots) * kGuardTiles * (kKeys / 32);
             float odd = 0.f;  // NaN once an output of this thread is not finite
             const bool any_bad = __any_sync(0xffffffffu, lane < kGuardTiles * (kKeys / 32) && bad[lane]);
 #pragma unroll 1
@@ -716,7 +775,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 if (!w.n_keys[t]) continue;
                 const uint32_t par = (used >> t) & 1;
                 used ^= 1u << t;
-                ok = warp_wait(&l_full[t], par, status, abort) && warp_wait(&o_full[t], par, status, abort);
+                ok = warp_wait(&l_full[t], par, abort) && warp_wait(&o_full[t], par, abort);
                 if (!ok) break;
                 tmem_fence_after_sync();
                 const int i = w.i0 + t * a.tile_tokens + row / g;
@@ -724,32 +783,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 const float inv = 1.f / row_sum[t * kRows + row];
                 const int head = w.h * g + row % g;
                 __nv_bfloat16 *dst = a.out + (((long long)w.q0 + i) * a.num_q_heads + head) * D;
+                float o[16], next[16];
+                tmem_ld16(o_col + t * D, next);
+                tmem_wait_ld_regs(next);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 16) {
-                    float o[16];
-                    tmem_ld16(o_col + t * D + c, o);
-                    tmem_wait_ld_regs(o);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        o[e] *= inv;
-                        odd = fmaf(o[e], 0.f, odd);
-                    }
-                    if (any_bad) add_bad<D>(a, w, bad, i, c, o);
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 8)
-                            *reinterpret_cast<uint4 *>(dst + c + e) =
-                                make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
-                    }
+                    for (int e = 0; e < 16; ++e) o[e] = next[e];
+                    if (c + 16 < D) tmem_ld16(o_col + t * D + c + 16, next);
+                    put_row<D>(a, w, bad, any_bad, valid, i, c, inv, o, odd, dst);
+                    tmem_wait_ld_regs(next);
                 }
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_free[t]);
             }
-            if (__any_sync(0xffffffffu, odd != 0.f) && w.guard == kNoGuard && lane == 0) redo[k & 1] = 1;
+            if (__any_sync(0xffffffffu, odd != 0.f) && w.guard == kNoGuard && lane == 0) redo[k % kSlots] = 1;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[k & 1]);
+            if (lane == 0) mbar_arrive(&d_empty[k % kSlots]);
         }
     } else {
         // --------------------------- guard of V ---------------------------
@@ -765,18 +816,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t x = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
-            if (!warp_wait(&d_full[k & 1], (k >> 1) & 1, status, abort)) break;
-            const Item w = items[k & 1];
+            if (!warp_wait(&d_full[k % kSlots], (k / kSlots) & 1, abort)) break;
+            const Item w = items[k % kSlots];
             if (!w.valid) break;
             const int nt = max(w.n_keys[0], w.n_keys[1]);
-            uint32_t *bad = bad_keys + (k & 1) * kGuardTiles * (kKeys / 32);
+            uint32_t *bad = bad_keys + (k % kSlots) * kGuardTiles * (kKeys / 32);
             if (lane < 2 * kGuardTiles) bad[lane / 2 * (kKeys / 32) + row0 / 32 + lane % 2] = 0;
             __syncwarp();
             for (int j = 0; j < nt; ++j) {
                 // waited for in turn: a phase's parity tells it from the one
                 // before only
                 const uint32_t y = x + 2 * j + 1;
-                if (!warp_wait(&kv_full[y % kStages], (y / kStages) & 1, status, abort)) { ok = false; break; }
+                if (!warp_wait(&kv_full[y % kStages], (y / kStages) & 1, abort)) { ok = false; break; }
                 if (j < w.guard) continue;
                 uint4 *vt = reinterpret_cast<uint4 *>(smem + M::kOffKv + (y % kStages) * M::kTile);
                 const int rows = min(kKeys, w.n - j * kKeys);
@@ -821,8 +872,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             x += 2 * nt;
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bad_full[k & 1]);
-                mbar_arrive(&d_empty[k & 1]);
+                mbar_arrive(&bad_full[k % kSlots]);
+                mbar_arrive(&d_empty[k % kSlots]);
             }
         }
     }
@@ -831,6 +882,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     __syncthreads();
     tmem_fence_after_sync();
     if (warp == kMmaWarp) tmem_dealloc(tm, kTmemCols);
+    if (threadIdx.x == 0 && s_abort) raise_status(status, PKV_DEV_TIMEOUT);
 }
 
 // ---------------------------------------------------------------------------
@@ -944,6 +996,7 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
     a.group = num_q_heads / num_kv_heads;
     a.tile_tokens = kRows / a.group;
     a.scale = scale;
+    a.wide_out = aligned(out, 32);
     a.status = status;
     CUtensorMap q_map, k_map, v_map;
     rc = encode_q(&q_map, q, num_tokens, q_stride, num_q_heads, head_size, a.group);
