@@ -25,7 +25,7 @@
 // term) is what the tensor core takes.
 //
 // Warps: 0 MMA issue and TMEM, 1 copies and the item list, 2-3 guard of V, 4-7
-// softmax of A, 8-11 of B, 12-15 output. The grid is persistent. The host does not know
+// softmax of A, 8-11 of B, 12-15 output. The host does not know
 // the lengths, and no workspace is needed: items are numbered by tile level
 // (longest keys first) over all sequences, every CTA counts the tiles once,
 // and its copy warp finds its next item by a binary search over levels while
@@ -90,7 +90,7 @@ struct Item {
 
 struct Bars {
     static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6 /* [tile][part] */, kPvDone = 10, kOFull = 12,
-                         kLFull = 14, kOFree = 16, kDrain = 18, kDFull = 19, kDEmpty = kDFull + kSlots,
+                         kLFull = 14, kOFree = 16, kDrain = 18, kBlock = 19, kDFull = 20, kDEmpty = kDFull + kSlots,
                          kBadFull = kDEmpty + kSlots, kKvFull = kBadFull + kSlots;
 };
 
@@ -107,7 +107,8 @@ struct Smem {
     static constexpr int kOffQ = 0;
     static constexpr int kOffKv = 2 * kTile;
     static constexpr int kOffItem = kOffKv + kStages * kTile;
-    static constexpr int kOffBar = kOffItem + kSlots * (int)sizeof(Item);
+    static constexpr int kOffBlock = kOffItem + kSlots * (int)sizeof(Item);  // the launch control's answer
+    static constexpr int kOffBar = kOffBlock + 16;
     static constexpr int kBars = Bars::kKvFull + 2 * kStages + kStages / 2;
     static constexpr int kOffSum = kOffBar + kBars * 8;  // float [tile][row]: sums of p
     static constexpr int kOffBad = kOffSum + 2 * kRows * 4;  // bits [slot][guarded tile][key]
@@ -167,6 +168,27 @@ __device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, volati
     }
     return true;
 }
+// Cluster launch control: asks the hardware for a block of this launch that
+// has not started, to be done here instead; its index is ~0 when none is left
+// (after which there must be no further request).
+__device__ __forceinline__ void block_request(void *answer, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t block_answer(const void *answer) {
+    uint32_t index;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tmov.u32 %0, 0xffffffff;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(index)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return index;
+}
+
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -252,7 +274,7 @@ __device__ __forceinline__ int seq_tiles(const PromptArgs &a, int r, bool report
         return 0;
     }
     const int per = 2 * a.tile_tokens;
-    return (int)(((long long)q1 - q0 + per - 1) / per);
+    return (int)(((uint32_t)(q1 - q0) + per - 1) / (uint32_t)per);
 }
 
 __device__ __forceinline__ __nv_bfloat162 pair_of(uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); }
@@ -365,6 +387,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             mbar_init(&o_free[i], 4);
         }
         mbar_init(drain, 1);
+        mbar_init(bar + Bars::kBlock, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
@@ -421,9 +444,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t x = 0;           // K and V tiles issued
         uint32_t q_used = 0, q_any = 0;  // bit t: parity of Q_t's tiles copied; any copied
         bool ok = true;
-        // The CTA's k-th item.
-        auto find = [&](int k) {
-            const long long it = (long long)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        // Item `it` of the launch.
+        auto find = [&](long long it) {
             Item w{};
             if (it < total) {
                 // largest level m with items_from(m) > it
@@ -438,9 +460,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         above = c;
                     }
                 }
-                const long long idx = it - above;
-                long long want = idx / Hkv;  // the want-th sequence with more than lo tiles
-                w.h = (int)(idx % Hkv);
+                const uint32_t idx = (uint32_t)(it - above);  // below sequences x heads, which the host bounds
+                int want = (int)(idx / (uint32_t)Hkv);        // the want-th sequence with more than lo tiles
+                w.h = (int)(idx % (uint32_t)Hkv);
                 int r = 0;
 #pragma unroll 1
                 for (int r0 = 0; r0 < R; r0 += 32) {
@@ -448,7 +470,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     const int c = __popc(has);
                     if (want < c) {  // the lane with want set bits below its own
                         const unsigned at = __ballot_sync(
-                            0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == (int)want);
+                            0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == want);
                         r = r0 + __ffs(at) - 1;
                         break;
                     }
@@ -468,14 +490,29 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             return w;
         };
         Item w{}, ahead{};
-        int found = 0;        // items looked up
+        uint32_t asked = 0;   // blocks asked for
         bool again = false;
+        auto ask = [&]() {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar + Bars::kBlock, 16);
+                block_request(smem + M::kOffBlock, bar + Bars::kBlock);
+            }
+            ++asked;
+        };
+        auto answer = [&](uint32_t &index) {
+            if (!warp_wait(bar + Bars::kBlock, (asked - 1) & 1, abort)) return false;
+            index = block_answer(smem + M::kOffBlock);
+            fence_proxy_async_smem();  // read before the next answer is written
+            __syncwarp();
+            return true;
+        };
 #pragma unroll 1
         for (int k = -1; ok; ++k) {
             // Q_A, K(0), Q_B, V(0), K(1), V(1), ... of item k, by one lane; the
             // next item is looked up once the ring is full.
             const int all = 2 * max(w.n_keys[0], w.n_keys[1]);
             int i = 0;
+            if (k >= 0 && !again) ask();
 #pragma unroll 1
             for (int round = 0; round < 2 && ok; ++round) {
                 const int stop = round ? all : min(all, kStages);
@@ -500,7 +537,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (ok && round == 0 && !again) ahead = find(found++);
+                if (ok && round == 0 && !again) {
+                    uint32_t index = blockIdx.x;
+                    if (k >= 0) {
+                        ok = answer(index);
+                        // past the last item: blocks that have nothing to do
+                        while (ok && index != ~0u && index >= total) {
+                            ask();
+                            ok = answer(index);
+                        }
+                    }
+                    ahead = find(ok && index != ~0u ? (long long)index : total);
+                }
             }
             if (!ok) break;
             // The item that had the next slot is through, output and all: it,
@@ -527,6 +575,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         }
         if (!ok && lane == 0) {
             // let copies already issued land before the CTA can leave
+            if (asked) mbar_drain(bar + Bars::kBlock, (asked - 1) & 1, status, nullptr, 0);
             for (uint32_t y = x > (uint32_t)kStages ? x - kStages : 0; y < x; ++y)
                 mbar_drain(&kv_full[y % kStages], (y / kStages) & 1, status, nullptr, 0);
             for (int t = 0; t < 2; ++t)
@@ -967,7 +1016,7 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
                                             int32_t num_reqs, float scale, void *out, int32_t *status, void *stream) {
     if (head_size != 64 && head_size != 128) return PKV_E_HEAD_SIZE;
     if (num_tokens < 0 || num_reqs < 0 || num_kv_heads <= 0 || num_kv_heads > 4096) return PKV_E_DIMS;
-    if (num_tokens > INT32_MAX - 65536 || num_reqs > INT32_MAX - 65536) return PKV_E_DIMS;
+    if (num_tokens > INT32_MAX - 65536 || (long long)num_reqs * num_kv_heads > INT32_MAX - 65536) return PKV_E_DIMS;
     if (num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kRows) return PKV_E_GQA;
     if (!(scale > 0.f) || scale > 3.0e38f) return PKV_E_DIMS;
     if (num_tokens == 0 || num_reqs == 0) return PKV_OK;
@@ -1003,13 +1052,14 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
     if (!rc) rc = encode_kv(&k_map, k, num_tokens, k_stride, num_kv_heads, head_size);
     if (!rc) rc = encode_kv(&v_map, v, num_tokens, v_stride, num_kv_heads, head_size);
     if (rc) return rc;
-    // at most this many items: every sequence rounds up to whole pairs of tiles
-    const long long most = (num_tokens / (2LL * a.tile_tokens) + num_reqs) * num_kv_heads;
-    const int grid = (int)(most < sms ? most : sms);
+    // A block for every item there may be (every sequence rounds up to whole
+    // pairs of tiles); those that start fetch the others' items.
+    const long long grid = (num_tokens / (2LL * a.tile_tokens) + num_reqs) * num_kv_heads;
+    if (grid > INT32_MAX) return PKV_E_DIMS;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t err =
         head_size == 128
-            ? launch_pdl(prompt_kernel<128>, dim3(grid), dim3(kThreads), Smem<128>::kAlloc, st, q_map, k_map, v_map, a)
-            : launch_pdl(prompt_kernel<64>, dim3(grid), dim3(kThreads), Smem<64>::kAlloc, st, q_map, k_map, v_map, a);
+            ? launch_pdl(prompt_kernel<128>, dim3((unsigned)grid), dim3(kThreads), Smem<128>::kAlloc, st, q_map, k_map, v_map, a)
+            : launch_pdl(prompt_kernel<64>, dim3((unsigned)grid), dim3(kThreads), Smem<64>::kAlloc, st, q_map, k_map, v_map, a);
     return err == cudaSuccess ? PKV_OK : PKV_E_CUDA;
 }
