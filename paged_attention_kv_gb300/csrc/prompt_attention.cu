@@ -28,9 +28,11 @@
 // softmax of A, 8-11 of B, 12-15 output. The host does not know
 // the lengths, and no workspace is needed: items are numbered by tile level
 // (longest keys first) over all sequences, every CTA counts the tiles once,
-// and its copy warp finds its next item by a binary search over levels while
-// the current one runs. CTA b takes item b, then counts back from the end of
-// every second round, so that the rounds' longest items alternate.
+// and its copy warp finds an item by a binary search over levels. The launch
+// has a block for every item there may be; the blocks that start (one an SM)
+// fetch the items of the others from the hardware one by one, so that an SM
+// takes its next item when it is ready for it. (Items dealt out in turn left
+// the last SM working 17 % longer than the average on ragged prompts.)
 //
 // Every wait is bounded; on a timeout the CTA raises PKV_DEV_TIMEOUT, stops,
 // lets its copies and MMAs in flight finish and frees its TMEM.
@@ -289,12 +291,12 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t w) {
     return (odd_value(w) ? 0u : w & 0xffffu) | (odd_value(w >> 16) ? 0u : w & 0xffff0000u);
 }
 
-// The noted keys' values that are not finite, into columns [c, c + 16) of the
+// The noted keys' values that are not finite, into columns [c, c + 32) of the
 // output row of token i, for the keys it sees: their probability is above 0,
 // whatever it is.
 template <int D>
 __device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, const uint32_t *bad, int i, int c,
-                                        float (&o)[16]) {
+                                        float (&o)[32]) {
 #pragma unroll 1
     for (int b = 0; b < kGuardTiles * (kKeys / 32); ++b) {
         uint32_t bits = bad[b];
@@ -303,7 +305,7 @@ __device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, cons
             bits &= bits - 1;
             const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v + ((long long)w.q0 + key) * a.v_stride + w.h * D + c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 16; ++e) {
                 const uint32_t x = __ldg(v + e);
                 if (key <= i && odd_value(x)) o[2 * e] += __uint_as_float(x << 16);
                 if (key <= i && odd_value(x >> 16)) o[2 * e + 1] += __uint_as_float(x & 0xffff0000u);
@@ -312,28 +314,38 @@ __device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, cons
     }
 }
 
-// Columns [c, c + 16) of an output row: O / l, rounded, in one 32-byte store
+// Columns [c, c + 32) of an output row: O / l, rounded, in 32-byte stores
 // (16-byte stores, a sector half filled, held the output warps twice as long).
 template <int D>
 __device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, const uint32_t *bad, bool any_bad, bool valid,
-                                        int i, int c, float inv, float (&o)[16], float &odd, __nv_bfloat16 *dst) {
+                                        int i, int c, float inv, float (&o)[32], __nv_bfloat162 &odd,
+                                        __nv_bfloat16 *dst) {
+    const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        o[e] *= inv;
-        odd = fmaf(o[e], 0.f, odd);
+    for (int e = 0; e < 32; e += 2) {
+        const float2 v = fmul2(make_float2(o[e], o[e + 1]), inv2);
+        o[e] = v.x;
+        o[e + 1] = v.y;
     }
     if (any_bad) add_bad<D>(a, w, bad, i, c, o);
-    if (!valid) return;
-    uint32_t p[8];
+    uint32_t p[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+    for (int e = 0; e < 16; ++e) {
+        p[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+        odd = __hfma2(pair_of(p[e]), __floats2bfloat162_rn(0.f, 0.f), odd);
+    }
+    if (!valid) return;
     if (a.wide_out) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c), "r"(p[0]), "r"(p[1]),
-                     "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]), "r"(p[7])
-                     : "memory");
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + 2 * e), "r"(p[e]),
+                         "r"(p[e + 1]), "r"(p[e + 2]), "r"(p[e + 3]), "r"(p[e + 4]), "r"(p[e + 5]), "r"(p[e + 6]),
+                         "r"(p[e + 7])
+                         : "memory");
     } else {
-        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(p[0], p[1], p[2], p[3]);
-        *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4 *>(dst + c + 2 * e) = make_uint4(p[e], p[e + 1], p[e + 2], p[e + 3]);
     }
 }
 
@@ -654,20 +666,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     ok = wait(at(Bars::kKvFull + 2 * kStages + v), (v_used >> v) & 1);
                     v_used ^= 1u << v;
                 }
-                if (ok && j == 0) {  // the previous item's O has been read
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (!ok || !(t ? nB : nA)) continue;
-                        ok = wait(at(Bars::kOFree + t), ((o_used >> t) & 1) ^ 1);
-                        o_used ^= 1u << t;
-                    }
-                }
                 if (!ok) break;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int n_t = t ? nB : nA;
                     if (j >= n_t) continue;
                     const uint32_t par = (t ? pv1 : pv0) & 1;
+                    if (j == 0) {  // the previous item's O has been read
+                        if (!wait(at(Bars::kOFree + t), ((o_used >> t) & 1) ^ 1)) { ok = false; break; }
+                        o_used ^= 1u << t;
+                    }
                     if (!wait(at(Bars::kPFull + 2 * t), par)) { ok = false; break; }
                     tmem_fence_after_sync();
                     pv_part(t, 0, yv, j == 0);
@@ -817,7 +825,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             if (!w.valid) break;
             if (!warp_wait(&bad_full[k % kSlots], (k / kSlots) & 1, abort)) break;
             const uint32_t *bad = bad_keys + (k % kSlots) * kGuardTiles * (kKeys / 32);
-            float odd = 0.f;  // NaN once an output of this thread is not finite
+            __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);  // NaN once an output of a valid row is not finite
             const bool any_bad = __any_sync(0xffffffffu, lane < kGuardTiles * (kKeys / 32) && bad[lane]);
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
@@ -832,22 +840,20 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 const float inv = 1.f / row_sum[t * kRows + row];
                 const int head = w.h * g + row % g;
                 __nv_bfloat16 *dst = a.out + (((long long)w.q0 + i) * a.num_q_heads + head) * D;
-                float o[16], next[16];
-                tmem_ld16(o_col + t * D, next);
-                tmem_wait_ld_regs(next);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = next[e];
-                    if (c + 16 < D) tmem_ld16(o_col + t * D + c + 16, next);
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(o_col + t * D + c, o);
+                    tmem_wait_ld_regs(o);
                     put_row<D>(a, w, bad, any_bad, valid, i, c, inv, o, odd, dst);
-                    tmem_wait_ld_regs(next);
                 }
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_free[t]);
             }
-            if (__any_sync(0xffffffffu, odd != 0.f) && w.guard == kNoGuard && lane == 0) redo[k % kSlots] = 1;
+            const float2 sum = __bfloat1622float2(odd);
+            if (__any_sync(0xffffffffu, sum.x != 0.f || sum.y != 0.f) && w.guard == kNoGuard && lane == 0)
+                redo[k % kSlots] = 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[k % kSlots]);
         }
@@ -938,38 +944,30 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 // host side
 // ---------------------------------------------------------------------------
 
-struct PromptDevice {
-    int sm_count = 0;
-    bool ready = false;
-};
 std::mutex g_mu;
-PromptDevice g_dev[64];
+bool g_ready[64];  // by device: kernel attributes set
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-int prompt_device(int *sm_count) {
+int prompt_setup() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_E_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
-    PromptDevice &d = g_dev[dev];
-    if (!d.ready) {
-        if (cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<64>::kAlloc) !=
+    if (g_ready[dev]) return PKV_OK;
+    if (cudaFuncSetAttribute(prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<64>::kAlloc) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<128>::kAlloc) !=
+            cudaSuccess)
+        return PKV_E_CUDA;
+    if (!g_encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
                 cudaSuccess ||
-            cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Smem<128>::kAlloc) != cudaSuccess)
+            found != cudaDriverEntryPointSuccess || !fn)
             return PKV_E_CUDA;
-        if (!g_encode) {
-            void *fn = nullptr;
-            cudaDriverEntryPointQueryResult found;
-            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
-                    cudaSuccess ||
-                found != cudaDriverEntryPointSuccess || !fn)
-                return PKV_E_CUDA;
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-        }
-        d.ready = true;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    *sm_count = d.sm_count;
+    g_ready[dev] = true;
     return PKV_OK;
 }
 
@@ -1026,8 +1024,7 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
         return PKV_E_ALIGN;
     const long long wq = (long long)num_q_heads * head_size, wkv = (long long)num_kv_heads * head_size;
     if (!stride_ok(q_stride, wq) || !stride_ok(k_stride, wkv) || !stride_ok(v_stride, wkv)) return PKV_E_DIMS;
-    int sms = 0;
-    int rc = prompt_device(&sms);
+    int rc = prompt_setup();
     if (rc) return rc;
     PromptArgs a{};
     a.q = static_cast<const __nv_bfloat16 *>(q);
