@@ -59,7 +59,16 @@ constexpr int kThreads = 512;
 // Four warpgroups of 128 at launch: 2 * (72 + 184) = 4 * 128.
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;           // S_A 0, S_B 128, O_A 256, O_B 256 + D
+// TMEM columns: S_A 0, S_B 128, O_A 256, O_B 256 + D. P lies over the first
+// half of its S for D = 128, where nothing is left; for D = 64 it has columns of
+// its own, 384 and 448, and the next S need not wait for the product of P.
+constexpr uint32_t kColO = 256;
+template <int D>
+constexpr bool kOwnP = D == 64;
+template <int D>
+__device__ __forceinline__ constexpr uint32_t col_p(int t) {
+    return kOwnP<D> ? 384 + t * 64 : t * 128;
+}
 // P is handed on in two parts of 96 and 32 keys: the product of the first (six
 // MMAs, 384 cycles) runs while the second is made, and little is left to do
 // once the second is there.
@@ -92,7 +101,7 @@ struct Item {
 
 struct Bars {
     static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6 /* [tile][part] */, kPvDone = 10, kOFull = 12,
-                         kLFull = 14, kOFree = 16, kDrain = 18, kBlock = 19, kDFull = 20, kDEmpty = kDFull + kSlots,
+                         kLFull = 14, kOFree = 16, kSTaken = 18, kDrain = 20, kBlock = 21, kDFull = 22, kDEmpty = kDFull + kSlots,
                          kBadFull = kDEmpty + kSlots, kKvFull = kBadFull + kSlots;
 };
 
@@ -364,7 +373,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     uint64_t *q_full = bar + Bars::kQFull, *q_empty = bar + Bars::kQEmpty, *s_full = bar + Bars::kSFull;
     uint64_t *p_full = bar + Bars::kPFull, *pv_done = bar + Bars::kPvDone, *d_full = bar + Bars::kDFull;
     uint64_t *d_empty = bar + Bars::kDEmpty, *o_full = bar + Bars::kOFull, *l_full = bar + Bars::kLFull;
-    uint64_t *o_free = bar + Bars::kOFree, *drain = bar + Bars::kDrain;
+    uint64_t *o_free = bar + Bars::kOFree, *s_taken = bar + Bars::kSTaken, *drain = bar + Bars::kDrain;
     float *row_sum = reinterpret_cast<float *>(smem + M::kOffSum);
     uint64_t *bad_full = bar + Bars::kBadFull;
     uint64_t *kv_full = bar + Bars::kKvFull, *kv_empty = kv_full + kStages, *v_safe = kv_empty + kStages;
@@ -397,6 +406,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             mbar_init(&o_full[i], 1);
             mbar_init(&l_full[i], 4);
             mbar_init(&o_free[i], 4);
+            mbar_init(&s_taken[i], 4);
         }
         mbar_init(drain, 1);
         mbar_init(bar + Bars::kBlock, 1);
@@ -611,7 +621,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             const uint32_t b_lo = v_lo + (y % kStages) * (M::kTile >> 4);
 #pragma unroll
             for (int kk = part * (kFirstKeys / 16); kk < (part ? kKeys : kFirstKeys) / 16; ++kk)
-                mma_ts(tmu + kColO + t * D, tmu + t * kKeys + kk * 8, b_lo + kk * (2048 >> 4), kIdPV,
+                mma_ts(tmu + kColO + t * D, tmu + col_p<D>(t) + kk * 8, b_lo + kk * (2048 >> 4), kIdPV,
                        kk > 0 ? 1u : 1u - fresh);
         };
         auto s_product = [&](int t, uint32_t y) {
@@ -621,6 +631,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 mma_ss(tmu + t * kKeys, a_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2,
                        b_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2, kIdS, kk > 0 ? 1u : 0u);
         };
+        // What S_t's columns have to wait for before a new S: with P in them its
+        // product, else only the softmax's reading.
+        constexpr int kSFree = kOwnP<D> ? Bars::kSTaken : Bars::kPvDone;
         uint32_t x = 0;                   // K and V tiles of the items so far
         uint32_t pv0 = 0, pv1 = 0;        // PV products issued for A, B
         uint32_t q_used = 0, o_used = 0;  // parity bits by query tile: Q tiles taken, outputs written
@@ -645,9 +658,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 if (n_t == 0) continue;
                 ok = wait(at(Bars::kQFull + t), (q_used >> t) & 1);
                 q_used ^= 1u << t;
-                // S_t goes into columns that hold the P of t's previous
-                // product: that one has to be over first.
-                if (ok && done > 0) ok = wait(at(Bars::kPvDone + t), (done - 1) & 1);
+                if (ok && done > 0) ok = wait(at(kSFree + t), (done - 1) & 1);
                 if (!ok) break;
                 tmem_fence_after_sync();
                 s_product(t, x);
@@ -672,6 +683,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     const int n_t = t ? nB : nA;
                     if (j >= n_t) continue;
                     const uint32_t par = (t ? pv1 : pv0) & 1;
+                    auto next_s = [&]() {
+                        if ((t == 0 || j + 1 >= nA) && !kv_wait(yk)) return false;
+                        if (!wait(at(kSFree + t), par)) return false;
+                        tmem_fence_after_sync();
+                        s_product(t, yk);
+                        commit(at(Bars::kSFull + t));
+                        if (t == 1 || j + 1 >= nB) kv_release(yk);
+                        if (j + 2 == n_t) commit(at(Bars::kQEmpty + t));
+                        return true;
+                    };
+                    if (kOwnP<D> && j + 1 < n_t && !next_s()) { ok = false; break; }
                     if (j == 0) {  // the previous item's O has been read
                         if (!wait(at(Bars::kOFree + t), ((o_used >> t) & 1) ^ 1)) { ok = false; break; }
                         o_used ^= 1u << t;
@@ -685,17 +707,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     commit(at(Bars::kPvDone + t));
                     if (t) ++pv1; else ++pv0;
                     if (t == 1 || j >= nB) kv_release(yv);
-                    if (j + 1 == n_t) {
-                        commit(at(Bars::kOFull + t));
-                        continue;
-                    }
-                    if ((t == 0 || j + 1 >= nA) && !kv_wait(yk)) { ok = false; break; }
-                    if (!wait(at(Bars::kPvDone + t), par)) { ok = false; break; }
-                    tmem_fence_after_sync();
-                    s_product(t, yk);
-                    commit(at(Bars::kSFull + t));
-                    if (t == 1 || j + 1 >= nB) kv_release(yk);
-                    if (j + 2 == n_t) commit(at(Bars::kQEmpty + t));
+                    if (j + 1 == n_t) commit(at(Bars::kOFull + t));
+                    if (!kOwnP<D> && j + 1 < n_t && !next_s()) { ok = false; break; }
                 }
                 if (!ok) break;
             }
@@ -713,6 +726,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const int row = (warp & 3) * 32 + lane;   // its row = TMEM lane
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tm + lane_off + t * kKeys, o_col = tm + lane_off + kColO + t * D;
+        const uint32_t p_col = tm + lane_off + col_p<D>(t);
         const float scale_log2 = a.scale * kLog2e;
         const int g = a.group;
         uint32_t x = 0;   // K and V tiles of the items so far
@@ -769,11 +783,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     const float top = row_max(s) * scale_log2;
                     sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
                     const bool moves = j > 0 && top > m + kRescaleThreshold;
-                    if (!__any_sync(0xffffffffu, moves)) break;
+                    const bool any = __any_sync(0xffffffffu, moves);
+                    if (kOwnP<D> && n > 0) {  // O and P are at rest once the product before is over
+                        ok = warp_wait(&pv_done[t], (n - 1) & 1, abort);
+                        if (!ok) break;
+                        tmem_fence_after_sync();
+                    }
+                    if (!any) break;
                     const float alpha = moves ? fast_exp2(m - top) : 1.f;
                     if (moves) m = top;
                     l *= alpha;
-                    // PV(j - 1) was over before S(j) was issued: O is at rest.
+                    // (P over S: PV(j - 1) was over before S(j) was issued.)
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         float o[16];
@@ -784,20 +804,26 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         tmem_st16(o_col + c * 16, o);
                     }
                 }
+                if (!ok) break;
+                if (kOwnP<D>) {
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_taken[t]);
+                }
                 auto hand_on = [&](int part) {
                     tmem_wait_st();
                     tmem_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[2 * t + part]);
                 };
-                store_p(s_col, p);
+                store_p(p_col, p);
                 hand_on(0);
                 keep(s[3]);  // its exponentials not ahead of the first part's hand-over
                 {
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     uint32_t q[16];
                     exps(s[3], scale_log2, m, part, q);
-                    tmem_st16u(s_col + kFirstKeys / 2, q);
+                    tmem_st16u(p_col + kFirstKeys / 2, q);
                     hand_on(1);
                     l += sum + ((part[0].x + part[0].y) + (part[1].x + part[1].y));
                 }
