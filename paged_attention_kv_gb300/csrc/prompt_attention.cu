@@ -13,10 +13,9 @@
 // copied once (one TMA box each) and serve both tiles:
 //   S_t = Q_t K^T     tcgen05.mma, bf16 operands in 128-byte-swizzled shared
 //                     memory, fp32 accumulator in TMEM;
-//   P_t               one thread per row: S to registers, causal mask, row
-//                     maximum, exponentials against a running reference that
-//                     moves (O rescaled) only when the maximum outgrows it by
-//                     2^8; bf16 pairs over S's own columns in TMEM, handed on
+//   P_t               one thread per row: S to registers, causal mask,
+//                     exponentials against a running reference that moves (O
+//                     rescaled) only when some p outgrows 2^14; bf16 pairs over S's own columns in TMEM, handed on
 //                     in two parts so that the product of the first keys runs
 //                     during the exponentials of the last;
 //   O_t += P_t V      tcgen05.mma, A = P_t from TMEM, B = V as it lies.
@@ -73,7 +72,7 @@ __device__ __forceinline__ constexpr uint32_t col_p(int t) {
 // MMAs, 384 cycles) runs while the second is made, and little is left to do
 // once the second is there.
 constexpr int kFirstKeys = 96;
-constexpr float kRescaleThreshold = 8.f;  // log2 units: P stays <= 2^8
+constexpr float kRescaleBits = 14.f, kRescaleSum = 16384.f;  // P stays <= 2^14, exact in bf16's range and in l
 constexpr int kSlots = 4;                 // items between the copy warp and the output
 constexpr int kNoGuard = INT_MAX;
 constexpr int kGuardTiles = 3;            // an item's at most 256 tokens touch at most three key tiles
@@ -256,15 +255,14 @@ __device__ __forceinline__ void exps(const float (&s)[32], float scale_log2, flo
     }
 }
 
-__device__ __forceinline__ float row_max(const float (&s)[4][32]) {
-    float mx[4];
+__device__ __forceinline__ float max32(const float (&s)[32]) {
+    float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        mx[c] = fmaxf(s[c][0], s[c][1]);
-#pragma unroll
-        for (int e = 2; e < 32; e += 2) mx[c] = fmax3(mx[c], s[c][e], s[c][e + 1]);
+    for (int e = 4; e < 32; e += 4) {
+        a = fmax3(a, s[e], s[e + 1]);
+        b = fmax3(b, s[e + 2], s[e + 3]);
     }
-    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    return fmaxf(a, b);
 }
 
 __device__ __forceinline__ void store_p(uint32_t col, const uint32_t (&p)[48]) {
@@ -757,11 +755,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 float s[4][32];
                 uint32_t p[kFirstKeys / 2];
                 float sum;
-                // P of the first kFirstKeys keys, against the reference as it
-                // stands: the exponentials need not wait for the row's maximum,
-                // which is taken beside them. Where a row of the warp outgrows
-                // its reference (rare), O follows and the tile is done again; S
-                // is still there.
+                // P against a reference that need not be the maximum: with all p
+                // below 2^kRescaleBits nothing overflows, and the common factor
+                // falls out of O / l. So after a row's first tile, whose maximum
+                // sets the reference, the maximum is not taken: where the sum of
+                // the first keys' p or the largest of the last keys' scores is
+                // past the bound (rare), the reference moves up to the maximum,
+                // O follows, and the tile is done again; S is still there.
+                bool moves = j == 0;
                 while (true) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
@@ -776,22 +777,34 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                             for (int e = 0; e < 32; ++e) s[c][e] = c * 32 + e <= lim ? s[c][e] : -INFINITY;
                         }
                     }
-                    if (j == 0) m = row_max(s) * scale_log2;  // key 0 is visible to every row
+                    float alpha = 1.f;
+                    const bool any = __any_sync(0xffffffffu, moves);
+                    if (any) {
+                        // key 0 is visible to every row: the first tile's maximum is a score
+                        const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3]))) * scale_log2;
+                        if (j == 0) {
+                            m = top;
+                        } else if (moves && top > m) {
+                            alpha = fast_exp2(m - top);
+                            m = top;
+                        }
+                    }
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int c = 0; c < kFirstKeys / 32; ++c) exps(s[c], scale_log2, m, part, p + 16 * c);
-                    const float top = row_max(s) * scale_log2;
+                    const float last = fmaf(max32(s[3]), scale_log2, -m);
                     sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
-                    const bool moves = j > 0 && top > m + kRescaleThreshold;
-                    const bool any = __any_sync(0xffffffffu, moves);
                     if (kOwnP<D> && n > 0) {  // O and P are at rest once the product before is over
                         ok = warp_wait(&pv_done[t], (n - 1) & 1, abort);
                         if (!ok) break;
                         tmem_fence_after_sync();
                     }
-                    if (!any) break;
-                    const float alpha = moves ? fast_exp2(m - top) : 1.f;
-                    if (moves) m = top;
+                    if (!any) {
+                        moves = sum > kRescaleSum || last > kRescaleBits;
+                        if (!__any_sync(0xffffffffu, moves)) break;
+                        continue;
+                    }
+                    if (j == 0) break;
                     l *= alpha;
                     // (P over S: PV(j - 1) was over before S(j) was issued.)
 #pragma unroll 1
@@ -803,6 +816,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         for (int e = 0; e < 16; ++e) o[e] *= alpha;
                         tmem_st16(o_col + c * 16, o);
                     }
+                    break;
                 }
                 if (!ok) break;
                 if (kOwnP<D>) {
