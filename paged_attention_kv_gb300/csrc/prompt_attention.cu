@@ -15,19 +15,19 @@
 //                     memory, fp32 accumulator in TMEM;
 //   P_t               one thread per row: S to registers, causal mask,
 //                     exponentials against a running reference that moves (O
-//                     rescaled) only when some p outgrows 2^14; bf16 pairs over S's own columns in TMEM, handed on
-//                     in two parts so that the product of the first keys runs
-//                     during the exponentials of the last;
+//                     rescaled) only when some p outgrows 2^14; bf16 pairs in
+//                     TMEM, handed on in two parts so that the product of the
+//                     first keys runs during the exponentials of the last;
 //   O_t += P_t V      tcgen05.mma, A = P_t from TMEM, B = V as it lies.
 // The softmax of A runs while the tensor core works for B and the other way
-// round. The sums l are of the unrounded p; rounding P to bf16 (2^-9 of each
-// term) is what the tensor core takes.
+// round. The sums l are of the unrounded p; rounding P to bf16 (at most 2^-8 of
+// each term, half a step) is what the tensor core takes.
 //
 // Warps: 0 MMA issue and TMEM, 1 copies and the item list, 2-3 guard of V, 4-7
-// softmax of A, 8-11 of B, 12-15 output. The host does not know
-// the lengths, and no workspace is needed: items are numbered by tile level
-// (longest keys first) over all sequences, every CTA counts the tiles once,
-// and its copy warp finds an item by a binary search over levels. The launch
+// softmax of A, 8-11 of B, 12-15 output. The host does not know the lengths, and
+// no workspace is needed: items are numbered by tile level (longest keys first)
+// over all sequences, every CTA counts the tiles once, and its copy warp finds
+// an item by a binary search over levels. The launch
 // has a block for every item there may be; the blocks that start (one an SM)
 // fetch the items of the others from the hardware one by one, so that an SM
 // takes its next item when it is ready for it. (Items dealt out in turn left
@@ -119,7 +119,7 @@ struct Smem {
     static constexpr int kOffItem = kOffKv + kStages * kTile;
     static constexpr int kOffBlock = kOffItem + kSlots * (int)sizeof(Item);  // the launch control's answer
     static constexpr int kOffBar = kOffBlock + 16;
-    static constexpr int kBars = Bars::kKvFull + 2 * kStages + kStages / 2;
+    static constexpr int kBars = Bars::kKvFull + 3 * kStages;  // K/V full, empty; by V slot: guarded, safe
     static constexpr int kOffSum = kOffBar + kBars * 8;  // float [tile][row]: sums of p
     static constexpr int kOffBad = kOffSum + 2 * kRows * 4;  // bits [slot][guarded tile][key]
     static constexpr int kOffRedo = kOffBad + kSlots * kGuardTiles * (kKeys / 8);  // int [slot]
@@ -335,13 +335,13 @@ __device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, cons
         o[e + 1] = v.y;
     }
     if (any_bad) add_bad<D>(a, w, bad, i, c, o);
+    if (!valid) return;
     uint32_t p[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         p[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
         odd = __hfma2(pair_of(p[e]), __floats2bfloat162_rn(0.f, 0.f), odd);
     }
-    if (!valid) return;
     if (a.wide_out) {
 #pragma unroll
         for (int e = 0; e < 16; e += 8)
@@ -375,6 +375,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     float *row_sum = reinterpret_cast<float *>(smem + M::kOffSum);
     uint64_t *bad_full = bar + Bars::kBadFull;
     uint64_t *kv_full = bar + Bars::kKvFull, *kv_empty = kv_full + kStages, *v_safe = kv_empty + kStages;
+    uint64_t *v_guard = v_safe + kStages / 2;
     uint32_t *bad_keys = reinterpret_cast<uint32_t *>(smem + M::kOffBad);
     volatile int *redo = reinterpret_cast<volatile int *>(smem + M::kOffRedo);
     Item *items = reinterpret_cast<Item *>(smem + M::kOffItem);
@@ -411,7 +412,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
-            if (i % 2) mbar_init(&v_safe[i / 2], 2);
+            if (i % 2) {
+                mbar_init(&v_safe[i / 2], 2);
+                mbar_init(&v_guard[i / 2], 1);
+            }
         }
         mbar_fence_init();
     }
@@ -429,7 +433,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         unsigned long long sum = 0;
 #pragma unroll 1
         for (int r = threadIdx.x; r < a.num_reqs; r += kThreads) {
-            const int n = seq_tiles(a, r, blockIdx.x == 0);
+            const int n = seq_tiles(a, r, true);
             if (r < kSeqCache) seq[r] = n;
             most = max(most, n);
             sum += n;
@@ -459,16 +463,23 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             for (int d = 16; d; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
             return c * Hkv;
         };
-        int hi = s_levels;        // items_from(hi) <= every item still to come
+        // Items come in rising order, so the search goes on downward; were one
+        // to come out of order, it would start anew.
+        int hi = s_levels;        // items_from(hi) <= the item looked for
         long long above = 0;      // items_from(hi)
         uint32_t x = 0;           // K and V tiles issued
         uint32_t q_used = 0, q_any = 0;  // bit t: parity of Q_t's tiles copied; any copied
+        uint32_t g_used = 0, g_any = 0;  // by V slot: guarded tiles copied
         bool ok = true;
         // Item `it` of the launch.
         auto find = [&](long long it) {
             Item w{};
             if (it < total) {
                 // largest level m with items_from(m) > it
+                if (it < above) {
+                    hi = s_levels;
+                    above = 0;
+                }
                 int lo = 0;
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
@@ -551,9 +562,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         }
                         const int st = x % kStages;
                         if (!lane_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, abort)) { ok = false; break; }
-                        mbar_arrive_expect_tx(&kv_full[st], kKeys * D * 2);
+                        // A guarded V tile is told to the guard, which tells the
+                        // MMA warp; its turn at kv_full passes at once.
+                        uint64_t *full = &kv_full[st];
+                        if ((i & 1) && (i >> 1) >= w.guard) {
+                            mbar_arrive(full);
+                            full = &v_guard[st / 2];
+                            g_used ^= 1u << (st / 2);
+                            g_any |= 1u << (st / 2);
+                        }
+                        mbar_arrive_expect_tx(full, kKeys * D * 2);
                         tma_load_4d(smem + M::kOffKv + st * M::kTile, i & 1 ? &v_map : &k_map, 0,
-                                    w.q0 + (i >> 1) * kKeys, 0, w.h, &kv_full[st]);
+                                    w.q0 + (i >> 1) * kKeys, 0, w.h, full);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -600,6 +620,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 mbar_drain(&kv_full[y % kStages], (y / kStages) & 1, status, nullptr, 0);
             for (int t = 0; t < 2; ++t)
                 if (q_any >> t & 1) mbar_drain(&q_full[t], ((q_used >> t) & 1) ^ 1, status, nullptr, 0);
+            for (int v = 0; v < kStages / 2; ++v)
+                if (g_any >> v & 1) mbar_drain(&v_guard[v], ((g_used >> v) & 1) ^ 1, status, nullptr, 0);
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------- MMA issue ----------------------------
@@ -727,7 +749,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const uint32_t p_col = tm + lane_off + col_p<D>(t);
         const float scale_log2 = a.scale * kLog2e;
         const int g = a.group;
-        uint32_t x = 0;   // K and V tiles of the items so far
         uint32_t n = 0, n_out = 0;  // key tiles and items this query tile has been through
         for (int k = 0;; ++k) {
             if (!warp_wait(&d_full[k % kSlots], (k / kSlots) & 1, abort)) break;
@@ -735,11 +756,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[k % kSlots]);
             if (!w.valid) break;
-            const int n_t = w.n_keys[t], nt = max(w.n_keys[0], w.n_keys[1]);
-            if (n_t == 0) {
-                x += 2 * nt;
-                continue;
-            }
+            const int n_t = w.n_keys[t];
+            if (n_t == 0) continue;
             const int i0 = w.i0 + t * a.tile_tokens;
             const int i = i0 + row / g;
             const bool valid = row < a.tile_tokens * g && i < w.n;
@@ -780,10 +798,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     float alpha = 1.f;
                     const bool any = __any_sync(0xffffffffu, moves);
                     if (any) {
-                        // key 0 is visible to every row: the first tile's maximum is a score
                         const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3]))) * scale_log2;
                         if (j == 0) {
-                            m = top;
+                            m = fmaxf(top, -1e30f);  // a number even where every score is minus infinity
                         } else if (moves && top > m) {
                             alpha = fast_exp2(m - top);
                             m = top;
@@ -842,7 +859,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     l += sum + ((part[0].x + part[0].y) + (part[1].x + part[1].y));
                 }
             }
-            x += 2 * nt;
             if (!ok || !warp_wait(&o_free[t], (n_out & 1) ^ 1, abort)) break;
             ++n_out;
             row_sum[t * kRows + row] = l;
@@ -908,7 +924,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         // that see them. (Looking over every item's tiles cost 3 to 5 %.)
         setmaxnreg_dec<kOtherRegs>();
         const int row0 = (warp - kGuardWarp) * (kKeys / 2);  // each warp has half of a tile's keys
-        uint32_t x = 0;
+        uint32_t x = 0, g_used = 0;  // g_used: parity bits of guarded tiles by V slot
         bool ok = true;
         for (int k = 0; ok; ++k) {
             if (!warp_wait(&d_full[k % kSlots], (k / kSlots) & 1, abort)) break;
@@ -918,12 +934,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             uint32_t *bad = bad_keys + (k % kSlots) * kGuardTiles * (kKeys / 32);
             if (lane < 2 * kGuardTiles) bad[lane / 2 * (kKeys / 32) + row0 / 32 + lane % 2] = 0;
             __syncwarp();
-            for (int j = 0; j < nt; ++j) {
-                // waited for in turn: a phase's parity tells it from the one
-                // before only
-                const uint32_t y = x + 2 * j + 1;
-                if (!warp_wait(&kv_full[y % kStages], (y / kStages) & 1, abort)) { ok = false; break; }
-                if (j < w.guard) continue;
+            for (int j = w.guard; j < nt; ++j) {
+                const uint32_t y = x + 2 * j + 1, v = y / 2 % (kStages / 2);
+                if (!warp_wait(&v_guard[v], (g_used >> v) & 1, abort)) { ok = false; break; }
+                g_used ^= 1u << v;
                 uint4 *vt = reinterpret_cast<uint4 *>(smem + M::kOffKv + (y % kStages) * M::kTile);
                 const int rows = min(kKeys, w.n - j * kKeys);
                 // A value times 0 is NaN unless it is finite: one packed
@@ -962,7 +976,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&v_safe[y / 2 % (kStages / 2)]);
+                if (lane == 0) mbar_arrive(&v_safe[v]);
             }
             x += 2 * nt;
             __syncwarp();

@@ -375,6 +375,45 @@ def test_prompt_values_that_are_not_finite_reach_only_their_readers(d, bad, whic
         assert bool(((g - w).abs()[ok] <= (w.abs() * 2.0 ** -8 + 0.05)[ok]).all())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_scores_of_minus_infinity(d):
+    """Keys whose score is minus infinity for every row: a row that sees no
+    other key is not a number, as in the formula; the others leave them out,
+    even where they fill a row's first key tiles."""
+    lens, dead = [420], 300
+    q, k, v, qsl, scale = run_prompt(lens, 4, 1, d, 18)
+    q.copy_(q.abs() + 0.01)
+    k[:dead] = -float("inf")
+    got = pkv.pkv_prompt_attention(q, k, v, qsl, scale)
+    assert bool(torch.isnan(got[:dead]).all())
+    want, mag = po.prompt(q[dead:], k[dead:], v[dead:], [lens[0] - dead], scale)
+    assert po.worst(got[dead:], want, po.prompt_tolerance(want, mag)) <= 1.0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_nothing_finite_anywhere_ends(d):
+    """Every item is done twice, the second time guarded."""
+    lens = [700, 1, 333]
+    q, k, v, qsl, scale = run_prompt(lens, 8, 2, d, 19)
+    for x in (q, k, v):
+        x.fill_(float("nan"))
+    status = i32([0])
+    got = pkv.pkv_prompt_attention(q, k, v, qsl, scale, status=status)
+    assert bool(torch.isnan(got).all()) and pkv.pkv_read_status(status) == 0
+    q, k, _, qsl, scale = run_prompt(lens, 8, 2, d, 19)
+    got = pkv.pkv_prompt_attention(q, k, v, qsl, scale, status=status)
+    assert bool(torch.isnan(got).all()) and pkv.pkv_read_status(status) == 0
+
+
+def test_prompt_odd_output_address():
+    """An output on a 16-byte boundary that is no 32-byte one."""
+    lens = [70, 200]
+    q, k, v, qsl, scale = run_prompt(lens, 4, 2, 64, 21)
+    out = torch.empty(q.numel() + 8, dtype=torch.bfloat16, device=DEV)[8:].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    assert torch.equal(check_prompt(q, k, v, lens, qsl, scale, out=out), pkv.pkv_prompt_attention(q, k, v, qsl, scale))
+
+
 def test_prompt_bad_bounds_are_reported_and_skipped():
     lens = [40, 40, 40]
     q, k, v, qsl, scale = run_prompt(lens, 4, 2, 64, 16)
