@@ -152,6 +152,15 @@ __device__ __forceinline__ uint32_t timer_lo() {
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
     return t;
 }
+__device__ __forceinline__ bool is_done(uint32_t bar, uint32_t parity) {  // asked by a whole warp, without waiting
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+}
 // By a whole warp, which leaves it with one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
@@ -659,13 +668,23 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t q_used = 0, o_used = 0;  // parity bits by query tile: Q tiles taken, outputs written
         uint32_t v_used = 0;              // by V slot: guarded tiles
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            if (!wait(at(Bars::kDFull + k % kSlots), (k / kSlots) & 1)) { ok = false; break; }
+        int have = -1, next_a = 0, next_b = 0, next_guard = 0;  // the item read last
+        auto read = [&](int k) {
             const Item w = items[k % kSlots];
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[k % kSlots]);
-            if (!uniform(w.valid)) break;
-            const int nA = uniform(w.n_keys[0]), nB = uniform(w.n_keys[1]), nt = max(nA, nB), guard = uniform(w.guard);
+            next_a = uniform(w.n_keys[0]);  // none: the end
+            next_b = uniform(w.n_keys[1]);
+            next_guard = uniform(w.guard);
+            have = k;
+        };
+        for (int k = 0; ok; ++k) {
+            if (have < k) {
+                if (!wait(at(Bars::kDFull + k % kSlots), (k / kSlots) & 1)) { ok = false; break; }
+                read(k);
+            }
+            const int nA = next_a, nB = next_b, nt = max(nA, nB), guard = next_guard;
+            if (nt == 0) break;
             // S_A(0), S_B(0); then step j: O_t += P_t(j) V(j) and S_t(j + 1),
             // for A, then for B. A sees no more key tiles than B, unless B is
             // empty. What can be asked for ahead (the next tiles) is, while
@@ -717,6 +736,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     if (j == 0) {  // the previous item's O has been read
                         if (!wait(at(Bars::kOFree + t), ((o_used >> t) & 1) ^ 1)) { ok = false; break; }
                         o_used ^= 1u << t;
+                        if (t == 0 && is_done(at(Bars::kDFull + (k + 1) % kSlots), ((k + 1) / kSlots) & 1)) read(k + 1);
                     }
                     if (!wait(at(Bars::kPFull + 2 * t), par)) { ok = false; break; }
                     tmem_fence_after_sync();
