@@ -424,8 +424,9 @@ int paged_qk_norm_rope(const pkv_rope_desc *desc, const void *q, const void *k, 
  *             other; head_size 64 or 128, at most 128 q heads per kv head
  *  query_start_loc  int32 [num_reqs + 1]. A sequence may be empty. One with
  *             bounds that descend or leave [0, num_tokens] is skipped and
- *             raises PKV_DEV_BAD_QSL. Rows outside every sequence are left
- *             as they were.
+ *             raises PKV_DEV_BAD_QSL (so do sequences that overlap to more
+ *             rows than there are; then nothing is computed). Rows outside
+ *             every sequence are left as they were.
  *  scale      finite and greater than 0
  *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the inputs
  *  status     optional device int32, PKV_DEV_* bits OR-ed in

@@ -394,47 +394,34 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     // broadcast: the compiler then knows that a role's branch is the whole warp's (see uniform())
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        s_abort = 0;
-        s_levels = 0;
-        s_tiles = 0;
-        for (int i = 0; i < kSlots; ++i) {
-            redo[i] = 0;
-            mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], 15);  // the MMA, guard, softmax and output warps
-            mbar_init(&bad_full[i], 2);
+    if (warp == kCopyWarp) {
+        // barriers by index, with the arrivals that each waits for
+        if (lane == 0) {
+            s_abort = 0;
+            s_levels = 0;
+            s_tiles = 0;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[2 * i], 4);
-            mbar_init(&p_full[2 * i + 1], 4);
-            mbar_init(&pv_done[i], 1);
-            mbar_init(&o_full[i], 1);
-            mbar_init(&l_full[i], 4);
-            mbar_init(&o_free[i], 4);
-            mbar_init(&s_taken[i], 4);
-        }
-        mbar_init(drain, 1);
-        mbar_init(bar + Bars::kBlock, 1);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
-            if (i % 2) {
-                mbar_init(&v_safe[i / 2], 2);
-                mbar_init(&v_guard[i / 2], 1);
-            }
+        if (lane < kSlots) redo[lane] = 0;
+        for (int i = lane; i < M::kBars; i += 32) {
+            const bool four = (i >= Bars::kPFull && i < Bars::kPFull + 4) || (i >= Bars::kLFull && i < Bars::kLFull + 2) ||
+                              (i >= Bars::kOFree && i < Bars::kOFree + 2) || (i >= Bars::kSTaken && i < Bars::kSTaken + 2);
+            const int v_safe0 = Bars::kKvFull + 2 * kStages;
+            const bool two = (i >= Bars::kBadFull && i < Bars::kBadFull + kSlots) ||
+                             (i >= v_safe0 && i < v_safe0 + kStages / 2);
+            // an item's description: the MMA, guard, softmax and output warps
+            const bool all = i >= Bars::kDEmpty && i < Bars::kDEmpty + kSlots;
+            mbar_init(bar + i, all ? 15 : four ? 4 : two ? 2 : 1);
         }
         mbar_fence_init();
     }
-    if (warp == kCopyWarp && lane == 0) {
+    if (warp == kGuardWarp && lane == 0) {
         tma_prefetch_desc(&q_map);
         tma_prefetch_desc(&k_map);
         tma_prefetch_desc(&v_map);
     }
     pdl_launch_dependents();
     pdl_wait();
+    // not before the wait: the kernel before may have TMEM to take yet
     if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
     __syncthreads();
     {
@@ -459,29 +446,35 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     if (warp == kCopyWarp) {
         // ------------------------ items, Q, K and V ------------------------
         setmaxnreg_dec<kOtherRegs>();
-        const int Hkv = a.num_kv_heads, R = a.num_reqs;
-        const long long total = (long long)s_tiles * Hkv;
+        const uint32_t Hkv = a.num_kv_heads;
+        const int R = a.num_reqs;
+        // More items than the launch has blocks: the sequences overlap, and
+        // none is computed.
+        uint32_t total = 0;
+        if (s_tiles * Hkv <= gridDim.x) {
+            total = (uint32_t)s_tiles * Hkv;
+        } else if (lane == 0) {
+            raise_status(status, PKV_DEV_BAD_QSL);
+        }
         auto tiles_of = [&](int r) { return r < kSeqCache ? seq[r] : seq_tiles(a, r, false); };
         // Items of level m or above (level m: a sequence's m-th pair of query
         // tiles, so m grows with the keys seen).
         auto items_from = [&](int m) {
-            long long c = 0;
+            uint32_t c = 0;
 #pragma unroll 1
             for (int r = lane; r < R; r += 32) c += max(0, tiles_of(r) - m);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
-            return c * Hkv;
+            return __reduce_add_sync(0xffffffffu, c) * Hkv;
         };
         // Items come in rising order, so the search goes on downward; were one
         // to come out of order, it would start anew.
         int hi = s_levels;        // items_from(hi) <= the item looked for
-        long long above = 0;      // items_from(hi)
+        uint32_t above = 0;       // items_from(hi)
         uint32_t x = 0;           // K and V tiles issued
         uint32_t q_used = 0, q_any = 0;  // bit t: parity of Q_t's tiles copied; any copied
         uint32_t g_used = 0, g_any = 0;  // by V slot: guarded tiles copied
         bool ok = true;
         // Item `it` of the launch.
-        auto find = [&](long long it) {
+        auto find = [&](uint32_t it) {
             Item w{};
             if (it < total) {
                 // largest level m with items_from(m) > it
@@ -492,7 +485,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 int lo = 0;
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    const long long c = items_from(mid);
+                    const uint32_t c = items_from(mid);
                     if (c > it) {
                         lo = mid;
                     } else {
@@ -500,9 +493,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         above = c;
                     }
                 }
-                const uint32_t idx = (uint32_t)(it - above);  // below sequences x heads, which the host bounds
-                int want = (int)(idx / (uint32_t)Hkv);        // the want-th sequence with more than lo tiles
-                w.h = (int)(idx % (uint32_t)Hkv);
+                const uint32_t idx = it - above;
+                int want = (int)(idx / Hkv);  // the want-th sequence with more than lo tiles
+                w.h = (int)(idx - want * Hkv);
                 int r = 0;
 #pragma unroll 1
                 for (int r0 = 0; r0 < R; r0 += 32) {
@@ -596,7 +589,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                             ok = answer(index);
                         }
                     }
-                    ahead = find(ok && index != ~0u ? (long long)index : total);
+                    ahead = find(ok ? index : ~0u);
                 }
             }
             if (!ok) break;

@@ -431,6 +431,14 @@ def test_prompt_bad_bounds_are_reported_and_skipped():
             assert bool((out[rest] == 3).all())
 
 
+def test_prompt_overlapping_sequences_are_refused():
+    q, k, v, _, scale = run_prompt([400], 4, 2, 64, 22)
+    out, status = torch.full_like(q, 3.0), i32([0])
+    pkv.pkv_prompt_attention(q, k, v, i32([0, 400, 0, 400, 0, 400, 0, 400, 0, 400]), scale, out=out, status=status)
+    assert pkv.pkv_read_status(status) == pkv.PKV_DEV_BAD_QSL
+    assert bool((out == 3).all())
+
+
 def test_prompt_agrees_with_chunked_paged_attention():
     """The same prompt through the pool, in two chunks, gives the same rows."""
     lens = [500]
