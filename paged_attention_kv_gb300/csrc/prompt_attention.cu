@@ -20,7 +20,8 @@
 //                     first keys runs during the exponentials of the last;
 //   O_t += P_t V      tcgen05.mma, A = P_t from TMEM, B = V as it lies.
 // The softmax of A runs while the tensor core works for B and the other way
-// round. The sums l are of the unrounded p; rounding P to bf16 (at most 2^-8 of
+// round. (Where there are few items, an item is one query tile, and A and B are
+// its even and odd key tiles, joined at the end.) The sums l are of the unrounded p; rounding P to bf16 (at most 2^-8 of
 // each term, half a step) is what the tensor core takes.
 //
 // Warps: 0 MMA issue and TMEM, 1 copies and the item list, 2-3 guard of V, 4-7
@@ -84,7 +85,8 @@ struct PromptArgs {
     long long q_stride, k_stride, v_stride;
     __nv_bfloat16 *out;
     const int32_t *qsl;
-    int num_tokens, num_reqs, num_q_heads, num_kv_heads, group, tile_tokens;  // tile_tokens = 128 / group
+    int num_tokens, num_reqs, num_q_heads, num_kv_heads, group;
+    int tile_tokens, item_tokens;  // tokens of a query tile (128 / group), of an item
     float scale;
     int wide_out;  // out is on a 32-byte boundary
     int32_t *status;
@@ -104,6 +106,13 @@ struct Bars {
                          kBadFull = kDEmpty + kSlots, kKvFull = kBadFull + kSlots;
 };
 
+// Key tiles whose K and V an item copies: those that its tiles share, or, where
+// they split the keys, all of both.
+template <bool kSplit>
+__device__ __forceinline__ int item_tiles(const Item &w) {
+    return kSplit ? w.n_keys[0] + w.n_keys[1] : max(w.n_keys[0], w.n_keys[1]);
+}
+
 __device__ __forceinline__ Item guarded(Item w) {
     w.guard = w.i0 / kKeys;
     return w;
@@ -119,9 +128,10 @@ struct Smem {
     static constexpr int kOffItem = kOffKv + kStages * kTile;
     static constexpr int kOffBlock = kOffItem + kSlots * (int)sizeof(Item);  // the launch control's answer
     static constexpr int kOffBar = kOffBlock + 16;
-    static constexpr int kBars = Bars::kKvFull + 3 * kStages;  // K/V full, empty; by V slot: guarded, safe
+    static constexpr int kBars = Bars::kKvFull + 4 * kStages;  // K/V full, empty; guarded V: there, safe
     static constexpr int kOffSum = kOffBar + kBars * 8;  // float [tile][row]: sums of p
-    static constexpr int kOffBad = kOffSum + 2 * kRows * 4;  // bits [slot][guarded tile][key]
+    static constexpr int kOffMax = kOffSum + 2 * kRows * 4;  // float [tile][row]: references (split items)
+    static constexpr int kOffBad = kOffMax + 2 * kRows * 4;  // bits [slot][guarded tile][key]
     static constexpr int kOffRedo = kOffBad + kSlots * kGuardTiles * (kKeys / 8);  // int [slot]
     static constexpr int kOffSeq = kOffRedo + kSlots * 4;
     static constexpr int kBytes = kOffSeq + kSeqCache * 4;
@@ -291,8 +301,7 @@ __device__ __forceinline__ int seq_tiles(const PromptArgs &a, int r, bool report
         if (report) raise_status(a.status, PKV_DEV_BAD_QSL);
         return 0;
     }
-    const int per = 2 * a.tile_tokens;
-    return (int)(((uint32_t)(q1 - q0) + per - 1) / (uint32_t)per);
+    return (int)(((uint32_t)(q1 - q0) + a.item_tokens - 1) / (uint32_t)a.item_tokens);
 }
 
 __device__ __forceinline__ __nv_bfloat162 pair_of(uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); }
@@ -365,7 +374,7 @@ __device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, cons
     }
 }
 
-template <int D>
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptArgs a) {
@@ -382,9 +391,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     uint64_t *d_empty = bar + Bars::kDEmpty, *o_full = bar + Bars::kOFull, *l_full = bar + Bars::kLFull;
     uint64_t *o_free = bar + Bars::kOFree, *s_taken = bar + Bars::kSTaken, *drain = bar + Bars::kDrain;
     float *row_sum = reinterpret_cast<float *>(smem + M::kOffSum);
+    float *row_ref = reinterpret_cast<float *>(smem + M::kOffMax);
     uint64_t *bad_full = bar + Bars::kBadFull;
     uint64_t *kv_full = bar + Bars::kKvFull, *kv_empty = kv_full + kStages, *v_safe = kv_empty + kStages;
-    uint64_t *v_guard = v_safe + kStages / 2;
+    uint64_t *v_guard = v_safe + kStages;
     uint32_t *bad_keys = reinterpret_cast<uint32_t *>(smem + M::kOffBad);
     volatile int *redo = reinterpret_cast<volatile int *>(smem + M::kOffRedo);
     Item *items = reinterpret_cast<Item *>(smem + M::kOffItem);
@@ -407,7 +417,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                               (i >= Bars::kOFree && i < Bars::kOFree + 2) || (i >= Bars::kSTaken && i < Bars::kSTaken + 2);
             const int v_safe0 = Bars::kKvFull + 2 * kStages;
             const bool two = (i >= Bars::kBadFull && i < Bars::kBadFull + kSlots) ||
-                             (i >= v_safe0 && i < v_safe0 + kStages / 2);
+                             (i >= v_safe0 && i < v_safe0 + kStages);
             // an item's description: the MMA, guard, softmax and output warps
             const bool all = i >= Bars::kDEmpty && i < Bars::kDEmpty + kSlots;
             mbar_init(bar + i, all ? 15 : four ? 4 : two ? 2 : 1);
@@ -471,7 +481,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t above = 0;       // items_from(hi)
         uint32_t x = 0;           // K and V tiles issued
         uint32_t q_used = 0, q_any = 0;  // bit t: parity of Q_t's tiles copied; any copied
-        uint32_t g_used = 0, g_any = 0;  // by V slot: guarded tiles copied
+        uint32_t g_used = 0, g_any = 0;  // by stage: guarded V tiles copied
         bool ok = true;
         // Item `it` of the launch.
         auto find = [&](uint32_t it) {
@@ -512,12 +522,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 w.valid = 1;
                 w.q0 = __ldg(a.qsl + r);
                 w.n = __ldg(a.qsl + r + 1) - w.q0;
-                w.i0 = lo * 2 * a.tile_tokens;
+                w.i0 = lo * a.item_tokens;
                 w.guard = kNoGuard;
+                if (kSplit) {
+                    const int all = (min(w.n, w.i0 + a.tile_tokens) + kKeys - 1) / kKeys;
+                    w.n_keys[0] = (all + 1) / 2;
+                    w.n_keys[1] = all / 2;
+                } else {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int last = min(w.n, w.i0 + (t + 1) * a.tile_tokens);  // past the tile's last token
-                    w.n_keys[t] = last > w.i0 + t * a.tile_tokens ? (last + kKeys - 1) / kKeys : 0;
+                    for (int t = 0; t < 2; ++t) {
+                        const int last = min(w.n, w.i0 + (t + 1) * a.tile_tokens);  // past the tile's last token
+                        w.n_keys[t] = last > w.i0 + t * a.tile_tokens ? (last + kKeys - 1) / kKeys : 0;
+                    }
                 }
             }
             return w;
@@ -541,9 +557,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         };
 #pragma unroll 1
         for (int k = -1; ok; ++k) {
-            // Q_A, K(0), Q_B, V(0), K(1), V(1), ... of item k, by one lane; the
-            // next item is looked up once the ring is full.
-            const int all = 2 * max(w.n_keys[0], w.n_keys[1]);
+            // Q_A, K(0), Q_B, V(0), K(1), V(1), ... of item k, by one lane (split:
+            // one Q; K(0), K(1), V(0), K(2), V(1), ..., as the products take
+            // them); the next item is looked up once the ring is full.
+            const int tiles = item_tiles<kSplit>(w), all = 2 * tiles;
             int i = 0;
             if (k >= 0 && !again) ask();
 #pragma unroll 1
@@ -552,7 +569,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 if (lane == 0) {
 #pragma unroll 1
                     for (; i < stop; ++i, ++x) {
-                        if (i < 2 && w.n_keys[i]) {
+                        if (i < (kSplit ? 1 : 2) && w.n_keys[i]) {
                             if (!lane_wait(&q_empty[i], ((q_used >> i) & 1) ^ 1, abort)) { ok = false; break; }
                             q_used ^= 1u << i;
                             q_any |= 1u << i;
@@ -562,20 +579,27 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                                 tma_load_3d(smem + M::kOffQ + i * M::kTile + b * M::kHalf, &q_map, b * 64,
                                             w.h * a.group, w.q0 + w.i0 + i * a.tile_tokens, &q_full[i]);
                         }
+                        int j = i >> 1;
+                        bool is_v = i & 1;
+                        if (kSplit) {
+                            const int f = i - 2;  // behind K(0), K(1)
+                            is_v = i > 0 && (f < 0 ? tiles == 1 : !(f & 1) || f >= 2 * (tiles - 2));
+                            j = f < 0 ? (is_v ? 0 : i) : f >= 2 * (tiles - 2) ? f - (tiles - 2) : is_v ? f >> 1 : (f >> 1) + 2;
+                        }
                         const int st = x % kStages;
                         if (!lane_wait(&kv_empty[st], ((x / kStages) & 1) ^ 1, abort)) { ok = false; break; }
                         // A guarded V tile is told to the guard, which tells the
                         // MMA warp; its turn at kv_full passes at once.
                         uint64_t *full = &kv_full[st];
-                        if ((i & 1) && (i >> 1) >= w.guard) {
+                        if (is_v && j >= w.guard) {
                             mbar_arrive(full);
-                            full = &v_guard[st / 2];
-                            g_used ^= 1u << (st / 2);
-                            g_any |= 1u << (st / 2);
+                            full = &v_guard[st];
+                            g_used ^= 1u << st;
+                            g_any |= 1u << st;
                         }
                         mbar_arrive_expect_tx(full, kKeys * D * 2);
-                        tma_load_4d(smem + M::kOffKv + st * M::kTile, i & 1 ? &v_map : &k_map, 0,
-                                    w.q0 + (i >> 1) * kKeys, 0, w.h, full);
+                        tma_load_4d(smem + M::kOffKv + st * M::kTile, is_v ? &v_map : &k_map, 0, w.q0 + j * kKeys, 0,
+                                    w.h, full);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -622,7 +646,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 mbar_drain(&kv_full[y % kStages], (y / kStages) & 1, status, nullptr, 0);
             for (int t = 0; t < 2; ++t)
                 if (q_any >> t & 1) mbar_drain(&q_full[t], ((q_used >> t) & 1) ^ 1, status, nullptr, 0);
-            for (int v = 0; v < kStages / 2; ++v)
+            for (int v = 0; v < kStages; ++v)
                 if (g_any >> v & 1) mbar_drain(&v_guard[v], ((g_used >> v) & 1) ^ 1, status, nullptr, 0);
         }
     } else if (warp == kMmaWarp) {
@@ -647,7 +671,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                        kk > 0 ? 1u : 1u - fresh);
         };
         auto s_product = [&](int t, uint32_t y) {
-            const uint32_t a_lo = q_lo + t * (M::kTile >> 4), b_lo = k_lo + (y % kStages) * (M::kTile >> 4);
+            const uint32_t a_lo = q_lo + (kSplit ? 0 : t) * (M::kTile >> 4), b_lo = k_lo + (y % kStages) * (M::kTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 mma_ss(tmu + t * kKeys, a_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2,
@@ -659,7 +683,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         uint32_t x = 0;                   // K and V tiles of the items so far
         uint32_t pv0 = 0, pv1 = 0;        // PV products issued for A, B
         uint32_t q_used = 0, o_used = 0;  // parity bits by query tile: Q tiles taken, outputs written
-        uint32_t v_used = 0;              // by V slot: guarded tiles
+        uint32_t v_used = 0;              // by stage: guarded V tiles
+        auto v_wait = [&](uint32_t y, bool guarded) {
+            if (!guarded) return kv_wait(y);
+            const uint32_t st = y % kStages;
+            const bool there = wait(at(Bars::kKvFull + 2 * kStages + st), (v_used >> st) & 1);
+            v_used ^= 1u << st;
+            return there;
+        };
         bool ok = true;
         int have = -1, next_a = 0, next_b = 0, next_guard = 0;  // the item read last
         auto read = [&](int k) {
@@ -676,8 +707,62 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 if (!wait(at(Bars::kDFull + k % kSlots), (k / kSlots) & 1)) { ok = false; break; }
                 read(k);
             }
-            const int nA = next_a, nB = next_b, nt = max(nA, nB), guard = next_guard;
+            const int nA = next_a, nB = next_b, nt = max(nA, nB), guard = next_guard;  // split: A has no fewer
             if (nt == 0) break;
+            if (kSplit) {
+                // The same steps, where A has the even key tiles and B the odd
+                // ones of one query tile: every K and V is taken by one product.
+                const int tiles = nA + nB;
+                uint32_t y = x;
+                ok = wait(at(Bars::kQFull), q_used & 1);
+                q_used ^= 1;
+                auto s_tile = [&](int t, uint32_t at_y, int tile) {
+                    const uint32_t done = t ? pv1 : pv0;
+                    if (!kv_wait(at_y)) return false;
+                    if (kOwnP<D> && tile >= 2) {
+                        if (!wait(at(kSFree + t), done & 1)) return false;
+                    } else if (done > 0 && !wait(at(kSFree + t), (done - 1) & 1)) {
+                        return false;
+                    }
+                    tmem_fence_after_sync();
+                    s_product(t, at_y);
+                    commit(at(Bars::kSFull + t));
+                    kv_release(at_y);
+                    if (tile + 1 == tiles) commit(at(Bars::kQEmpty));
+                    return true;
+                };
+                if (ok) ok = s_tile(0, y++, 0);
+                if (ok && nB) ok = s_tile(1, y++, 1);
+#pragma unroll 1
+                for (int j = 0; j < nA && ok; ++j) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int n_t = t ? nB : nA, tile = 2 * j + t;
+                        if (j >= n_t) continue;
+                        const uint32_t par = (t ? pv1 : pv0) & 1, yv = y++;
+                        if (kOwnP<D> && j + 1 < n_t && !s_tile(t, y++, tile + 2)) { ok = false; break; }
+                        if (j == 0) {  // the previous item's O has been read
+                            if (!wait(at(Bars::kOFree + t), ((o_used >> t) & 1) ^ 1)) { ok = false; break; }
+                            o_used ^= 1u << t;
+                            if (t == 0 && is_done(at(Bars::kDFull + (k + 1) % kSlots), ((k + 1) / kSlots) & 1)) read(k + 1);
+                        }
+                        if (!v_wait(yv, tile >= guard) || !wait(at(Bars::kPFull + 2 * t), par)) { ok = false; break; }
+                        tmem_fence_after_sync();
+                        pv_part(t, 0, yv, j == 0);
+                        if (!wait(at(Bars::kPFull + 2 * t + 1), par)) { ok = false; break; }
+                        tmem_fence_after_sync();
+                        pv_part(t, 1, yv, 0);
+                        commit(at(Bars::kPvDone + t));
+                        if (t) ++pv1; else ++pv0;
+                        kv_release(yv);
+                        if (j + 1 == n_t) commit(at(Bars::kOFull + t));
+                        if (!kOwnP<D> && j + 1 < n_t && !s_tile(t, y++, tile + 2)) { ok = false; break; }
+                    }
+                }
+                if (!ok) break;
+                x = y;
+                continue;
+            }
             // S_A(0), S_B(0); then step j: O_t += P_t(j) V(j) and S_t(j + 1),
             // for A, then for B. A sees no more key tiles than B, unless B is
             // empty. What can be asked for ahead (the next tiles) is, while
@@ -702,13 +787,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll 1
             for (int j = 0; j < nt; ++j) {
                 const uint32_t yv = x + 2 * j + 1, yk = yv + 1;  // V(j), K(j + 1)
-                if (j < guard) {
-                    ok = kv_wait(yv);
-                } else {
-                    const uint32_t v = yv / 2 % (kStages / 2);
-                    ok = wait(at(Bars::kKvFull + 2 * kStages + v), (v_used >> v) & 1);
-                    v_used ^= 1u << v;
-                }
+                ok = v_wait(yv, j >= guard);
                 if (!ok) break;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -771,7 +850,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             if (!w.valid) break;
             const int n_t = w.n_keys[t];
             if (n_t == 0) continue;
-            const int i0 = w.i0 + t * a.tile_tokens;
+            const int i0 = w.i0 + (kSplit ? 0 : t * a.tile_tokens);
             const int i = i0 + row / g;
             const bool valid = row < a.tile_tokens * g && i < w.n;
             // Rows past the tile's tokens hold other tokens or nothing; what
@@ -799,8 +878,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
-                    if ((j + 1) * kKeys - 1 > first_limit) {
-                        const int lim = limit - j * kKeys, sure = first_limit - j * kKeys;
+                    const int key0 = (kSplit ? 2 * j + t : j) * kKeys;
+                    if (key0 + kKeys - 1 > first_limit) {
+                        const int lim = limit - key0, sure = first_limit - key0;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             if (c * 32 + 31 <= sure) continue;
@@ -875,6 +955,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             if (!ok || !warp_wait(&o_free[t], (n_out & 1) ^ 1, abort)) break;
             ++n_out;
             row_sum[t * kRows + row] = l;
+            if (kSplit) row_ref[t * kRows + row] = m;
             __syncwarp();
             if (lane == 0) mbar_arrive(&l_full[t]);
         }
@@ -896,8 +977,52 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             const uint32_t *bad = bad_keys + (k % kSlots) * kGuardTiles * (kKeys / 32);
             __nv_bfloat162 odd = __floats2bfloat162_rn(0.f, 0.f);  // NaN once an output of a valid row is not finite
             const bool any_bad = __any_sync(0xffffffffu, lane < kGuardTiles * (kKeys / 32) && bad[lane]);
+            if (kSplit) {
+                // One row from two: out = sum_t O_t 2^(m_t - m) / sum_t l_t 2^(m_t - m).
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (!w.n_keys[t]) continue;
+                    const uint32_t par = (used >> t) & 1;
+                    used ^= 1u << t;
+                    ok = warp_wait(&l_full[t], par, abort) && warp_wait(&o_full[t], par, abort);
+                }
+                if (!ok) break;
+                tmem_fence_after_sync();
+                const bool both = w.n_keys[1] > 0;
+                const int i = w.i0 + row / g;
+                const bool valid = row < a.tile_tokens * g && i < w.n;
+                const float m0 = row_ref[row], m1 = both ? row_ref[kRows + row] : m0, m = fmaxf(m0, m1);
+                float f0 = fast_exp2(m0 - m), f1 = both ? fast_exp2(m1 - m) : 0.f;
+                const float inv = 1.f / (row_sum[row] * f0 + (both ? row_sum[kRows + row] * f1 : 0.f));
+                f0 *= inv;
+                f1 *= inv;
+                const int head = w.h * g + row % g;
+                __nv_bfloat16 *dst = a.out + (((long long)w.q0 + i) * a.num_q_heads + head) * D;
 #pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(o_col + c, o);
+                    tmem_wait_ld_regs(o);
+                    if (both) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 16) {
+                            float q[16];
+                            tmem_ld16(o_col + D + c + e, q);
+                            tmem_wait_ld_regs(q);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[e + i] = fmaf(q[i], f1, o[e + i] * f0);
+                        }
+                    }
+                    put_row<D>(a, w, bad, any_bad, valid, i, c, both ? 1.f : f0, o, odd, dst);
+                }
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&o_free[0]);
+                    if (both) mbar_arrive(&o_free[1]);
+                }
+            }
+#pragma unroll 1
+            for (int t = 0; t < 2 && !kSplit; ++t) {
                 if (!w.n_keys[t]) continue;
                 const uint32_t par = (used >> t) & 1;
                 used ^= 1u << t;
@@ -943,12 +1068,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             if (!warp_wait(&d_full[k % kSlots], (k / kSlots) & 1, abort)) break;
             const Item w = items[k % kSlots];
             if (!w.valid) break;
-            const int nt = max(w.n_keys[0], w.n_keys[1]);
+            const int nt = item_tiles<kSplit>(w);
             uint32_t *bad = bad_keys + (k % kSlots) * kGuardTiles * (kKeys / 32);
             if (lane < 2 * kGuardTiles) bad[lane / 2 * (kKeys / 32) + row0 / 32 + lane % 2] = 0;
             __syncwarp();
             for (int j = w.guard; j < nt; ++j) {
-                const uint32_t y = x + 2 * j + 1, v = y / 2 % (kStages / 2);
+                const uint32_t y = x + (kSplit ? min(2 * j + 2, 2 * nt - 1) : 2 * j + 1), v = y % kStages;  // V(j)
                 if (!warp_wait(&v_guard[v], (g_used >> v) & 1, abort)) { ok = false; break; }
                 g_used ^= 1u << v;
                 uint4 *vt = reinterpret_cast<uint4 *>(smem + M::kOffKv + (y % kStages) * M::kTile);
@@ -1012,18 +1137,21 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 // ---------------------------------------------------------------------------
 
 std::mutex g_mu;
-bool g_ready[64];  // by device: kernel attributes set
+int g_sms[64];  // by device: its SMs, once the kernels' attributes are set
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-int prompt_setup() {
+int prompt_setup(int *sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_E_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
-    if (g_ready[dev]) return PKV_OK;
-    if (cudaFuncSetAttribute(prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<64>::kAlloc) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<128>::kAlloc) !=
-            cudaSuccess)
+    *sms = g_sms[dev];
+    if (*sms) return PKV_OK;
+    const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaFuncSetAttribute(prompt_kernel<64, false>, smem, Smem<64>::kAlloc) != cudaSuccess ||
+        cudaFuncSetAttribute(prompt_kernel<64, true>, smem, Smem<64>::kAlloc) != cudaSuccess ||
+        cudaFuncSetAttribute(prompt_kernel<128, false>, smem, Smem<128>::kAlloc) != cudaSuccess ||
+        cudaFuncSetAttribute(prompt_kernel<128, true>, smem, Smem<128>::kAlloc) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return PKV_E_CUDA;
     if (!g_encode) {
         void *fn = nullptr;
@@ -1034,7 +1162,7 @@ int prompt_setup() {
             return PKV_E_CUDA;
         g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    g_ready[dev] = true;
+    g_sms[dev] = *sms;
     return PKV_OK;
 }
 
@@ -1091,7 +1219,8 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
         return PKV_E_ALIGN;
     const long long wq = (long long)num_q_heads * head_size, wkv = (long long)num_kv_heads * head_size;
     if (!stride_ok(q_stride, wq) || !stride_ok(k_stride, wkv) || !stride_ok(v_stride, wkv)) return PKV_E_DIMS;
-    int rc = prompt_setup();
+    int sms = 0;
+    int rc = prompt_setup(&sms);
     if (rc) return rc;
     PromptArgs a{};
     a.q = static_cast<const __nv_bfloat16 *>(q);
@@ -1117,13 +1246,21 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
     if (!rc) rc = encode_kv(&v_map, v, num_tokens, v_stride, num_kv_heads, head_size);
     if (rc) return rc;
     // A block for every item there may be (every sequence rounds up to whole
-    // pairs of tiles); those that start fetch the others' items.
-    const long long grid = (num_tokens / (2LL * a.tile_tokens) + num_reqs) * num_kv_heads;
+    // items); those that start fetch the others' items.
+    auto items = [&](int tokens) { return ((long long)num_tokens / tokens + num_reqs) * num_kv_heads; };
+    // While items of two query tiles leave SMs idle, items of one, its keys split
+    // between A and B: half the steps, and twice the SMs (one prompt of 512
+    // tokens, 72 such items at most: 14.0 -> 11.5 us; 2048 tokens of 12/4 heads,
+    // 100: 30.5 -> 25.4). Beyond, K and V copied twice and twice the items cost
+    // more (4 x 300 tokens, 176: 14.1 -> 17.1 us; the ragged batch of 24: 64.6 -> 86.9).
+    const bool split = items(2 * a.tile_tokens) <= sms;
+    a.item_tokens = split ? a.tile_tokens : 2 * a.tile_tokens;
+    const long long grid = items(a.item_tokens);
     if (grid > INT32_MAX) return PKV_E_DIMS;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t err =
-        head_size == 128
-            ? launch_pdl(prompt_kernel<128>, dim3((unsigned)grid), dim3(kThreads), Smem<128>::kAlloc, st, q_map, k_map, v_map, a)
-            : launch_pdl(prompt_kernel<64>, dim3((unsigned)grid), dim3(kThreads), Smem<64>::kAlloc, st, q_map, k_map, v_map, a);
+    auto kernel = head_size == 128 ? (split ? prompt_kernel<128, true> : prompt_kernel<128, false>)
+                                   : (split ? prompt_kernel<64, true> : prompt_kernel<64, false>);
+    const cudaError_t err = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads),
+                                       head_size == 128 ? Smem<128>::kAlloc : Smem<64>::kAlloc, st, q_map, k_map, v_map, a);
     return err == cudaSuccess ? PKV_OK : PKV_E_CUDA;
 }

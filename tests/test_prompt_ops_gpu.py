@@ -280,6 +280,12 @@ def run_prompt(lens, hq, hkv, d, seed, packed=False, tail=0, scale=None):
     return q, k, v, qsl, scale or d ** -0.5
 
 
+def crowd(qsl, extra=200):
+    """The same sequences with empty ones behind them: enough for the kernel's
+    form for many items, where a few items have their keys split."""
+    return torch.cat([qsl, qsl[-1:].repeat(extra)])
+
+
 def check_prompt(q, k, v, lens, qsl, scale, out=None):
     status = i32([0])
     got = pkv.pkv_prompt_attention(q, k, v, qsl, scale, out=out, status=status)
@@ -293,9 +299,10 @@ def check_prompt(q, k, v, lens, qsl, scale, out=None):
 @pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (8, 8, 128), (4, 1, 64), (16, 2, 64)])
 @pytest.mark.parametrize("lens", [[1], [2], [17, 40], [128], [129], [255, 1, 0, 256], [0, 0, 300], [64, 65, 63],
                                   [511, 513]], ids=lambda x: "-".join(map(str, x)))
-def test_prompt_matches_the_definition(hq, hkv, d, lens):
+@pytest.mark.parametrize("many", [False, True])
+def test_prompt_matches_the_definition(hq, hkv, d, lens, many):
     q, k, v, qsl, scale = run_prompt(lens, hq, hkv, d, 7 + sum(lens))
-    check_prompt(q, k, v, lens, qsl, scale)
+    check_prompt(q, k, v, lens, crowd(qsl) if many else qsl, scale)
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(3, 1, 128), (10, 2, 64), (32, 4, 64), (32, 8, 128), (12, 4, 128), (128, 1, 64),
@@ -304,6 +311,7 @@ def test_prompt_group_sizes(hq, hkv, d):
     lens = [5, 140, 33]
     q, k, v, qsl, scale = run_prompt(lens, hq, hkv, d, hq, packed=True)
     check_prompt(q, k, v, lens, qsl, scale)
+    check_prompt(q, k, v, lens, crowd(qsl), scale)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -324,11 +332,15 @@ def test_prompt_many_sequences():
     check_prompt(q, k, v, lens, qsl, scale)
 
 
-def test_prompt_rising_scores_move_the_reference():
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_rising_scores_move_the_reference(many, d):
     """Scores that grow along the keys by far more than 2^8: the running
     reference moves and O is rescaled, in every tile."""
     lens = [1000, 300]
-    q, k, v, qsl, scale = run_prompt(lens, 4, 2, 128, 13)
+    q, k, v, qsl, scale = run_prompt(lens, 4, 2, d, 13)
+    if many:
+        qsl = crowd(qsl)
     q.copy_(q.abs())
     ramp = torch.linspace(0, 2.0, 1300, device=DEV)[:, None, None]
     k.copy_(k * 0.1 + ramp)
@@ -344,15 +356,17 @@ def test_prompt_rows_behind_the_last_sequence_are_left():
     q, k, v, qsl, scale = run_prompt(lens, 8, 2, 128, 14, tail=50)
     for x in (q, k, v):
         x[133:] = float("nan")
-    out = torch.full_like(q, 7.0)
-    got = check_prompt(q, k, v, lens, qsl, scale, out=out)
-    assert bool((got[133:] == 7).all())
+    for bounds in (qsl, crowd(qsl)):
+        out = torch.full_like(q, 7.0)
+        got = check_prompt(q, k, v, lens, bounds, scale, out=out)
+        assert bool((got[133:] == 7).all())
 
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("which", ["k", "v"])
-def test_prompt_values_that_are_not_finite_reach_only_their_readers(d, bad, which):
+@pytest.mark.parametrize("many", [False, True])
+def test_prompt_values_that_are_not_finite_reach_only_their_readers(d, bad, which, many):
     """A token with such a value is seen by itself and what follows in its
     sequence: earlier rows, and the neighbouring sequences, keep their values."""
     lens = [150, 200, 90]
@@ -360,7 +374,7 @@ def test_prompt_values_that_are_not_finite_reach_only_their_readers(d, bad, whic
     want, mag = po.prompt(q, k, v, lens, scale)
     at = 150 + 70
     (k if which == "k" else v)[at] = bad
-    got = pkv.pkv_prompt_attention(q, k, v, qsl, scale)
+    got = pkv.pkv_prompt_attention(q, k, v, crowd(qsl) if many else qsl, scale)
     sees = torch.zeros(440, dtype=torch.bool, device=DEV)
     sees[at:350] = True
     tol = po.prompt_tolerance(want, mag)
@@ -375,8 +389,9 @@ def test_prompt_values_that_are_not_finite_reach_only_their_readers(d, bad, whic
         assert bool(((g - w).abs()[ok] <= (w.abs() * 2.0 ** -8 + 0.05)[ok]).all())
 
 
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
-def test_prompt_scores_of_minus_infinity(d):
+def test_prompt_scores_of_minus_infinity(d, many):
     """Keys whose score is minus infinity for every row: a row that sees no
     other key is not a number, as in the formula; the others leave them out,
     even where they fill a row's first key tiles."""
@@ -384,7 +399,7 @@ def test_prompt_scores_of_minus_infinity(d):
     q, k, v, qsl, scale = run_prompt(lens, 4, 1, d, 18)
     q.copy_(q.abs() + 0.01)
     k[:dead] = -float("inf")
-    got = pkv.pkv_prompt_attention(q, k, v, qsl, scale)
+    got = pkv.pkv_prompt_attention(q, k, v, crowd(qsl) if many else qsl, scale)
     assert bool(torch.isnan(got[:dead]).all())
     want, mag = po.prompt(q[dead:], k[dead:], v[dead:], [lens[0] - dead], scale)
     assert po.worst(got[dead:], want, po.prompt_tolerance(want, mag)) <= 1.0
@@ -398,11 +413,13 @@ def test_prompt_nothing_finite_anywhere_ends(d):
     for x in (q, k, v):
         x.fill_(float("nan"))
     status = i32([0])
-    got = pkv.pkv_prompt_attention(q, k, v, qsl, scale, status=status)
-    assert bool(torch.isnan(got).all()) and pkv.pkv_read_status(status) == 0
+    for bounds in (qsl, crowd(qsl)):
+        got = pkv.pkv_prompt_attention(q, k, v, bounds, scale, status=status)
+        assert bool(torch.isnan(got).all()) and pkv.pkv_read_status(status) == 0
     q, k, _, qsl, scale = run_prompt(lens, 8, 2, d, 19)
-    got = pkv.pkv_prompt_attention(q, k, v, qsl, scale, status=status)
-    assert bool(torch.isnan(got).all()) and pkv.pkv_read_status(status) == 0
+    for bounds in (qsl, crowd(qsl)):
+        got = pkv.pkv_prompt_attention(q, k, v, bounds, scale, status=status)
+        assert bool(torch.isnan(got).all()) and pkv.pkv_read_status(status) == 0
 
 
 def test_prompt_odd_output_address():
