@@ -354,7 +354,8 @@ int paged_attention_static(const void *q, int32_t num_tokens, int32_t num_q_head
  * Ordering: nothing is read before every earlier kernel on the stream has
  * completed, and kernels launched behind it on the stream start only when it
  * has: the tables may go straight to paged_attention and
- * paged_kv_write_slots.
+ * paged_kv_write_slots. Make the first call on a device with more than 4096
+ * rows before any capture.
  */
 int paged_build_tables(const int32_t *query_lens, const int32_t *context_lens, int32_t num_reqs,
                        const int32_t *free_blocks, int32_t num_free, const int32_t *free_cursor, int32_t num_tokens,
@@ -378,7 +379,8 @@ int paged_build_tables(const int32_t *query_lens, const int32_t *context_lens, i
  *
  * q goes to q_out; k to k_out (if given) and to the pool (if given), v to the
  * pool, by slot_mapping as in paged_kv_write (negative: not written to the
- * pool; at or beyond 16 * num_blocks: not written, PKV_DEV_BAD_SLOT). One of
+ * pool; at or beyond 16 * num_blocks: not written, PKV_DEV_BAD_SLOT). Tokens
+ * of one call that name the same slot leave either one's values there. One of
  * k_out and kv_cache has to be given. A token with a negative position on any
  * axis is padding: nothing of it is written. A position at or beyond
  * num_positions raises PKV_DEV_BAD_POS and is treated the same way.
@@ -427,7 +429,7 @@ int paged_qk_norm_rope(const pkv_rope_desc *desc, const void *q, const void *k, 
  *             raises PKV_DEV_BAD_QSL (so do sequences that overlap to more
  *             rows than there are; then nothing is computed). Rows outside
  *             every sequence are left as they were.
- *  scale      finite and greater than 0
+ *  scale      greater than 0, at most 1e30
  *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the inputs
  *  status     optional device int32, PKV_DEV_* bits OR-ed in
  *

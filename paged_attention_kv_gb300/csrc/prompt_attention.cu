@@ -1218,7 +1218,7 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
     if (num_tokens < 0 || num_reqs < 0 || num_kv_heads <= 0 || num_kv_heads > 4096) return PKV_E_DIMS;
     if (num_tokens > INT32_MAX - 65536 || (long long)num_reqs * num_kv_heads > INT32_MAX - 65536) return PKV_E_DIMS;
     if (num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kRows) return PKV_E_GQA;
-    if (!(scale > 0.f) || scale > 3.0e38f) return PKV_E_DIMS;
+    if (!(scale > 0.f) || scale > 1e30f) return PKV_E_DIMS;
     if (num_tokens == 0 || num_reqs == 0) return PKV_OK;
     if (!q || !k || !v || !query_start_loc || !out) return PKV_E_NULL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(query_start_loc, 4) ||

@@ -291,6 +291,10 @@ extern "C" PKV_API int paged_qk_norm_rope(const pkv_rope_desc *d, const void *q,
     if (num_tokens == 0) return PKV_OK;
     if (!q || !k || !positions || !cos_sin || !q_out || (kv_cache && (!v || !slot_mapping))) return PKV_E_NULL;
     if (!k_out && !kv_cache) return PKV_E_NULL;
+    // in place: a token's rows are where they were
+    if (num_tokens > 1 && ((q_out == q && d->q_out_stride != d->q_stride) ||
+                           (k_out == k && d->k_out_stride != d->k_stride)))
+        return PKV_E_DIMS;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
         !aligned(cos_sin, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(kv_cache, 16) ||
         !aligned(positions, 4) || !aligned(slot_mapping, 4) || !aligned(status, 4))

@@ -67,6 +67,7 @@ def rope(desc=None, **kw):
     ({}, dict(slots=0), pkv.PKV_E_NULL), ({}, dict(ko=0, kv=0), pkv.PKV_E_NULL), ({}, dict(qo=0), pkv.PKV_E_NULL),
     ({}, dict(q=0x1008), pkv.PKV_E_ALIGN), ({}, dict(cs=0x7008), pkv.PKV_E_ALIGN),
     ({}, dict(kw=0x5002), pkv.PKV_E_ALIGN), ({}, dict(pos=0x6002), pkv.PKV_E_ALIGN),
+    (dict(q_stride=6144), dict(qo=0x1000), pkv.PKV_E_DIMS), (dict(k_out_stride=6144), dict(ko=0x2000), pkv.PKV_E_DIMS),
 ])
 def test_qk_norm_rope_host_validation(desc, kw, code):
     assert rope(desc, **kw) == code
@@ -86,7 +87,7 @@ def prompt(**kw):
     (dict(r=-1), pkv.PKV_E_DIMS), (dict(hkv=0), pkv.PKV_E_DIMS), (dict(hkv=5), pkv.PKV_E_GQA),
     (dict(hq=0), pkv.PKV_E_GQA), (dict(hq=129, hkv=1), pkv.PKV_E_GQA), (dict(scale=0.0), pkv.PKV_E_DIMS),
     (dict(scale=-1.0), pkv.PKV_E_DIMS), (dict(scale=float("nan")), pkv.PKV_E_DIMS),
-    (dict(scale=float("inf")), pkv.PKV_E_DIMS), (dict(qs=4092), pkv.PKV_E_DIMS), (dict(ks=1020), pkv.PKV_E_DIMS),
+    (dict(scale=float("inf")), pkv.PKV_E_DIMS), (dict(scale=2e30), pkv.PKV_E_DIMS), (dict(qs=4092), pkv.PKV_E_DIMS), (dict(ks=1020), pkv.PKV_E_DIMS),
     (dict(vs=1016), pkv.PKV_E_DIMS), (dict(t=0), pkv.PKV_OK), (dict(r=0), pkv.PKV_OK), (dict(q=0), pkv.PKV_E_NULL),
     (dict(qsl=0), pkv.PKV_E_NULL), (dict(out=0), pkv.PKV_E_NULL), (dict(k=0x2008), pkv.PKV_E_ALIGN),
     (dict(out=0x5004), pkv.PKV_E_ALIGN), (dict(qsl=0x4002), pkv.PKV_E_ALIGN),
