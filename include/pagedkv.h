@@ -354,8 +354,8 @@ int paged_attention_static(const void *q, int32_t num_tokens, int32_t num_q_head
  * Ordering: nothing is read before every earlier kernel on the stream has
  * completed, and kernels launched behind it on the stream start only when it
  * has: the tables may go straight to paged_attention and
- * paged_kv_write_slots. Make the first call on a device with more than 4096
- * rows before any capture.
+ * paged_kv_write_slots. Make the first call on a device that updates in place
+ * with more than 4096 rows before any capture.
  */
 int paged_build_tables(const int32_t *query_lens, const int32_t *context_lens, int32_t num_reqs,
                        const int32_t *free_blocks, int32_t num_free, const int32_t *free_cursor, int32_t num_tokens,

@@ -6,17 +6,20 @@
 //
 // Request r with L0 tokens of context and n new ones ends at L1 = L0 + n and
 // takes ceil(L1 / 16) - ceil(L0 / 16) new blocks; both prefix sums (tokens,
-// blocks) come from one scan. Every CTA of the cluster scans all requests
-// (a kilobyte or two from L2), which costs less than handing the result on,
-// and then fills its share of the tokens; the new token at a block's first
-// position also writes the block-table entry, so no entry is written twice.
-// The lengths and the cursor may be updated in place: they are written by
-// rank 0 once the whole cluster has read them (a cluster barrier per
-// kThreads requests). Bound by its launch and the round trips to memory one
-// behind another (lengths, free ids, rows): 4.4 us back to back for 256 decode
-// requests, 9.8 us for 700 prompts of 145k tokens together.
+// blocks) come from one scan. Every CTA scans all requests (a kilobyte or two
+// from L2), which costs less than handing the result on, and then fills its
+// share of the tokens; the new token at a block's first position also writes
+// the block-table entry, so no entry is written twice. Where the lengths or the
+// cursor are updated in place, rank 0 writes them once every CTA has read them:
+// the grid is then one cluster, with a cluster barrier per kThreads requests.
+// Otherwise nothing is read that another CTA writes, and the CTAs are as many as
+// the rows want. Bound by its launch and the round trips to memory one behind
+// another (lengths, free ids, rows): 4.3 us back to back for 256 decode
+// requests, 4.6 us for 200 prompts of 103k tokens together, 6.2 us for 700 of
+// 138k (in place 9.7).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 #include <mutex>
@@ -36,11 +39,6 @@ struct TableArgs {
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 
 // Tokens and blocks summed side by side, each clamped to its cap: one more
 // than the step's rows, one more than the ids left. A sum at its cap refuses
@@ -79,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs 
     __shared__ int s_base[kThreads];       // its first new id in free_blocks
     __shared__ uint32_t s_taken;           // ids handed out so far
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = blockIdx.x;  // the grid is one cluster, or no CTA waits for another
     const int T = a.num_tokens;
     if (tid == 0) s_taken = 0;
     // No early trigger: kernels of this library that read the tables ahead
@@ -209,6 +207,15 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs 
     __threadfence();
 }
 
+// Rows a CTA fills at four a thread; CTAs beyond those resident at once take turns.
+constexpr int kRowsPerThread = 4;
+constexpr int kMaxCtas256 = 608, kMaxCtas1024 = 152;
+
+int ctas_for(int rows, int threads, int most) {
+    const int per = threads * kRowsPerThread;
+    return std::min(most, std::max(1, (rows + per - 1) / per));
+}
+
 // The largest cluster this device takes, 16 or the 8 that every one takes.
 std::mutex g_mu;
 int g_cluster[64];
@@ -233,7 +240,7 @@ int large_cluster(int *ctas) {
 }
 
 template <int kThreads>
-cudaError_t launch(const TableArgs &a, int ctas, cudaStream_t st) {
+cudaError_t launch(const TableArgs &a, int ctas, int cluster, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
@@ -242,7 +249,7 @@ cudaError_t launch(const TableArgs &a, int ctas, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -277,20 +284,27 @@ extern "C" PKV_API int paged_build_tables(const int32_t *query_lens, const int32
                       num_tokens,  num_blocks,   block_table, seq_lens,     query_start_loc, positions, slot_mapping,
                       free_cursor_out, status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // One CTA while its scan, not the rows, takes the time (256 threads are
-    // sooner started than 1024: 4.4 against 5.4 us for 256 decode requests);
-    // beyond, as many as a cluster takes (700 prompts, 145k rows: 13.9 us with 8
-    // CTAs, 9.9 with 16).
+    // CTAs of 256 threads start sooner and meet sooner than those of 1024 (256
+    // decode requests: 4.4 against 5.4 us; 2304 rows of 196 requests: 3 CTAs of
+    // 256 4.7 us, one of 1024 6.0), but more requests than threads make the scan
+    // go round again (700 prompts, 138k rows: 10.4 against 6.2 us).
+    const bool small = num_reqs <= 256;
     cudaError_t err;
-    if (num_tokens <= 1024 && num_reqs <= 256) {
-        err = launch<256>(a, 1, st);
-    } else if (num_tokens <= 4096) {
-        err = launch<1024>(a, 1, st);
+    if (seq_lens != context_lens && (!free_cursor || free_cursor_out != free_cursor)) {
+        err = small ? launch<256>(a, ctas_for(num_tokens, 256, kMaxCtas256), 1, st)
+                    : launch<1024>(a, ctas_for(num_tokens, 1024, kMaxCtas1024), 1, st);
+    } else if (small && num_tokens <= 8 * 256 * kRowsPerThread) {
+        const int ctas = ctas_for(num_tokens, 256, 8);  // a cluster that every device takes
+        err = launch<256>(a, ctas, ctas, st);
     } else {
-        int ctas = 0;
-        const int rc = large_cluster(&ctas);
-        if (rc) return rc;
-        err = launch<1024>(a, ctas, st);
+        // One CTA while its scan, not the rows, takes the time; beyond, as
+        // many as a cluster takes (700 prompts: 13.9 us with 8 CTAs, 9.7 with 16).
+        int ctas = 1;
+        if (num_tokens > 1024 * kRowsPerThread) {
+            const int rc = large_cluster(&ctas);
+            if (rc) return rc;
+        }
+        err = launch<1024>(a, ctas, ctas, st);
     }
     return err == cudaSuccess ? PKV_OK : PKV_E_CUDA;
 }

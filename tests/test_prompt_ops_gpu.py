@@ -63,7 +63,8 @@ def check_tables(new, old, free, table, T, nb, cursor=None, expect_status=0):
 
 @pytest.mark.parametrize("reqs,max_new,max_old,pad", [
     (1, 1, 0, 0), (1, 1, 16, 0), (1, 17, 15, 3), (7, 40, 100, 0), (64, 1, 2000, 5), (300, 64, 300, 33),
-    (1023, 3, 40, 0), (1024, 1, 64, 1), (1025, 2, 20, 0), (2500, 9, 100, 11), (3, 9000, 50, 2), (20, 2000, 1, 0)])
+    (1023, 3, 40, 0), (1024, 1, 64, 1), (1025, 2, 20, 0), (2500, 9, 100, 11), (3, 9000, 50, 2), (20, 2000, 1, 0),
+    (256, 9, 70, 4), (257, 9, 70, 4), (200, 1300, 90, 7), (2, 400000, 33, 1), (1100, 700, 5, 3)])
 def test_tables_match_the_definition(reqs, max_new, max_old, pad):
     rng = np.random.default_rng(reqs * 7 + max_new)
     new, old, free, table, nb = make_tables(rng, reqs, max_new, max_old)
@@ -124,7 +125,7 @@ def test_tables_huge_lengths_do_not_wrap():
                  expect_status=pkv.PKV_DEV_BAD_LEN | pkv.PKV_DEV_BAD_QSL)
 
 
-@pytest.mark.parametrize("reqs,max_new", [(40, 5), (1500, 12)])
+@pytest.mark.parametrize("reqs,max_new", [(40, 5), (1500, 12), (200, 40), (30, 500), (100, 200)])
 def test_tables_in_place_over_many_steps(reqs, max_new):
     """Lengths and cursor updated in place, step after step without the host."""
     rng = np.random.default_rng(reqs)
