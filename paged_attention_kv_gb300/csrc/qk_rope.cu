@@ -34,10 +34,30 @@ namespace {
 // flight without much spilling (32768 tokens of 32/8 heads x 128 columns: 147
 // us; two blocks 168, four blocks, at 64 registers, 169).
 constexpr int kBlocksPerSm = 3;
-// Warps wanted before a token's heads stay with one warp: as many as run at
-// once. More warps repeat the token's look-ups for nothing (2240 tokens: 10.3
-// us at 4,864; 19,456 or one step a warp, 1.3 times that; one warp a token, 1.9).
-constexpr int kWarpsWanted = 4864;
+// The warps that run at once, and what a warp's look-ups (position, cosines and
+// sines, first heads on their way) cost, in steps of the heads it takes.
+constexpr int kWarpsAtOnce = kBlocksPerSm * 8 * 152;
+constexpr int kLookUpSteps = 1;
+
+// Warps that share a token's heads: those for which the rounds of warps, each
+// with its look-ups and its steps, come to the least, and the most of these. Few
+// tokens get as many as run at once (512 tokens of 10 steps: 7 warps a token 3.6
+// us, 10 4.4, 1 7.0), many one each, which looks things up once (8192 tokens: 35
+// us, 6 warps 48); between, it goes by how the rounds fill (2240 tokens: 1, 2, 3
+// and 4 warps 13.6, 13.1, 12.4, 14.2 us).
+int parts_for(long long tokens, int steps) {
+    int best = 1;
+    long long least = LLONG_MAX;
+    for (int p = 1; p <= steps && (p == 1 || tokens * p <= 4 * kWarpsAtOnce); ++p) {
+        const long long rounds = (tokens * p + kWarpsAtOnce - 1) / kWarpsAtOnce;
+        const long long cost = rounds * ((steps + p - 1) / p + kLookUpSteps);
+        if (cost <= least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return best;
+}
 
 struct RopeArgs {
     const __nv_bfloat16 *q, *k, *v, *q_weight, *k_weight;
@@ -327,11 +347,8 @@ extern "C" PKV_API int paged_qk_norm_rope(const pkv_rope_desc *d, const void *q,
     a.inv_d = 1.f / (float)d->head_size;
     a.status = status;
     const int lanes = d->head_size <= 64 ? 4 : d->head_size <= 128 ? 8 : 16;
-    const int steps = (d->num_q_heads + 2 * d->num_kv_heads + 32 / lanes - 1) / (32 / lanes);
-    // A token's heads are shared out over more warps while the tokens alone
-    // do not fill the GPU.
-    a.parts = 1;
-    while (a.parts < steps && (long long)num_tokens * a.parts < kWarpsWanted) ++a.parts;
+    const int heads = d->num_q_heads + (kv_cache ? 2 : 1) * d->num_kv_heads, at_once = 32 / lanes;
+    a.parts = parts_for(num_tokens, (heads + at_once - 1) / at_once);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t err = lanes == 4 ? launch<4>(a, d->interleaved != 0, st)
                             : lanes == 8 ? launch<8>(a, d->interleaved != 0, st)

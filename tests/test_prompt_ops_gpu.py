@@ -250,7 +250,7 @@ def test_padding_and_bad_positions_leave_their_rows():
     assert torch.equal(pool[0, 1, :, 4], v[4])
 
 
-@pytest.mark.parametrize("tokens", [700, 9000])
+@pytest.mark.parametrize("tokens", [700, 1300, 2500, 9000])
 def test_norm_rope_large_batches(tokens):
     gen = gen_of(tokens)
     q, k = randn(gen, tokens, 12, 128), randn(gen, tokens, 4, 128)
