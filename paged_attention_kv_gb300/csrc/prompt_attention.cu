@@ -346,8 +346,17 @@ __device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, cons
     }
 }
 
+// To 2^-23 of the value, a step and a half of fp32; the output is rounded to 2^-8.
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Columns [c, c + 32) of an output row: O / l, rounded, in 32-byte stores
-// (16-byte stores, a sector half filled, held the output warps twice as long).
+// (16-byte stores, a sector half filled, held the output warps twice as long)
+// that pass by L1, whose memory the operands are read from too (24 ragged prompts
+// 64.0 -> 60.3 us; through shared memory and TMA 63.8).
 template <int D>
 __device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, const uint32_t *bad, bool any_bad, bool valid,
                                         int i, int c, float inv, float (&o)[32], __nv_bfloat162 &odd,
@@ -370,7 +379,7 @@ __device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, cons
     if (a.wide_out) {
 #pragma unroll
         for (int e = 0; e < 16; e += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + 2 * e), "r"(p[e]),
+            asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + 2 * e), "r"(p[e]),
                          "r"(p[e + 1]), "r"(p[e + 2]), "r"(p[e + 3]), "r"(p[e + 4]), "r"(p[e + 5]), "r"(p[e + 6]),
                          "r"(p[e + 7])
                          : "memory");
@@ -451,7 +460,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             most = max(most, n);
             sum += n;
         }
-        if (sum) {
+        // One atomic a warp: a 64-bit one in shared memory tries again while
+        // others are at it.
+        most = __reduce_max_sync(0xffffffffu, most);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (sum && lane == 0) {
             atomicMax(&s_levels, most);
             atomicAdd(&s_tiles, sum);
         }
@@ -848,6 +862,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const uint32_t p_col = tm + lane_off + col_p<D>(t);
         const float scale_log2 = a.scale * kLog2e;
         const int g = a.group;
+        const int row_token = row / g;
+        const bool row_used = row < a.tile_tokens * g;
         uint32_t n = 0, n_out = 0;  // key tiles and items this query tile has been through
         for (int k = 0;; ++k) {
             if (!warp_wait(&d_full[k % kSlots], (k / kSlots) & 1, abort)) break;
@@ -858,8 +874,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             const int n_t = w.n_keys[t];
             if (n_t == 0) continue;
             const int i0 = w.i0 + (kSplit ? 0 : t * a.tile_tokens);
-            const int i = i0 + row / g;
-            const bool valid = row < a.tile_tokens * g && i < w.n;
+            const int i = i0 + row_token;
+            const bool valid = row_used && i < w.n;
             // Rows past the tile's tokens hold other tokens or nothing; what
             // they compute is dropped.
             const int limit = valid ? i : min(w.n, i0 + a.tile_tokens) - 1;
@@ -974,6 +990,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const int row = (warp & 3) * 32 + lane;
         const uint32_t o_col = tm + ((uint32_t)((warp & 3) * 32) << 16) + kColO;
         const int g = a.group;
+        const int row_token = row / g, row_head = row % g;
+        const bool row_used = row < a.tile_tokens * g;
         uint32_t used = 0;  // parity bits of the outputs so far
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -1036,10 +1054,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 ok = warp_wait(&l_full[t], par, abort) && warp_wait(&o_full[t], par, abort);
                 if (!ok) break;
                 tmem_fence_after_sync();
-                const int i = w.i0 + t * a.tile_tokens + row / g;
-                const bool valid = row < a.tile_tokens * g && i < w.n;
-                const float inv = 1.f / row_sum[t * kRows + row];
-                const int head = w.h * g + row % g;
+                const int i = w.i0 + t * a.tile_tokens + row_token;
+                const bool valid = row_used && i < w.n;
+                const float inv = rcp(row_sum[t * kRows + row]);
+                const int head = w.h * g + row_head;
                 __nv_bfloat16 *dst = a.out + (((long long)w.q0 + i) * a.num_q_heads + head) * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
