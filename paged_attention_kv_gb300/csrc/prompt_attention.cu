@@ -180,10 +180,12 @@ __device__ __forceinline__ bool is_done(uint32_t bar, uint32_t parity) {  // ask
 }
 // By a whole warp, which leaves it with one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
-    const uint32_t t0 = timer_lo();
+    uint32_t t0 = 0;
+#pragma unroll 1
     while (!__all_sync(0xffffffffu, try_wait(bar, parity))) {
-        if (__any_sync(0xffffffffu, timer_lo() - t0 > (uint32_t)kWaitTimeoutNs || *abort)) {
+        const uint32_t now = timer_lo();
+        t0 = t0 ? t0 : now | 1;
+        if (__any_sync(0xffffffffu, now - t0 + 1 > (uint32_t)kWaitTimeoutNs || *abort)) {
             *abort = 1;
             return false;
         }
@@ -323,24 +325,23 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t w) {
     return (odd_value(w) ? 0u : w & 0xffffu) | (odd_value(w >> 16) ? 0u : w & 0xffff0000u);
 }
 
-// The noted keys' values that are not finite, into columns [c, c + 32) of the
-// output row of token i, for the keys it sees: their probability is above 0,
-// whatever it is.
+// The noted keys' values that are not finite, added to the output row of token
+// i, just written by this thread, for the keys it sees: their probability is
+// above 0, whatever it is, and what they are added to is not finite then.
 template <int D>
-__device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, const uint32_t *bad, int i, int c,
-                                        float (&o)[32]) {
+__device__ __forceinline__ void add_bad(const PromptArgs &a, const Item &w, const uint32_t *bad, int i, __nv_bfloat16 *dst) {
 #pragma unroll 1
     for (int b = 0; b < kGuardTiles * (kKeys / 32); ++b) {
         uint32_t bits = bad[b];
         while (bits) {
             const int key = w.guard * kKeys + b * 32 + __ffs(bits) - 1;
             bits &= bits - 1;
-            const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v + ((long long)w.q0 + key) * a.v_stride + w.h * D + c);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t x = __ldg(v + e);
-                if (key <= i && odd_value(x)) o[2 * e] += __uint_as_float(x << 16);
-                if (key <= i && odd_value(x >> 16)) o[2 * e + 1] += __uint_as_float(x & 0xffff0000u);
+            if (key > i) continue;
+            const __nv_bfloat16 *v = a.v + ((long long)w.q0 + key) * a.v_stride + w.h * D;
+#pragma unroll 1
+            for (int e = 0; e < D; ++e) {
+                const float x = __bfloat162float(v[e]);
+                if (!(fabsf(x) < INFINITY)) dst[e] = __float2bfloat16_rn(__bfloat162float(dst[e]) + x);
             }
         }
     }
@@ -357,9 +358,7 @@ __device__ __forceinline__ float rcp(float x) {
 // (16-byte stores, a sector half filled, held the output warps twice as long)
 // that pass by L1, whose memory the operands are read from too (24 ragged prompts
 // 64.0 -> 60.3 us; through shared memory and TMA 63.8).
-template <int D>
-__device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, const uint32_t *bad, bool any_bad, bool valid,
-                                        int i, int c, float inv, float (&o)[32], __nv_bfloat162 &odd,
+__device__ __forceinline__ void put_row(bool wide, bool valid, int c, float inv, float (&o)[32], __nv_bfloat162 &odd,
                                         __nv_bfloat16 *dst) {
     const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
@@ -368,7 +367,6 @@ __device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, cons
         o[e] = v.x;
         o[e + 1] = v.y;
     }
-    if (any_bad) add_bad<D>(a, w, bad, i, c, o);
     if (!valid) return;
     uint32_t p[16];
 #pragma unroll
@@ -376,12 +374,12 @@ __device__ __forceinline__ void put_row(const PromptArgs &a, const Item &w, cons
         p[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
         odd = __hfma2(pair_of(p[e]), __floats2bfloat162_rn(0.f, 0.f), odd);
     }
-    if (a.wide_out) {
+    if (wide) {
 #pragma unroll
         for (int e = 0; e < 16; e += 8)
-            asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + 2 * e), "r"(p[e]),
-                         "r"(p[e + 1]), "r"(p[e + 2]), "r"(p[e + 3]), "r"(p[e + 4]), "r"(p[e + 5]), "r"(p[e + 6]),
-                         "r"(p[e + 7])
+            asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c + 2 * e),
+                         "r"(p[e]), "r"(p[e + 1]), "r"(p[e + 2]), "r"(p[e + 3]), "r"(p[e + 4]), "r"(p[e + 5]),
+                         "r"(p[e + 6]), "r"(p[e + 7])
                          : "memory");
     } else {
 #pragma unroll
@@ -880,11 +878,91 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             // they compute is dropped.
             const int limit = valid ? i : min(w.n, i0 + a.tile_tokens) - 1;
             const int first_limit = __reduce_min_sync(0xffffffffu, limit);
+            const int last_limit = __reduce_max_sync(0xffffffffu, limit);
+            // Masked tiles in pieces, twice over S; not where the softmax is
+            // what bounds all (two query tiles of D = 64: 67.9 against 69.4 us).
+            constexpr bool kPieces = D == 128 || kSplit;
             float m = 0.f, l = 0.f;
             bool ok = true;
+            auto scale_o = [&](float alpha) {
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    float o[16];
+                    tmem_ld16(o_col + c * 16, o);
+                    tmem_wait_ld_regs(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                    tmem_st16(o_col + c * 16, o);
+                }
+            };
             for (int j = 0; j < n_t; ++j, ++n) {
                 if (!warp_wait(&s_full[t], n & 1, abort)) { ok = false; break; }
                 tmem_fence_after_sync();
+                auto hand_on = [&](int part) {
+                    tmem_wait_st();
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * t + part]);
+                };
+                const int key0 = (kSplit ? 2 * j + t : j) * kKeys;
+                const bool masked = key0 + kKeys - 1 > first_limit;
+                if (kPieces && masked) {
+                    // A tile with masked keys: 32 keys at a time, first for the
+                    // maximum, then for p; keys that no row of the warp sees are
+                    // neither read nor computed, and only pieces where the rows
+                    // differ are compared key by key (prompts of 17 and 40 tokens
+                    // 6.9 -> 6.6 us, ragged ones 59.4 -> 58.4).
+                    const int lim = limit - key0, sure = first_limit - key0, seen = last_limit - key0;
+                    float c[32], top = -INFINITY;
+                    auto piece = [&](int at) {
+                        tmem_ld32(s_col + at, c);
+                        tmem_wait_ld_regs(c);
+                        if (at + 31 > sure) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) c[e] = e <= lim - at ? c[e] : -INFINITY;
+                        }
+                    };
+#pragma unroll 1
+                    for (int at = 0; at < kKeys && at <= seen; at += 32) {
+                        piece(at);
+                        top = fmaxf(top, max32(c));
+                    }
+                    top *= scale_log2;
+                    if (kOwnP<D> && n > 0) {
+                        ok = warp_wait(&pv_done[t], (n - 1) & 1, abort);
+                        if (!ok) break;
+                        tmem_fence_after_sync();
+                    }
+                    if (j == 0) {
+                        m = fmaxf(top, -1e30f);
+                    } else if (__any_sync(0xffffffffu, top - m > kRescaleBits)) {
+                        const float alpha = top > m ? fast_exp2(m - top) : 1.f;
+                        m = fmaxf(m, top);
+                        l *= alpha;
+                        scale_o(alpha);
+                    }
+                    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int at = 0; at < kKeys; at += 32) {
+                        uint32_t q[16];
+                        if (at <= seen) {
+                            piece(at);
+                            exps(c, scale_log2, m, part, q);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) q[e] = 0;
+                        }
+                        if (kOwnP<D> && at == kKeys - 32) {
+                            tmem_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s_taken[t]);
+                        }
+                        tmem_st16u(p_col + at / 2, q);
+                        if (at + 32 >= kFirstKeys) hand_on(at + 32 > kFirstKeys);
+                    }
+                    l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                    continue;
+                }
                 float s[4][32];
                 uint32_t p[kFirstKeys / 2];
                 float sum;
@@ -901,8 +979,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, s[c]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
-                    const int key0 = (kSplit ? 2 * j + t : j) * kKeys;
-                    if (key0 + kKeys - 1 > first_limit) {
+                    if (!kPieces && masked) {
                         const int lim = limit - key0, sure = first_limit - key0;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -940,15 +1017,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     if (j == 0) break;
                     l *= alpha;
                     // (P over S: PV(j - 1) was over before S(j) was issued.)
-#pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        float o[16];
-                        tmem_ld16(o_col + c * 16, o);
-                        tmem_wait_ld_regs(o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                        tmem_st16(o_col + c * 16, o);
-                    }
+                    scale_o(alpha);
                     break;
                 }
                 if (!ok) break;
@@ -957,12 +1026,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_taken[t]);
                 }
-                auto hand_on = [&](int part) {
-                    tmem_wait_st();
-                    tmem_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * t + part]);
-                };
                 store_p(p_col, p);
                 hand_on(0);
                 keep(s[3]);  // its exponentials not ahead of the first part's hand-over
@@ -1037,8 +1100,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                             for (int i = 0; i < 16; ++i) o[e + i] = fmaf(q[i], f1, o[e + i] * f0);
                         }
                     }
-                    put_row<D>(a, w, bad, any_bad, valid, i, c, both ? 1.f : f0, o, odd, dst);
+                    put_row(a.wide_out, valid, c, both ? 1.f : f0, o, odd, dst);
                 }
+                if (any_bad && valid) add_bad<D>(a, w, bad, i, dst);
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
@@ -1064,8 +1128,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     float o[32];
                     tmem_ld32(o_col + t * D + c, o);
                     tmem_wait_ld_regs(o);
-                    put_row<D>(a, w, bad, any_bad, valid, i, c, inv, o, odd, dst);
+                    put_row(a.wide_out, valid, c, inv, o, odd, dst);
                 }
+                if (any_bad && valid) add_bad<D>(a, w, bad, i, dst);
                 tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_free[t]);
@@ -1110,7 +1175,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll 1
                 for (int b = 0; b < D / 64; ++b) {
                     const uint4 *half = vt + (b * kKeys + row0) * 8 + lane;
-#pragma unroll
+#pragma unroll 2
                     for (int c = 0; c < kKeys / 2 * 8 / 32; ++c) {
                         const uint4 v = half[c * 32];
                         odd = __hfma2(pair_of(v.x), zero, odd);
