@@ -689,12 +689,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 mma_ts(tmu + kColO + t * D, tmu + col_p<D>(t) + kk * 8, b_lo + kk * (2048 >> 4), kIdPV,
                        kk > 0 ? 1u : 1u - fresh);
         };
-        auto s_product = [&](int t, uint32_t y) {
+        // S of a last tile: the keys used, in thirty-twos as the softmax reads
+        // them (ragged prompts 58.5 -> 57.6 us; with D = 64 a narrower product is
+        // no shorter, and one of P that leaves out keys costs more than it saves).
+        constexpr bool kNarrow = D == 128;
+        auto id_keys = [&](int sixteens) { return kIdS - ((uint32_t)(8 - (sixteens + 1) / 2 * 2) << 18); };
+        auto s_product = [&](int t, uint32_t y, uint32_t ids) {
             const uint32_t a_lo = q_lo + (kSplit ? 0 : t) * (M::kTile >> 4), b_lo = k_lo + (y % kStages) * (M::kTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 mma_ss(tmu + t * kKeys, a_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2,
-                       b_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2, kIdS, kk > 0 ? 1u : 0u);
+                       b_lo + (kk / 4) * (M::kHalf >> 4) + (kk % 4) * 2, ids, kk > 0 ? 1u : 0u);
         };
         // What S_t's columns have to wait for before a new S: with P in them its
         // product, else only the softmax's reading.
@@ -712,6 +717,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         };
         bool ok = true;
         int have = -1, next_a = 0, next_b = 0, next_guard = 0;  // the item read last
+        int next_ka = 0, next_kb = 0;  // keys that its last tiles are used with, in sixteens
         auto read = [&](int k) {
             const Item w = items[k % kSlots];
             __syncwarp();
@@ -719,6 +725,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             next_a = uniform(w.n_keys[0]);  // none: the end
             next_b = uniform(w.n_keys[1]);
             next_guard = uniform(w.guard);
+            const int end_a = min(w.n, w.i0 + a.tile_tokens), end_b = min(w.n, w.i0 + 2 * a.tile_tokens);
+            next_ka = uniform((end_a - (w.n_keys[0] - 1) * kKeys + 15) / 16);
+            next_kb = uniform((end_b - (w.n_keys[1] - 1) * kKeys + 15) / 16);
             have = k;
         };
         for (int k = 0; ok; ++k) {
@@ -726,7 +735,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 if (!wait(at(Bars::kDFull + k % kSlots), (k / kSlots) & 1)) { ok = false; break; }
                 read(k);
             }
-            const int nA = next_a, nB = next_b, nt = max(nA, nB), guard = next_guard;  // split: A has no fewer
+            const int nA = next_a, nB = next_b, nt = max(nA, nB), guard = next_guard, kA = next_ka, kB = next_kb;  // split: A has no fewer
             if (nt == 0) break;
             if (kSplit) {
                 // The same steps, where A has the even key tiles and B the odd
@@ -744,7 +753,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         return false;
                     }
                     tmem_fence_after_sync();
-                    s_product(t, at_y);
+                    s_product(t, at_y, kIdS);
                     commit(at(Bars::kSFull + t));
                     kv_release(at_y);
                     if (tile + 1 == tiles) commit(at(Bars::kQEmpty));
@@ -797,7 +806,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 if (ok && done > 0) ok = wait(at(kSFree + t), (done - 1) & 1);
                 if (!ok) break;
                 tmem_fence_after_sync();
-                s_product(t, x);
+                s_product(t, x, kNarrow && n_t == 1 ? id_keys(t ? kB : kA) : kIdS);
                 commit(at(Bars::kSFull + t));
                 if (n_t == 1) commit(at(Bars::kQEmpty + t));
             }
@@ -817,7 +826,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         if ((t == 0 || j + 1 >= nA) && !kv_wait(yk)) return false;
                         if (!wait(at(kSFree + t), par)) return false;
                         tmem_fence_after_sync();
-                        s_product(t, yk);
+                        s_product(t, yk, kNarrow && j + 2 == n_t ? id_keys(t ? kB : kA) : kIdS);
                         commit(at(Bars::kSFull + t));
                         if (t == 1 || j + 1 >= nB) kv_release(yk);
                         if (j + 2 == n_t) commit(at(Bars::kQEmpty + t));
