@@ -945,8 +945,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     if (j == 0) {
                         m = fmaxf(top, -1e30f);
                     } else if (__any_sync(0xffffffffu, top - m > kRescaleBits)) {
-                        const float alpha = top > m ? fast_exp2(m - top) : 1.f;
-                        m = fmaxf(m, top);
+                        // each row by its own scores: what the others of the warp
+                        // hold (some hold nothing) must not show in its bits
+                        const bool moves = top - m > kRescaleBits;
+                        const float alpha = moves ? fast_exp2(m - top) : 1.f;
+                        if (moves) m = top;
                         l *= alpha;
                         scale_o(alpha);
                     }

@@ -352,6 +352,24 @@ def test_prompt_rising_scores_move_the_reference(many, d):
     assert po.worst(got, want, po.prompt_tolerance(want, mag)) <= 1.0
 
 
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [290, 200])
+def test_prompt_rows_do_not_show_in_each_other(at, many, d):
+    """A token whose scores move its own reference changes no bit of the others'
+    outputs, in tiles with masked keys and without."""
+    q, k, v, qsl, scale = run_prompt([300], 4, 1, d, 17)
+    if many:
+        qsl = crowd(qsl)
+    k[64:] += 0.1 * k[64:].sign()
+    before = pkv.pkv_prompt_attention(q, k, v, qsl, scale).clone()
+    q[at] = 8.0 * k[at - 1]
+    after = pkv.pkv_prompt_attention(q, k, v, qsl, scale)
+    same = [i for i in range(300) if i != at]
+    assert torch.equal(before[same], after[same])
+    assert not torch.equal(before[at], after[at])
+
+
 def test_prompt_rows_behind_the_last_sequence_are_left():
     lens = [33, 100]
     q, k, v, qsl, scale = run_prompt(lens, 8, 2, 128, 14, tail=50)
