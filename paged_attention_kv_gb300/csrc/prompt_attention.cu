@@ -36,9 +36,9 @@
 //
 // Bound, for long prompts, by the turn from a P product to the S that takes over
 // its columns and by softmax parts that come late: the tensor core is at work
-// 68 % of the time. Measured: 4 prompts of 4096 tokens, 32/8 heads of 128: 375 us,
+// 69 % of the time. Measured: 4 prompts of 4096 tokens, 32/8 heads of 128: 375 us,
 // 1.47 PFLOP/s (0.77 of the 1.92 measured for a large bf16 product); one of
-// 16384: 1342 us, 1.64 PFLOP/s; 24 ragged ones of 16 to 2048: 64 us, 0.77
+// 16384: 1342 us, 1.64 PFLOP/s; 24 ragged ones of 16 to 2048: 57 us, 0.86
 // PFLOP/s, where items of three key tiles start and end as long as they run.
 //
 // Every wait is bounded; on a timeout the CTA raises PKV_DEV_TIMEOUT, stops,
@@ -1354,7 +1354,7 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
     // between A and B: half the steps, and twice the SMs (one prompt of 512
     // tokens, 72 such items at most: 14.0 -> 11.5 us; 2048 tokens of 12/4 heads,
     // 100: 30.5 -> 25.4). Beyond, K and V copied twice and twice the items cost
-    // more (4 x 300 tokens, 176: 14.1 -> 17.1 us; the ragged batch of 24: 64.6 -> 86.9).
+    // more (4 x 300 tokens, 176: 14.1 -> 17.1 us; a ragged batch of 24: 64.6 -> 86.9).
     const bool split = items(2 * a.tile_tokens) <= sms;
     a.item_tokens = split ? a.tile_tokens : 2 * a.tile_tokens;
     const long long grid = items(a.item_tokens);
