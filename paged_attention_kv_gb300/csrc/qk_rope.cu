@@ -16,7 +16,7 @@
 // within a lane; a warp stays with one token, so that positions, cosines and
 // sines are read once for all the heads it takes. Two steps of heads are in
 // flight ahead of the one at work; the arithmetic is on packed pairs (the
-// scalar form was bound by instruction issue: 158 against 147 us).
+// scalar form was bound by instruction issue: 158 against 147 us then).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,21 +30,23 @@
 namespace pkv {
 namespace {
 
-// Three blocks of 8 warps an SM: 80 registers hold a warp's two heads in
-// flight without much spilling (32768 tokens of 32/8 heads x 128 columns: 147
-// us; two blocks 168, four blocks, at 64 registers, 169).
-constexpr int kBlocksPerSm = 3;
+// 24 warps an SM: 80 registers hold a warp's two heads in flight without much
+// spilling (32768 tokens of 32/8 heads x 128 columns: 147 us in blocks of 256
+// threads; with 16 warps 168, with 32, at 64 registers, 169). Small blocks, since
+// a block's place is free for the next only when its last warp is done (64
+// threads: 144 us, 2240 tokens 12.4 -> 11.9).
+constexpr int kThreads = 64, kBlocksPerSm = 12;
 // The warps that run at once, and what a warp's look-ups (position, cosines and
 // sines, first heads on their way) cost, in steps of the heads it takes.
-constexpr int kWarpsAtOnce = kBlocksPerSm * 8 * 152;
+constexpr int kWarpsAtOnce = kBlocksPerSm * (kThreads / 32) * 152;
 constexpr int kLookUpSteps = 1;
 
 // Warps that share a token's heads: those for which the rounds of warps, each
 // with its look-ups and its steps, come to the least, and the most of these. Few
-// tokens get as many as run at once (512 tokens of 10 steps: 7 warps a token 3.6
-// us, 10 4.4, 1 7.0), many one each, which looks things up once (8192 tokens: 35
-// us, 6 warps 48); between, it goes by how the rounds fill (2240 tokens: 1, 2, 3
-// and 4 warps 13.6, 13.1, 12.4, 14.2 us).
+// tokens get as many as run at once (512 tokens of 10 steps: 7 warps a token 3.7
+// us, 10 4.5, 1 6.5), many one each, which looks things up once (6000 tokens: 25
+// us, 7 warps 35); between, it goes by how the rounds fill (2240 tokens: 1, 2, 3
+// and 4 warps 13.5, 12.4, 11.9, 13.0 us).
 int parts_for(long long tokens, int steps) {
     int best = 1;
     long long least = LLONG_MAX;
@@ -93,7 +95,7 @@ __device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
 }
 
 template <int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(256, kBlocksPerSm) qk_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int kHeads = 32 / kLanes;  // heads a warp holds at once
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, j = lane % kLanes;
@@ -266,9 +268,10 @@ __global__ void __launch_bounds__(256, kBlocksPerSm) qk_rope_kernel(const __grid
 template <int kLanes>
 cudaError_t launch(const RopeArgs &a, bool interleaved, cudaStream_t st) {
     const long long units = (long long)a.num_tokens * a.parts;
-    const dim3 grid((unsigned)((units + 7) / 8));
-    return interleaved ? launch_pdl(qk_rope_kernel<kLanes, true>, grid, dim3(256), 0, st, a)
-                       : launch_pdl(qk_rope_kernel<kLanes, false>, grid, dim3(256), 0, st, a);
+    const int warps = kThreads / 32;
+    const dim3 grid((unsigned)((units + warps - 1) / warps));
+    return interleaved ? launch_pdl(qk_rope_kernel<kLanes, true>, grid, dim3(kThreads), 0, st, a)
+                       : launch_pdl(qk_rope_kernel<kLanes, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 bool stride_ok(long long stride, long long width, int tokens) {
