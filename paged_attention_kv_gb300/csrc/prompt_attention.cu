@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 #include <cstdint>
 #include <mutex>
@@ -352,6 +353,17 @@ __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The scale of a row whose reference is the score m: the call's, or, where that
+// would take the reference past 2^30, a power of two that does not. scale * s -
+// reference is rounded once and so keeps the reference's own rounding, half a
+// step of it: below 2^5 up to 2^30, and soon more than p has exponents for; with
+// a power of two there is none. Scores of that size that differ at all are 2^5
+// apart with either scale, so that the largest alone counts.
+__device__ __forceinline__ float row_scale(float scale, float m) {
+    const float cap = rcp(fabsf(m) * 0x1p-30f);
+    return fminf(scale, __uint_as_float(__float_as_uint(cap) & 0x7f800000u));
 }
 
 // Columns [c, c + 32) of an output row: O / l, rounded, in 32-byte stores
@@ -867,7 +879,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tm + lane_off + t * kKeys, o_col = tm + lane_off + kColO + t * D;
         const uint32_t p_col = tm + lane_off + col_p<D>(t);
-        const float scale_log2 = a.scale * kLog2e;
         const int g = a.group;
         const int row_token = row / g;
         const bool row_used = row < a.tile_tokens * g;
@@ -891,7 +902,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             // Masked tiles in pieces, twice over S; not where the softmax is
             // what bounds all (two query tiles of D = 64: 67.9 against 69.4 us).
             constexpr bool kPieces = D == 128 || kSplit;
-            float m = 0.f, l = 0.f;
+            // The row's reference, as a score and scaled, its scale, its sum of
+            // p. Products with the scale are rounded by themselves: p, alpha and
+            // the join of split rows have to mean the same reference.
+            float m_score = 0.f, m = 0.f, sc = 0.f, l = 0.f;
+            auto scaled = [&](float score) { return __fmul_rn(score, sc); };
+            auto refer = [&](float score) {
+                m_score = score;
+                sc = row_scale(a.scale * kLog2e, score);
+                m = scaled(score);
+            };
             bool ok = true;
             auto scale_o = [&](float alpha) {
 #pragma unroll 1
@@ -936,20 +956,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         piece(at);
                         top = fmaxf(top, max32(c));
                     }
-                    top *= scale_log2;
                     if (kOwnP<D> && n > 0) {
                         ok = warp_wait(&pv_done[t], (n - 1) & 1, abort);
                         if (!ok) break;
                         tmem_fence_after_sync();
                     }
                     if (j == 0) {
-                        m = fmaxf(top, -1e30f);
-                    } else if (__any_sync(0xffffffffu, top - m > kRescaleBits)) {
+                        refer(fmaxf(top, -FLT_MAX));
+                    } else if (__any_sync(0xffffffffu, scaled(top) - m > kRescaleBits)) {
                         // each row by its own scores: what the others of the warp
                         // hold (some hold nothing) must not show in its bits
-                        const bool moves = top - m > kRescaleBits;
-                        const float alpha = moves ? fast_exp2(m - top) : 1.f;
-                        if (moves) m = top;
+                        const bool moves = scaled(top) - m > kRescaleBits;
+                        const float alpha = moves ? fast_exp2(m - scaled(top)) : 1.f;
+                        if (moves) refer(top);
                         l *= alpha;
                         scale_o(alpha);
                     }
@@ -959,7 +978,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                         uint32_t q[16];
                         if (at <= seen) {
                             piece(at);
-                            exps(c, scale_log2, m, part, q);
+                            exps(c, sc, m, part, q);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) q[e] = 0;
@@ -1003,18 +1022,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                     float alpha = 1.f;
                     const bool any = __any_sync(0xffffffffu, moves);
                     if (any) {
-                        const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3]))) * scale_log2;
+                        const float top = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
                         if (j == 0) {
-                            m = fmaxf(top, -1e30f);  // a number even where every score is minus infinity
-                        } else if (moves && top > m) {
-                            alpha = fast_exp2(m - top);
-                            m = top;
+                            refer(fmaxf(top, -FLT_MAX));  // a number even where every score is minus infinity
+                        } else if (moves && scaled(top) > m) {
+                            alpha = fast_exp2(m - scaled(top));
+                            refer(top);
                         }
                     }
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < kFirstKeys / 32; ++c) exps(s[c], scale_log2, m, part, p + 16 * c);
-                    const float last = fmaf(max32(s[3]), scale_log2, -m);
+                    for (int c = 0; c < kFirstKeys / 32; ++c) exps(s[c], sc, m, part, p + 16 * c);
+                    const float last = fmaf(max32(s[3]), sc, -m);
                     sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
                     if (kOwnP<D> && n > 0) {  // O and P are at rest once the product before is over
                         ok = warp_wait(&pv_done[t], (n - 1) & 1, abort);
@@ -1044,7 +1063,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 {
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     uint32_t q[16];
-                    exps(s[3], scale_log2, m, part, q);
+                    exps(s[3], sc, m, part, q);
                     tmem_st16u(p_col + kFirstKeys / 2, q);
                     hand_on(1);
                     l += sum + ((part[0].x + part[0].y) + (part[1].x + part[1].y));
@@ -1053,7 +1072,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             if (!ok || !warp_wait(&o_free[t], (n_out & 1) ^ 1, abort)) break;
             ++n_out;
             row_sum[t * kRows + row] = l;
-            if (kSplit) row_ref[t * kRows + row] = m;
+            if (kSplit) row_ref[t * kRows + row] = m_score;
             __syncwarp();
             if (lane == 0) mbar_arrive(&l_full[t]);
         }
@@ -1090,7 +1109,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                 const bool both = w.n_keys[1] > 0;
                 const int i = w.i0 + row / g;
                 const bool valid = row < a.tile_tokens * g && i < w.n;
-                const float m0 = row_ref[row], m1 = both ? row_ref[kRows + row] : m0, m = fmaxf(m0, m1);
+                const float ref0 = row_ref[row], ref1 = both ? row_ref[kRows + row] : ref0;
+                const float sc = row_scale(a.scale * kLog2e, fmaxf(fabsf(ref0), fabsf(ref1)));
+                const float m0 = __fmul_rn(ref0, sc), m1 = __fmul_rn(ref1, sc), m = fmaxf(m0, m1);
                 float f0 = fast_exp2(m0 - m), f1 = both ? fast_exp2(m1 - m) : 0.f;
                 const float inv = 1.f / (row_sum[row] * f0 + (both ? row_sum[kRows + row] * f1 : 0.f));
                 f0 *= inv;
