@@ -9,6 +9,7 @@ library has not been built, importing this module fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -144,6 +145,19 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _memory_of(stream, t):
+    """Context in which a call on ``stream`` makes its tensors: memory of that
+    stream. The current stream's may still be in use by work queued there, and
+    would be given to its next tensors before the call is done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream).value or 0
+        device = t.device if isinstance(t, torch.Tensor) and t.is_cuda else None
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
@@ -343,7 +357,10 @@ class PreparedCall:
     """One of the library's calls with its arguments checked and converted
     once. Calling the object enqueues it on the given (or the current) stream
     of the tensors' device and returns ``outputs``; the buffers it was made
-    with are read and written each time, and kept alive."""
+    with are read and written each time, and kept alive. Outputs that were not
+    given are memory of the stream current when it was made, as any tensor of
+    that moment: another stream that the object is called on waits for that one
+    first (``Stream.wait_stream``)."""
 
     def __init__(self, name: str, args: tuple, device, outputs, keep: tuple):
         self.name, self.args, self.device, self.outputs, self._keep = name, args, device, outputs, keep
@@ -436,10 +453,11 @@ def paged_build_tables(query_lens, context_lens, free_blocks, block_table, num_t
     returns ``(seq_lens, query_start_loc, positions, slot_mapping, cursor)``
     of the step. Pass ``seq_lens=context_lens`` and ``cursor_out=cursor`` to
     update them in place."""
-    return prepare_build_tables(query_lens, context_lens, free_blocks, block_table, num_tokens, num_blocks,
-                                cursor=cursor, cursor_out=cursor_out, seq_lens=seq_lens,
-                                query_start_loc=query_start_loc, positions=positions, slot_mapping=slot_mapping,
-                                status=status)(stream)
+    with _memory_of(stream, query_lens):
+        return prepare_build_tables(query_lens, context_lens, free_blocks, block_table, num_tokens, num_blocks,
+                                    cursor=cursor, cursor_out=cursor_out, seq_lens=seq_lens,
+                                    query_start_loc=query_start_loc, positions=positions, slot_mapping=slot_mapping,
+                                    status=status)(stream)
 
 
 def prepare_qk_norm_rope(q, k, positions, cos_sin, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -517,9 +535,11 @@ def paged_qk_norm_rope(q, k, positions, cos_sin, *, q_weight=None, k_weight=None
     or [axes][T] with ``axis_sections``), and with ``kv_cache`` writes k and v
     to its slots. Returns ``(q_out, k_out)``; ``k_out`` is None when only the
     pool was asked for."""
-    return prepare_qk_norm_rope(q, k, positions, cos_sin, q_weight=q_weight, k_weight=k_weight, eps=eps,
-                                interleaved=interleaved, axis_sections=axis_sections, v=v, slot_mapping=slot_mapping,
-                                kv_cache=kv_cache, q_out=q_out, k_out=k_out, status=status)(stream)
+    with _memory_of(stream, q):
+        return prepare_qk_norm_rope(q, k, positions, cos_sin, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                    interleaved=interleaved, axis_sections=axis_sections, v=v,
+                                    slot_mapping=slot_mapping, kv_cache=kv_cache, q_out=q_out, k_out=k_out,
+                                    status=status)(stream)
 
 
 def prepare_prompt_attention(q, k, v, query_start_loc, scale: float, *, out=None, status=None) -> PreparedCall:
@@ -553,7 +573,8 @@ def pkv_prompt_attention(q, k, v, query_start_loc, scale: float, *, out=None, st
     (grouped heads). q, k and v may be slices of one projection's rows. Rows
     outside every sequence are left as they were (in a fresh ``out``:
     undefined)."""
-    return prepare_prompt_attention(q, k, v, query_start_loc, scale, out=out, status=status)(stream)
+    with _memory_of(stream, q):
+        return prepare_prompt_attention(q, k, v, query_start_loc, scale, out=out, status=status)(stream)
 
 
 def _event_handle(ev, stream) -> int:
