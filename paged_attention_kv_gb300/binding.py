@@ -201,7 +201,8 @@ def paged_slot_mapping(block_table, seq_lens, query_start_loc, num_tokens: int, 
     if query_start_loc.shape[0] != num_reqs + 1 or block_table.shape[0] != num_reqs:
         raise ValueError("block_table, seq_lens and query_start_loc disagree on the number of requests")
     if slot_mapping is None:
-        slot_mapping = torch.empty(num_tokens, dtype=torch.int32, device=seq_lens.device)
+        with _memory_of(stream, seq_lens):
+            slot_mapping = torch.empty(num_tokens, dtype=torch.int32, device=seq_lens.device)
     _want(slot_mapping, torch.int32, 1, "slot_mapping")
     if slot_mapping.shape[0] < num_tokens:
         raise ValueError("slot_mapping is shorter than num_tokens")
@@ -237,7 +238,8 @@ def paged_kv_gather_blocks(kv_cache, block_ids, staging=None, status=None, strea
     _want(block_ids, torch.int32, 1, "block_ids")
     n = block_ids.shape[0]
     if staging is None:
-        staging = torch.empty((n, block_bytes(kv_cache)), dtype=torch.uint8, device=kv_cache.device)
+        with _memory_of(stream, kv_cache):
+            staging = torch.empty((n, block_bytes(kv_cache)), dtype=torch.uint8, device=kv_cache.device)
     _want(staging, torch.uint8, 2, "staging")
     if staging.shape[0] < n or staging.shape[1] != block_bytes(kv_cache):
         raise ValueError("staging must be [num_ids][block_bytes] bytes")
@@ -306,12 +308,14 @@ def paged_attention(q, kv_cache, block_table, seq_lens, query_start_loc, scale: 
     if query_start_loc.shape[0] != num_reqs + 1 or block_table.shape[0] != num_reqs:
         raise ValueError("block_table, seq_lens and query_start_loc disagree on the number of requests")
     if out is None:
-        out = torch.empty_like(q)
+        with _memory_of(stream, q):
+            out = torch.empty_like(q)
     _want(out, torch.bfloat16, 3, "out")
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = alloc_workspace(num_reqs, t, hq, kv_cache)
+        with _memory_of(stream, q):
+            workspace = alloc_workspace(num_reqs, t, hq, kv_cache)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     nbytes = workspace.numel() * workspace.element_size()

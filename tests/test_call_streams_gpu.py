@@ -45,7 +45,26 @@ def prompt_call():
     return lambda **kw: pkv.pkv_prompt_attention(q, k, v, qsl, 0.125, **kw)
 
 
-CALLS = {"tables": tables_call, "rope": rope_call, "prompt": prompt_call}
+def slots_call():
+    table = torch.randperm(400, device=DEV).int().view(40, 10)
+    lens, qsl = i32([150] * 40), i32([100 * r for r in range(41)])
+    return lambda **kw: pkv.paged_slot_mapping(table, lens, qsl, 4000, 400, **kw)
+
+
+def gather_call():
+    pool, ids = randn(4, 90, 2, 2, 16, 64), torch.randperm(90, device=DEV)[:70].int()
+    return lambda **kw: pkv.paged_kv_gather_blocks(pool, ids, **kw)
+
+
+def attention_call():
+    pool, q = randn(5, 400, 2, 2, 16, 64), randn(6, 40, 8, 64)
+    table = torch.randperm(400, device=DEV).int().view(40, 10)
+    lens, qsl = i32([150] * 40), i32(list(range(41)))
+    return lambda **kw: pkv.paged_attention(q, pool, table, lens, qsl, 0.125, **kw)
+
+
+CALLS = {"tables": tables_call, "rope": rope_call, "prompt": prompt_call, "slots": slots_call, "gather": gather_call,
+         "attention": attention_call}
 
 
 @pytest.mark.parametrize("form", ["stream", "handle"])
@@ -95,3 +114,20 @@ def test_the_default_stream_by_handle(name):
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g, w)
+
+
+def test_attention_keeps_its_own_workspace_until_it_is_done():
+    """The workspace that paged_attention makes for a call on another stream is
+    not given to the current stream's next tensors while the call is queued."""
+    call = attention_call()
+    want = call().clone()
+    size = pkv.paged_attention_workspace_bytes(40, 40, 8, 400, 2, 64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    got = call(stream=side)
+    mine = [torch.full((size // 8,), 7, dtype=torch.int64, device=DEV) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(bool((x == 7).all()) for x in mine)
