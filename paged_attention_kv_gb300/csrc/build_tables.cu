@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(kThreads) build_tables_kernel(const TableArgs 
     __threadfence();
 }
 
-// Rows a CTA fills at four a thread; CTAs beyond those resident at once take turns.
+// Rows a CTA fills at four a thread; as many CTAs as are at work at once, 1024
+// threads an SM, take the rows in turn.
 constexpr int kRowsPerThread = 4;
-constexpr int kMaxCtas256 = 608, kMaxCtas1024 = 152;
 
 int ctas_for(int rows, int threads, int most) {
     const int per = threads * kRowsPerThread;
@@ -291,8 +291,11 @@ extern "C" PKV_API int paged_build_tables(const int32_t *query_lens, const int32
     const bool small = num_reqs <= 256;
     cudaError_t err;
     if (seq_lens != context_lens && (!free_cursor || free_cursor_out != free_cursor)) {
-        err = small ? launch<256>(a, ctas_for(num_tokens, 256, kMaxCtas256), 1, st)
-                    : launch<1024>(a, ctas_for(num_tokens, 1024, kMaxCtas1024), 1, st);
+        int sms = 0;
+        const int rc = device_sms(&sms);
+        if (rc) return rc;
+        err = small ? launch<256>(a, ctas_for(num_tokens, 256, 4 * sms), 1, st)
+                    : launch<1024>(a, ctas_for(num_tokens, 1024, sms), 1, st);
     } else if (small && num_tokens <= 8 * 256 * kRowsPerThread) {
         const int ctas = ctas_for(num_tokens, 256, 8);  // a cluster that every device takes
         err = launch<256>(a, ctas, ctas, st);

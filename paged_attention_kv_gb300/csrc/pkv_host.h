@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <utility>
@@ -27,6 +28,20 @@ inline int check_cache_desc(const pkv_cache_desc &d, bool attention) {
     }
     if (d.num_blocks > INT32_MAX / PKV_BLOCK_SIZE) return PKV_E_DIMS;
     if (d.num_kv_heads > 4096 || d.head_size > 4096) return PKV_E_DIMS;
+    return PKV_OK;
+}
+
+// SMs of the current device, asked once.
+inline int device_sms(int *sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_E_CUDA;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PKV_E_CUDA;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
     return PKV_OK;
 }
 

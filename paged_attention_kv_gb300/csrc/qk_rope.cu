@@ -26,6 +26,7 @@
 #include "pagedkv.h"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
+#include "rope_plan.h"
 
 namespace pkv {
 namespace {
@@ -36,30 +37,6 @@ namespace {
 // a block's place is free for the next only when its last warp is done (64
 // threads: 144 us, 2240 tokens 12.4 -> 11.9).
 constexpr int kThreads = 64, kBlocksPerSm = 12;
-// The warps that run at once, and what a warp's look-ups (position, cosines and
-// sines, first heads on their way) cost, in steps of the heads it takes.
-constexpr int kWarpsAtOnce = kBlocksPerSm * (kThreads / 32) * 152;
-constexpr int kLookUpSteps = 1;
-
-// Warps that share a token's heads: those for which the rounds of warps, each
-// with its look-ups and its steps, come to the least, and the most of these. Few
-// tokens get as many as run at once (512 tokens of 10 steps: 7 warps a token 3.7
-// us, 10 4.5, 1 6.5), many one each, which looks things up once (6000 tokens: 25
-// us, 7 warps 35); between, it goes by how the rounds fill (2240 tokens: 1, 2, 3
-// and 4 warps 13.5, 12.4, 11.9, 13.0 us).
-int parts_for(long long tokens, int steps) {
-    int best = 1;
-    long long least = LLONG_MAX;
-    for (int p = 1; p <= steps && (p == 1 || tokens * p <= 4 * kWarpsAtOnce); ++p) {
-        const long long rounds = (tokens * p + kWarpsAtOnce - 1) / kWarpsAtOnce;
-        const long long cost = rounds * ((steps + p - 1) / p + kLookUpSteps);
-        if (cost <= least) {
-            least = cost;
-            best = p;
-        }
-    }
-    return best;
-}
 
 struct RopeArgs {
     const __nv_bfloat16 *q, *k, *v, *q_weight, *k_weight;
@@ -351,7 +328,10 @@ extern "C" PKV_API int paged_qk_norm_rope(const pkv_rope_desc *d, const void *q,
     a.status = status;
     const int lanes = d->head_size <= 64 ? 4 : d->head_size <= 128 ? 8 : 16;
     const int heads = d->num_q_heads + (kv_cache ? 2 : 1) * d->num_kv_heads, at_once = 32 / lanes;
-    a.parts = parts_for(num_tokens, (heads + at_once - 1) / at_once);
+    int sms = 0;
+    const int rc = device_sms(&sms);
+    if (rc) return rc;
+    a.parts = rope_parts(num_tokens, (heads + at_once - 1) / at_once, (long long)sms * kBlocksPerSm * (kThreads / 32));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t err = lanes == 4 ? launch<4>(a, d->interleaved != 0, st)
                             : lanes == 8 ? launch<8>(a, d->interleaved != 0, st)
