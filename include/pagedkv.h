@@ -326,7 +326,8 @@ int paged_attention_static(const void *q, int32_t num_tokens, int32_t num_q_head
  *  query_lens       int32 [num_reqs]; 0 is allowed
  *  context_lens     int32 [num_reqs]
  *  free_blocks      int32 [num_free], ids nobody holds (may be NULL if num_free is 0)
- *  free_cursor      int32, the first unused entry of free_blocks; NULL: 0
+ *  free_cursor      int32, the first unused entry of free_blocks; NULL: 0 (so
+ *                   a later step would hand the same ids out again)
  *  block_table      int32 [num_reqs][max_blocks_per_req], extended in place;
  *                   the entry of a partly filled last block is read
  *  seq_lens         int32 [num_reqs] (output; may be context_lens: updated in place)
@@ -415,7 +416,8 @@ int paged_qk_norm_rope(const pkv_rope_desc *desc, const void *q, const void *k, 
 /*
  * Causal attention of whole prompts (a prompt's first step, or a model used
  * without a pool): sequences packed behind one another, each token attending
- * to its own sequence up to itself. For token i of sequence r, row t =
+ * to its own sequence up to itself and to nothing in the pool, so that a
+ * request with a context before the step needs paged_attention. For token i of sequence r, row t =
  * query_start_loc[r] + i, and query head hq, kv head h = hq / (num_q_heads /
  * num_kv_heads):
  *

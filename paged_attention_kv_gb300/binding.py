@@ -456,7 +456,8 @@ def paged_build_tables(query_lens, context_lens, free_blocks, block_table, num_t
     ``cursor`` on, in request order), extends ``block_table`` in place and
     returns ``(seq_lens, query_start_loc, positions, slot_mapping, cursor)``
     of the step. Pass ``seq_lens=context_lens`` and ``cursor_out=cursor`` to
-    update them in place."""
+    update them in place; without a ``cursor`` a call hands out ``free_blocks``
+    from its first entry on, whatever an earlier one took."""
     with _memory_of(stream, query_lens):
         return prepare_build_tables(query_lens, context_lens, free_blocks, block_table, num_tokens, num_blocks,
                                     cursor=cursor, cursor_out=cursor_out, seq_lens=seq_lens,
@@ -574,8 +575,9 @@ def pkv_prompt_attention(q, k, v, query_start_loc, scale: float, *, out=None, st
                          stream=None) -> torch.Tensor:
     """Causal attention of packed prompts: row ``query_start_loc[r] + i`` of q
     sees rows ``query_start_loc[r] .. query_start_loc[r] + i`` of k and v
-    (grouped heads). q, k and v may be slices of one projection's rows. Rows
-    outside every sequence are left as they were (in a fresh ``out``:
+    (grouped heads), and nothing of the pool: it is for prompts without a
+    context before the step (others: ``paged_attention``). q, k and v may be
+    slices of one projection's rows. Rows outside every sequence are left as they were (in a fresh ``out``:
     undefined)."""
     with _memory_of(stream, q):
         return prepare_prompt_attention(q, k, v, query_start_loc, scale, out=out, status=status)(stream)
