@@ -509,11 +509,11 @@ int pkv_pipeline_sync(pkv_pipeline *pipeline);
 int pkv_pipeline_destroy(pkv_pipeline *pipeline);
 
 /*
- * Failure-detection self-test: runs one thread that waits, with the bounded
- * wait every pipeline stage of the attention kernels uses, on an mbarrier
- * that nothing arrives on. After timeout_us (1 .. 1000000) the wait gives
- * up, PKV_DEV_TIMEOUT is ORed into *status (device, 4-byte aligned, not
- * cleared by the call) and the kernel returns; the CUDA context stays
+ * Failure-detection self-test: waits, with each of the bounded waits that the
+ * pipeline stages of the attention kernels use, on mbarriers that nothing
+ * arrives on. After timeout_us (1 .. 1000000) the waits give up,
+ * PKV_DEV_TIMEOUT is ORed into *status (device, 4-byte aligned, not cleared by
+ * the call) once all have, and the kernel returns; the CUDA context stays
  * usable. A stuck stage in a real launch is reported the same way, after
  * 2 s. Returns PKV_E_* for bad arguments or a launch error.
  */

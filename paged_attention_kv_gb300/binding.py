@@ -593,8 +593,8 @@ def _event_handle(ev, stream) -> int:
 
 
 def pkv_selftest_bounded_wait(status: torch.Tensor, timeout_us: int = 2000, stream=None) -> None:
-    """Run the bounded-wait self-test: a wait on an mbarrier nothing arrives
-    on gives up after ``timeout_us`` and ORs PKV_DEV_TIMEOUT into ``status``."""
+    """Run the bounded-wait self-test: waits on mbarriers that nothing arrives
+    on give up after ``timeout_us`` and OR PKV_DEV_TIMEOUT into ``status``."""
     _want(status, torch.int32, 1, "status")
     _check(LIB.pkv_selftest_bounded_wait(_ptr(status), int(timeout_us), _stream(stream)), "pkv_selftest_bounded_wait")
 

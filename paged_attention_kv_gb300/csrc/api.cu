@@ -7,24 +7,46 @@
 #include "pagedkv.h"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
+#include "pkv_short_wait.cuh"
 
 using namespace pkv;
 
 namespace {
 
-// One thread waits on an mbarrier that nothing arrives on, with the same
-// bounded wait every pipeline stage uses, so the give-up path (status bit,
-// abort flag, kernel returns) runs without a stuck pipeline.
+// Three warps wait on mbarriers that nothing arrives on, each with one of the
+// bounded waits that pipeline stages use, so that the ways to give up (abort
+// flag, status bit, kernel returns) run without a stuck pipeline: one thread as
+// the attention kernels, a warp and one thread as the prompt kernel. The status
+// word shows PKV_DEV_TIMEOUT if all three gave up.
 __global__ void selftest_wait_kernel(int32_t *status, unsigned long long timeout_ns) {
-    __shared__ uint64_t bar;
-    __shared__ int abort_flag;
-    if (threadIdx.x != 0) return;
-    abort_flag = 0;
-    mbar_init(&bar, 1);
-    mbar_fence_init();
-    volatile int *abort = &abort_flag;
-    if (mbar_wait(&bar, 0, status, abort, timeout_ns)) raise_status(status, PKV_DEV_OVERFLOW);  // cannot complete
-    mbar_arrive(&bar);  // complete the phase before the CTA exits
+    __shared__ uint64_t bar[3];
+    __shared__ int abort_flag[3];
+    __shared__ int32_t first;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        first = 0;
+        for (int i = 0; i < 3; ++i) {
+            abort_flag[i] = 0;
+            mbar_init(bar + i, 1);
+        }
+        mbar_fence_init();
+    }
+    __syncthreads();
+    volatile int *abort = abort_flag + warp;
+    bool done = false;
+    if (warp == 0) {
+        if (lane == 0) done = mbar_wait(bar, 0, &first, abort, timeout_ns);
+    } else if (warp == 1) {
+        done = warp_wait(smem_u32(bar + 1), 0, abort, (uint32_t)timeout_ns);
+    } else if (lane == 0) {
+        done = lane_wait(bar + 2, 0, abort, (uint32_t)timeout_ns);
+    }
+    const bool any_done = __syncthreads_or(done);
+    if (lane == 0) mbar_arrive(bar + warp);  // complete the phase before the CTA exits
+    if (threadIdx.x == 0) {
+        if (any_done) raise_status(status, PKV_DEV_OVERFLOW);  // cannot complete
+        if (abort_flag[0] && abort_flag[1] && abort_flag[2]) raise_status(status, first);
+    }
 }
 
 }  // namespace
@@ -33,7 +55,7 @@ extern "C" PKV_API int pkv_selftest_bounded_wait(int32_t *status, uint32_t timeo
     if (!status) return PKV_E_NULL;
     if (!aligned(status, 4)) return PKV_E_ALIGN;
     if (timeout_us == 0 || timeout_us > 1000000) return PKV_E_DIMS;
-    selftest_wait_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(status, 1000ull * timeout_us);
+    selftest_wait_kernel<<<1, 96, 0, static_cast<cudaStream_t>(stream)>>>(status, 1000ull * timeout_us);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_E_CUDA;
 }
 
