@@ -432,7 +432,8 @@ int paged_qk_norm_rope(const pkv_rope_desc *desc, const void *q, const void *k, 
  *             rows than there are; then nothing is computed). Rows outside
  *             every sequence are left as they were.
  *  scale      greater than 0, at most 1e30
- *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the inputs
+ *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the
+ *             inputs (out at q, k or v: PKV_E_DIMS)
  *  status     optional device int32, PKV_DEV_* bits OR-ed in
  *
  * A value that is not finite reaches the rows that may see its token and no

@@ -562,6 +562,8 @@ def prepare_prompt_attention(q, k, v, query_start_loc, scale: float, *, out=None
     _want(out, torch.bfloat16, 3, "out")
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
+    if t and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+        raise ValueError("out must not be q, k or v")
     if status is not None:
         _want(status, torch.int32, 1, "status")
     _same_device(q.device, k=k, v=v, query_start_loc=query_start_loc, out=out, status=status)

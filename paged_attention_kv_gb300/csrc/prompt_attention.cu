@@ -1284,6 +1284,8 @@ extern "C" PKV_API int pkv_prompt_attention(const void *q, int64_t q_stride, con
         return PKV_E_ALIGN;
     const long long wq = (long long)num_q_heads * head_size, wkv = (long long)num_kv_heads * head_size;
     if (!stride_ok(q_stride, wq) || !stride_ok(k_stride, wkv) || !stride_ok(v_stride, wkv)) return PKV_E_DIMS;
+    // a row that is done again reads its inputs again
+    if (out == q || out == k || out == v) return PKV_E_DIMS;
     int sms = 0;
     int rc = prompt_setup(&sms);
     if (rc) return rc;
