@@ -436,7 +436,10 @@ int paged_qk_norm_rope(const pkv_rope_desc *desc, const void *q, const void *k, 
  *             inputs (out at q, k or v: PKV_E_DIMS)
  *  status     optional device int32, PKV_DEV_* bits OR-ed in
  *
- * A value that is not finite reaches the rows that may see its token and no
+ * Scores, their maxima and sums and the output's sums are held in 32 bits; the
+ * probabilities are rounded to bf16 (2^-8 of each) for the product with v, and
+ * the output once more. Finite scores of any size give finite rows; a value
+ * that is not finite reaches the rows that may see its token and no
  * other. Needs no workspace; calls may overlap. As with
  * paged_attention, make the first call on a device before any capture.
  */

@@ -16,7 +16,7 @@
 // the rows want. Bound by its launch and the round trips to memory one behind
 // another (lengths, free ids, rows): 4.3 us back to back for 256 decode
 // requests, 4.6 us for 200 prompts of 103k tokens together, 6.2 us for 700 of
-// 138k (in place 9.7).
+// 138k (in place, where 16 SMs write all rows, 9.7 to 11.5).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -21,14 +21,20 @@
 //   O_t += P_t V      tcgen05.mma, A = P_t from TMEM, B = V as it lies.
 // The softmax of A runs while the tensor core works for B and the other way
 // round. (Where there are few items, an item is one query tile, and A and B are
-// its even and odd key tiles, joined at the end.) The sums l are of the unrounded p; rounding P to bf16 (at most 2^-8 of
-// each term, half a step) is what the tensor core takes.
+// its even and odd key tiles, joined at the end.) The sums l are of the unrounded
+// p; P is rounded to bf16 (at most 2^-8 of each term, half a step), since a
+// product's operands have one type and V is bf16. It shows: rms error 0.0019 to
+// 0.0020 of the output against 64 bits, where the output's own rounding makes
+// 0.0016. The rounding of the reference is one step of m for a whole row and
+// falls out; see row_scale() for scores so large that it would not.
 //
 // Warps: 0 MMA issue and TMEM, 1 copies and the item list, 2-3 guard of V, 4-7
 // softmax of A, 8-11 of B, 12-15 output. The host does not know the lengths, and
 // no workspace is needed: items are numbered by tile level (longest keys first)
 // over all sequences, every CTA counts the tiles once, and its copy warp finds
-// an item by a binary search over levels. The launch
+// an item by a binary search over levels. Each probe reads every sequence, which
+// is nothing at 24 and what sets the time at thousands (prompts of 200 tokens: 4.8
+// us an item and SM with 150 of them, 5.6 with 700, 17 with 4000). The launch
 // has a block for every item there may be; the blocks that start (one an SM)
 // fetch the items of the others from the hardware one by one, so that an SM
 // takes its next item when it is ready for it. (Items dealt out in turn left
@@ -36,10 +42,13 @@
 //
 // Bound, for long prompts, by the turn from a P product to the S that takes over
 // its columns and by softmax parts that come late: the tensor core is at work
-// 69 % of the time. Measured: 4 prompts of 4096 tokens, 32/8 heads of 128: 375 us,
-// 1.47 PFLOP/s (0.77 of the 1.92 measured for a large bf16 product); one of
-// 16384: 1342 us, 1.64 PFLOP/s; 24 ragged ones of 16 to 2048: 57 us, 0.86
-// PFLOP/s, where items of three key tiles start and end as long as they run.
+// 69 % of the time. Measured, over several boxes: 4 prompts of 4096 tokens, 32/8
+// heads of 128: 373 to 383 us, 1.44 to 1.47 PFLOP/s (0.75 to 0.77 of the 1.92
+// measured for a large bf16 product); one of 16384: 1342 to 1372 us, 1.60 to 1.64
+// PFLOP/s; 24 ragged ones of 16 to 2048: 57 to 60 us, 0.82 to 0.86 PFLOP/s, where
+// items of three key tiles start and end as long as they run. With heads of 64
+// (6 prompts of 700 to 4096: 68 to 69 us) neither the tensor core (34 %) nor the
+// exponentials (34 %) fill the time: two softmax warps a scheduler wait for TMEM.
 //
 // Every wait is bounded; on a timeout the CTA raises PKV_DEV_TIMEOUT, stops,
 // lets its copies and MMAs in flight finish and frees its TMEM.
@@ -180,9 +189,12 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 // A value that all lanes hold, as the compiler can know it too.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
 
-// Shared-memory matrix descriptors (128-byte swizzle) as their two words: the
-// low one holds the address and the leading offset, the high one is the same
-// for every operand here (8-row groups 1024 bytes apart).
+// pkv_device.cuh's umma_..._warp forms with the shared-memory matrix descriptors
+// (128-byte swizzle) as their two words, and its commit by address: what changes
+// from MMA to MMA is one 32-bit sum, which stays in a uniform register, where
+// 64-bit descriptors and generic pointers did not. The low word holds the address
+// and the leading offset, the high one is the same for every operand here (8-row
+// groups 1024 bytes apart).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
     return ((addr & 0x3FFFF) >> 4) | ((lbo >> 4) << 16);
