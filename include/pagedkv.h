@@ -24,7 +24,12 @@
  *   paged_qk_norm_rope  - norms of the q and k heads, their rotation by the
  *                         tokens' positions and the KV write, in one pass;
  *   pkv_prompt_attention - causal attention of whole prompts from their
- *                         contiguous q, k and v, without the pool.
+ *                         contiguous q, k and v, without the pool;
+ *   paged_kv4_write, paged_kv4_read, paged_kv4_attention - a pool held in 4
+ *                         bits: writing it, reading it back, and attention over it;
+ *   paged_fork_tables, paged_copy_blocks - requests that go on from others
+ *                         (parallel samples, beams) and the pages they share,
+ *                         copy and give back.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -86,6 +91,8 @@ extern "C" {
 #define PKV_DEV_OVERFLOW 0x20    /* internal work list overflow (never expected) */
 #define PKV_DEV_BAD_POS 0x40     /* a position at or beyond the rotation table's num_positions */
 #define PKV_DEV_NO_BLOCKS 0x80   /* a request needs more blocks than free_blocks has left */
+#define PKV_DEV_BAD_PAGES 0x100  /* a row's parent is none of the rows, a block was given up more often than held, or the
+                                    free list's cursor does not fit it */
 
 typedef struct {
     int32_t num_blocks;    /* blocks in the pool */
@@ -447,6 +454,161 @@ int pkv_prompt_attention(const void *q, int64_t q_stride, const void *k, int64_t
                          int64_t v_stride, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
                          int32_t head_size, const int32_t *query_start_loc, int32_t num_reqs, float scale, void *out,
                          int32_t *status, void *stream);
+
+/*
+ * The 4-bit pool
+ * --------------
+ * One uint8 tensor per layer, [num_blocks][num_kv_heads][18 * head_size], for
+ * head sizes 64 and 128: 0.28 of the bf16 pool's bytes. A value of K is
+ *     k_scale * e2m1 code * e4m3 scale of its 16 columns
+ * (V with v_scale); k_scale and v_scale are powers of two from 2^-60 to 2^60
+ * that the caller keeps (1 unless a layer's values fill e4m3's range, 2^-9 to
+ * 448, badly). A group whose largest magnitude is A, after division by k_scale,
+ * gets the scale A / 6 rounded to e4m3, at least 2^-9; a value the code nearest
+ * to value / scale (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign); both round ties to
+ * even. Magnitudes past 2688, infinities too, become 2688; a group with a NaN
+ * becomes NaN. The values that result are exact in bf16 and in fp16.
+ *
+ * Bytes of a (block, kv head), D = head_size; a byte of codes holds an even
+ * column in its low four bits and the next column above:
+ *     0      K codes   [16 tokens][D / 2]
+ *     8 D    V codes   [2][8][4][2][D / 16]: token 8 a + 2 c + d, bytes of the
+ *                      b-th eighth of the columns, for index [a][b][c][d]
+ *     16 D   K scales  [8][4][2][D / 64]: token 8 c + a, group D / 64 * b + d,
+ *                      for index [a][b][c][d]
+ *     17 D   V scales  [D / 16][4][2][2]: group a, token 8 c + 2 b + d
+ * Blocks move as a whole (paged_copy_blocks).
+ */
+
+/* Bytes of the 4-bit pool of one layer. Host only. */
+int paged_kv4_cache_bytes(const pkv_cache_desc *desc, size_t *bytes);
+
+/*
+ * Writes K and V of new tokens to their slots of the 4-bit pool, as
+ * paged_kv_write does to the bf16 pool: a negative slot is skipped, one at or
+ * beyond 16 * num_blocks is skipped and raises PKV_DEV_BAD_SLOT, slots must be
+ * distinct within one call.
+ *
+ *  k, v       bf16; strides are elements from token to token (a multiple of 8,
+ *             at least num_kv_heads * head_size), heads of a token next to each other
+ *  status     optional device int32, PKV_DEV_* bits OR-ed in
+ */
+int paged_kv4_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int32_t *slot_mapping,
+                    int32_t num_tokens, void *kv4_cache, const pkv_cache_desc *desc, float k_scale, float v_scale,
+                    int32_t *status, void *stream);
+
+/*
+ * The values that the pool holds at the given slots, as bf16 (exactly):
+ * k_out and v_out bf16 [num_tokens][num_kv_heads][head_size], one of them may be
+ * NULL. Rows of negative slots are left as they were; those of slots at or beyond
+ * 16 * num_blocks too, and raise PKV_DEV_BAD_SLOT. The same slot may be named
+ * several times.
+ */
+int paged_kv4_read(const void *kv4_cache, const pkv_cache_desc *desc, const int32_t *slot_mapping, int32_t num_tokens,
+                   float k_scale, float v_scale, void *k_out, void *v_out, int32_t *status, void *stream);
+
+/* Workspace bytes of paged_kv4_attention, for any batch, on the current device. */
+int paged_kv4_attention_workspace_bytes(const pkv_cache_desc *desc, size_t *bytes);
+
+/*
+ * paged_attention over the 4-bit pool: causal attention with grouped heads of a
+ * ragged batch, K and V read through the block tables. Decode tokens and chunks
+ * mix freely.
+ *
+ *  q          bf16; q_stride elements from token to token (a multiple of 8, at
+ *             least num_q_heads * head_size), heads of a token next to each other;
+ *             at most 128 q heads per kv head
+ *  max_query_len  a bound on the new tokens of any request, or 0. It chooses
+ *             between forms for up to 8, up to 16 and more rows (tokens times q
+ *             heads per kv head); a bound that is too small costs time and nothing else
+ *  scale      greater than 0, at most 1e30
+ *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the
+ *             inputs. Rows outside every request, and rows of requests with bad
+ *             metadata, are left as they were.
+ *  workspace  device scratch, 16-byte aligned, of any contents; calls that may
+ *             run at the same time need one each
+ *  status     optional device int32, PKV_DEV_* bits OR-ed in: a request whose
+ *             bounds descend or leave [0, num_tokens] (PKV_DEV_BAD_QSL) or whose
+ *             length is below its new tokens or past its table (PKV_DEV_BAD_LEN)
+ *             is skipped; a block id outside the pool (PKV_DEV_BAD_BLOCK) gives
+ *             that request's rows unspecified values, and no other's
+ *
+ * Scores, sums and the output's sums are held in 32 bits; the probabilities are
+ * rounded to fp16 (2^-11 of each, or 2^-25 of the largest where that is more) for
+ * the product with V, and the output once more. Scores have to be finite in 32 bits. A value that is not finite reaches
+ * the rows that may see its token and no other; tokens past a request's length
+ * may hold anything. The result does not depend on timing. Nothing is read
+ * before every earlier kernel on the stream has completed. Make the first call
+ * of each head size on a device before any capture.
+ */
+int paged_kv4_attention(const void *q, int64_t q_stride, int32_t num_tokens, int32_t num_q_heads,
+                        const void *kv4_cache, const pkv_cache_desc *desc, const int32_t *block_table,
+                        int32_t num_reqs, int32_t max_blocks_per_req, const int32_t *seq_lens,
+                        const int32_t *query_start_loc, int32_t max_query_len, float scale, float k_scale,
+                        float v_scale, void *out, void *workspace, size_t workspace_bytes, int32_t *status,
+                        void *stream);
+
+/*
+ * Rows of a block table that go on from other rows: parallel samples of a
+ * prompt, beam search, and requests that end. Row r of the new tables goes on
+ * from row parents[r] of the old ones, or is empty (-1). With L = seq_lens[p] of
+ * a parent p:
+ *     seq_lens_out[r] = L            (0 where the row is empty)
+ *     block_table_out[r][e] = block_table[p][e]      for e < ceil(L / 16), else -1
+ * but where L is no multiple of 16, all children of p but the first get a block
+ * of their own for the last entry, in row order from the free list, and
+ * copy_src[r], copy_dst[r] name the copy to be made (-1, -1 for all other rows):
+ * run paged_copy_blocks on every layer's pool before the rows are written to.
+ * Old rows that nobody goes on from give their blocks up.
+ *
+ * shares[b] counts the rows that hold block b beyond the first: 0 for blocks
+ * that one row or nobody holds, so that blocks from paged_build_tables need no
+ * entry. A block that its last holder gave up goes back to the free list:
+ * free_blocks[cursor ..] are the free ones, as paged_build_tables takes them, and
+ * the call first puts the blocks given up right before the cursor (in the order of
+ * rows and entries, a block of several rows at its first place), then takes new
+ * ones from there.
+ *
+ *  parents          int32 [num_rows], at most PKV_MAX_FORK_ROWS rows
+ *  block_table      int32 [num_rows][max_blocks_per_req], num_rows * max_blocks_per_req at most 2^29
+ *  seq_lens         int32 [num_rows]
+ *  shares           int32 [num_blocks], updated in place
+ *  free_blocks      int32 [num_free], updated in place
+ *  free_cursor      int32, updated in place
+ *  block_table_out, seq_lens_out   other memory than block_table and seq_lens
+ *  copy_src, copy_dst              int32 [num_rows] (outputs)
+ *  status           optional device int32, PKV_DEV_* bits OR-ed in
+ *
+ * The last, partly filled block of a row must be its own. A parent that is no
+ * row counts as -1 (PKV_DEV_BAD_PAGES); a length below 0 or past 16 *
+ * max_blocks_per_req as 0 (PKV_DEV_BAD_LEN); entries outside [0, num_blocks) are
+ * passed on and neither counted nor copied (PKV_DEV_BAD_BLOCK). A row for which the
+ * free list has no block gets entry -1 and no copy (PKV_DEV_NO_BLOCKS). A block
+ * given up more often than held stays out of the free list, blocks that do not fit
+ * before the cursor are lost, and a cursor outside [0, num_free] is left as it
+ * is, nothing being put back or taken (PKV_DEV_BAD_PAGES).
+ *
+ * Ordering as paged_build_tables: nothing is read before every earlier kernel on
+ * the stream has completed, and kernels behind it start only when it has.
+ */
+#define PKV_MAX_FORK_ROWS 4096
+int paged_fork_tables(const int32_t *parents, int32_t num_rows, const int32_t *block_table,
+                      int32_t max_blocks_per_req, const int32_t *seq_lens, int32_t num_blocks, int32_t *shares,
+                      int32_t *free_blocks, int32_t num_free, int32_t *free_cursor, int32_t *block_table_out,
+                      int32_t *seq_lens_out, int32_t *copy_src, int32_t *copy_dst, int32_t *status, void *stream);
+
+/*
+ * Copies block src[i] over block dst[i] in each of num_pools pools (a model's
+ * layers, at most PKV_MAX_POOLS a call) of blocks of block_bytes bytes: a
+ * multiple of 16, 64 * num_kv_heads * head_size for the bf16 pool, 18 *
+ * num_kv_heads * head_size for the 4-bit one. Pairs with a negative entry are
+ * skipped; those with one at or beyond num_blocks too, and raise
+ * PKV_DEV_BAD_BLOCK. The dst must be distinct and none of them the src of
+ * another pair. `pools` is a host array of device pointers, read during the call.
+ */
+#define PKV_MAX_POOLS 128
+int paged_copy_blocks(void *const *pools, int32_t num_pools, int64_t block_bytes, int32_t num_blocks,
+                      const int32_t *src, const int32_t *dst, int32_t num_pairs, int32_t *status, void *stream);
 
 /*
  * Host-buffer step pipeline: steps whose inputs come from, and whose output

@@ -39,13 +39,16 @@ PKV_DEV_TIMEOUT = 0x10
 PKV_DEV_OVERFLOW = 0x20
 PKV_DEV_BAD_POS = 0x40
 PKV_DEV_NO_BLOCKS = 0x80
+PKV_DEV_BAD_PAGES = 0x100
 
 EXPORTED = ("pkv_kv_cache_bytes", "paged_slot_mapping", "paged_kv_write", "paged_kv_write_slots",
             "paged_kv_gather_blocks",
             "paged_kv_scatter_blocks", "paged_attention_workspace_bytes",
             "paged_attention_min_workspace_bytes", "paged_attention", "paged_attention_timed",
             "paged_attention_bounded", "paged_attention_static", "paged_build_tables", "paged_qk_norm_rope",
-            "pkv_prompt_attention", "pkv_pipeline_create", "pkv_pipeline_next",
+            "pkv_prompt_attention", "paged_kv4_cache_bytes", "paged_kv4_write", "paged_kv4_read",
+            "paged_kv4_attention_workspace_bytes", "paged_kv4_attention", "paged_fork_tables", "paged_copy_blocks",
+            "pkv_pipeline_create", "pkv_pipeline_next",
             "pkv_pipeline_submit", "pkv_pipeline_sync", "pkv_pipeline_destroy", "pkv_read_status", "pkv_selftest_bounded_wait", "pkv_status_string")
 
 
@@ -73,6 +76,8 @@ class RopeDesc(ctypes.Structure):
 
 
 PIPELINE_MAX_DEPTH = 4
+MAX_FORK_ROWS = 4096
+MAX_POOLS = 128
 
 
 class PipelineDesc(ctypes.Structure):
@@ -115,6 +120,15 @@ def _load():
                                        vp, vp]
     lib.pkv_prompt_attention.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, vp, i32, ctypes.c_float, vp,
                                          vp, vp]
+    f32 = ctypes.c_float
+    lib.paged_kv4_cache_bytes.argtypes = [desc_p, ctypes.POINTER(sz)]
+    lib.paged_kv4_write.argtypes = [vp, i64, vp, i64, vp, i32, vp, desc_p, f32, f32, vp, vp]
+    lib.paged_kv4_read.argtypes = [vp, desc_p, vp, i32, f32, f32, vp, vp, vp, vp]
+    lib.paged_kv4_attention_workspace_bytes.argtypes = [desc_p, ctypes.POINTER(sz)]
+    lib.paged_kv4_attention.argtypes = [vp, i64, i32, i32, vp, desc_p, vp, i32, i32, vp, vp, i32, f32, f32, f32, vp, vp,
+                                        sz, vp, vp]
+    lib.paged_fork_tables.argtypes = [vp, i32, vp, i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.paged_copy_blocks.argtypes = [ctypes.POINTER(vp), i32, i64, i32, vp, vp, i32, vp, vp]
     lib.pkv_selftest_bounded_wait.argtypes = [vp, ctypes.c_uint32, vp]
     lib.pkv_pipeline_create.argtypes = [ctypes.POINTER(PipelineDesc), ctypes.POINTER(vp)]
     lib.pkv_pipeline_next.argtypes = [vp, ctypes.POINTER(i32)]
@@ -583,6 +597,247 @@ def pkv_prompt_attention(q, k, v, query_start_loc, scale: float, *, out=None, st
     undefined)."""
     with _memory_of(stream, q):
         return prepare_prompt_attention(q, k, v, query_start_loc, scale, out=out, status=status)(stream)
+
+
+def kv4_desc(kv4_cache: torch.Tensor) -> CacheDesc:
+    """Descriptor of a 4-bit pool, uint8 [num_blocks][num_kv_heads][18 * head_size]."""
+    _want(kv4_cache, torch.uint8, 3, "kv4_cache")
+    nb, hkv, row = kv4_cache.shape
+    if row % 18:
+        raise ValueError(f"kv4_cache must be [num_blocks][num_kv_heads][18 * head_size], got {tuple(kv4_cache.shape)}")
+    return CacheDesc(nb, BLOCK_SIZE, hkv, row // 18)
+
+
+def paged_kv4_cache_bytes(num_blocks: int, num_kv_heads: int, head_size: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.paged_kv4_cache_bytes(ctypes.byref(CacheDesc(num_blocks, BLOCK_SIZE, num_kv_heads, head_size)),
+                                     ctypes.byref(out)), "paged_kv4_cache_bytes")
+    return out.value
+
+
+def alloc_kv4_cache(num_blocks: int, num_kv_heads: int, head_size: int, device="cuda") -> torch.Tensor:
+    """A 4-bit pool of zeros for one layer."""
+    paged_kv4_cache_bytes(num_blocks, num_kv_heads, head_size)  # checks the sizes
+    return torch.zeros((num_blocks, num_kv_heads, 18 * head_size), dtype=torch.uint8, device=device)
+
+
+def _want_slots(slot_mapping, n: int):
+    _want(slot_mapping, torch.int32, 1, "slot_mapping")
+    if slot_mapping.shape[0] < n:
+        raise ValueError("slot_mapping is shorter than the tokens")
+
+
+def _want_status(status):
+    if status is not None:
+        _want(status, torch.int32, 1, "status")
+        if status.shape[0] < 1:
+            raise ValueError("status must have an entry")
+
+
+def prepare_kv4_write(k, v, slot_mapping, kv4_cache, *, k_scale: float = 1.0, v_scale: float = 1.0,
+                      status=None) -> PreparedCall:
+    """The checked call of ``paged_kv4_write``, to be called every step."""
+    desc = kv4_desc(kv4_cache)
+    t, hkv, d, k_stride = _want_rows(k, "k")
+    tv, hv, dv, v_stride = _want_rows(v, "v")
+    if (t, hkv, d) != (tv, hv, dv) or (hkv, d) != (desc.num_kv_heads, desc.head_size):
+        raise ValueError("k and v must be [num_tokens][num_kv_heads][head_size] matching kv4_cache")
+    _want_slots(slot_mapping, t)
+    _want_status(status)
+    _same_device(kv4_cache.device, k=k, v=v, slot_mapping=slot_mapping, status=status)
+    i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    args = (_ptr(k), i64(k_stride), _ptr(v), i64(v_stride), _ptr(slot_mapping), i32(t), _ptr(kv4_cache),
+            ctypes.byref(desc), f32(k_scale), f32(v_scale), _ptr(status))
+    return PreparedCall("paged_kv4_write", args, kv4_cache.device, None, (desc, k, v, slot_mapping, kv4_cache, status))
+
+
+def paged_kv4_write(k, v, slot_mapping, kv4_cache, *, k_scale: float = 1.0, v_scale: float = 1.0, status=None,
+                    stream=None) -> None:
+    """K and V of new tokens into the 4-bit pool (``alloc_kv4_cache``) at
+    ``slot_mapping``, as ``paged_kv_write`` for the bf16 pool. k and v may be
+    slices of one projection's rows. The scales are powers of two."""
+    prepare_kv4_write(k, v, slot_mapping, kv4_cache, k_scale=k_scale, v_scale=v_scale, status=status)(stream)
+
+
+def prepare_kv4_read(kv4_cache, slot_mapping, *, k_scale: float = 1.0, v_scale: float = 1.0, k_out=None, v_out=None,
+                     status=None) -> PreparedCall:
+    """The checked call of ``paged_kv4_read``, to be called every step."""
+    desc = kv4_desc(kv4_cache)
+    _want(slot_mapping, torch.int32, 1, "slot_mapping")
+    shape = (slot_mapping.shape[0], desc.num_kv_heads, desc.head_size)
+    if k_out is None and v_out is None:
+        k_out, v_out = (torch.zeros(shape, dtype=torch.bfloat16, device=kv4_cache.device) for _ in range(2))
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _want(t, torch.bfloat16, 3, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be [slots][num_kv_heads][head_size]")
+    _want_status(status)
+    _same_device(kv4_cache.device, slot_mapping=slot_mapping, k_out=k_out, v_out=v_out, status=status)
+    i32, f32 = ctypes.c_int32, ctypes.c_float
+    args = (_ptr(kv4_cache), ctypes.byref(desc), _ptr(slot_mapping), i32(shape[0]), f32(k_scale), f32(v_scale),
+            _ptr(k_out), _ptr(v_out), _ptr(status))
+    return PreparedCall("paged_kv4_read", args, kv4_cache.device, (k_out, v_out),
+                        (desc, kv4_cache, slot_mapping, status))
+
+
+def paged_kv4_read(kv4_cache, slot_mapping, *, k_scale: float = 1.0, v_scale: float = 1.0, k_out=None, v_out=None,
+                   status=None, stream=None):
+    """What the 4-bit pool holds at ``slot_mapping``, as ``(k, v)`` in bf16
+    (exactly). Rows of negative slots are left as they were (in fresh outputs:
+    zero)."""
+    with _memory_of(stream, kv4_cache):
+        return prepare_kv4_read(kv4_cache, slot_mapping, k_scale=k_scale, v_scale=v_scale, k_out=k_out, v_out=v_out,
+                                status=status)(stream)
+
+
+def alloc_kv4_workspace(kv4_cache: torch.Tensor) -> torch.Tensor:
+    """Workspace of ``paged_kv4_attention``, for any batch over this pool."""
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(kv4_cache.device):
+        _check(LIB.paged_kv4_attention_workspace_bytes(ctypes.byref(kv4_desc(kv4_cache)), ctypes.byref(out)),
+               "paged_kv4_attention_workspace_bytes")
+    return torch.empty((out.value + 7) // 8, dtype=torch.int64, device=kv4_cache.device)
+
+
+def prepare_kv4_attention(q, kv4_cache, block_table, seq_lens, query_start_loc, scale: float, *, k_scale: float = 1.0,
+                          v_scale: float = 1.0, max_query_len: int = 0, out=None, workspace=None,
+                          status=None) -> PreparedCall:
+    """The checked call of ``paged_kv4_attention``, to be called every step."""
+    desc = kv4_desc(kv4_cache)
+    t, hq, d, q_stride = _want_rows(q, "q")
+    if d != desc.head_size:
+        raise ValueError("q head_size differs from kv4_cache")
+    _want(block_table, torch.int32, 2, "block_table")
+    _want(seq_lens, torch.int32, 1, "seq_lens")
+    _want(query_start_loc, torch.int32, 1, "query_start_loc")
+    r = seq_lens.shape[0]
+    if query_start_loc.shape[0] != r + 1 or block_table.shape[0] != r:
+        raise ValueError("block_table, seq_lens and query_start_loc disagree on the number of requests")
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
+    _want(out, torch.bfloat16, 3, "out")
+    if tuple(out.shape) != (t, hq, d):
+        raise ValueError("out must have q's shape")
+    if t and out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be q")
+    if workspace is None:
+        workspace = alloc_kv4_workspace(kv4_cache)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _want_status(status)
+    _same_device(kv4_cache.device, q=q, block_table=block_table, seq_lens=seq_lens, query_start_loc=query_start_loc,
+                 out=out, workspace=workspace, status=status)
+    i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    args = (_ptr(q), i64(q_stride), i32(t), i32(hq), _ptr(kv4_cache), ctypes.byref(desc), _ptr(block_table), i32(r),
+            i32(block_table.shape[1]), _ptr(seq_lens), _ptr(query_start_loc), i32(max_query_len), f32(scale),
+            f32(k_scale), f32(v_scale), _ptr(out), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel() * workspace.element_size()), _ptr(status))
+    return PreparedCall("paged_kv4_attention", args, kv4_cache.device, out,
+                        (desc, q, kv4_cache, block_table, seq_lens, query_start_loc, workspace, status))
+
+
+def paged_kv4_attention(q, kv4_cache, block_table, seq_lens, query_start_loc, scale: float, *, k_scale: float = 1.0,
+                        v_scale: float = 1.0, max_query_len: int = 0, out=None, workspace=None, status=None,
+                        stream=None) -> torch.Tensor:
+    """``paged_attention`` over the 4-bit pool. q may be a slice of a
+    projection's rows. ``workspace`` (``alloc_kv4_workspace``) may hold anything;
+    calls that may run at the same time need one each."""
+    with _memory_of(stream, q):
+        return prepare_kv4_attention(q, kv4_cache, block_table, seq_lens, query_start_loc, scale, k_scale=k_scale,
+                                     v_scale=v_scale, max_query_len=max_query_len, out=out, workspace=workspace,
+                                     status=status)(stream)
+
+
+def prepare_fork_tables(parents, block_table, seq_lens, shares, free_blocks, cursor, *, block_table_out=None,
+                        seq_lens_out=None, copy_src=None, copy_dst=None, status=None) -> PreparedCall:
+    """The checked call of ``paged_fork_tables``, to be called every step."""
+    _want(block_table, torch.int32, 2, "block_table")
+    dev, (r, width) = block_table.device, block_table.shape
+    if block_table_out is None:
+        block_table_out = torch.empty_like(block_table)
+    _want(block_table_out, torch.int32, 2, "block_table_out")
+    if block_table_out.shape != block_table.shape:
+        raise ValueError("block_table_out must have block_table's shape")
+
+    def rows(t, name):
+        if t is None:
+            return torch.empty(r, dtype=torch.int32, device=dev)
+        _want(t, torch.int32, 1, name)
+        if t.shape[0] < r:
+            raise ValueError(f"{name} has {t.shape[0]} entries, {r} are needed")
+        return t
+
+    for t, name in ((parents, "parents"), (seq_lens, "seq_lens")):
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+        rows(t, name)
+    seq_lens_out, copy_src, copy_dst = (rows(t, n) for t, n in ((seq_lens_out, "seq_lens_out"),
+                                                                (copy_src, "copy_src"), (copy_dst, "copy_dst")))
+    for t, name in ((shares, "shares"), (free_blocks, "free_blocks"), (cursor, "cursor")):
+        _want(t, torch.int32, 1, name)
+    if cursor.shape[0] < 1:
+        raise ValueError("cursor must have an entry")
+    _want_status(status)
+    _same_device(dev, parents=parents, seq_lens=seq_lens, shares=shares, free_blocks=free_blocks, cursor=cursor,
+                 block_table_out=block_table_out, seq_lens_out=seq_lens_out, copy_src=copy_src, copy_dst=copy_dst,
+                 status=status)
+    i32 = ctypes.c_int32
+    args = (_ptr(parents), i32(r), _ptr(block_table), i32(width), _ptr(seq_lens), i32(shares.shape[0]), _ptr(shares),
+            _ptr(free_blocks), i32(free_blocks.shape[0]), _ptr(cursor), _ptr(block_table_out), _ptr(seq_lens_out),
+            _ptr(copy_src), _ptr(copy_dst), _ptr(status))
+    return PreparedCall("paged_fork_tables", args, dev, (block_table_out, seq_lens_out, copy_src, copy_dst),
+                        (parents, block_table, seq_lens, shares, free_blocks, cursor, status))
+
+
+def paged_fork_tables(parents, block_table, seq_lens, shares, free_blocks, cursor, *, block_table_out=None,
+                      seq_lens_out=None, copy_src=None, copy_dst=None, status=None, stream=None):
+    """Row r of the new tables goes on from row ``parents[r]`` (-1: it is
+    empty): full blocks shared, a partly filled last one copied for all children
+    but the first, blocks of rows that nobody goes on from given back.
+    ``shares`` has an entry per block of the pool; it, ``free_blocks`` and
+    ``cursor`` are updated in place. Returns ``(block_table, seq_lens, copy_src,
+    copy_dst)``; pass the last two to ``paged_copy_blocks`` with every layer's
+    pool."""
+    with _memory_of(stream, block_table):
+        return prepare_fork_tables(parents, block_table, seq_lens, shares, free_blocks, cursor,
+                                   block_table_out=block_table_out, seq_lens_out=seq_lens_out, copy_src=copy_src,
+                                   copy_dst=copy_dst, status=status)(stream)
+
+
+def prepare_copy_blocks(pools, copy_src, copy_dst, *, status=None) -> PreparedCall:
+    """The checked call of ``paged_copy_blocks``, to be called every step."""
+    pools = list(pools)
+    if not 1 <= len(pools) <= MAX_POOLS:
+        raise ValueError(f"{len(pools)} pools, 1 to {MAX_POOLS} are supported")
+    for p in pools:
+        if p.dtype == torch.uint8:
+            kv4_desc(p)
+        else:
+            _want(p, torch.bfloat16, 5, "pools")
+        if p.shape != pools[0].shape or p.dtype != pools[0].dtype:
+            raise ValueError("all pools must have one shape and type")
+    nb = pools[0].shape[0]
+    nbytes = pools[0].numel() // max(nb, 1) * pools[0].element_size()
+    for t, name in ((copy_src, "copy_src"), (copy_dst, "copy_dst")):
+        _want(t, torch.int32, 1, name)
+    if copy_src.shape != copy_dst.shape:
+        raise ValueError("copy_src and copy_dst must have the same length")
+    _want_status(status)
+    dev = pools[0].device
+    _same_device(dev, copy_src=copy_src, copy_dst=copy_dst, status=status, **{f"pools[{i}]": p for i, p in enumerate(pools)})
+    i32 = ctypes.c_int32
+    where = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
+    args = (where, i32(len(pools)), ctypes.c_int64(nbytes), i32(nb), _ptr(copy_src), _ptr(copy_dst),
+            i32(copy_src.shape[0]), _ptr(status))
+    return PreparedCall("paged_copy_blocks", args, dev, None, (where, pools, copy_src, copy_dst, status))
+
+
+def paged_copy_blocks(pools, copy_src, copy_dst, *, status=None, stream=None) -> None:
+    """Block ``copy_src[i]`` over block ``copy_dst[i]`` in each of ``pools``
+    (the layers' pools, all bf16 or all 4-bit); pairs with a negative entry are
+    skipped."""
+    prepare_copy_blocks(pools, copy_src, copy_dst, status=status)(stream)
 
 
 def _event_handle(ev, stream) -> int:

@@ -1,0 +1,354 @@
+// Rows of a block table that go on from other rows (parallel samples of a
+// prompt, beam search), and the block copies that this takes ("Inside vLLM",
+// page 1, "Prefix Caching": blocks of 16 that several requests' tables name).
+//
+// A row's full blocks are shared with the row it goes on from; a partly filled
+// last block, which the row will write to, is kept by the first child and copied
+// for the others. shares[b] counts the rows that hold block b beyond the first,
+// so blocks that paged_build_tables hands out need no entry of their own. Rows
+// that nobody goes on from give their blocks up; a block given up by its last
+// holder goes back in front of the free list, in the order of rows and entries.
+// Whichever row brings a count below zero, the entry with the lowest index takes
+// the block (an atomic minimum on the count itself), so the order of the free
+// list does not depend on the order of atomics.
+//
+// One cluster does it all, with a barrier between counting, claiming, giving
+// back and handing out. Rows with exactly one child change no count.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kMaxCtas = 8;
+constexpr int kFree = INT_MIN / 2;  // counts below this are claims: INT_MIN + entry
+
+struct ForkArgs {
+    const int32_t *parents, *table, *lens;
+    int rows, width, num_blocks;
+    int32_t *shares, *free_blocks;
+    int num_free;
+    int32_t *cursor, *table_out, *lens_out, *copy_src, *copy_dst, *status;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Stores v to `at` (a shared address) of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_to(uint32_t at, uint32_t rank, int v) {
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.b32 [a], %2;\n\t}" ::"r"(at), "r"(rank), "r"(v)
+                 : "memory");
+}
+
+// Counts seen after a cluster barrier: written by atomics, read past L1.
+__device__ __forceinline__ int seen(const int32_t *p) { return __ldcg(p); }
+
+__global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a) {
+    __shared__ int s_children[PKV_MAX_FORK_ROWS], s_first[PKV_MAX_FORK_ROWS];
+    __shared__ int s_warp[32], s_total[kMaxCtas];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x, ctas = gridDim.x;  // the grid is one cluster
+    const int R = a.rows;
+    for (int r = tid; r < R; r += kThreads) {
+        s_children[r] = 0;
+        s_first[r] = INT_MAX;
+    }
+    pdl_wait();
+    __syncthreads();
+    int bits = 0;
+    // the blocks of a row: 0 and flagged where its length is out of range
+    auto length = [&](int r) {
+        const int n = __ldg(a.lens + r);
+        if (n >= 0 && n <= (long long)a.width * PKV_BLOCK_SIZE) return n;
+        bits |= PKV_DEV_BAD_LEN;
+        return 0;
+    };
+    auto parent = [&](int r) {
+        const int p = __ldg(a.parents + r);
+        if (p >= -1 && p < R) return p;
+        bits |= PKV_DEV_BAD_PAGES;
+        return -1;
+    };
+    auto block = [&](int r, int e) {
+        const int b = __ldg(a.table + (long long)r * a.width + e);
+        if (b >= 0 && b < a.num_blocks) return b;
+        bits |= PKV_DEV_BAD_BLOCK;
+        return -1;
+    };
+    for (int r = tid; r < R; r += kThreads) {
+        const int p = parent(r);
+        if (p >= 0) {
+            atomicAdd(s_children + p, 1);
+            atomicMin(s_first + p, r);
+        }
+    }
+    const int cur = *a.cursor;
+    const bool list = cur >= 0 && cur <= a.num_free;
+    if (!list) bits |= PKV_DEV_BAD_PAGES;
+    __syncthreads();
+
+    // this CTA's rows, one a warp at a time
+    const int per = (R + ctas - 1) / ctas, r0 = min(R, rank * per), r1 = min(R, r0 + per);
+    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
+        const int c = s_children[r];
+        if (c == 1) continue;
+        const int n = length(r), full = n / PKV_BLOCK_SIZE, held = c ? full : (n + 15) / PKV_BLOCK_SIZE;
+        for (int e = lane; e < held; e += 32) {
+            const int b = block(r, e);
+            if (b >= 0) atomicAdd(a.shares + b, c - 1);
+        }
+    }
+    cluster_sync();
+    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
+        if (s_children[r]) continue;
+        const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
+        for (int e = lane; e < held; e += 32) {
+            const int b = block(r, e);
+            if (b < 0) continue;
+            const int v = seen(a.shares + b);
+            if (v == -1 || v < kFree) atomicMin(a.shares + b, INT_MIN + (r * a.width + e));
+            else if (v < -1) bits |= PKV_DEV_BAD_PAGES;  // given up more often than held
+        }
+    }
+    cluster_sync();
+    // blocks that this CTA's rows give back
+    int mine = 0;
+    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
+        if (s_children[r]) continue;
+        const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
+        int got = 0;
+        for (int e0 = 0; e0 < held; e0 += 32) {
+            const int e = e0 + lane, b = e < held ? block(r, e) : -1;
+            got += __popc(__ballot_sync(0xffffffffu, b >= 0 && seen(a.shares + b) == INT_MIN + (r * a.width + e)));
+        }
+        if (lane == 0) s_first[r] = got;  // a row without children has no first one
+        mine += got;
+    }
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+        const int sum = __reduce_add_sync(0xffffffffu, s_warp[lane]);
+        if (lane < ctas) store_to(smem_u32(s_total + rank), lane, sum);
+    }
+    cluster_sync();
+    int before = 0, given = 0;
+    for (int i = 0; i < ctas; ++i) {
+        if (i < rank) before += s_total[i];
+        given += s_total[i];
+    }
+    if (!list) given = 0;
+    if (given > cur && list) bits |= PKV_DEV_BAD_PAGES;  // more than were ever taken
+    const int base = list ? cur - given : 0;             // where the first one goes
+    // every row's place: a sum over the rows before it, a thread per row
+    for (int c0 = r0; c0 < r1; c0 += kThreads) {
+        const int r = c0 + tid;
+        const int n = r < r1 && !s_children[r] ? s_first[r] : 0;
+        int v = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += o;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = v;
+        __syncthreads();
+        int sum = 0, all = 0;
+        for (int i = 0; i < 32; ++i) {
+            if (i < warp) sum += s_warp[i];
+            all += s_warp[i];
+        }
+        if (r < r1 && !s_children[r]) s_first[r] = before + sum + v - n;
+        before += all;
+    }
+    __syncthreads();
+    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
+        if (s_children[r]) continue;
+        const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
+        int at = base + s_first[r];
+        for (int e0 = 0; e0 < held; e0 += 32) {
+            const int e = e0 + lane, b = e < held ? block(r, e) : -1;
+            const int v = b >= 0 ? seen(a.shares + b) : 0;
+            const bool take = v == INT_MIN + (r * a.width + e) && b >= 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, take);
+            if (take) {
+                const int to = at + __popc(all & ((1u << lane) - 1));
+                if (list && to >= 0) a.free_blocks[to] = b;
+            }
+            if (take || (v < 0 && v >= kFree)) a.shares[b] = 0;
+            at += __popc(all);
+        }
+    }
+    cluster_sync();
+    // the new rows; every CTA numbers the copies of all rows
+    const int from = max(base, 0);
+    int copies = 0;
+    for (int c0 = 0; c0 < R; c0 += kThreads) {
+        const int r = c0 + tid;
+        const int p = r < R ? parent(r) : -1;
+        const int n = p >= 0 ? length(p) : 0;
+        const bool copy = p >= 0 && n % PKV_BLOCK_SIZE && s_first[p] != r;
+        const uint32_t all = __ballot_sync(0xffffffffu, copy);
+        __syncthreads();
+        if (lane == 0) s_warp[warp] = __popc(all);
+        __syncthreads();
+        int sum = copies, sums = 0;
+        for (int i = 0; i < 32; ++i) {
+            if (i < warp) sum += s_warp[i];
+            sums += s_warp[i];
+        }
+        // rows of this pass, a warp at a time
+        const int k = from + sum + __popc(all & ((1u << lane) - 1));
+        int src = -1, dst = -1;
+        const bool own = r >= r0 && r < r1;
+        if (own) {
+            if (copy) {
+                src = block(p, n / PKV_BLOCK_SIZE);
+                if (list && k < a.num_free) {
+                    dst = __ldcg(a.free_blocks + k);
+                    if (dst < 0 || dst >= a.num_blocks) {
+                        dst = -1;
+                        bits |= PKV_DEV_BAD_BLOCK;
+                    }
+                } else {
+                    bits |= PKV_DEV_NO_BLOCKS;
+                }
+                if (src < 0 || dst < 0) src = -1;
+            }
+            a.lens_out[r] = n;
+            a.copy_src[r] = src;
+            a.copy_dst[r] = src < 0 ? -1 : dst;
+        }
+        for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo; todo &= todo - 1) {
+            const int i = __ffs(todo) - 1;
+            const int pi = __shfl_sync(0xffffffffu, p, i), ni = __shfl_sync(0xffffffffu, n, i);
+            const int di = __shfl_sync(0xffffffffu, dst, i), ci = __shfl_sync(0xffffffffu, (int)copy, i);
+            const int held = (ni + 15) / PKV_BLOCK_SIZE;
+            const int32_t *line = a.table + (long long)max(pi, 0) * a.width;
+            int32_t *to = a.table_out + (long long)(c0 + warp * 32 + i) * a.width;
+            for (int e = lane; e < a.width; e += 32)
+                to[e] = e >= held ? -1 : ci && e == held - 1 ? di : __ldg(line + e);
+        }
+        copies += sums;
+    }
+    if (rank == 0 && tid == 0 && list) *a.cursor = from + min(copies, a.num_free - from);
+    if (bits) raise_status(a.status, bits);
+    __threadfence();
+}
+
+constexpr int kCopyThreads = 256;
+
+struct CopyArgs {
+    uint4 *pools[PKV_MAX_POOLS];
+    const int32_t *src, *dst;
+    long long vecs;  // 16-byte chunks of a block
+    int num_pairs, num_blocks, splits;
+    int32_t *status;
+};
+
+// A CTA copies one part of one block of one pool.
+__global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
+    constexpr int kUnroll = 4;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int i = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
+    const int s = __ldg(a.src + i), d = __ldg(a.dst + i);
+    if (s < 0 || d < 0) return;
+    if (s >= a.num_blocks || d >= a.num_blocks) {
+        if (threadIdx.x == 0 && part == 0 && blockIdx.y == 0) raise_status(a.status, PKV_DEV_BAD_BLOCK);
+        return;
+    }
+    uint4 *pool = a.pools[blockIdx.y];
+    const uint4 *from = pool + s * a.vecs;
+    uint4 *to = pool + d * a.vecs;
+    const long long end = a.vecs;
+    for (long long base = (long long)part * kCopyThreads * kUnroll + threadIdx.x; base < end;
+         base += (long long)a.splits * kCopyThreads * kUnroll) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (base + u * kCopyThreads < end) v[u] = __ldcs(from + base + u * kCopyThreads);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (base + u * kCopyThreads < end) to[base + u * kCopyThreads] = v[u];
+    }
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" PKV_API int paged_fork_tables(const int32_t *parents, int32_t num_rows, const int32_t *block_table,
+                                         int32_t max_blocks_per_req, const int32_t *seq_lens, int32_t num_blocks,
+                                         int32_t *shares, int32_t *free_blocks, int32_t num_free, int32_t *free_cursor,
+                                         int32_t *block_table_out, int32_t *seq_lens_out, int32_t *copy_src,
+                                         int32_t *copy_dst, int32_t *status, void *stream) {
+    if (num_rows < 0 || num_rows > PKV_MAX_FORK_ROWS || max_blocks_per_req < 0 || num_free < 0 || num_blocks <= 0)
+        return PKV_E_DIMS;
+    if (num_blocks > INT32_MAX / PKV_BLOCK_SIZE || max_blocks_per_req > INT32_MAX / PKV_BLOCK_SIZE ||
+        (long long)num_rows * max_blocks_per_req > (1 << 29) || num_free > INT32_MAX - 65536)
+        return PKV_E_DIMS;
+    if (num_rows == 0) return PKV_OK;
+    if (!parents || !seq_lens || !shares || !free_cursor || !seq_lens_out || !copy_src || !copy_dst ||
+        (num_free > 0 && !free_blocks) || (max_blocks_per_req > 0 && (!block_table || !block_table_out)))
+        return PKV_E_NULL;
+    if (!aligned(parents, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(shares, 4) ||
+        !aligned(free_blocks, 4) || !aligned(free_cursor, 4) || !aligned(block_table_out, 4) ||
+        !aligned(seq_lens_out, 4) || !aligned(copy_src, 4) || !aligned(copy_dst, 4) || !aligned(status, 4))
+        return PKV_E_ALIGN;
+    if (block_table_out == block_table || seq_lens_out == seq_lens) return PKV_E_DIMS;
+    const ForkArgs a{parents, block_table, seq_lens, num_rows, max_blocks_per_req, num_blocks, shares, free_blocks,
+                     num_free, free_cursor, block_table_out, seq_lens_out, copy_src, copy_dst, status};
+    const int ctas = num_rows <= 32 ? 1 : kMaxCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fork_tables_kernel, a) == cudaSuccess ? PKV_OK : PKV_E_CUDA;
+}
+
+extern "C" PKV_API int paged_copy_blocks(void *const *pools, int32_t num_pools, int64_t block_bytes, int32_t num_blocks,
+                                         const int32_t *src, const int32_t *dst, int32_t num_pairs, int32_t *status,
+                                         void *stream) {
+    if (num_pools < 0 || num_pools > PKV_MAX_POOLS || num_pairs < 0 || num_pairs > INT32_MAX / 64 || num_blocks <= 0 ||
+        block_bytes <= 0 || block_bytes % 16)
+        return PKV_E_DIMS;
+    if (num_pools == 0 || num_pairs == 0) return PKV_OK;
+    if (!pools || !src || !dst) return PKV_E_NULL;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(status, 4)) return PKV_E_ALIGN;
+    CopyArgs a{};
+    for (int i = 0; i < num_pools; ++i) {
+        if (!pools[i]) return PKV_E_NULL;
+        if (!aligned(pools[i], 16)) return PKV_E_ALIGN;
+        a.pools[i] = static_cast<uint4 *>(pools[i]);
+    }
+    a.src = src;
+    a.dst = dst;
+    a.vecs = block_bytes / 16;
+    a.num_pairs = num_pairs;
+    a.num_blocks = num_blocks;
+    a.splits = (int)std::min<long long>(4, std::max<long long>(1, a.vecs / (kCopyThreads * 4)));
+    a.status = status;
+    return launch_pdl(copy_blocks_kernel, dim3(num_pairs * a.splits, num_pools), dim3(kCopyThreads), 0,
+                      static_cast<cudaStream_t>(stream), a) == cudaSuccess
+               ? PKV_OK
+               : PKV_E_CUDA;
+}

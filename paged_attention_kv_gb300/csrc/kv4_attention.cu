@@ -1,0 +1,761 @@
+// Causal attention with grouped heads over the 4-bit pool (kv4_format.cuh), for
+// a ragged batch of decode tokens and chunks.
+//
+// For a row (query token, head) with keys j = 0 .. p:
+//     out = sum_j softmax_j(scale q . K_j) V_j,  K_j = k_scale * codes * scales
+// A warp works alone. It takes an item's blocks of 16 keys one after another
+// through its own ring of bulk copies, turns the codes into fp16 fragments in
+// registers (exactly: six significant bits), and runs both products transposed,
+// S^T (16 keys x 8 rows) = K Q^T and O^T (D x 8 rows) += V^T P^T, on mma.sync
+// m16n8k16, so that the 4 to 8 rows of a decode token's head group fill the N
+// side and K and V are made once for up to four such groups of rows. An item is
+// (request, tile of 8 kMaxNt rows, kv head) and its cost a number of keys; all
+// items in a row are cut into equal shares, one a warp (kv4_plan.h). An item that
+// lies in several shares leaves one partial (m, l, O) a share, and the second
+// kernel joins them, in order, so that the result does not depend on timing.
+//
+// Softmax: scores stay unscaled; a row's reference m is the largest score of its
+// first block, and moves only when a score passes it by 2^10 (p then still fits
+// fp16), so that a block costs one vote and no exchange between lanes. p is 2^x
+// in 32 bits, rounded to fp16 (2^-11 of each) for the product with V; sums are
+// held in 32 bits.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "kv4_format.cuh"
+#include "kv4_plan.h"
+#include "pagedkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+#include "pkv_short_wait.cuh"
+
+namespace pkv {
+namespace {
+
+// Warps of a CTA (one CTA an SM) and copies a warp has in flight, by the rows
+// of a tile.
+template <int kMaxNt>
+constexpr int kWarps = kMaxNt == 4 ? 8 : 12;
+template <int D, int kMaxNt>
+constexpr int kStages = D == 64 ? 12 : 7;
+
+struct __align__(16) Kv4Record {
+    int32_t parts;  // shares that the item lies in; 0: no item starts in this share and ends in another
+    int32_t rows, token, head;  // of the tile: rows, first row's token and head within its group, as below
+    float mul[32];  // each row's factor from scores to exponents of 2
+};
+
+struct Kv4Args {
+    const __nv_bfloat16 *q;
+    long long q_stride;
+    const uint8_t *pool;
+    const int32_t *table, *lens, *qsl;
+    int num_tokens, num_kv_heads, group, num_reqs, max_blocks, num_blocks;
+    float scale_log2, v_scale;
+    __nv_bfloat16 *out;
+    Kv4Record *records;
+    float *parts;
+    int32_t *status;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return as_u32(__floats2half2_rn(lo, hi)); }
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// What a lane reads of a tile (lane 4 g + t).
+template <int D>
+struct Lane {
+    static constexpr int kW = D / 32;  // words of codes a lane has of a K token, and of a pair of V tokens
+    uint32_t k[2][kW], v[2][kW], ks, vs;
+
+    __device__ __forceinline__ void load(uint32_t tile, int lane) {
+        if constexpr (D == 128) {
+            lds(k[0], tile + 16 * lane);
+            lds(k[1], tile + 4 * D + 16 * lane);
+            lds(v[0], tile + 8 * D + 16 * lane);
+            lds(v[1], tile + 12 * D + 16 * lane);
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ks) : "r"(tile + 16 * D + 4 * lane));
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vs) : "r"(tile + 17 * D + 4 * lane));
+        } else {
+            lds(k[0], tile + 8 * lane);
+            lds(k[1], tile + 4 * D + 8 * lane);
+            lds(v[0], tile + 8 * D + 8 * lane);
+            lds(v[1], tile + 12 * D + 8 * lane);
+            asm volatile("{\n\t.reg .b16 s;\n\tld.shared.b16 s, [%1];\n\tcvt.u32.u16 %0, s;\n\t}" : "=r"(ks) : "r"(tile + 16 * D + 2 * lane));
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vs) : "r"(tile + 17 * D + 16 * (lane >> 3) + 4 * (lane & 3)));
+        }
+    }
+    static __device__ __forceinline__ void lds(uint32_t (&w)[4], uint32_t at) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+    }
+    static __device__ __forceinline__ void lds(uint32_t (&w)[2], uint32_t at) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    }
+};
+
+// A whole warp's state for one item of up to 8 kNt rows. Of O^T a lane holds,
+// for rows 8 n + 2 t and 8 n + 2 t + 1, the D / 8 columns from D / 8 * g on.
+template <int D, int kNt, int kStg>
+struct Item {
+    static constexpr int kK = D / 16;  // steps of 16 columns
+    float o[kNt][kK][4];
+    float2 m[kNt], l[kNt], mul[kNt];
+    uint32_t q[kNt][kK][2];
+
+    // q rows as fp16 fragments, each scaled by a power of two to lie in (-4, 4);
+    // mul takes that back. Rows past `rows` are zero.
+    __device__ __forceinline__ void load_q(const Kv4Args &a, int token0, int row0, int rows, int head, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+            const int row = 8 * n + g;
+            uint4 w[D / 32];
+            uint32_t top = 0;
+            if (row < rows) {
+                const int rr = row0 + row, tok = rr / a.group;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + (long long)(token0 + tok) * a.q_stride + (long long)(head * a.group + rr - tok * a.group) * D) + t * (D / 32);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) w[i] = __ldg(src + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t mk = 0x7fff7fffu;
+                const uint32_t x = __vmaxu2(__vmaxu2(w[i].x & mk, w[i].y & mk), __vmaxu2(w[i].z & mk, w[i].w & mk));
+                top = max(top, max(x & 0xffffu, x >> 16));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // exponent of the largest value; a row that small is as good as
+            // zero below 2^-63, one that is not finite keeps its values
+            int e = (int)(top >> 7);
+            e = e == 255 ? 127 : min(max(e, 64), 253);
+            const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[n][2 * i + j / 2][j & 1] =
+                        pack_f16x2(__uint_as_float(x[j] << 16) * down, __uint_as_float(x[j] & 0xffff0000u) * down);
+            }
+            const float f = row < rows ? up * a.scale_log2 : 0.0f;
+            mul[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
+            m[n] = make_float2(-INFINITY, -INFINITY);
+            l[n] = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kK; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[n][i][c] = 0.0f;
+        }
+    }
+
+    // The row's reference becomes the largest score so far.
+    static __device__ __forceinline__ void move(float &m, float &l, float mul, float top, float *f) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float to = fmaxf(m, top);
+        *f = m == to ? 1.0f : m == -INFINITY ? 0.0f : fast_exp2((m - to) * mul);
+        m = to;
+        l *= *f;
+    }
+    __device__ __forceinline__ void move_references(const float (&s)[kNt][4]) {
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+            float fx, fy;
+            move(m[n].x, l[n].x, mul[n].x, fmaxf(s[n][0], s[n][2]), &fx);
+            move(m[n].y, l[n].y, mul[n].y, fmaxf(s[n][1], s[n][3]), &fy);
+#pragma unroll
+            for (int i = 0; i < kK; ++i) {
+                o[n][i][0] *= fx;
+                o[n][i][1] *= fy;
+                o[n][i][2] *= fx;
+                o[n][i][3] *= fy;
+            }
+        }
+    }
+
+    // One block. key0: its first key's position; kMasked: rows end within it, row
+    // r (of the tile) at limit0 + (row0 + r) / group - first token.
+    template <bool kMasked>
+    __device__ __forceinline__ void block(Lane<D> &x, bool first, int key0, int limit0, int row0, int group, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        float s[kNt][4];
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[n][c] = 0.0f;
+        // K scales: tokens g and g + 8, one or two groups of this lane's quarter
+        __half2 sc[2][2];
+        {
+            if constexpr (D == 128) {
+                const __half2 a = kv4_scales(x.ks), b = kv4_scales(x.ks >> 16);
+                sc[0][0] = __low2half2(a);
+                sc[0][1] = __high2half2(a);
+                sc[1][0] = __low2half2(b);
+                sc[1][1] = __high2half2(b);
+            } else {
+                const __half2 a = kv4_scales(x.ks);
+                sc[0][0] = sc[0][1] = __low2half2(a);
+                sc[1][0] = sc[1][1] = __high2half2(a);
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < Lane<D>::kW; ++w) {
+            const int p = w * 2 / Lane<D>::kW;
+            {
+                const uint32_t f[4] = {as_u32(__hmul2(kv4_pair<0>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<0>(x.k[1][w]), sc[1][p])),
+                                       as_u32(__hmul2(kv4_pair<1>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<1>(x.k[1][w]), sc[1][p]))};
+#pragma unroll
+                for (int n = 0; n < kNt; ++n) mma_f16(s[n], f, q[n][2 * w][0], q[n][2 * w][1]);
+            }
+            {
+                const uint32_t f[4] = {as_u32(__hmul2(kv4_pair<2>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<2>(x.k[1][w]), sc[1][p])),
+                                       as_u32(__hmul2(kv4_pair<3>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<3>(x.k[1][w]), sc[1][p]))};
+#pragma unroll
+                for (int n = 0; n < kNt; ++n) mma_f16(s[n], f, q[n][2 * w + 1][0], q[n][2 * w + 1][1]);
+            }
+        }
+        if constexpr (kMasked) {
+#pragma unroll
+            for (int n = 0; n < kNt; ++n) {
+                const int ra = row0 + 8 * n + 2 * t, first_tok = row0 / group;
+                const int la = limit0 + ra / group - first_tok - key0, lb = limit0 + (ra + 1) / group - first_tok - key0;
+                if (g >= la) s[n][0] = -INFINITY;
+                if (g >= lb) s[n][1] = -INFINITY;
+                if (g + 8 >= la) s[n][2] = -INFINITY;
+                if (g + 8 >= lb) s[n][3] = -INFINITY;
+            }
+            move_references(s);
+        } else {
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < kNt; ++n) {
+                const float2 a = fmul2(fadd2(make_float2(s[n][0], s[n][1]), make_float2(-m[n].x, -m[n].y)), mul[n]);
+                const float2 b = fmul2(fadd2(make_float2(s[n][2], s[n][3]), make_float2(-m[n].x, -m[n].y)), mul[n]);
+                top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
+            }
+            if (__any_sync(0xffffffffu, top > 10.0f) || first) move_references(s);
+        }
+        uint32_t p[kNt][2];
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+            // a row that has seen no key yet has no reference: its scores are all -inf
+            const float mx = kMasked && m[n].x == -INFINITY ? 0.0f : m[n].x, my = kMasked && m[n].y == -INFINITY ? 0.0f : m[n].y;
+            const float2 a = fmul2(fadd2(make_float2(s[n][0], s[n][1]), make_float2(-mx, -my)), mul[n]);
+            const float2 b = fmul2(fadd2(make_float2(s[n][2], s[n][3]), make_float2(-mx, -my)), mul[n]);
+            float e[4] = {fast_exp2(a.x), fast_exp2(a.y), fast_exp2(b.x), fast_exp2(b.y)};
+            if constexpr (kMasked) {  // a factor of 0 (a scale or q near the smallest value) times -inf is no number
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (s[n][c] == -INFINITY) e[c] = 0.0f;
+            }
+            l[n] = fadd2(l[n], fadd2(make_float2(e[0], e[1]), make_float2(e[2], e[3])));
+            p[n][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
+            p[n][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
+        }
+        __half2 va = kv4_scales(x.vs), vb = kv4_scales(x.vs >> 16);  // tokens 2 t, 2 t + 1 and 8 on
+#pragma unroll
+        for (int w = 0; w < Lane<D>::kW / 2; ++w) {
+            // low and high codes of two tokens side by side
+            constexpr int kH = Lane<D>::kW / 2;
+            const uint32_t a0 = x.v[0][w], a1 = x.v[0][w + kH], b0 = x.v[1][w], b1 = x.v[1][w + kH];
+            const uint32_t lo = 0x0f0f0f0fu;
+            const uint32_t ae = (a0 & lo) | ((a1 << 4) & ~lo), ao = ((a0 >> 4) & lo) | (a1 & ~lo);
+            const uint32_t be = (b0 & lo) | ((b1 << 4) & ~lo), bo = ((b0 >> 4) & lo) | (b1 & ~lo);
+            pv<0>(4 * w, ae, ao, be, bo, va, vb, p);
+            pv<1>(4 * w + 1, ae, ao, be, bo, va, vb, p);
+            pv<2>(4 * w + 2, ae, ao, be, bo, va, vb, p);
+            pv<3>(4 * w + 3, ae, ao, be, bo, va, vb, p);
+        }
+    }
+    template <int kB>
+    __device__ __forceinline__ void pv(int i, uint32_t ae, uint32_t ao, uint32_t be, uint32_t bo, __half2 va, __half2 vb,
+                                       const uint32_t (&p)[kNt][2]) {
+        const uint32_t f[4] = {as_u32(__hmul2(kv4_pair<kB>(ae), va)), as_u32(__hmul2(kv4_pair<kB>(ao), va)),
+                               as_u32(__hmul2(kv4_pair<kB>(be), vb)), as_u32(__hmul2(kv4_pair<kB>(bo), vb))};
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) mma_f16(o[n][i], f, p[n][0], p[n][1]);
+    }
+
+    // V scales of tokens at or past `end` (of this block) become zero, and those
+    // that are no number too: the rows that see their token become NaN here,
+    // in this lane's columns, the others must not.
+    __device__ __forceinline__ void guard(Lane<D> &x, int end, int key0, int limit0, int row0, int group, int lane) {
+        const int t = lane & 3;
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int tok = 8 * (i >> 1) + 2 * t + (i & 1);
+            const uint32_t byte = x.vs >> (8 * i) & 0x7fu;
+            if (tok >= end)
+                x.vs &= ~(0xffu << (8 * i));
+            else if (byte == 0x7fu)
+                bad |= 1u << tok;
+        }
+        if (!__any_sync(0xffffffffu, bad != 0)) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((x.vs >> (8 * i) & 0x7fu) == 0x7fu) x.vs &= ~(0xffu << (8 * i));
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);  // the four lanes of one g: the same columns
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+        const float nan = __uint_as_float(0x7fffffffu);
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int lim = limit0 + (row0 + 8 * n + 2 * t + c) / group - row0 / group - key0;
+                const uint32_t sees = lim >= 16 ? 0xffffu : lim <= 0 ? 0u : (1u << lim) - 1;
+                if (bad & sees)
+#pragma unroll
+                    for (int i = 0; i < kK; ++i) o[n][i][c] = o[n][i][c + 2] = nan;
+            }
+        }
+    }
+};
+
+// Everything a warp needs of its ring.
+template <int D, int kStg>
+struct Ring {
+    uint32_t buf, bar;  // shared addresses
+    uint32_t at;        // blocks taken so far
+    uint32_t issued;    // copies started so far
+
+    __device__ __forceinline__ void start(const uint8_t *src, int lane) {
+        const uint32_t st = issued % kStg;
+        if (lane == 0) {
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar + 8 * st), "r"(Kv4Tile<D>::kBytes) : "memory");
+            bulk_copy(buf + st * Kv4Tile<D>::kBytes, src, Kv4Tile<D>::kBytes, bar + 8 * st);
+        }
+        ++issued;
+    }
+};
+
+struct Where {
+    int r, i, h;          // request, tile, kv head
+    Kv4Request q;
+    long long start;      // the item's first position
+};
+
+template <int D, int kMaxNt>
+struct Kernel {
+    static constexpr int kStg = kStages<D, kMaxNt>;
+    static constexpr int kW = kWarps<kMaxNt>;
+    static constexpr int kRows = 8 * kMaxNt;
+    static constexpr int kMinShare = 8 * 16 * 4;  // eight blocks of a decode token
+    static constexpr size_t kSmem = (size_t)kW * kStg * Kv4Tile<D>::kBytes;
+    static constexpr size_t kPart = (size_t)kRows * (D + 2);  // floats of a partial: O rows, then (m, l) of each
+
+    // Blocks [b0, b1) of an item; false: a wait gave up.
+    template <int kNt>
+    static __device__ bool run(const Kv4Args &a, Ring<D, kStg> &ring, const Where &w, const Kv4Tiling &tl, int b0, int b1,
+                               float *part, Kv4Record *rec, volatile int *abort, int lane) {
+        Item<D, kNt, kStg> it;
+        const int row0 = w.i * kRows, rows = tl.rows;
+        const int32_t *ids = a.table + (long long)w.r * a.max_blocks;
+        const uint8_t *heads = a.pool + (long long)w.h * Kv4Tile<D>::kBytes;
+        const long long block_bytes = (long long)a.num_kv_heads * Kv4Tile<D>::kBytes;
+        int bits = 0;
+        // ids are looked up 32 at a time, the next 32 ahead
+        int have = b0 + lane < b1 ? __ldg(ids + b0 + lane) : 0;
+        int next = b0 + 32 + lane < b1 ? __ldg(ids + b0 + 32 + lane) : 0;
+        int base = b0;  // of `have`
+        int put = b0;   // next block to copy
+        auto start = [&]() {
+            if (put - base == 32) {
+                base += 32;
+                have = next;
+                next = base + 32 + lane < b1 ? __ldg(ids + base + 32 + lane) : 0;
+            }
+            int id = __shfl_sync(0xffffffffu, have, put - base);
+            if (id < 0 || id >= a.num_blocks) {
+                bits = PKV_DEV_BAD_BLOCK;
+                id = 0;
+            }
+            ring.start(heads + id * block_bytes, lane);
+            ++put;
+        };
+#pragma unroll 1
+        for (int i = 0; i < kStg && put < b1; ++i) start();
+        it.load_q(a, w.q.q0, row0, rows, w.h, lane);
+        const int limit0 = w.q.len - w.q.n + row0 / a.group + 1;  // keys that the first row sees
+        const int plain = limit0 / 16;                            // blocks that every row sees whole
+        const int end = tl.keys;                                  // keys that the last row sees
+        bool ok = true;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            const uint32_t st = ring.at % kStg;
+            if (!warp_wait(ring.bar + 8 * st, ring.at / kStg & 1, abort)) {
+                ok = false;
+                break;
+            }
+            Lane<D> x;
+            x.load(ring.buf + st * Kv4Tile<D>::kBytes, lane);
+            ++ring.at;
+            __syncwarp();
+            if (put < b1) start();
+            if (b < plain) {
+                it.template block<false>(x, b == b0, 16 * b, 0, 0, 1, lane);
+            } else {
+                it.guard(x, end - 16 * b, 16 * b, limit0, row0, a.group, lane);
+                it.template block<true>(x, b == b0, 16 * b, limit0, row0, a.group, lane);
+            }
+        }
+        if (bits && lane == 0) raise_status(a.status, bits);
+        if (!ok) return false;
+        finish<kNt>(a, it, w, row0, rows, part, rec, lane);
+        return true;
+    }
+
+    template <int kNt>
+    static __device__ void finish(const Kv4Args &a, Item<D, kNt, kStg> &it, const Where &w, int row0, int rows, float *part,
+                                  Kv4Record *rec, int lane) {
+        constexpr int kC = D / 8;  // columns a lane holds
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = c ? it.l[n].y : it.l[n].x;
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const int row = 8 * n + 2 * t + c;
+                if (row >= rows) continue;
+                if (part) {
+                    float4 *to = reinterpret_cast<float4 *>(part + row * D + kC * g);
+#pragma unroll
+                    for (int i = 0; i < kC / 4; ++i)
+                        to[i] = make_float4(it.o[n][2 * i][c], it.o[n][2 * i][c + 2], it.o[n][2 * i + 1][c], it.o[n][2 * i + 1][c + 2]);
+                    if (g == 0) {
+                        reinterpret_cast<float2 *>(part + kRows * D)[row] = make_float2(c ? it.m[n].y : it.m[n].x, l);
+                        if (rec) rec->mul[row] = c ? it.mul[n].y : it.mul[n].x;
+                    }
+                } else {
+                    const float f = a.v_scale / l;
+                    const int rr = row0 + row, tok = rr / a.group;
+                    uint4 *to = reinterpret_cast<uint4 *>(
+                        a.out + ((long long)(w.q.q0 + tok) * a.num_kv_heads * a.group + w.h * a.group + rr - tok * a.group) * D + kC * g);
+#pragma unroll
+                    for (int i = 0; i < kC / 8; ++i)
+                        to[i] = make_uint4(pack_bf16x2(it.o[n][4 * i][c] * f, it.o[n][4 * i][c + 2] * f),
+                                           pack_bf16x2(it.o[n][4 * i + 1][c] * f, it.o[n][4 * i + 1][c + 2] * f),
+                                           pack_bf16x2(it.o[n][4 * i + 2][c] * f, it.o[n][4 * i + 2][c + 2] * f),
+                                           pack_bf16x2(it.o[n][4 * i + 3][c] * f, it.o[n][4 * i + 3][c + 2] * f));
+                }
+            }
+        }
+    }
+};
+
+// Request r's description, and the status bits of one that is skipped.
+__device__ __forceinline__ Kv4Request request_of(const Kv4Args &a, int r, int rows, int *bits) {
+    const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), len = __ldg(a.lens + r);
+    int n = q1 - q0;
+    if (q0 < 0 || n < 0 || q1 > a.num_tokens) {
+        *bits |= PKV_DEV_BAD_QSL;
+        n = 0;
+    } else if (n > 0 && (len < n || len > (long long)a.max_blocks * PKV_BLOCK_SIZE)) {
+        *bits |= PKV_DEV_BAD_LEN;
+        n = 0;
+    }
+    return kv4_request(q0, n, len, a.group, rows);
+}
+
+template <int D, int kMaxNt>
+__global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(const Kv4Args a) {
+    using K = Kernel<D, kMaxNt>;
+    constexpr int kThreads = 32 * K::kW;
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    __shared__ __align__(8) uint64_t s_bar[K::kW * K::kStg];
+    __shared__ long long s_sum[kThreads];
+    __shared__ long long s_warp[K::kW];
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < K::kW * K::kStg; i += kThreads) mbar_init(s_bar + i, 1);
+    if (tid == 0) s_abort = 0;
+    mbar_fence_init();
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // Every CTA adds up the costs of all requests.
+    int bits = 0;
+    if (blockIdx.x == 0 && tid == 0 && (a.qsl[0] != 0 || a.qsl[a.num_reqs] != a.num_tokens)) bits |= PKV_DEV_BAD_QSL;
+    auto scan = [&](int r0, long long *total) {  // inclusive sums of requests r0 .. r0 + kThreads - 1 to s_sum
+        const int r = r0 + tid;
+        long long v = 0;
+        if (r < a.num_reqs) {
+            const Kv4Request q = request_of(a, r, K::kRows, &bits);
+            v = kv4_cost(q, a.num_kv_heads, q.tiles);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += o;
+        }
+        if (lane == 31) s_warp[warp] = v;
+        __syncthreads();
+        long long before = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < K::kW; ++i) {
+            if (i < warp) before += s_warp[i];
+            all += s_warp[i];
+        }
+        s_sum[tid] = v + before;
+        *total = all;
+        __syncthreads();
+    };
+    long long total = 0;
+    if (a.num_reqs <= kThreads) {
+        scan(0, &total);
+    } else {
+        for (int r0 = 0; r0 < a.num_reqs; r0 += kThreads) {
+            long long part;
+            scan(r0, &part);
+            total += part;
+        }
+    }
+    if (blockIdx.x == 0 && bits) raise_status(a.status, bits);
+
+    const Kv4Shares sh = kv4_shares(total, (int)gridDim.x * K::kW, K::kMinShare);
+    const int share = warp * (int)gridDim.x + (int)blockIdx.x;  // neighbouring shares on different SMs
+    long long from = 0, to = 0;
+    if (share < sh.count) {
+        from = sh.begin(share);
+        to = sh.begin(share + 1);
+    }
+    // the request that position `from` lies in, and its first position
+    int r = -1;
+    long long first = 0;
+    {
+        long long base = 0;
+        for (int r0 = 0; r0 < a.num_reqs; r0 += kThreads) {
+            long long all = total;
+            if (a.num_reqs > kThreads) scan(r0, &all);
+            if (r < 0 && from < to && from < base + all) {
+                int lo = 0, hi = kThreads - 1;  // the first with base + s_sum > from
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (base + s_sum[mid] > from) hi = mid; else lo = mid + 1;
+                }
+                r = r0 + lo;
+                first = base + (lo ? s_sum[lo - 1] : 0);
+            }
+            base += all;
+            if (a.num_reqs > kThreads) __syncthreads();
+        }
+    }
+    Kv4Record *rec = a.records + share;
+    int parts = 0;
+    if (r >= 0) {
+        int none = 0;
+        Where w;
+        w.r = r;
+        w.q = request_of(a, r, K::kRows, &none);
+        kv4_locate(w.q, a.num_kv_heads, from - first, &w.i, &w.h, &w.start);
+        w.start += first;
+        Ring<D, K::kStg> ring{smem_u32(s_ring) + (uint32_t)(warp * K::kStg * Kv4Tile<D>::kBytes), smem_u32(s_bar + warp * K::kStg), 0, 0};
+        while (true) {
+            const Kv4Tiling tl = kv4_tile(w.q, w.i, a.group, K::kRows);
+            const long long cost = kv4_item_cost(w.q, w.i), stop = w.start + cost;
+            const int b0 = from > w.start ? kv4_block_at(from - w.start, cost, tl.blocks) : 0;
+            const int b1 = to < stop ? kv4_block_at(to - w.start, cost, tl.blocks) : tl.blocks;
+            const bool begun = w.start < from, cut = stop > to;
+            float *part = begun || cut ? a.parts + ((size_t)2 * share + (begun ? 0 : 1)) * K::kPart : nullptr;
+            if (!begun && cut) {
+                parts = sh.index(stop - 1) - share + 1;
+                if (lane == 0) {
+                    rec->rows = tl.rows;
+                    rec->token = w.q.q0 * a.group + w.i * K::kRows;  // rows counted from the batch's first
+                    rec->head = w.h;
+                }
+            }
+            bool ok;
+            Kv4Record *mine = begun ? nullptr : rec;
+            if (kMaxNt == 1 || tl.rows <= 8) ok = K::template run<1>(a, ring, w, tl, b0, b1, part, mine, &s_abort, lane);
+            else if (kMaxNt == 2 || tl.rows <= 16) ok = K::template run<kMaxNt >= 2 ? 2 : 1>(a, ring, w, tl, b0, b1, part, mine, &s_abort, lane);
+            else ok = K::template run<kMaxNt>(a, ring, w, tl, b0, b1, part, mine, &s_abort, lane);
+            if (!ok) {
+                // nothing may still be on its way into this SM's memory when the CTA ends
+                int never = 0;
+                for (; ring.at < ring.issued; ++ring.at)
+                    if (!warp_wait(ring.bar + 8 * (ring.at % K::kStg), ring.at / K::kStg & 1, &never)) break;
+                if (lane == 0) raise_status(a.status, PKV_DEV_TIMEOUT);
+                parts = 0;
+                break;
+            }
+            if (stop >= to) break;
+            w.start = stop;
+            if (++w.h == a.num_kv_heads) {
+                w.h = 0;
+                if (++w.i == w.q.tiles) {
+                    w.i = 0;
+                    do {
+                        w.q = request_of(a, ++w.r, K::kRows, &none);
+                    } while (w.q.tiles == 0);  // one follows: positions up to `to` belong to requests
+                }
+            }
+        }
+    }
+    if (lane == 0) rec->parts = parts;
+}
+
+// Joins the partials of the items that lie in several shares: a warp per row.
+template <int D, int kRows>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4Args a, int shares) {
+    constexpr int kF = D / 32;  // columns a lane holds
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int k = blockIdx.x; k < shares; k += gridDim.x) {
+        const Kv4Record *rec = a.records + k;
+        const int n = rec->parts, rows = rec->rows;
+        if (n < 2) continue;
+        for (int row = warp; row < rows; row += 8) {
+            const float mul = rec->mul[row];
+            // the first share's partial is its second one, the others' their first
+            auto part = [&](int i) { return a.parts + ((size_t)2 * (k + i) + (i == 0)) * kRows * (D + 2); };
+            float top = -INFINITY;
+            for (int i = lane; i < n; i += 32) top = fmaxf(top, reinterpret_cast<const float2 *>(part(i) + kRows * D)[row].x);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            float sum = 0.0f, acc[kF];
+#pragma unroll
+            for (int c = 0; c < kF; ++c) acc[c] = 0.0f;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                float f = 0.0f;
+                if (i0 + lane < n) {
+                    const float2 ml = reinterpret_cast<const float2 *>(part(i0 + lane) + kRows * D)[row];
+                    f = ml.x == top ? 1.0f : ml.x == -INFINITY ? 0.0f : fast_exp2((ml.x - top) * mul);
+                    sum += f * ml.y;
+                }
+#pragma unroll 8
+                for (int i = 0; i < min(32, n - i0); ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i);
+                    const float *o = part(i0 + i) + row * D + kF * lane;
+#pragma unroll
+                    for (int c = 0; c < kF; ++c) acc[c] += fi * o[c];
+                }
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const float f = a.v_scale / sum;
+            const int rr = rec->token + row, tok = rr / a.group;
+            __nv_bfloat16 *to = a.out + ((long long)tok * a.num_kv_heads * a.group + rec->head * a.group + rr - tok * a.group) * D + kF * lane;
+#pragma unroll
+            for (int c = 0; c < kF; c += 2) *reinterpret_cast<uint32_t *>(to + c) = pack_bf16x2(acc[c] * f, acc[c + 1] * f);
+        }
+    }
+}
+
+constexpr int kMaxRowsPerSm = 2 * 8 * 32;  // partial rows of one SM's warps: 12 x 2 x 16 at most otherwise
+static_assert(2 * kWarps<4> * 32 <= kMaxRowsPerSm && 2 * kWarps<2> * 16 <= kMaxRowsPerSm && 2 * kWarps<1> * 8 <= kMaxRowsPerSm, "");
+constexpr int kMaxWarps = 12;
+
+size_t records_bytes(int sms) { return (size_t)sms * kMaxWarps * sizeof(Kv4Record); }
+size_t workspace_bytes(int sms, int head_size) {
+    return records_bytes(sms) + (size_t)sms * kMaxRowsPerSm * (head_size + 2) * sizeof(float);
+}
+
+std::mutex g_mu;
+bool g_ready[64][2][3];
+
+template <int D, int kMaxNt>
+int launch(const Kv4Args &a, int sms, int which, cudaStream_t st) {
+    using K = Kernel<D, kMaxNt>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_E_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        if (!g_ready[dev][D == 128][which]) {
+            if (cudaFuncSetAttribute(kv4_attention_kernel<D, kMaxNt>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)K::kSmem) != cudaSuccess)
+                return PKV_E_CUDA;
+            g_ready[dev][D == 128][which] = true;
+        }
+    }
+    if (launch_pdl(kv4_attention_kernel<D, kMaxNt>, dim3(sms), dim3(32 * K::kW), K::kSmem, st, a) != cudaSuccess)
+        return PKV_E_CUDA;
+    const int shares = sms * K::kW;
+    if (launch_pdl(kv4_join_kernel<D, K::kRows>, dim3(std::min(shares, 4 * sms)), dim3(256), 0, st, a, shares) != cudaSuccess)
+        return PKV_E_CUDA;
+    return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" PKV_API int paged_kv4_attention_workspace_bytes(const pkv_cache_desc *desc, size_t *bytes) {
+    if (!desc || !bytes) return PKV_E_NULL;
+    const int rc = check_cache_desc(*desc, /*attention=*/true);
+    if (rc) return rc;
+    int sms = 0;
+    const int rs = device_sms(&sms);
+    if (rs) return rs;
+    *bytes = workspace_bytes(sms, desc->head_size);
+    return PKV_OK;
+}
+
+extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int32_t num_tokens, int32_t num_q_heads,
+                                           const void *kv4_cache, const pkv_cache_desc *desc,
+                                           const int32_t *block_table, int32_t num_reqs, int32_t max_blocks_per_req,
+                                           const int32_t *seq_lens, const int32_t *query_start_loc,
+                                           int32_t max_query_len, float scale, float k_scale, float v_scale, void *out,
+                                           void *workspace, size_t workspace_size, int32_t *status, void *stream) {
+    if (!desc) return PKV_E_NULL;
+    const int rc = check_cache_desc(*desc, /*attention=*/true);
+    if (rc) return rc;
+    if (num_tokens < 0 || num_reqs < 0 || max_blocks_per_req < 0 || max_query_len < 0) return PKV_E_DIMS;
+    if (max_blocks_per_req > INT32_MAX / PKV_BLOCK_SIZE) return PKV_E_DIMS;
+    if (num_q_heads <= 0 || num_q_heads % desc->num_kv_heads) return PKV_E_GQA;
+    const int group = num_q_heads / desc->num_kv_heads;
+    if (group > 128 || (long long)num_tokens * group > INT32_MAX - 1024) return PKV_E_DIMS;
+    if (!(scale > 0.0f && scale <= 1e30f) || !kv4_scale_ok(k_scale) || !kv4_scale_ok(v_scale)) return PKV_E_DIMS;
+    if (q_stride % 8 || q_stride < 0 || (num_tokens > 1 && q_stride < (int64_t)num_q_heads * desc->head_size))
+        return PKV_E_DIMS;
+    if (num_tokens == 0 || num_reqs == 0) return PKV_OK;
+    if (!q || !kv4_cache || !block_table || !seq_lens || !query_start_loc || !out || !workspace) return PKV_E_NULL;
+    if (!aligned(q, 16) || !aligned(kv4_cache, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(status, 4))
+        return PKV_E_ALIGN;
+    int sms = 0;
+    const int rs = device_sms(&sms);
+    if (rs) return rs;
+    if (workspace_size < workspace_bytes(sms, desc->head_size)) return PKV_E_WORKSPACE;
+    const float scale_log2 = scale * 1.4426950408889634f * k_scale;
+    if (!std::isfinite(scale_log2)) return PKV_E_DIMS;
+    const Kv4Args a{static_cast<const __nv_bfloat16 *>(q), q_stride, static_cast<const uint8_t *>(kv4_cache), block_table,
+                    seq_lens, query_start_loc, num_tokens, desc->num_kv_heads, group, num_reqs, max_blocks_per_req,
+                    desc->num_blocks, scale_log2, v_scale, static_cast<__nv_bfloat16 *>(out),
+                    static_cast<Kv4Record *>(workspace),
+                    reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + records_bytes(sms)), status};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // rows that the longest request has of a kv head
+    const long long rows = (long long)(max_query_len ? max_query_len : num_tokens) * group;
+    if (desc->head_size == 128)
+        return rows <= 8 ? launch<128, 1>(a, sms, 0, st) : rows <= 16 ? launch<128, 2>(a, sms, 1, st) : launch<128, 4>(a, sms, 2, st);
+    return rows <= 8 ? launch<64, 1>(a, sms, 0, st) : rows <= 16 ? launch<64, 2>(a, sms, 1, st) : launch<64, 4>(a, sms, 2, st);
+}

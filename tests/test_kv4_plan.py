@@ -1,0 +1,128 @@
+"""How attention over the 4-bit pool cuts a batch into shares (kv4_plan.h): on
+the host, every block of every item in exactly one share, and every cut item's
+partials counted."""
+import os
+import random
+import subprocess
+
+import pytest
+
+REPO = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+PROGRAM = r"""
+#include <cstdio>
+#include <vector>
+#include "kv4_plan.h"
+using namespace pkv;
+// in: reqs group heads rows most least, then (n, len) of each. Walks every share as a warp of the kernel does.
+int main() {
+    int R, group, heads, rows, most, least;
+    while (scanf("%d %d %d %d %d %d", &R, &group, &heads, &rows, &most, &least) == 6) {
+        std::vector<Kv4Request> q(R);
+        std::vector<long long> first(R + 1, 0);
+        int q0 = 0;
+        for (int r = 0; r < R; ++r) {
+            int n, len;
+            if (scanf("%d %d", &n, &len) != 2) return 1;
+            q[r] = kv4_request(q0, n, len, group, rows);
+            q0 += n;
+            first[r + 1] = first[r] + kv4_cost(q[r], heads, q[r].tiles);
+        }
+        const long long total = first[R];
+        const Kv4Shares sh = kv4_shares(total, most, least);
+        // next block expected of each item, and partials seen / announced
+        std::vector<std::vector<int>> next(R), seen(R), told(R);
+        for (int r = 0; r < R; ++r) next[r].assign(q[r].tiles * heads, 0), seen[r].assign(q[r].tiles * heads, 0), told[r].assign(q[r].tiles * heads, -1);
+        for (int k = 0; k < sh.count; ++k) {
+            const long long from = sh.begin(k), to = sh.begin(k + 1);
+            if (!(from < to)) { printf("empty share %d\n", k); return 1; }
+            int r = 0;
+            while (first[r + 1] <= from) ++r;
+            int i, h, slots = 0;
+            long long start;
+            kv4_locate(q[r], heads, from - first[r], &i, &h, &start);
+            start += first[r];
+            while (true) {
+                const Kv4Tiling tl = kv4_tile(q[r], i, group, rows);
+                const long long cost = kv4_item_cost(q[r], i), stop = start + cost;
+                if (!(start <= from || start < to) || stop <= from || tl.rows < 1 || tl.keys < 1 || tl.keys > q[r].len) { printf("bad item\n"); return 1; }
+                const int b0 = from > start ? kv4_block_at(from - start, cost, tl.blocks) : 0;
+                const int b1 = to < stop ? kv4_block_at(to - start, cost, tl.blocks) : tl.blocks;
+                int &n = next[r][i * heads + h];
+                if (b0 != n || b1 < b0 || b1 > tl.blocks) { printf("blocks %d..%d, %d next\n", b0, b1, n); return 1; }
+                n = b1;
+                const bool begun = start < from, cut = stop > to;
+                if (begun || cut) {
+                    seen[r][i * heads + h]++;
+                    if (begun && slots) { printf("a continued item after another\n"); return 1; }
+                }
+                ++slots;
+                if (!begun && cut) told[r][i * heads + h] = sh.index(stop - 1) - k + 1;
+                if (stop >= to) break;
+                start = stop;
+                if (++h == heads) {
+                    h = 0;
+                    if (++i == q[r].tiles) {
+                        i = 0;
+                        do ++r; while (q[r].tiles == 0);
+                    }
+                }
+            }
+        }
+        for (int r = 0; r < R; ++r)
+            for (int i = 0; i < q[r].tiles; ++i)
+                for (int h = 0; h < heads; ++h) {
+                    const int k = i * heads + h, blocks = kv4_tile(q[r], i, group, rows).blocks;
+                    if (next[r][k] != blocks) { printf("r %d i %d h %d: %d of %d blocks\n", r, i, h, next[r][k], blocks); return 1; }
+                    if (seen[r][k] != (told[r][k] < 0 ? 0 : told[r][k])) { printf("partials %d, told %d\n", seen[r][k], told[r][k]); return 1; }
+                }
+        printf("ok %d\n", sh.count);
+    }
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def program(tmp_path_factory):
+    d = tmp_path_factory.mktemp("kv4_plan")
+    (d / "plan.cpp").write_text(PROGRAM)
+    exe = str(d / "plan")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-I",
+                    os.path.join(REPO, "paged_attention_kv_gb300", "csrc"), str(d / "plan.cpp"), "-o", exe], check=True)
+    return exe
+
+
+def walk(program, batches):
+    text = "\n".join(" ".join(map(str, [len(reqs), *head] + [x for r in reqs for x in r])) for head, reqs in batches)
+    res = subprocess.run([program], input=text, capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout[-500:]
+    lines = res.stdout.split("\n")[:-1]
+    assert len(lines) == len(batches) and all(x.startswith("ok") for x in lines)
+    return [int(x.split()[1]) for x in lines]
+
+
+def test_named_batches(program):
+    counts = walk(program, [
+        ((8, 4, 8, 1824, 512), [(1, 17), (1, 40)]),
+        ((4, 8, 8, 1824, 512), [(1, 1)]),
+        ((4, 8, 32, 1216, 512), [(0, 0), (512, 512), (0, 5), (1, 2_000_000), (300, 301), (0, 0)]),
+        ((128, 1, 32, 1216, 512), [(3, 90)] * 40),
+        ((3, 5, 8, 1824, 512), [(7, 1000)] * 9),
+        ((4, 8, 8, 1824, 512), [(1, 3000)] * 256),
+        ((4, 8, 8, 1824, 512), []), ((4, 8, 8, 1824, 512), [(0, 0)] * 7)])
+    assert counts[-2:] == [0, 0] and counts[5] == 1824
+
+
+def test_random_batches(program):
+    rng = random.Random(4)
+    batches = []
+    for _ in range(400):
+        rows = rng.choice((8, 16, 32))
+        reqs = []
+        for _ in range(rng.randint(1, 40)):
+            n = rng.choice((0, 1, 1, rng.randint(1, 9), rng.randint(1, 400)))
+            reqs.append((n, n + rng.choice((0, 0, rng.randint(0, 50), rng.randint(0, 5000)))))
+        batches.append(((rng.choice((1, 2, 3, 4, 5, 8, 16, 33, 128)), rng.randint(1, 8), rows, rng.choice((1, 7, 1216, 1824)),
+                         rng.choice((1, 64, 512, 4096))), reqs))
+    walk(program, batches)
