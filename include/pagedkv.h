@@ -93,6 +93,7 @@ extern "C" {
 #define PKV_DEV_NO_BLOCKS 0x80   /* a request needs more blocks than free_blocks has left */
 #define PKV_DEV_BAD_PAGES 0x100  /* a row's parent is none of the rows, a block was given up more often than held, or the
                                     free list's cursor does not fit it */
+#define PKV_DEV_BAD_WORKSPACE 0x200  /* paged_kv4_attention: the workspace was not prepared */
 
 typedef struct {
     int32_t num_blocks;    /* blocks in the pool */
@@ -511,6 +512,15 @@ int paged_kv4_read(const void *kv4_cache, const pkv_cache_desc *desc, const int3
 int paged_kv4_attention_workspace_bytes(const pkv_cache_desc *desc, size_t *bytes);
 
 /*
+ * Prepares a workspace of paged_kv4_attention: once before its first call, on
+ * that call's stream or ordered before it. Every call leaves the workspace as
+ * it has to be for the next; after PKV_DEV_TIMEOUT, or when anything else wrote
+ * to it, prepare it again. (A part of the output needs the last CTA that holds a
+ * piece of it to know that it is the last: those counters are here.)
+ */
+int paged_kv4_attention_init(const pkv_cache_desc *desc, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * paged_attention over the 4-bit pool: causal attention with grouped heads of a
  * ragged batch, K and V read through the block tables. Decode tokens and chunks
  * mix freely.
@@ -525,8 +535,10 @@ int paged_kv4_attention_workspace_bytes(const pkv_cache_desc *desc, size_t *byte
  *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the
  *             inputs. Rows outside every request, and rows of requests with bad
  *             metadata, are left as they were.
- *  workspace  device scratch, 16-byte aligned, of any contents; calls that may
- *             run at the same time need one each
+ *  workspace  device scratch, 16-byte aligned, prepared by
+ *             paged_kv4_attention_init (else PKV_DEV_BAD_WORKSPACE, and rows whose
+ *             context several CTAs share may be left unwritten or wrong); calls that
+ *             may run at the same time need one each
  *  status     optional device int32, PKV_DEV_* bits OR-ed in: a request whose
  *             bounds descend or leave [0, num_tokens] (PKV_DEV_BAD_QSL) or whose
  *             length is below its new tokens or past its table (PKV_DEV_BAD_LEN)

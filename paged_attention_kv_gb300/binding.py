@@ -40,6 +40,7 @@ PKV_DEV_OVERFLOW = 0x20
 PKV_DEV_BAD_POS = 0x40
 PKV_DEV_NO_BLOCKS = 0x80
 PKV_DEV_BAD_PAGES = 0x100
+PKV_DEV_BAD_WORKSPACE = 0x200
 
 EXPORTED = ("pkv_kv_cache_bytes", "paged_slot_mapping", "paged_kv_write", "paged_kv_write_slots",
             "paged_kv_gather_blocks",
@@ -47,7 +48,7 @@ EXPORTED = ("pkv_kv_cache_bytes", "paged_slot_mapping", "paged_kv_write", "paged
             "paged_attention_min_workspace_bytes", "paged_attention", "paged_attention_timed",
             "paged_attention_bounded", "paged_attention_static", "paged_build_tables", "paged_qk_norm_rope",
             "pkv_prompt_attention", "paged_kv4_cache_bytes", "paged_kv4_write", "paged_kv4_read",
-            "paged_kv4_attention_workspace_bytes", "paged_kv4_attention", "paged_fork_tables", "paged_copy_blocks",
+            "paged_kv4_attention_workspace_bytes", "paged_kv4_attention_init", "paged_kv4_attention", "paged_fork_tables", "paged_copy_blocks",
             "pkv_pipeline_create", "pkv_pipeline_next",
             "pkv_pipeline_submit", "pkv_pipeline_sync", "pkv_pipeline_destroy", "pkv_read_status", "pkv_selftest_bounded_wait", "pkv_status_string")
 
@@ -125,6 +126,7 @@ def _load():
     lib.paged_kv4_write.argtypes = [vp, i64, vp, i64, vp, i32, vp, desc_p, f32, f32, vp, vp]
     lib.paged_kv4_read.argtypes = [vp, desc_p, vp, i32, f32, f32, vp, vp, vp, vp]
     lib.paged_kv4_attention_workspace_bytes.argtypes = [desc_p, ctypes.POINTER(sz)]
+    lib.paged_kv4_attention_init.argtypes = [desc_p, vp, sz, vp]
     lib.paged_kv4_attention.argtypes = [vp, i64, i32, i32, vp, desc_p, vp, i32, i32, vp, vp, i32, f32, f32, f32, vp, vp,
                                         sz, vp, vp]
     lib.paged_fork_tables.argtypes = [vp, i32, vp, i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
@@ -691,13 +693,17 @@ def paged_kv4_read(kv4_cache, slot_mapping, *, k_scale: float = 1.0, v_scale: fl
                                 status=status)(stream)
 
 
-def alloc_kv4_workspace(kv4_cache: torch.Tensor) -> torch.Tensor:
-    """Workspace of ``paged_kv4_attention``, for any batch over this pool."""
-    out = ctypes.c_size_t(0)
-    with torch.cuda.device(kv4_cache.device):
-        _check(LIB.paged_kv4_attention_workspace_bytes(ctypes.byref(kv4_desc(kv4_cache)), ctypes.byref(out)),
+def alloc_kv4_workspace(kv4_cache: torch.Tensor, stream=None) -> torch.Tensor:
+    """Workspace of ``paged_kv4_attention`` for any batch over this pool,
+    prepared on ``stream``. Calls that may run at the same time need one each."""
+    out, desc = ctypes.c_size_t(0), kv4_desc(kv4_cache)
+    with torch.cuda.device(kv4_cache.device), _memory_of(stream, kv4_cache):
+        _check(LIB.paged_kv4_attention_workspace_bytes(ctypes.byref(desc), ctypes.byref(out)),
                "paged_kv4_attention_workspace_bytes")
-    return torch.empty((out.value + 7) // 8, dtype=torch.int64, device=kv4_cache.device)
+        ws = torch.empty((out.value + 7) // 8, dtype=torch.int64, device=kv4_cache.device)
+        _check(LIB.paged_kv4_attention_init(ctypes.byref(desc), _ptr(ws), ws.numel() * 8, _stream(None)),
+               "paged_kv4_attention_init")
+    return ws
 
 
 def prepare_kv4_attention(q, kv4_cache, block_table, seq_lens, query_start_loc, scale: float, *, k_scale: float = 1.0,
@@ -741,8 +747,9 @@ def paged_kv4_attention(q, kv4_cache, block_table, seq_lens, query_start_loc, sc
                         v_scale: float = 1.0, max_query_len: int = 0, out=None, workspace=None, status=None,
                         stream=None) -> torch.Tensor:
     """``paged_attention`` over the 4-bit pool. q may be a slice of a
-    projection's rows. ``workspace`` (``alloc_kv4_workspace``) may hold anything;
-    calls that may run at the same time need one each."""
+    projection's rows. ``workspace``: from ``alloc_kv4_workspace``, kept from
+    call to call; calls that may run at the same time need one each (without it
+    every call makes its own)."""
     with _memory_of(stream, q):
         return prepare_kv4_attention(q, kv4_cache, block_table, seq_lens, query_start_loc, scale, k_scale=k_scale,
                                      v_scale=v_scale, max_query_len=max_query_len, out=out, workspace=workspace,

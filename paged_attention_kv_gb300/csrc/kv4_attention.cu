@@ -10,9 +10,13 @@
 // m16n8k16, so that the 4 to 8 rows of a decode token's head group fill the N
 // side and K and V are made once for up to four such groups of rows. An item is
 // (request, tile of 8 kMaxNt rows, kv head) and its cost a number of keys; all
-// items in a row are cut into equal shares, one a warp (kv4_plan.h). An item that
-// lies in several shares leaves one partial (m, l, O) a share, and the second
-// kernel joins them, in order, so that the result does not depend on timing.
+// items in a row are cut into equal shares, one a warp (kv4_plan.h), neighbouring
+// shares in one CTA. An item that lies in several shares leaves one partial
+// (m, l, O) a share, in the layout of the fragments: the first of its warps in a
+// CTA joins those of the CTA, through shared memory, and where it lies in several
+// CTAs, the last of them to arrive joins theirs, always in order, so that the
+// result does not depend on timing. Every CTA adds the requests' costs up itself:
+// one launch.
 //
 // Softmax: scores stay unscaled; a row's reference m is the largest score of its
 // first block, and moves only when a score passes it by 2^10 (p then still fits
@@ -42,13 +46,11 @@ namespace {
 template <int kMaxNt>
 constexpr int kWarps = kMaxNt == 4 ? 8 : 12;
 template <int D, int kMaxNt>
-constexpr int kStages = D == 64 ? 12 : 7;
+constexpr int kStages = (D == 64 ? 2 : 1) * (kMaxNt == 1 ? 6 : 4);
 
-struct __align__(16) Kv4Record {
-    int32_t parts;  // shares that the item lies in; 0: no item starts in this share and ends in another
-    int32_t rows, token, head;  // of the tile: rows, first row's token and head within its group, as below
-    float mul[32];  // each row's factor from scores to exponents of 2
-};
+// Counters of arrivals between calls, so that a workspace that nobody prepared is
+// noticed (every byte 0x5a).
+constexpr int kNobody = 0x5a5a5a5a;
 
 struct Kv4Args {
     const __nv_bfloat16 *q;
@@ -58,8 +60,8 @@ struct Kv4Args {
     int num_tokens, num_kv_heads, group, num_reqs, max_blocks, num_blocks;
     float scale_log2, v_scale;
     __nv_bfloat16 *out;
-    Kv4Record *records;
-    float *parts;
+    int *arrived;   // the workspace: of each CTA, the arrivals for the item that begins there and ends in another,
+    float4 *parts;  // and two partials: of the item that began before it, and of that one
     int32_t *status;
 };
 
@@ -299,6 +301,57 @@ struct Item {
         for (int n = 0; n < kNt; ++n) mma_f16(o[n][i], f, p[n][0], p[n][1]);
     }
 
+    // Partials, 32 lanes side by side: O, (m, l) of each 8 rows, and kMul: mul.
+    static constexpr int kVecs = kNt * (kK + 1);
+    template <bool kMul>
+    __device__ __forceinline__ void store(float4 *to, int lane) const {
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+#pragma unroll
+            for (int i = 0; i < kK; ++i) to[(n * kK + i) * 32 + lane] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+            to[(kNt * kK + n) * 32 + lane] = make_float4(m[n].x, m[n].y, l[n].x, l[n].y);
+            if (kMul) to[(kVecs + n) * 32 + lane] = make_float4(mul[n].x, mul[n].y, 0.0f, 0.0f);
+        }
+    }
+    // Joins a partial to this one; kGlobal: written by another SM, with mul,
+    // which `first` takes over with everything else.
+    static __device__ __forceinline__ void factors(float m, float n, float mul, float *to, float *f, float *g) {
+        *to = fmaxf(m, n);
+        *f = m == *to ? 1.0f : m == -INFINITY ? 0.0f : fast_exp2((m - *to) * mul);
+        *g = n == *to ? 1.0f : n == -INFINITY ? 0.0f : fast_exp2((n - *to) * mul);
+    }
+    template <bool kGlobal>
+    __device__ __forceinline__ void join(const float4 *from, bool first, int lane) {
+        auto get = [&](int i) { return kGlobal ? __ldcg(from + i * 32 + lane) : from[i * 32 + lane]; };
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+            float4 v[kK];
+#pragma unroll
+            for (int i = 0; i < kK; ++i) v[i] = get(n * kK + i);
+            const float4 st = get(kNt * kK + n);
+            float fx, fy, gx, gy;
+            if (kGlobal && first) {
+                const float4 x = get(kVecs + n);
+                mul[n] = make_float2(x.x, x.y);
+                m[n] = make_float2(st.x, st.y);
+                l[n] = make_float2(st.z, st.w);
+#pragma unroll
+                for (int i = 0; i < kK; ++i) o[n][i][0] = v[i].x, o[n][i][1] = v[i].y, o[n][i][2] = v[i].z, o[n][i][3] = v[i].w;
+                continue;
+            }
+            factors(m[n].x, st.x, mul[n].x, &m[n].x, &fx, &gx);
+            factors(m[n].y, st.y, mul[n].y, &m[n].y, &fy, &gy);
+            l[n] = make_float2(l[n].x * fx + st.z * gx, l[n].y * fy + st.w * gy);
+#pragma unroll
+            for (int i = 0; i < kK; ++i) {
+                o[n][i][0] = o[n][i][0] * fx + v[i].x * gx;
+                o[n][i][1] = o[n][i][1] * fy + v[i].y * gy;
+                o[n][i][2] = o[n][i][2] * fx + v[i].z * gx;
+                o[n][i][3] = o[n][i][3] * fy + v[i].w * gy;
+            }
+        }
+    }
+
     // V scales of tokens at or past `end` (of this block) become zero, and those
     // that are no number too: the rows that see their token become NaN here,
     // in this lane's columns, the others must not.
@@ -353,9 +406,20 @@ struct Ring {
 };
 
 struct Where {
-    int r, i, h;          // request, tile, kv head
+    int r, i, h;      // request, tile, kv head
     Kv4Request q;
-    long long start;      // the item's first position
+    long long start;  // the item's first position
+};
+
+// What an item's warps have in common, and this warp's place among the CTA's.
+struct Team {
+    int warp, cta, shares;  // shares of this CTA, one a warp
+    int first, last;        // the item's shares
+    bool begun, cut;        // it began in a share before this one, it ends in one behind
+    Kv4Shares sh;
+    uint8_t *area;          // shared memory: a partial of each warp
+    volatile int *abort;
+    bool met;               // this warp has been at the CTA's barrier
 };
 
 template <int D, int kMaxNt>
@@ -364,13 +428,15 @@ struct Kernel {
     static constexpr int kW = kWarps<kMaxNt>;
     static constexpr int kRows = 8 * kMaxNt;
     static constexpr int kMinShare = 8 * 16 * 4;  // eight blocks of a decode token
-    static constexpr size_t kSmem = (size_t)kW * kStg * Kv4Tile<D>::kBytes;
-    static constexpr size_t kPart = (size_t)kRows * (D + 2);  // floats of a partial: O rows, then (m, l) of each
+    static constexpr size_t kRing = (size_t)kW * kStg * Kv4Tile<D>::kBytes;
+    static constexpr int kArea = Item<D, kMaxNt, kStg>::kVecs * 512;    // bytes of a partial in shared memory
+    static constexpr int kPart = (Item<D, kMaxNt, kStg>::kVecs + kMaxNt) * 32;  // float4 of one in the workspace
+    static constexpr size_t kSmem = kRing + (size_t)kW * kArea;
 
     // Blocks [b0, b1) of an item; false: a wait gave up.
     template <int kNt>
     static __device__ bool run(const Kv4Args &a, Ring<D, kStg> &ring, const Where &w, const Kv4Tiling &tl, int b0, int b1,
-                               float *part, Kv4Record *rec, volatile int *abort, int lane) {
+                               Team &team, int lane) {
         Item<D, kNt, kStg> it;
         const int row0 = w.i * kRows, rows = tl.rows;
         const int32_t *ids = a.table + (long long)w.r * a.max_blocks;
@@ -402,14 +468,10 @@ struct Kernel {
         const int limit0 = w.q.len - w.q.n + row0 / a.group + 1;  // keys that the first row sees
         const int plain = limit0 / 16;                            // blocks that every row sees whole
         const int end = tl.keys;                                  // keys that the last row sees
-        bool ok = true;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const uint32_t st = ring.at % kStg;
-            if (!warp_wait(ring.bar + 8 * st, ring.at / kStg & 1, abort)) {
-                ok = false;
-                break;
-            }
+            if (!warp_wait(ring.bar + 8 * st, ring.at / kStg & 1, team.abort)) return false;
             Lane<D> x;
             x.load(ring.buf + st * Kv4Tile<D>::kBytes, lane);
             ++ring.at;
@@ -423,14 +485,50 @@ struct Kernel {
             }
         }
         if (bits && lane == 0) raise_status(a.status, bits);
-        if (!ok) return false;
-        finish<kNt>(a, it, w, row0, rows, part, rec, lane);
+        hand_over<kNt>(a, it, w, row0, rows, team, lane);
         return true;
     }
 
+    // An item's end in this share: its output, or this share's part of it.
     template <int kNt>
-    static __device__ void finish(const Kv4Args &a, Item<D, kNt, kStg> &it, const Where &w, int row0, int rows, float *part,
-                                  Kv4Record *rec, int lane) {
+    static __device__ __forceinline__ void hand_over(const Kv4Args &a, Item<D, kNt, kStg> &it, const Where &w, int row0, int rows,
+                                                     Team &team, int lane) {
+        if (team.begun && team.warp > 0) {  // for the first of its warps in this CTA
+            it.template store<false>(reinterpret_cast<float4 *>(team.area + team.warp * kArea), lane);
+            return;
+        }
+        const int base = team.cta * team.sh.per_cta;
+        if (team.cut) {
+            team.met = true;
+            __syncthreads();
+            if (*team.abort) return;
+            const int upto = min(team.last - base, team.shares - 1);
+            for (int i = team.warp + 1; i <= upto; ++i)
+                it.template join<false>(reinterpret_cast<const float4 *>(team.area + i * kArea), false, lane);
+        }
+        if (team.first < base || team.last >= base + team.shares) {
+            const int c0 = team.first / team.sh.per_cta, n = team.last / team.sh.per_cta - c0 + 1;
+            auto part = [&](int c) { return a.parts + ((size_t)2 * c + (c == c0)) * kPart; };
+            it.template store<true>(part(team.cta), lane);
+            __syncwarp();
+            int seen = 0;
+            if (lane == 0) {
+                __threadfence();
+                seen = atomicAdd(a.arrived + c0, 1) - kNobody;
+                if (seen == n - 1) atomicExch(a.arrived + c0, kNobody);
+                if (seen < 0 || seen >= n) raise_status(a.status, PKV_DEV_BAD_WORKSPACE);
+                __threadfence();
+            }
+            seen = __shfl_sync(0xffffffffu, seen, 0);
+            if (seen != n - 1) return;
+            __syncwarp();  // the other lanes' loads behind lane 0's fence
+            for (int i = 0; i < n; ++i) it.template join<true>(part(c0 + i), i == 0, lane);
+        }
+        output<kNt>(a, it, w, row0, rows, lane);
+    }
+
+    template <int kNt>
+    static __device__ __forceinline__ void output(const Kv4Args &a, Item<D, kNt, kStg> &it, const Where &w, int row0, int rows, int lane) {
         constexpr int kC = D / 8;  // columns a lane holds
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -443,27 +541,16 @@ struct Kernel {
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 const int row = 8 * n + 2 * t + c;
                 if (row >= rows) continue;
-                if (part) {
-                    float4 *to = reinterpret_cast<float4 *>(part + row * D + kC * g);
+                const float f = a.v_scale / l;
+                const int rr = row0 + row, tok = rr / a.group;
+                uint4 *to = reinterpret_cast<uint4 *>(
+                    a.out + ((long long)(w.q.q0 + tok) * a.num_kv_heads * a.group + w.h * a.group + rr - tok * a.group) * D + kC * g);
 #pragma unroll
-                    for (int i = 0; i < kC / 4; ++i)
-                        to[i] = make_float4(it.o[n][2 * i][c], it.o[n][2 * i][c + 2], it.o[n][2 * i + 1][c], it.o[n][2 * i + 1][c + 2]);
-                    if (g == 0) {
-                        reinterpret_cast<float2 *>(part + kRows * D)[row] = make_float2(c ? it.m[n].y : it.m[n].x, l);
-                        if (rec) rec->mul[row] = c ? it.mul[n].y : it.mul[n].x;
-                    }
-                } else {
-                    const float f = a.v_scale / l;
-                    const int rr = row0 + row, tok = rr / a.group;
-                    uint4 *to = reinterpret_cast<uint4 *>(
-                        a.out + ((long long)(w.q.q0 + tok) * a.num_kv_heads * a.group + w.h * a.group + rr - tok * a.group) * D + kC * g);
-#pragma unroll
-                    for (int i = 0; i < kC / 8; ++i)
-                        to[i] = make_uint4(pack_bf16x2(it.o[n][4 * i][c] * f, it.o[n][4 * i][c + 2] * f),
-                                           pack_bf16x2(it.o[n][4 * i + 1][c] * f, it.o[n][4 * i + 1][c + 2] * f),
-                                           pack_bf16x2(it.o[n][4 * i + 2][c] * f, it.o[n][4 * i + 2][c + 2] * f),
-                                           pack_bf16x2(it.o[n][4 * i + 3][c] * f, it.o[n][4 * i + 3][c + 2] * f));
-                }
+                for (int i = 0; i < kC / 8; ++i)
+                    to[i] = make_uint4(pack_bf16x2(it.o[n][4 * i][c] * f, it.o[n][4 * i][c + 2] * f),
+                                       pack_bf16x2(it.o[n][4 * i + 1][c] * f, it.o[n][4 * i + 1][c + 2] * f),
+                                       pack_bf16x2(it.o[n][4 * i + 2][c] * f, it.o[n][4 * i + 2][c + 2] * f),
+                                       pack_bf16x2(it.o[n][4 * i + 3][c] * f, it.o[n][4 * i + 3][c + 2] * f));
             }
         }
     }
@@ -487,122 +574,95 @@ template <int D, int kMaxNt>
 __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(const Kv4Args a) {
     using K = Kernel<D, kMaxNt>;
     constexpr int kThreads = 32 * K::kW;
-    extern __shared__ __align__(128) uint8_t s_ring[];
+    extern __shared__ __align__(128) uint8_t s_mem[];  // rings, then a partial of each warp
     __shared__ __align__(8) uint64_t s_bar[K::kW * K::kStg];
-    __shared__ long long s_sum[kThreads];
-    __shared__ long long s_warp[K::kW];
+    __shared__ long long s_sum[kThreads], s_warp[K::kW];
     __shared__ int s_abort;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     for (int i = tid; i < K::kW * K::kStg; i += kThreads) mbar_init(s_bar + i, 1);
     if (tid == 0) s_abort = 0;
     mbar_fence_init();
     pdl_launch_dependents();
     pdl_wait();
 
-    // Every CTA adds up the costs of all requests.
-    int bits = 0;
-    if (blockIdx.x == 0 && tid == 0 && (a.qsl[0] != 0 || a.qsl[a.num_reqs] != a.num_tokens)) bits |= PKV_DEV_BAD_QSL;
-    auto scan = [&](int r0, long long *total) {  // inclusive sums of requests r0 .. r0 + kThreads - 1 to s_sum
-        const int r = r0 + tid;
-        long long v = 0;
-        if (r < a.num_reqs) {
-            const Kv4Request q = request_of(a, r, K::kRows, &bits);
-            v = kv4_cost(q, a.num_kv_heads, q.tiles);
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, v, d);
-            if (lane >= d) v += o;
-        }
-        if (lane == 31) s_warp[warp] = v;
-        __syncthreads();
-        long long before = 0, all = 0;
-#pragma unroll
-        for (int i = 0; i < K::kW; ++i) {
-            if (i < warp) before += s_warp[i];
-            all += s_warp[i];
-        }
-        s_sum[tid] = v + before;
-        *total = all;
-        __syncthreads();
-    };
-    long long total = 0;
-    if (a.num_reqs <= kThreads) {
-        scan(0, &total);
-    } else {
-        for (int r0 = 0; r0 < a.num_reqs; r0 += kThreads) {
-            long long part;
-            scan(r0, &part);
-            total += part;
-        }
-    }
-    if (blockIdx.x == 0 && bits) raise_status(a.status, bits);
-
-    const Kv4Shares sh = kv4_shares(total, (int)gridDim.x * K::kW, K::kMinShare);
-    const int share = warp * (int)gridDim.x + (int)blockIdx.x;  // neighbouring shares on different SMs
-    long long from = 0, to = 0;
-    if (share < sh.count) {
-        from = sh.begin(share);
-        to = sh.begin(share + 1);
-    }
-    // the request that position `from` lies in, and its first position
-    int r = -1;
-    long long first = 0;
+    // The costs of all requests: `each` of them a thread, in order.
+    const int each = (a.num_reqs + kThreads - 1) / kThreads;
+    long long sum = 0;
     {
-        long long base = 0;
-        for (int r0 = 0; r0 < a.num_reqs; r0 += kThreads) {
-            long long all = total;
-            if (a.num_reqs > kThreads) scan(r0, &all);
-            if (r < 0 && from < to && from < base + all) {
-                int lo = 0, hi = kThreads - 1;  // the first with base + s_sum > from
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (base + s_sum[mid] > from) hi = mid; else lo = mid + 1;
-                }
-                r = r0 + lo;
-                first = base + (lo ? s_sum[lo - 1] : 0);
-            }
-            base += all;
-            if (a.num_reqs > kThreads) __syncthreads();
+        int bits = 0;
+        if (cta == 0 && tid == 0 && (a.qsl[0] != 0 || a.qsl[a.num_reqs] != a.num_tokens)) bits |= PKV_DEV_BAD_QSL;
+        for (int r = tid * each; r < min((tid + 1) * each, a.num_reqs); ++r) {
+            const Kv4Request q = request_of(a, r, K::kRows, &bits);
+            sum += kv4_cost(q, a.num_kv_heads, q.tiles);
         }
+        if (cta == 0 && bits) raise_status(a.status, bits);
     }
-    Kv4Record *rec = a.records + share;
-    int parts = 0;
-    if (r >= 0) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int i = 0; i < K::kW; ++i) {
+        if (i < warp) sum += s_warp[i];
+        total += s_warp[i];
+    }
+    s_sum[tid] = sum;
+    __syncthreads();
+
+    Team team;
+    team.sh = kv4_shares(total, (int)gridDim.x, K::kW, K::kMinShare);
+    team.warp = warp;
+    team.cta = cta;
+    team.shares = min(team.sh.per_cta, team.sh.count - cta * team.sh.per_cta);
+    team.area = s_mem + K::kRing;
+    team.abort = &s_abort;
+    team.met = false;
+    if (team.shares <= 0) return;
+    if (warp < team.shares) {
+        const int share = cta * team.sh.per_cta + warp;
+        const long long from = team.sh.begin(share), to = team.sh.begin(share + 1);
         int none = 0;
         Where w;
-        w.r = r;
-        w.q = request_of(a, r, K::kRows, &none);
-        kv4_locate(w.q, a.num_kv_heads, from - first, &w.i, &w.h, &w.start);
-        w.start += first;
-        Ring<D, K::kStg> ring{smem_u32(s_ring) + (uint32_t)(warp * K::kStg * Kv4Tile<D>::kBytes), smem_u32(s_bar + warp * K::kStg), 0, 0};
+        {
+            int lo = 0, hi = kThreads - 1;  // the first thread with s_sum > from
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (s_sum[mid] > from) hi = mid; else lo = mid + 1;
+            }
+            long long first = lo ? s_sum[lo - 1] : 0;
+            for (w.r = lo * each;; ++w.r) {  // of its requests, the one that `from` lies in
+                w.q = request_of(a, w.r, K::kRows, &none);
+                const long long cost = kv4_cost(w.q, a.num_kv_heads, w.q.tiles);
+                if (from < first + cost) break;
+                first += cost;
+            }
+            kv4_locate(w.q, a.num_kv_heads, from - first, &w.i, &w.h, &w.start);
+            w.start += first;
+        }
+        Ring<D, K::kStg> ring{smem_u32(s_mem) + (uint32_t)(warp * K::kStg * Kv4Tile<D>::kBytes), smem_u32(s_bar + warp * K::kStg), 0, 0};
         while (true) {
             const Kv4Tiling tl = kv4_tile(w.q, w.i, a.group, K::kRows);
             const long long cost = kv4_item_cost(w.q, w.i), stop = w.start + cost;
-            const int b0 = from > w.start ? kv4_block_at(from - w.start, cost, tl.blocks) : 0;
-            const int b1 = to < stop ? kv4_block_at(to - w.start, cost, tl.blocks) : tl.blocks;
-            const bool begun = w.start < from, cut = stop > to;
-            float *part = begun || cut ? a.parts + ((size_t)2 * share + (begun ? 0 : 1)) * K::kPart : nullptr;
-            if (!begun && cut) {
-                parts = sh.index(stop - 1) - share + 1;
-                if (lane == 0) {
-                    rec->rows = tl.rows;
-                    rec->token = w.q.q0 * a.group + w.i * K::kRows;  // rows counted from the batch's first
-                    rec->head = w.h;
-                }
-            }
+            team.begun = w.start < from;
+            team.cut = stop > to;
+            team.first = team.begun ? team.sh.index(w.start) : share;
+            team.last = team.cut ? team.sh.index(stop - 1) : share;
+            const int b0 = team.begun ? kv4_block_at(from - w.start, cost, tl.blocks) : 0;
+            const int b1 = team.cut ? kv4_block_at(to - w.start, cost, tl.blocks) : tl.blocks;
             bool ok;
-            Kv4Record *mine = begun ? nullptr : rec;
-            if (kMaxNt == 1 || tl.rows <= 8) ok = K::template run<1>(a, ring, w, tl, b0, b1, part, mine, &s_abort, lane);
-            else if (kMaxNt == 2 || tl.rows <= 16) ok = K::template run<kMaxNt >= 2 ? 2 : 1>(a, ring, w, tl, b0, b1, part, mine, &s_abort, lane);
-            else ok = K::template run<kMaxNt>(a, ring, w, tl, b0, b1, part, mine, &s_abort, lane);
+            if (kMaxNt == 1 || tl.rows <= 8) ok = K::template run<1>(a, ring, w, tl, b0, b1, team, lane);
+            else if (kMaxNt == 2 || tl.rows <= 16) ok = K::template run<kMaxNt >= 2 ? 2 : 1>(a, ring, w, tl, b0, b1, team, lane);
+            else ok = K::template run<kMaxNt>(a, ring, w, tl, b0, b1, team, lane);
             if (!ok) {
                 // nothing may still be on its way into this SM's memory when the CTA ends
                 int never = 0;
                 for (; ring.at < ring.issued; ++ring.at)
                     if (!warp_wait(ring.bar + 8 * (ring.at % K::kStg), ring.at / K::kStg & 1, &never)) break;
                 if (lane == 0) raise_status(a.status, PKV_DEV_TIMEOUT);
-                parts = 0;
                 break;
             }
             if (stop >= to) break;
@@ -618,64 +678,13 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
             }
         }
     }
-    if (lane == 0) rec->parts = parts;
+    if (!team.met) __syncthreads();
 }
 
-// Joins the partials of the items that lie in several shares: a warp per row.
-template <int D, int kRows>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4Args a, int shares) {
-    constexpr int kF = D / 32;  // columns a lane holds
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int k = blockIdx.x; k < shares; k += gridDim.x) {
-        const Kv4Record *rec = a.records + k;
-        const int n = rec->parts, rows = rec->rows;
-        if (n < 2) continue;
-        for (int row = warp; row < rows; row += 8) {
-            const float mul = rec->mul[row];
-            // the first share's partial is its second one, the others' their first
-            auto part = [&](int i) { return a.parts + ((size_t)2 * (k + i) + (i == 0)) * kRows * (D + 2); };
-            float top = -INFINITY;
-            for (int i = lane; i < n; i += 32) top = fmaxf(top, reinterpret_cast<const float2 *>(part(i) + kRows * D)[row].x);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            float sum = 0.0f, acc[kF];
-#pragma unroll
-            for (int c = 0; c < kF; ++c) acc[c] = 0.0f;
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                float f = 0.0f;
-                if (i0 + lane < n) {
-                    const float2 ml = reinterpret_cast<const float2 *>(part(i0 + lane) + kRows * D)[row];
-                    f = ml.x == top ? 1.0f : ml.x == -INFINITY ? 0.0f : fast_exp2((ml.x - top) * mul);
-                    sum += f * ml.y;
-                }
-#pragma unroll 8
-                for (int i = 0; i < min(32, n - i0); ++i) {
-                    const float fi = __shfl_sync(0xffffffffu, f, i);
-                    const float *o = part(i0 + i) + row * D + kF * lane;
-#pragma unroll
-                    for (int c = 0; c < kF; ++c) acc[c] += fi * o[c];
-                }
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float f = a.v_scale / sum;
-            const int rr = rec->token + row, tok = rr / a.group;
-            __nv_bfloat16 *to = a.out + ((long long)tok * a.num_kv_heads * a.group + rec->head * a.group + rr - tok * a.group) * D + kF * lane;
-#pragma unroll
-            for (int c = 0; c < kF; c += 2) *reinterpret_cast<uint32_t *>(to + c) = pack_bf16x2(acc[c] * f, acc[c + 1] * f);
-        }
-    }
-}
-
-constexpr int kMaxRowsPerSm = 2 * 8 * 32;  // partial rows of one SM's warps: 12 x 2 x 16 at most otherwise
-static_assert(2 * kWarps<4> * 32 <= kMaxRowsPerSm && 2 * kWarps<2> * 16 <= kMaxRowsPerSm && 2 * kWarps<1> * 8 <= kMaxRowsPerSm, "");
-constexpr int kMaxWarps = 12;
-
-size_t records_bytes(int sms) { return (size_t)sms * kMaxWarps * sizeof(Kv4Record); }
+// Places in the workspace, for any batch and form.
+size_t parts_at(int sms) { return ((size_t)sms * sizeof(int) + 255) / 256 * 256; }
 size_t workspace_bytes(int sms, int head_size) {
-    return records_bytes(sms) + (size_t)sms * kMaxRowsPerSm * (head_size + 2) * sizeof(float);
+    return parts_at(sms) + (size_t)2 * sms * sizeof(float4) * (head_size == 128 ? Kernel<128, 4>::kPart : Kernel<64, 4>::kPart);
 }
 
 std::mutex g_mu;
@@ -697,9 +706,6 @@ int launch(const Kv4Args &a, int sms, int which, cudaStream_t st) {
     }
     if (launch_pdl(kv4_attention_kernel<D, kMaxNt>, dim3(sms), dim3(32 * K::kW), K::kSmem, st, a) != cudaSuccess)
         return PKV_E_CUDA;
-    const int shares = sms * K::kW;
-    if (launch_pdl(kv4_join_kernel<D, K::kRows>, dim3(std::min(shares, 4 * sms)), dim3(256), 0, st, a, shares) != cudaSuccess)
-        return PKV_E_CUDA;
     return PKV_OK;
 }
 
@@ -717,6 +723,22 @@ extern "C" PKV_API int paged_kv4_attention_workspace_bytes(const pkv_cache_desc 
     if (rs) return rs;
     *bytes = workspace_bytes(sms, desc->head_size);
     return PKV_OK;
+}
+
+extern "C" PKV_API int paged_kv4_attention_init(const pkv_cache_desc *desc, void *workspace, size_t workspace_size,
+                                                void *stream) {
+    if (!desc) return PKV_E_NULL;
+    const int rc = check_cache_desc(*desc, /*attention=*/true);
+    if (rc) return rc;
+    if (!workspace) return PKV_E_NULL;
+    if (!aligned(workspace, 16)) return PKV_E_ALIGN;
+    int sms = 0;
+    const int rs = device_sms(&sms);
+    if (rs) return rs;
+    if (workspace_size < workspace_bytes(sms, desc->head_size)) return PKV_E_WORKSPACE;
+    return cudaMemsetAsync(workspace, kNobody & 0xff, parts_at(sms), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_E_CUDA;
 }
 
 extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int32_t num_tokens, int32_t num_q_heads,
@@ -747,11 +769,11 @@ extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int3
     if (workspace_size < workspace_bytes(sms, desc->head_size)) return PKV_E_WORKSPACE;
     const float scale_log2 = scale * 1.4426950408889634f * k_scale;
     if (!std::isfinite(scale_log2)) return PKV_E_DIMS;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Kv4Args a{static_cast<const __nv_bfloat16 *>(q), q_stride, static_cast<const uint8_t *>(kv4_cache), block_table,
                     seq_lens, query_start_loc, num_tokens, desc->num_kv_heads, group, num_reqs, max_blocks_per_req,
                     desc->num_blocks, scale_log2, v_scale, static_cast<__nv_bfloat16 *>(out),
-                    static_cast<Kv4Record *>(workspace),
-                    reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + records_bytes(sms)), status};
+                    reinterpret_cast<int *>(ws), reinterpret_cast<float4 *>(ws + parts_at(sms)), status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // rows that the longest request has of a kv head
     const long long rows = (long long)(max_query_len ? max_query_len : num_tokens) * group;

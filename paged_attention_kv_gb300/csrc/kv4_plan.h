@@ -34,14 +34,23 @@ struct Kv4Tiling {
 PKV_HD int kv4_weight(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 6 : 11; }
 constexpr int kKv4ItemCost = 128;
 
+// x / y for a quotient below 2^20, without a division of 64 bits (which takes
+// longer than all the rest here).
+PKV_HD int kv4_quotient(long long x, long long y) {
+    long long q = (long long)((float)x / (float)y);  // off by at most 1
+    if (q * y > x) --q;
+    if ((q + 1) * y <= x) ++q;
+    return (int)q;
+}
+
 PKV_HD Kv4Request kv4_request(int q0, int n, int len, int group, int rows) {
     Kv4Request q{q0, n, len, 0, 0, 0};
-    const long long all = (long long)n * group;
-    q.tiles = (int)((all + rows - 1) / rows);
+    const unsigned all = (unsigned)n * (unsigned)group;  // below 2^31
+    q.tiles = (int)((all + (unsigned)rows - 1) / (unsigned)rows);
     if (q.tiles <= 1) {
         q.c0 = (long long)kv4_weight((int)all) * len + kKv4ItemCost;
     } else {
-        const long long step = (long long)kv4_weight(rows) * rows / group;  // keys more from tile to tile
+        const int step = kv4_weight(rows) * rows / group;  // keys more from tile to tile
         q.c0 = (long long)kv4_weight(rows) * (len - n) + step + kKv4ItemCost;
         q.c1 = step;
     }
@@ -58,49 +67,53 @@ PKV_HD long long kv4_item_cost(const Kv4Request &q, int i) { return q.c0 + i * q
 PKV_HD void kv4_locate(const Kv4Request &q, int heads, long long off, int *i, int *h, long long *start) {
     int lo = 0, hi = q.tiles - 1;  // the last tile that starts at or before off
     while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
+        const int mid = lo + (hi - lo + 1) / 2;
         if (kv4_cost(q, heads, mid) <= off) lo = mid; else hi = mid - 1;
     }
     const long long first = kv4_cost(q, heads, lo), c = kv4_item_cost(q, lo);
     *i = lo;
-    *h = (int)((off - first) / c);
+    *h = kv4_quotient(off - first, c);
     *start = first + *h * c;
 }
 
 PKV_HD Kv4Tiling kv4_tile(const Kv4Request &q, int i, int group, int rows) {
-    const long long left = (long long)q.n * group - (long long)i * rows;
+    const unsigned from = (unsigned)i * (unsigned)rows, left = (unsigned)q.n * (unsigned)group - from;
     Kv4Tiling t;
-    t.rows = left < rows ? (int)left : rows;
-    t.keys = q.len - q.n + (int)(((long long)i * rows + t.rows - 1) / group) + 1;
-    t.blocks = (t.keys + 15) / 16;
+    t.rows = left < (unsigned)rows ? (int)left : rows;
+    t.keys = q.len - q.n + (int)((from + t.rows - 1) / (unsigned)group) + 1;
+    t.blocks = (int)(((unsigned)t.keys + 15) / 16);
     return t;
 }
 
-// The block at which position `off` of an item of this cost lies.
-PKV_HD int kv4_block_at(long long off, long long cost, int blocks) { return (int)(off * blocks / cost); }
+// The block at which position `off` of an item of this cost lies: both shares
+// that meet there work it out alike, and it does not fall as off rises.
+PKV_HD int kv4_block_at(long long off, long long cost, int blocks) {
+    const int b = (int)((float)off / (float)cost * (float)blocks);
+    return b < blocks ? b : blocks;
+}
 
 struct Kv4Shares {
-    int count;
-    long long total, each, rest;
+    long long total, each;
+    int count, per_cta;  // shares; of one CTA: CTA c has shares c * per_cta on
 
-    PKV_HD long long begin(int k) const { return each * k + rest * k / count; }
+    PKV_HD long long begin(int k) const { return k < count ? k * each : total; }
     // the share that a position lies in
-    PKV_HD int index(long long pos) const {
-        int k = (int)((double)pos / (double)total * count);
-        k = k < 0 ? 0 : k >= count ? count - 1 : k;
-        while (k + 1 < count && begin(k + 1) <= pos) ++k;
-        while (k > 0 && begin(k) > pos) --k;
-        return k;
-    }
+    PKV_HD int index(long long pos) const { return kv4_quotient(pos, each); }
 };
 
-// At most `most` shares of at least `least`.
-PKV_HD Kv4Shares kv4_shares(long long total, int most, int least) {
+// At most ctas * warps shares of at least `least`, over as many CTAs as there are.
+PKV_HD Kv4Shares kv4_shares(long long total, int ctas, int warps, int least) {
+    const int most = ctas * warps;
     Kv4Shares s;
     s.total = total;
-    s.count = total <= 0 ? 0 : total / least < 1 ? 1 : total / least > most ? most : (int)(total / least);
-    s.each = s.count ? total / s.count : 0;
-    s.rest = s.count ? total % s.count : 0;
+    if (total <= (long long)least * most) {
+        s.each = least;
+    } else {
+        s.each = (long long)((float)total / (float)most);
+        while (s.each * most < total) s.each += 1 + (s.each >> 22);
+    }
+    s.count = total <= 0 ? 0 : kv4_quotient(total - 1, s.each) + 1;
+    s.per_cta = (s.count + ctas - 1) / ctas;
     return s;
 }
 

@@ -214,7 +214,7 @@ def test_many_requests(reqs):
     b.check(pkv.paged_kv4_attention(*b.tensors(), b.scale))
 
 
-def test_scales_and_slices_and_a_dirty_workspace():
+def test_scales_and_slices_and_one_workspace():
     b = Batch(5, 8, 2, 128, [300, 40, 7], [1, 6, 2])
     q, pool, table, lens, qsl = b.tensors()
     rows = torch.full((9, 8 * 128 + 64), 3.0, dtype=torch.bfloat16, device=DEV)
@@ -223,10 +223,26 @@ def test_scales_and_slices_and_a_dirty_workspace():
     ws = pkv.alloc_kv4_workspace(pool)
     outs = []
     for fill in (0, -1, 0x7fc000007fc00000):
-        ws.fill_(fill)
+        ws[200:].fill_(fill)  # what partials were there before does not matter, the counters in front do
         outs.append(pkv.paged_kv4_attention(sliced, pool, table, lens, qsl, b.scale, k_scale=0.25, v_scale=8.0, workspace=ws))
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
     b.check(outs[0], k_by=0.25, v_by=8.0)
+
+
+def test_a_workspace_that_was_not_prepared_is_reported():
+    b = Batch(5, 8, 2, 128, [9000, 4000], [1, 2])
+    q, pool, table, lens, qsl = b.tensors()
+    ws = pkv.alloc_kv4_workspace(pool)
+    for fill in (0, -1, 5):
+        st = status()
+        pkv.paged_kv4_attention(q, pool, table, lens, qsl, b.scale, workspace=torch.full_like(ws, fill), status=st)
+        assert pkv.pkv_read_status(st) == pkv.PKV_DEV_BAD_WORKSPACE
+    st = status()
+    for _ in range(3):
+        b.check(pkv.paged_kv4_attention(q, pool, table, lens, qsl, b.scale, workspace=ws, status=st))
+    assert pkv.pkv_read_status(st) == 0
+    with pytest.raises(pkv.PagedKVError):
+        pkv.paged_kv4_attention(q, pool, table, lens, qsl, b.scale, workspace=ws[:-1])
 
 
 def test_rows_of_no_request_and_requests_without_queries_are_left():

@@ -14,10 +14,10 @@ PROGRAM = r"""
 #include <vector>
 #include "kv4_plan.h"
 using namespace pkv;
-// in: reqs group heads rows most least, then (n, len) of each. Walks every share as a warp of the kernel does.
+// in: reqs group heads rows ctas warps least, then (n, len) of each. Walks every share as a warp of the kernel does.
 int main() {
-    int R, group, heads, rows, most, least;
-    while (scanf("%d %d %d %d %d %d", &R, &group, &heads, &rows, &most, &least) == 6) {
+    int R, group, heads, rows, ctas, warps, least;
+    while (scanf("%d %d %d %d %d %d %d", &R, &group, &heads, &rows, &ctas, &warps, &least) == 7) {
         std::vector<Kv4Request> q(R);
         std::vector<long long> first(R + 1, 0);
         int q0 = 0;
@@ -29,7 +29,8 @@ int main() {
             first[r + 1] = first[r] + kv4_cost(q[r], heads, q[r].tiles);
         }
         const long long total = first[R];
-        const Kv4Shares sh = kv4_shares(total, most, least);
+        const Kv4Shares sh = kv4_shares(total, ctas, warps, least);
+        if (sh.per_cta > warps || (long long)sh.per_cta * ctas < sh.count) { printf("%d shares, %d a CTA\n", sh.count, sh.per_cta); return 1; }
         // next block expected of each item, and partials seen / announced
         std::vector<std::vector<int>> next(R), seen(R), told(R);
         for (int r = 0; r < R; ++r) next[r].assign(q[r].tiles * heads, 0), seen[r].assign(q[r].tiles * heads, 0), told[r].assign(q[r].tiles * heads, -1);
@@ -104,13 +105,13 @@ def walk(program, batches):
 
 def test_named_batches(program):
     counts = walk(program, [
-        ((8, 4, 8, 1824, 512), [(1, 17), (1, 40)]),
-        ((4, 8, 8, 1824, 512), [(1, 1)]),
-        ((4, 8, 32, 1216, 512), [(0, 0), (512, 512), (0, 5), (1, 2_000_000), (300, 301), (0, 0)]),
-        ((128, 1, 32, 1216, 512), [(3, 90)] * 40),
-        ((3, 5, 8, 1824, 512), [(7, 1000)] * 9),
-        ((4, 8, 8, 1824, 512), [(1, 3000)] * 256),
-        ((4, 8, 8, 1824, 512), []), ((4, 8, 8, 1824, 512), [(0, 0)] * 7)])
+        ((8, 4, 8, 152, 12, 512), [(1, 17), (1, 40)]),
+        ((4, 8, 8, 152, 12, 512), [(1, 1)]),
+        ((4, 8, 32, 152, 8, 512), [(0, 0), (512, 512), (0, 5), (1, 2_000_000), (300, 301), (0, 0)]),
+        ((128, 1, 32, 152, 8, 512), [(3, 90)] * 40),
+        ((3, 5, 8, 152, 12, 512), [(7, 1000)] * 9),
+        ((4, 8, 8, 152, 12, 512), [(1, 3000)] * 256),
+        ((4, 8, 8, 152, 12, 512), []), ((4, 8, 8, 152, 12, 512), [(0, 0)] * 7)])
     assert counts[-2:] == [0, 0] and counts[5] == 1824
 
 
@@ -123,6 +124,6 @@ def test_random_batches(program):
         for _ in range(rng.randint(1, 40)):
             n = rng.choice((0, 1, 1, rng.randint(1, 9), rng.randint(1, 400)))
             reqs.append((n, n + rng.choice((0, 0, rng.randint(0, 50), rng.randint(0, 5000)))))
-        batches.append(((rng.choice((1, 2, 3, 4, 5, 8, 16, 33, 128)), rng.randint(1, 8), rows, rng.choice((1, 7, 1216, 1824)),
+        batches.append(((rng.choice((1, 2, 3, 4, 5, 8, 16, 33, 128)), rng.randint(1, 8), rows, *rng.choice(((1, 1), (7, 1), (3, 5), (152, 8), (152, 12))),
                          rng.choice((1, 64, 512, 4096))), reqs))
     walk(program, batches)
