@@ -601,7 +601,8 @@ int paged_kv4_attention(const void *q, int64_t q_stride, int32_t num_tokens, int
  * is, nothing being put back or taken (PKV_DEV_BAD_PAGES).
  *
  * Ordering as paged_build_tables: nothing is read before every earlier kernel on
- * the stream has completed, and kernels behind it start only when it has.
+ * the stream has completed, and kernels behind it start only when it has. Make
+ * the first call with more than 256 rows on a device before any capture.
  */
 #define PKV_MAX_FORK_ROWS 4096
 int paged_fork_tables(const int32_t *parents, int32_t num_rows, const int32_t *block_table,

@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "pagedkv.h"
 #include "pkv_device.cuh"
@@ -28,8 +29,10 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kMaxCtas = 8;
-constexpr int kFree = INT_MIN / 2;  // counts below this are claims: INT_MIN + entry
+constexpr int kMaxCtas = 16;
+constexpr int kMinCtas = 8;           // that a cluster has on every device
+constexpr int kFree = INT_MIN / 2;    // counts below this are claims: INT_MIN + entry
+constexpr int kMaxOwn = PKV_MAX_FORK_ROWS / kMinCtas;  // rows of a CTA
 
 struct ForkArgs {
     const int32_t *parents, *table, *lens;
@@ -53,7 +56,7 @@ __device__ __forceinline__ void store_to(uint32_t at, uint32_t rank, int v) {
 __device__ __forceinline__ int seen(const int32_t *p) { return __ldcg(p); }
 
 __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a) {
-    __shared__ int s_children[PKV_MAX_FORK_ROWS], s_first[PKV_MAX_FORK_ROWS];
+    __shared__ int s_children[PKV_MAX_FORK_ROWS], s_first[PKV_MAX_FORK_ROWS], s_dst[kMaxOwn];
     __shared__ int s_warp[32], s_total[kMaxCtas];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, ctas = gridDim.x;  // the grid is one cluster
@@ -65,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
     pdl_wait();
     __syncthreads();
     int bits = 0;
-    // the blocks of a row: 0 and flagged where its length is out of range
+    // the tokens of a row: 0 and flagged where its length is out of range
     auto length = [&](int r) {
         const int n = __ldg(a.lens + r);
         if (n >= 0 && n <= (long long)a.width * PKV_BLOCK_SIZE) return n;
@@ -78,11 +81,19 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         bits |= PKV_DEV_BAD_PAGES;
         return -1;
     };
-    auto block = [&](int r, int e) {
-        const int b = __ldg(a.table + (long long)r * a.width + e);
-        if (b >= 0 && b < a.num_blocks) return b;
-        bits |= PKV_DEV_BAD_BLOCK;
-        return -1;
+    // four entries a lane of a row from e0 on: -1 past `held`, flagged where no block
+    constexpr int kU = 4;
+    auto blocks = [&](int r, int e0, int held, int (&b)[kU]) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int e = e0 + 32 * u + lane;
+            b[u] = e < held ? __ldg(a.table + (long long)r * a.width + e) : INT_MIN;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            if (b[u] != INT_MIN && (b[u] < 0 || b[u] >= a.num_blocks)) bits |= PKV_DEV_BAD_BLOCK;
+            if (b[u] < 0 || b[u] >= a.num_blocks) b[u] = -1;
+        }
     };
     for (int r = tid; r < R; r += kThreads) {
         const int p = parent(r);
@@ -102,21 +113,28 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         const int c = s_children[r];
         if (c == 1) continue;
         const int n = length(r), full = n / PKV_BLOCK_SIZE, held = c ? full : (n + 15) / PKV_BLOCK_SIZE;
-        for (int e = lane; e < held; e += 32) {
-            const int b = block(r, e);
-            if (b >= 0) atomicAdd(a.shares + b, c - 1);
+        for (int e0 = 0; e0 < held; e0 += 32 * kU) {
+            int b[kU];
+            blocks(r, e0, held, b);
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (b[u] >= 0) atomicAdd(a.shares + b[u], c - 1);
         }
     }
     cluster_sync();
     for (int r = r0 + warp; r < r1; r += kThreads / 32) {
         if (s_children[r]) continue;
         const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
-        for (int e = lane; e < held; e += 32) {
-            const int b = block(r, e);
-            if (b < 0) continue;
-            const int v = seen(a.shares + b);
-            if (v == -1 || v < kFree) atomicMin(a.shares + b, INT_MIN + (r * a.width + e));
-            else if (v < -1) bits |= PKV_DEV_BAD_PAGES;  // given up more often than held
+        for (int e0 = 0; e0 < held; e0 += 32 * kU) {
+            int b[kU], v[kU];
+            blocks(r, e0, held, b);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) v[u] = b[u] >= 0 ? seen(a.shares + b[u]) : 0;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                if (v[u] == -1 || v[u] < kFree) atomicMin(a.shares + b[u], INT_MIN + (r * a.width + e0 + 32 * u + lane));
+                else if (v[u] < -1) bits |= PKV_DEV_BAD_PAGES;  // given up more often than held
+            }
         }
     }
     cluster_sync();
@@ -126,10 +144,13 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         if (s_children[r]) continue;
         const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
         int got = 0;
-        for (int e0 = 0; e0 < held; e0 += 32) {
-            const int e = e0 + lane, b = e < held ? block(r, e) : -1;
-            got += __popc(__ballot_sync(0xffffffffu, b >= 0 && seen(a.shares + b) == INT_MIN + (r * a.width + e)));
+        for (int e0 = 0; e0 < held; e0 += 32 * kU) {
+            int b[kU];
+            blocks(r, e0, held, b);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) got += b[u] >= 0 && seen(a.shares + b[u]) == INT_MIN + (r * a.width + e0 + 32 * u + lane);
         }
+        got = __reduce_add_sync(0xffffffffu, got);
         if (lane == 0) s_first[r] = got;  // a row without children has no first one
         mine += got;
     }
@@ -148,47 +169,46 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
     if (!list) given = 0;
     if (given > cur && list) bits |= PKV_DEV_BAD_PAGES;  // more than were ever taken
     const int base = list ? cur - given : 0;             // where the first one goes
-    // every row's place: a sum over the rows before it, a thread per row
-    for (int c0 = r0; c0 < r1; c0 += kThreads) {
-        const int r = c0 + tid;
-        const int n = r < r1 && !s_children[r] ? s_first[r] : 0;
+    // every row's place: a sum over the CTA's rows before it (at most a thread each)
+    {
+        const int r = r0 + tid, n = r < r1 && !s_children[r] ? s_first[r] : 0;
         int v = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += o;
         }
-        __syncthreads();
         if (lane == 31) s_warp[warp] = v;
         __syncthreads();
-        int sum = 0, all = 0;
-        for (int i = 0; i < 32; ++i) {
-            if (i < warp) sum += s_warp[i];
-            all += s_warp[i];
-        }
+        int sum = lane < warp ? s_warp[lane] : 0;
+        sum = __reduce_add_sync(0xffffffffu, sum);
         if (r < r1 && !s_children[r]) s_first[r] = before + sum + v - n;
-        before += all;
     }
     __syncthreads();
     for (int r = r0 + warp; r < r1; r += kThreads / 32) {
         if (s_children[r]) continue;
         const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
         int at = base + s_first[r];
-        for (int e0 = 0; e0 < held; e0 += 32) {
-            const int e = e0 + lane, b = e < held ? block(r, e) : -1;
-            const int v = b >= 0 ? seen(a.shares + b) : 0;
-            const bool take = v == INT_MIN + (r * a.width + e) && b >= 0;
-            const uint32_t all = __ballot_sync(0xffffffffu, take);
-            if (take) {
-                const int to = at + __popc(all & ((1u << lane) - 1));
-                if (list && to >= 0) a.free_blocks[to] = b;
+        for (int e0 = 0; e0 < held; e0 += 32 * kU) {
+            int b[kU], v[kU];
+            blocks(r, e0, held, b);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) v[u] = b[u] >= 0 ? seen(a.shares + b[u]) : 0;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const bool take = v[u] == INT_MIN + (r * a.width + e0 + 32 * u + lane);
+                const uint32_t all = __ballot_sync(0xffffffffu, take);
+                if (take) {
+                    const int to = at + __popc(all & ((1u << lane) - 1));
+                    if (list && to >= 0) a.free_blocks[to] = b[u];
+                }
+                if (take || (v[u] < 0 && v[u] >= kFree)) a.shares[b[u]] = 0;
+                at += __popc(all);
             }
-            if (take || (v < 0 && v >= kFree)) a.shares[b] = 0;
-            at += __popc(all);
         }
     }
     cluster_sync();
-    // the new rows; every CTA numbers the copies of all rows
+    // the new rows; every CTA numbers the copies of all rows up to its own
     const int from = max(base, 0);
     int copies = 0;
     for (int c0 = 0; c0 < R; c0 += kThreads) {
@@ -200,18 +220,17 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         __syncthreads();
         if (lane == 0) s_warp[warp] = __popc(all);
         __syncthreads();
-        int sum = copies, sums = 0;
-        for (int i = 0; i < 32; ++i) {
-            if (i < warp) sum += s_warp[i];
-            sums += s_warp[i];
-        }
-        // rows of this pass, a warp at a time
-        const int k = from + sum + __popc(all & ((1u << lane) - 1));
-        int src = -1, dst = -1;
-        const bool own = r >= r0 && r < r1;
-        if (own) {
+        const int sum = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
+        const int sums = __reduce_add_sync(0xffffffffu, s_warp[lane]);
+        if (r >= r0 && r < r1) {
+            const int k = from + copies + sum + __popc(all & ((1u << lane) - 1));
+            int src = -1, dst = -1;
             if (copy) {
-                src = block(p, n / PKV_BLOCK_SIZE);
+                src = __ldg(a.table + (long long)p * a.width + n / PKV_BLOCK_SIZE);
+                if (src < 0 || src >= a.num_blocks) {
+                    src = -1;
+                    bits |= PKV_DEV_BAD_BLOCK;
+                }
                 if (list && k < a.num_free) {
                     dst = __ldcg(a.free_blocks + k);
                     if (dst < 0 || dst >= a.num_blocks) {
@@ -221,23 +240,31 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
                 } else {
                     bits |= PKV_DEV_NO_BLOCKS;
                 }
-                if (src < 0 || dst < 0) src = -1;
             }
+            s_dst[r - r0] = copy ? dst : INT_MIN;
             a.lens_out[r] = n;
-            a.copy_src[r] = src;
+            a.copy_src[r] = dst < 0 ? -1 : src;
             a.copy_dst[r] = src < 0 ? -1 : dst;
         }
-        for (uint32_t todo = __ballot_sync(0xffffffffu, own); todo; todo &= todo - 1) {
-            const int i = __ffs(todo) - 1;
-            const int pi = __shfl_sync(0xffffffffu, p, i), ni = __shfl_sync(0xffffffffu, n, i);
-            const int di = __shfl_sync(0xffffffffu, dst, i), ci = __shfl_sync(0xffffffffu, (int)copy, i);
-            const int held = (ni + 15) / PKV_BLOCK_SIZE;
-            const int32_t *line = a.table + (long long)max(pi, 0) * a.width;
-            int32_t *to = a.table_out + (long long)(c0 + warp * 32 + i) * a.width;
-            for (int e = lane; e < a.width; e += 32)
-                to[e] = e >= held ? -1 : ci && e == held - 1 ? di : __ldg(line + e);
-        }
         copies += sums;
+    }
+    __syncthreads();
+    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
+        const int p = parent(r), held = p >= 0 ? (length(p) + 15) / PKV_BLOCK_SIZE : 0, dst = s_dst[r - r0];
+        const int32_t *line = a.table + (long long)max(p, 0) * a.width;
+        int32_t *to = a.table_out + (long long)r * a.width;
+        for (int e0 = 0; e0 < a.width; e0 += 32 * kU) {
+            int b[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int e = e0 + 32 * u + lane;
+                b[u] = e < held ? __ldg(line + e) : -1;
+                if (e == held - 1 && dst != INT_MIN) b[u] = dst;
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (e0 + 32 * u + lane < a.width) to[e0 + 32 * u + lane] = b[u];
+        }
     }
     if (rank == 0 && tid == 0 && list) *a.cursor = from + min(copies, a.num_free - from);
     if (bits) raise_status(a.status, bits);
@@ -282,6 +309,28 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_
     }
 }
 
+// The largest cluster this device takes, 16 or the 8 that every one takes.
+std::mutex g_mu;
+int g_cluster[64];
+
+int largest_cluster(int *ctas) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_E_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_cluster[dev]) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMaxCtas);
+        cfg.blockDim = dim3(kThreads);
+        int n = 0;
+        if (cudaFuncSetAttribute(fork_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaOccupancyMaxPotentialClusterSize(&n, fork_tables_kernel, &cfg) != cudaSuccess)
+            return PKV_E_CUDA;
+        g_cluster[dev] = n >= kMaxCtas ? kMaxCtas : kMinCtas;
+    }
+    *ctas = g_cluster[dev];
+    return PKV_OK;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -308,7 +357,13 @@ extern "C" PKV_API int paged_fork_tables(const int32_t *parents, int32_t num_row
     if (block_table_out == block_table || seq_lens_out == seq_lens) return PKV_E_DIMS;
     const ForkArgs a{parents, block_table, seq_lens, num_rows, max_blocks_per_req, num_blocks, shares, free_blocks,
                      num_free, free_cursor, block_table_out, seq_lens_out, copy_src, copy_dst, status};
-    const int ctas = num_rows <= 32 ? 1 : kMaxCtas;
+    // a warp a row, as far as a cluster goes
+    int ctas = 1;
+    while (ctas < kMinCtas && ctas * (kThreads / 32) < num_rows) ctas *= 2;
+    if (ctas * (kThreads / 32) < num_rows) {
+        const int rc = largest_cluster(&ctas);
+        if (rc) return rc;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);

@@ -45,63 +45,146 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
     return c;
 }
 
+__device__ __forceinline__ float with_sign(float y, float x) {
+    return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));
+}
+
 // Eight values of a group (the other eight are in the neighbouring lane) as
-// codes; *scale: the group's scale byte.
+// codes; *scale: the group's scale byte. A quotient is x / s as x * (1 / s),
+// corrected once by its remainder, which one fused operation gives exactly: a tie
+// (x a code's border times s) comes out as that border itself, which the
+// reciprocal's own rounding would miss, and everything else is 2^-8 away from one.
 __device__ __forceinline__ uint32_t quantise(uint4 x, float inv, uint32_t *scale) {
     uint32_t top = max_bits(x);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const float want = fmaxf(__uint_as_float(top << 16) * inv / 6.0f, 0x1p-9f);
+    const float most = __uint_as_float(top << 16) * inv;
+    const float want = fmaxf(most / 6.0f, 0x1p-9f);
     uint16_t byte;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(byte) : "f"(want));
     if (top > 0x7f80u) byte = 0x7f;  // a NaN among them: the whole group is one
     *scale = byte & 0xffu;
-    const float s = __low2float(kv4_scales(byte));
+    const float s = __low2float(kv4_scales(byte)), r = 1.0f / s;
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = fmul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), make_float2(inv, inv));
+    if (isinf(most)) {  // an infinity has no remainder; the largest finite value becomes the same code
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = make_float2(fminf(fmaxf(v[i].x, -3e38f), 3e38f), fminf(fmaxf(v[i].y, -3e38f), 3e38f));
+    }
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xffff0000u) * inv;
-        codes |= codes2(lo / s, hi / s) << (8 * i);
+        const float2 q = fmul2(v[i], make_float2(r, r));
+        const float2 rem = ffma2(make_float2(-q.x, -q.y), make_float2(s, s), v[i]);
+        const float2 y = ffma2(rem, make_float2(r, r), q);
+        // the correction makes +0 of -0
+        codes |= codes2(with_sign(y.x, v[i].x), with_sign(y.y, v[i].y)) << (8 * i);
     }
     return codes;
 }
 
-// A warp per token: K chunks (8 columns of one head each), then V chunks.
+// A CTA has 16 tokens, and the block that starts among them if a run of tokens
+// fills it: those (prompts) are turned into whole tiles, one warp a head's K or V,
+// and leave as 16-byte chunks; other tokens (decode rows, a prompt's ends) are
+// written code by code, a warp each. 32768 tokens of 8 heads of 128: see below.
+constexpr int kWriteThreads = 512;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_write_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kWriteThreads, 2) kv4_write_kernel(const StoreArgs a) {
     using Tile = Kv4Tile<D>;
-    constexpr int kC = D / 8;  // chunks of a head
+    constexpr int kC = D / 8;             // chunks of 8 columns of a head
+    constexpr int kWarps = kWriteThreads / 32;
+    constexpr int kLoads = kC / 2;        // of a warp for one head's K or V of 16 tokens
+    constexpr int kPer = 32 / kC;         // tokens a load covers
+    __shared__ int s_slot[48];
+    __shared__ uint32_t s_full;
+    __shared__ __align__(16) uint8_t s_tile[kWarps][9 * D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int t0 = (int)blockIdx.x * PKV_BLOCK_SIZE;
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
+    if (tid < 48) {
+        const int t = t0 - 15 + tid;
+        s_slot[tid] = t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : -1;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        bool full = false;
+        if (lane < 16) {
+            const int slot = s_slot[15 + lane], row = slot & 15;
+            full = slot >= 0 && slot / PKV_BLOCK_SIZE < a.num_blocks;
+            for (int i = 0; i < 16; ++i) full &= s_slot[15 + lane - row + i] == slot - row + i;
+        }
+        const uint32_t all = __ballot_sync(0xffffffffu, full);
+        if (lane == 0) s_full = all;
+    }
+    __syncthreads();
+    const uint32_t full = s_full;
+    int first = -1;  // the token that a whole block starts at
+    for (int j = 0; j < 16; ++j)
+        if ((full >> j & 1) && (s_slot[15 + j] & 15) == 0) first = j;
+    if (first >= 0) {
+        uint8_t *tiles = a.pool + (long long)(s_slot[15 + first] / PKV_BLOCK_SIZE) * a.num_kv_heads * Tile::kBytes;
+        const int c = lane % kC;
+        for (int task = warp; task < 2 * a.num_kv_heads; task += kWarps) {
+            const int h = task >> 1;
+            const bool is_v = task & 1;
+            const uint4 *src = (is_v ? a.v + (t0 + first) * a.v_stride : a.k + (t0 + first) * a.k_stride) + h * kC + c;
+            const long long stride = is_v ? a.v_stride : a.k_stride;
+            uint4 x[kLoads];
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) x[j] = __ldg(src + (j * kPer + lane / kC) * stride);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int row = j * kPer + lane / kC;
+                uint32_t scale;
+                const uint32_t codes = quantise(x[j], is_v ? a.v_inv : a.k_inv, &scale);
+                // as in the tile, the scales right behind the codes
+                *reinterpret_cast<uint32_t *>(s_tile[warp] + (is_v ? Tile::v_code(row, c) - Tile::kV : Tile::k_code(row, c))) = codes;
+                if ((c & 1) == 0)
+                    s_tile[warp][8 * D + (is_v ? Tile::v_scale(row, c >> 1) - Tile::kVScale : Tile::k_scale(row, c >> 1) - Tile::kKScale)] =
+                        (uint8_t)scale;
+            }
+            __syncwarp();
+            uint8_t *to = tiles + (long long)h * Tile::kBytes;
+            const uint4 *from = reinterpret_cast<const uint4 *>(s_tile[warp]);
+            for (int i = lane; i < 9 * D / 16; i += 32)
+                *reinterpret_cast<uint4 *>(to + (i < D / 2 ? (is_v ? Tile::kV : 0) + 16 * i
+                                                            : (is_v ? Tile::kVScale : Tile::kKScale) + 16 * (i - D / 2))) = from[i];
+        }
+    }
     const int chunks = a.num_kv_heads * kC;  // a multiple of 8, so the two lanes of a group stay together
-    for (long long t = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5; t < a.num_tokens;
-         t += (long long)gridDim.x * kThreads / 32) {
-        const int slot = __ldg(a.slots + t);
-        if (slot < 0) continue;
+    for (int j = warp; j < 16; j += kWarps) {
+        const int slot = s_slot[15 + j];
+        if (slot < 0 || (full >> j & 1)) continue;
         const int blk = slot / PKV_BLOCK_SIZE, row = slot % PKV_BLOCK_SIZE;
         if (blk >= a.num_blocks) {
             if (lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
             continue;
         }
+        const long long t = t0 + j;
         uint8_t *tiles = a.pool + (long long)blk * a.num_kv_heads * Tile::kBytes;
         for (int i0 = 0; i0 < 2 * chunks; i0 += 128) {
             uint4 x[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + 32 * j + lane;
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u + lane;
                 if (i < 2 * chunks)
-                    x[j] = i < chunks ? __ldg(a.k + t * a.k_stride + i) : __ldg(a.v + t * a.v_stride + (i - chunks));
+                    x[u] = i < chunks ? __ldg(a.k + t * a.k_stride + i) : __ldg(a.v + t * a.v_stride + (i - chunks));
                 else
-                    x[j] = make_uint4(0, 0, 0, 0);
+                    x[u] = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (i0 + 32 * j >= 2 * chunks) break;
-                const int i = i0 + 32 * j + lane;
+            for (int u = 0; u < 4; ++u) {
+                if (i0 + 32 * u >= 2 * chunks) break;
+                const int i = i0 + 32 * u + lane;
                 const bool is_v = i >= chunks;
                 uint32_t scale;
-                const uint32_t codes = quantise(x[j], is_v ? a.v_inv : a.k_inv, &scale);
+                const uint32_t codes = quantise(x[u], is_v ? a.v_inv : a.k_inv, &scale);
                 if (i >= 2 * chunks) continue;
                 const int ii = is_v ? i - chunks : i;
                 const int h = ii / kC, c = ii % kC;
@@ -221,8 +304,8 @@ extern "C" PKV_API int paged_kv4_write(const void *k, int64_t k_stride, const vo
                       slot_mapping, num_tokens, desc->num_kv_heads, desc->num_blocks,
                       static_cast<uint8_t *>(kv4_cache), 1.0f / k_scale, 1.0f / v_scale, status};
     const auto kernel = desc->head_size == 128 ? kv4_write_kernel<128> : kv4_write_kernel<64>;
-    return launch_pdl(kernel, dim3(grid_for(num_tokens)), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
-                   cudaSuccess
+    return launch_pdl(kernel, dim3((unsigned)(((long long)num_tokens + 15) / 16)), dim3(kWriteThreads), 0,
+                      static_cast<cudaStream_t>(stream), a) == cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
 }
