@@ -8,7 +8,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <climits>
 #include <cstdint>
 
 #include "kv4_format.cuh"
@@ -19,7 +18,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;  // a warp per token of 16
+constexpr int kWarps = kThreads / 32;
 
 struct StoreArgs {
     const uint4 *k, *v;
@@ -31,12 +31,17 @@ struct StoreArgs {
     int32_t *status;
 };
 
-// The largest magnitude of 8 bf16 values as its bits (NaN above infinity above
-// all others).
-__device__ __forceinline__ uint32_t max_bits(uint4 x) {
+struct Group {
+    uint4 x, y;  // 16 bf16 values
+};
+
+// The largest magnitude of a group as its bits (NaN above infinity above all others).
+__device__ __forceinline__ uint32_t max_bits(const Group &g) {
     const uint32_t m = 0x7fff7fffu;
-    const uint32_t a = __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
-    return max(a & 0xffffu, a >> 16);
+    const uint32_t a = __vmaxu2(__vmaxu2(g.x.x & m, g.x.y & m), __vmaxu2(g.x.z & m, g.x.w & m));
+    const uint32_t b = __vmaxu2(__vmaxu2(g.y.x & m, g.y.y & m), __vmaxu2(g.y.z & m, g.y.w & m));
+    const uint32_t c = __vmaxu2(a, b);
+    return max(c & 0xffffu, c >> 16);
 }
 
 __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
@@ -45,65 +50,142 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
     return c;
 }
 
-__device__ __forceinline__ float with_sign(float y, float x) {
-    return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// Eight values of a group (the other eight are in the neighbouring lane) as
-// codes; *scale: the group's scale byte. A quotient is x / s as x * (1 / s),
-// corrected once by its remainder, which one fused operation gives exactly: a tie
-// (x a code's border times s) comes out as that border itself, which the
-// reciprocal's own rounding would miss, and everything else is 2^-8 away from one.
-__device__ __forceinline__ uint32_t quantise(uint4 x, float inv, uint32_t *scale) {
-    uint32_t top = max_bits(x);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const float most = __uint_as_float(top << 16) * inv;
-    const float want = fmaxf(most / 6.0f, 0x1p-9f);
+// A group as 16 codes and its scale byte. Quotients x / s are x * (1 / s), the
+// reciprocal to about 2^-23, corrected once by their remainder, which one fused
+// operation gives exactly: what is left is off by 2^-46, so that a tie (x a border
+// between codes times s) comes out as that border itself, and everything else is
+// 2^-8 away from one. The correction makes +0 of -0, hence the sign.
+__device__ __forceinline__ uint2 quantise(const Group &g, float inv, uint32_t *scale) {
+    const uint32_t top = max_bits(g);
+    const float most = fminf(__uint_as_float(top << 16) * inv, 3e38f);
+    constexpr float kSixth = 1.0f / 6.0f;
+    const float q6 = most * kSixth, want = fmaxf(fmaf(fmaf(q6, -6.0f, most), kSixth, q6), 0x1p-9f);
     uint16_t byte;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(byte) : "f"(want));
     if (top > 0x7f80u) byte = 0x7f;  // a NaN among them: the whole group is one
     *scale = byte & 0xffu;
-    const float s = __low2float(kv4_scales(byte)), r = 1.0f / s;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float2 v[4];
+    const float s = __low2float(kv4_scales(byte)), r = reciprocal(s);
+    const uint32_t w[8] = {g.x.x, g.x.y, g.x.z, g.x.w, g.y.x, g.y.y, g.y.z, g.y.w};
+    float2 v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
         v[i] = fmul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), make_float2(inv, inv));
-    if (isinf(most)) {  // an infinity has no remainder; the largest finite value becomes the same code
+    if (most >= 3e38f) {  // an infinity has no remainder; the largest finite value becomes the same code
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
             v[i] = make_float2(fminf(fmaxf(v[i].x, -3e38f), 3e38f), fminf(fmaxf(v[i].y, -3e38f), 3e38f));
     }
-    uint32_t codes = 0;
+    uint32_t codes[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float2 q = fmul2(v[i], make_float2(r, r));
-        const float2 rem = ffma2(make_float2(-q.x, -q.y), make_float2(s, s), v[i]);
+        const float2 rem = ffma2(q, make_float2(-s, -s), v[i]);
         const float2 y = ffma2(rem, make_float2(r, r), q);
-        // the correction makes +0 of -0
-        codes |= codes2(with_sign(y.x, v[i].x), with_sign(y.y, v[i].y)) << (8 * i);
+        const uint32_t lo = __float_as_uint(y.x) | (w[i] << 16 & 0x80000000u), hi = __float_as_uint(y.y) | (w[i] & 0x80000000u);
+        codes[i / 4] |= codes2(__uint_as_float(lo), __uint_as_float(hi)) << (8 * (i % 4));
     }
-    return codes;
+    return make_uint2(codes[0], codes[1]);
+}
+
+// Group g's codes of a token: 8 bytes, or two times 4 a row of D / 2 bytes apart
+// (V, D 64).
+template <int D>
+__device__ __forceinline__ void put_codes(uint8_t *tile, bool is_v, int row, int g, uint2 codes) {
+    using Tile = Kv4Tile<D>;
+    uint8_t *to = tile + (is_v ? Tile::v_code(row, 2 * g) : Tile::k_code(row, 2 * g));
+    if (D == 64) {
+        *reinterpret_cast<uint32_t *>(to) = codes.x;
+        *reinterpret_cast<uint32_t *>(to + (is_v ? D / 2 : 4)) = codes.y;
+    } else {
+        *reinterpret_cast<uint2 *>(to) = codes;
+    }
+}
+
+// One head's K or V of a whole block, by one warp: rows as they come in, codes
+// and scales to shared memory, from there to the tile in 16-byte chunks.
+template <int D, bool kV>
+__device__ __forceinline__ void write_tile(const uint4 *src, long long stride, float inv, uint8_t *to, uint8_t *mem, int lane) {
+    using Tile = Kv4Tile<D>;
+    constexpr int kG = D / 16, kPer = 32 / kG, kLoads = 16 / kPer;  // groups of a row, rows at a time
+    constexpr int kAhead = 2;
+    const int g = lane % kG;
+    __syncwarp();
+#pragma unroll 1
+    for (int j0 = 0; j0 < kLoads; j0 += kAhead) {
+        Group x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const uint4 *at = src + ((j0 + j) * kPer + lane / kG) * stride + 2 * g;
+            x[j] = Group{__ldg(at), __ldg(at + 1)};
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int row = (j0 + j) * kPer + lane / kG;
+            uint32_t scale;
+            const uint2 codes = quantise(x[j], inv, &scale);
+            // the part's codes, then its scales
+            put_codes<D>(mem - (kV ? Tile::kV : 0), kV, row, g, codes);
+            mem[8 * D + (kV ? Tile::v_scale(row, g) - Tile::kVScale : Tile::k_scale(row, g) - Tile::kKScale)] = (uint8_t)scale;
+        }
+    }
+    __syncwarp();
+    const uint4 *from = reinterpret_cast<const uint4 *>(mem);
+    for (int i = lane; i < 9 * D / 16; i += 32)
+        *reinterpret_cast<uint4 *>(to + (i < D / 2 ? (kV ? Tile::kV : 0) + 16 * i : (kV ? Tile::kVScale : Tile::kKScale) + 16 * (i - D / 2))) =
+            from[i];
+}
+
+// One token's K and V of `heads` heads, by one warp: a lane per group.
+template <int D>
+__device__ __forceinline__ void write_token(const uint4 *k, const uint4 *v, int heads, float k_inv, float v_inv, uint8_t *tiles,
+                                            int row, int lane) {
+    using Tile = Kv4Tile<D>;
+    constexpr int kG = D / 16, kAhead = 2;
+    const int n = heads * kG;
+    for (int i0 = lane; i0 < 2 * n; i0 += 32 * kAhead) {
+        Group x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = min(i0 + 32 * j, 2 * n - 1);
+            const uint4 *at = i < n ? k + 2 * i : v + 2 * (i - n);
+            x[j] = Group{__ldg(at), __ldg(at + 1)};
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + 32 * j;
+            if (i >= 2 * n) break;
+            const bool is_v = i >= n;
+            const int ii = is_v ? i - n : i, g = ii % kG;
+            uint32_t scale;
+            const uint2 codes = quantise(x[j], is_v ? v_inv : k_inv, &scale);
+            uint8_t *tile = tiles + (long long)(ii / kG) * Tile::kBytes;
+            put_codes<D>(tile, is_v, row, g, codes);
+            tile[is_v ? Tile::v_scale(row, g) : Tile::k_scale(row, g)] = (uint8_t)scale;
+        }
+    }
 }
 
 // A CTA has 16 tokens, and the block that starts among them if a run of tokens
-// fills it: those (prompts) are turned into whole tiles, one warp a head's K or V,
-// and leave as 16-byte chunks; other tokens (decode rows, a prompt's ends) are
-// written code by code, a warp each. 32768 tokens of 8 heads of 128: see below.
-constexpr int kWriteThreads = 512;
-
+// fills it: such blocks (prompts) are turned into whole tiles, other tokens (decode
+// rows, a prompt's ends) are written code by code.
 template <int D>
-__global__ void __launch_bounds__(kWriteThreads, 2) kv4_write_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) kv4_write_kernel(const StoreArgs a) {
     using Tile = Kv4Tile<D>;
-    constexpr int kC = D / 8;             // chunks of 8 columns of a head
-    constexpr int kWarps = kWriteThreads / 32;
-    constexpr int kLoads = kC / 2;        // of a warp for one head's K or V of 16 tokens
-    constexpr int kPer = 32 / kC;         // tokens a load covers
     __shared__ int s_slot[48];
     __shared__ uint32_t s_full;
     __shared__ __align__(16) uint8_t s_tile[kWarps][9 * D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = (int)blockIdx.x * PKV_BLOCK_SIZE;
+    // this CTA's heads: where tokens are few, several CTAs share theirs
+    const int per = (a.num_kv_heads + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int h0 = (int)blockIdx.y * per, heads = min(per, a.num_kv_heads - h0);
+    if (heads <= 0) return;
     pdl_launch_dependents();
     pdl_wait();
     if (tid < 48) {
@@ -123,78 +205,28 @@ __global__ void __launch_bounds__(kWriteThreads, 2) kv4_write_kernel(const Store
     }
     __syncthreads();
     const uint32_t full = s_full;
-    int first = -1;  // the token that a whole block starts at
-    for (int j = 0; j < 16; ++j)
-        if ((full >> j & 1) && (s_slot[15 + j] & 15) == 0) first = j;
-    if (first >= 0) {
+    const int mine = s_slot[15 + (lane & 15)];
+    const uint32_t begin = __ballot_sync(0xffffffffu, lane < 16 && (full >> lane & 1) && (mine & 15) == 0);
+    if (begin) {  // at most one: a run of 16 has one token in row 0
+        const int first = __ffs(begin) - 1;
         uint8_t *tiles = a.pool + (long long)(s_slot[15 + first] / PKV_BLOCK_SIZE) * a.num_kv_heads * Tile::kBytes;
-        const int c = lane % kC;
-        for (int task = warp; task < 2 * a.num_kv_heads; task += kWarps) {
-            const int h = task >> 1;
-            const bool is_v = task & 1;
-            const uint4 *src = (is_v ? a.v + (t0 + first) * a.v_stride : a.k + (t0 + first) * a.k_stride) + h * kC + c;
-            const long long stride = is_v ? a.v_stride : a.k_stride;
-            uint4 x[kLoads];
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) x[j] = __ldg(src + (j * kPer + lane / kC) * stride);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int row = j * kPer + lane / kC;
-                uint32_t scale;
-                const uint32_t codes = quantise(x[j], is_v ? a.v_inv : a.k_inv, &scale);
-                // as in the tile, the scales right behind the codes
-                *reinterpret_cast<uint32_t *>(s_tile[warp] + (is_v ? Tile::v_code(row, c) - Tile::kV : Tile::k_code(row, c))) = codes;
-                if ((c & 1) == 0)
-                    s_tile[warp][8 * D + (is_v ? Tile::v_scale(row, c >> 1) - Tile::kVScale : Tile::k_scale(row, c >> 1) - Tile::kKScale)] =
-                        (uint8_t)scale;
-            }
-            __syncwarp();
+        for (int task = warp; task < 2 * heads; task += kWarps) {
+            const int h = h0 + (task >> 1);
             uint8_t *to = tiles + (long long)h * Tile::kBytes;
-            const uint4 *from = reinterpret_cast<const uint4 *>(s_tile[warp]);
-            for (int i = lane; i < 9 * D / 16; i += 32)
-                *reinterpret_cast<uint4 *>(to + (i < D / 2 ? (is_v ? Tile::kV : 0) + 16 * i
-                                                            : (is_v ? Tile::kVScale : Tile::kKScale) + 16 * (i - D / 2))) = from[i];
+            if (task & 1) write_tile<D, true>(a.v + (t0 + first) * a.v_stride + h * (D / 8), a.v_stride, a.v_inv, to, s_tile[warp], lane);
+            else write_tile<D, false>(a.k + (t0 + first) * a.k_stride + h * (D / 8), a.k_stride, a.k_inv, to, s_tile[warp], lane);
         }
     }
-    const int chunks = a.num_kv_heads * kC;  // a multiple of 8, so the two lanes of a group stay together
-    for (int j = warp; j < 16; j += kWarps) {
-        const int slot = s_slot[15 + j];
-        if (slot < 0 || (full >> j & 1)) continue;
-        const int blk = slot / PKV_BLOCK_SIZE, row = slot % PKV_BLOCK_SIZE;
-        if (blk >= a.num_blocks) {
-            if (lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
-            continue;
-        }
-        const long long t = t0 + j;
-        uint8_t *tiles = a.pool + (long long)blk * a.num_kv_heads * Tile::kBytes;
-        for (int i0 = 0; i0 < 2 * chunks; i0 += 128) {
-            uint4 x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + 32 * u + lane;
-                if (i < 2 * chunks)
-                    x[u] = i < chunks ? __ldg(a.k + t * a.k_stride + i) : __ldg(a.v + t * a.v_stride + (i - chunks));
-                else
-                    x[u] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (i0 + 32 * u >= 2 * chunks) break;
-                const int i = i0 + 32 * u + lane;
-                const bool is_v = i >= chunks;
-                uint32_t scale;
-                const uint32_t codes = quantise(x[u], is_v ? a.v_inv : a.k_inv, &scale);
-                if (i >= 2 * chunks) continue;
-                const int ii = is_v ? i - chunks : i;
-                const int h = ii / kC, c = ii % kC;
-                uint8_t *tile = tiles + (long long)h * Tile::kBytes;
-                *reinterpret_cast<uint32_t *>(tile + (is_v ? Tile::v_code(row, c) : Tile::k_code(row, c))) = codes;
-                if ((c & 1) == 0)
-                    tile[is_v ? Tile::v_scale(row, c >> 1) : Tile::k_scale(row, c >> 1)] = (uint8_t)scale;
-            }
-        }
+    const int slot = s_slot[15 + warp];
+    if (slot < 0 || (full >> warp & 1)) return;
+    const int blk = slot / PKV_BLOCK_SIZE, row = slot % PKV_BLOCK_SIZE;
+    if (blk >= a.num_blocks) {
+        if (lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
+        return;
     }
+    const long long t = t0 + warp;
+    uint8_t *tiles = a.pool + ((long long)blk * a.num_kv_heads + h0) * Tile::kBytes;
+    write_token<D>(a.k + t * a.k_stride + h0 * (D / 8), a.v + t * a.v_stride + h0 * (D / 8), heads, a.k_inv, a.v_inv, tiles, row, lane);
 }
 
 struct LoadArgs {
@@ -206,55 +238,51 @@ struct LoadArgs {
     int32_t *status;
 };
 
-__device__ __forceinline__ uint32_t to_bf16x2(__half2 x, float s) {
-    const float2 f = __half22float2(x);
-    return pack_bf16x2(f.x * s, f.y * s);
-}
-
+// A warp per token: a lane per 8 columns, K's and V's side by side.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const LoadArgs a) {
     using Tile = Kv4Tile<D>;
-    constexpr int kC = D / 8;
+    constexpr int kC = D / 8, kAhead = 4;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int chunks = a.num_kv_heads * kC;
-    for (long long t = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5; t < a.num_tokens;
-         t += (long long)gridDim.x * kThreads / 32) {
-        const int slot = __ldg(a.slots + t);
-        if (slot < 0) continue;
-        const int blk = slot / PKV_BLOCK_SIZE, row = slot % PKV_BLOCK_SIZE;
-        if (blk >= a.num_blocks) {
-            if (lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
-            continue;
+    const long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int per = (a.num_kv_heads + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int h0 = (int)blockIdx.y * per, n = min(per, a.num_kv_heads - h0) * kC;
+    if (t >= a.num_tokens || n <= 0) return;
+    const int slot = __ldg(a.slots + t);
+    if (slot < 0) return;
+    const int blk = slot / PKV_BLOCK_SIZE, row = slot % PKV_BLOCK_SIZE;
+    if (blk >= a.num_blocks) {
+        if (lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
+        return;
+    }
+    const uint8_t *tiles = a.pool + ((long long)blk * a.num_kv_heads + h0) * Tile::kBytes;
+    const long long at = (t * a.num_kv_heads + h0) * kC;
+    const int i1 = a.v ? 2 * n : n;
+    for (int i0 = (a.k ? 0 : n) + lane; i0 < i1; i0 += 32 * kAhead) {
+        uint32_t codes[kAhead], byte[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = min(i0 + 32 * j, i1 - 1);
+            const bool is_v = i >= n;
+            const int ii = is_v ? i - n : i, c = ii % kC;
+            const uint8_t *tile = tiles + (long long)(ii / kC) * Tile::kBytes;
+            codes[j] = *reinterpret_cast<const uint32_t *>(tile + (is_v ? Tile::v_code(row, c) : Tile::k_code(row, c)));
+            byte[j] = tile[is_v ? Tile::v_scale(row, c >> 1) : Tile::k_scale(row, c >> 1)];
         }
-        const uint8_t *tiles = a.pool + (long long)blk * a.num_kv_heads * Tile::kBytes;
-        for (int i0 = 0; i0 < 2 * chunks; i0 += 128) {
-            uint32_t codes[4], scale[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + 32 * j + lane;
-                if (i >= 2 * chunks) continue;
-                const bool is_v = i >= chunks;
-                const int ii = is_v ? i - chunks : i;
-                const int h = ii / kC, c = ii % kC;
-                const uint8_t *tile = tiles + (long long)h * Tile::kBytes;
-                codes[j] = *reinterpret_cast<const uint32_t *>(tile + (is_v ? Tile::v_code(row, c) : Tile::k_code(row, c)));
-                scale[j] = tile[is_v ? Tile::v_scale(row, c >> 1) : Tile::k_scale(row, c >> 1)];
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + 32 * j + lane;
-                if (i >= 2 * chunks) continue;
-                const bool is_v = i >= chunks;
-                uint4 *out = is_v ? a.v : a.k;
-                if (!out) continue;
-                const __half2 s = kv4_scales(scale[j] * 0x101u);
-                const float by = is_v ? a.v_scale : a.k_scale;
-                out[t * chunks + (is_v ? i - chunks : i)] =
-                    make_uint4(to_bf16x2(__hmul2(kv4_pair<0>(codes[j]), s), by), to_bf16x2(__hmul2(kv4_pair<1>(codes[j]), s), by),
-                               to_bf16x2(__hmul2(kv4_pair<2>(codes[j]), s), by), to_bf16x2(__hmul2(kv4_pair<3>(codes[j]), s), by));
-            }
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + 32 * j;
+            if (i >= i1) break;
+            const bool is_v = i >= n;
+            const float s = __low2float(kv4_scales(byte[j])) * (is_v ? a.v_scale : a.k_scale);
+            auto pair = [&](__half2 x) {
+                const float2 f = fmul2(__half22float2(x), make_float2(s, s));
+                return pack_bf16x2(f.x, f.y);
+            };
+            (is_v ? a.v : a.k)[at + (is_v ? i - n : i)] =
+                make_uint4(pair(kv4_pair<0>(codes[j])), pair(kv4_pair<1>(codes[j])), pair(kv4_pair<2>(codes[j])), pair(kv4_pair<3>(codes[j])));
         }
     }
 }
@@ -271,8 +299,14 @@ int check_common(const void *pool, const pkv_cache_desc *desc, const int32_t *sl
     return PKV_OK;
 }
 
-int grid_for(int num_tokens) {
-    return std::max(1, std::min((num_tokens + kThreads / 32 - 1) / (kThreads / 32), 1 << 20));
+// CTAs of 16 tokens, and of a part of the heads where those leave SMs without two.
+int grid_for(int num_tokens, int heads, dim3 *grid) {
+    int sms = 0;
+    const int rc = device_sms(&sms);
+    if (rc) return rc;
+    const unsigned x = ((unsigned)num_tokens + kWarps - 1) / kWarps;
+    *grid = dim3(x, std::min<unsigned>(heads, std::max(1u, 2u * sms / x)));
+    return PKV_OK;
 }
 
 }  // namespace
@@ -304,8 +338,11 @@ extern "C" PKV_API int paged_kv4_write(const void *k, int64_t k_stride, const vo
                       slot_mapping, num_tokens, desc->num_kv_heads, desc->num_blocks,
                       static_cast<uint8_t *>(kv4_cache), 1.0f / k_scale, 1.0f / v_scale, status};
     const auto kernel = desc->head_size == 128 ? kv4_write_kernel<128> : kv4_write_kernel<64>;
-    return launch_pdl(kernel, dim3((unsigned)(((long long)num_tokens + 15) / 16)), dim3(kWriteThreads), 0,
-                      static_cast<cudaStream_t>(stream), a) == cudaSuccess
+    dim3 grid;
+    const int rg = grid_for(num_tokens, desc->num_kv_heads, &grid);
+    if (rg) return rg;
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
+                   cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
 }
@@ -321,7 +358,10 @@ extern "C" PKV_API int paged_kv4_read(const void *kv4_cache, const pkv_cache_des
                      desc->num_blocks, k_scale, v_scale, static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out),
                      status};
     const auto kernel = desc->head_size == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>;
-    return launch_pdl(kernel, dim3(grid_for(num_tokens)), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
+    dim3 grid;
+    const int rg = grid_for(num_tokens, desc->num_kv_heads, &grid);
+    if (rg) return rg;
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
                    cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
