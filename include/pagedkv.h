@@ -466,8 +466,8 @@ int pkv_prompt_attention(const void *q, int64_t q_stride, const void *k, int64_t
  * that the caller keeps (1 unless a layer's values fill e4m3's range, 2^-9 to
  * 448, badly). A group whose largest magnitude is A, after division by k_scale,
  * gets the scale A / 6 rounded to e4m3, at least 2^-9; a value the code nearest
- * to value / scale (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign); both round ties to
- * even. Magnitudes past 2688, infinities too, become 2688; a group with a NaN
+ * to value / scale (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign; -0 becomes 0); both
+ * round ties to even. Magnitudes past 2688, infinities too, become 2688; a group with a NaN
  * becomes NaN. The values that result are exact in bf16 and in fp16.
  *
  * Bytes of a (block, kv head), D = head_size; a byte of codes holds an even

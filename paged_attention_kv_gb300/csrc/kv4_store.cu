@@ -18,7 +18,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;  // a warp per token of 16
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 struct StoreArgs {
@@ -27,7 +27,7 @@ struct StoreArgs {
     const int32_t *slots;
     int num_tokens, num_kv_heads, num_blocks;
     uint8_t *pool;
-    float k_inv, v_inv;
+    float k_scale, v_scale, k_inv, v_inv;
     int32_t *status;
 };
 
@@ -44,10 +44,13 @@ __device__ __forceinline__ uint32_t max_bits(const Group &g) {
     return max(c & 0xffffu, c >> 16);
 }
 
-__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
-    uint32_t c;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(c) : "f"(lo), "f"(hi));
-    return c;
+__device__ __forceinline__ uint32_t codes8(float2 a, float2 b, float2 c, float2 d) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+    return w;
 }
 
 __device__ __forceinline__ float reciprocal(float x) {
@@ -56,12 +59,12 @@ __device__ __forceinline__ float reciprocal(float x) {
     return y;
 }
 
-// A group as 16 codes and its scale byte. Quotients x / s are x * (1 / s), the
-// reciprocal to about 2^-23, corrected once by their remainder, which one fused
-// operation gives exactly: what is left is off by 2^-46, so that a tie (x a border
-// between codes times s) comes out as that border itself, and everything else is
-// 2^-8 away from one. The correction makes +0 of -0, hence the sign.
-__device__ __forceinline__ uint2 quantise(const Group &g, float inv, uint32_t *scale) {
+// A group as 16 codes and its scale byte. Quotients x / (s * by) are x * (1 / (s *
+// by)), the reciprocal to about 2^-23, corrected once by their remainder, which one
+// fused operation gives exactly: what is left is off by 2^-46, so that a tie (x a
+// border between codes times s) comes out as that border itself, and everything
+// else is 2^-8 away from one. (The correction makes +0 of -0: code 0 for both.)
+__device__ __forceinline__ uint2 quantise(const Group &g, float by, float inv, uint32_t *scale) {
     const uint32_t top = max_bits(g);
     const float most = fminf(__uint_as_float(top << 16) * inv, 3e38f);
     constexpr float kSixth = 1.0f / 6.0f;
@@ -70,27 +73,23 @@ __device__ __forceinline__ uint2 quantise(const Group &g, float inv, uint32_t *s
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(byte) : "f"(want));
     if (top > 0x7f80u) byte = 0x7f;  // a NaN among them: the whole group is one
     *scale = byte & 0xffu;
-    const float s = __low2float(kv4_scales(byte)), r = reciprocal(s);
+    const float s = __low2float(kv4_scales(byte)), r = reciprocal(s) * inv, sb = -s * by;
     const uint32_t w[8] = {g.x.x, g.x.y, g.x.z, g.x.w, g.y.x, g.y.y, g.y.z, g.y.w};
-    float2 v[8];
+    float2 y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = fmul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), make_float2(inv, inv));
-    if (most >= 3e38f) {  // an infinity has no remainder; the largest finite value becomes the same code
+    for (int i = 0; i < 8; ++i) y[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    if (top == 0x7f80u) {  // an infinity has no remainder; the largest finite value becomes the same code
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = make_float2(fminf(fmaxf(v[i].x, -3e38f), 3e38f), fminf(fmaxf(v[i].y, -3e38f), 3e38f));
+            y[i] = make_float2(fminf(fmaxf(y[i].x, -3e38f), 3e38f), fminf(fmaxf(y[i].y, -3e38f), 3e38f));
     }
-    uint32_t codes[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 q = fmul2(v[i], make_float2(r, r));
-        const float2 rem = ffma2(q, make_float2(-s, -s), v[i]);
-        const float2 y = ffma2(rem, make_float2(r, r), q);
-        const uint32_t lo = __float_as_uint(y.x) | (w[i] << 16 & 0x80000000u), hi = __float_as_uint(y.y) | (w[i] & 0x80000000u);
-        codes[i / 4] |= codes2(__uint_as_float(lo), __uint_as_float(hi)) << (8 * (i % 4));
+        const float2 q = fmul2(y[i], make_float2(r, r));
+        const float2 rem = ffma2(q, make_float2(sb, sb), y[i]);
+        y[i] = ffma2(rem, make_float2(r, r), q);
     }
-    return make_uint2(codes[0], codes[1]);
+    return make_uint2(codes8(y[0], y[1], y[2], y[3]), codes8(y[4], y[5], y[6], y[7]));
 }
 
 // Group g's codes of a token: 8 bytes, or two times 4 a row of D / 2 bytes apart
@@ -110,7 +109,7 @@ __device__ __forceinline__ void put_codes(uint8_t *tile, bool is_v, int row, int
 // One head's K or V of a whole block, by one warp: rows as they come in, codes
 // and scales to shared memory, from there to the tile in 16-byte chunks.
 template <int D, bool kV>
-__device__ __forceinline__ void write_tile(const uint4 *src, long long stride, float inv, uint8_t *to, uint8_t *mem, int lane) {
+__device__ __forceinline__ void write_tile(const uint4 *src, long long stride, float by, float inv, uint8_t *to, uint8_t *mem, int lane) {
     using Tile = Kv4Tile<D>;
     constexpr int kG = D / 16, kPer = 32 / kG, kLoads = 16 / kPer;  // groups of a row, rows at a time
     constexpr int kAhead = 2;
@@ -128,7 +127,7 @@ __device__ __forceinline__ void write_tile(const uint4 *src, long long stride, f
         for (int j = 0; j < kAhead; ++j) {
             const int row = (j0 + j) * kPer + lane / kG;
             uint32_t scale;
-            const uint2 codes = quantise(x[j], inv, &scale);
+            const uint2 codes = quantise(x[j], by, inv, &scale);
             // the part's codes, then its scales
             put_codes<D>(mem - (kV ? Tile::kV : 0), kV, row, g, codes);
             mem[8 * D + (kV ? Tile::v_scale(row, g) - Tile::kVScale : Tile::k_scale(row, g) - Tile::kKScale)] = (uint8_t)scale;
@@ -143,8 +142,7 @@ __device__ __forceinline__ void write_tile(const uint4 *src, long long stride, f
 
 // One token's K and V of `heads` heads, by one warp: a lane per group.
 template <int D>
-__device__ __forceinline__ void write_token(const uint4 *k, const uint4 *v, int heads, float k_inv, float v_inv, uint8_t *tiles,
-                                            int row, int lane) {
+__device__ __forceinline__ void write_token(const uint4 *k, const uint4 *v, int heads, const StoreArgs &a, uint8_t *tiles, int row, int lane) {
     using Tile = Kv4Tile<D>;
     constexpr int kG = D / 16, kAhead = 2;
     const int n = heads * kG;
@@ -163,7 +161,7 @@ __device__ __forceinline__ void write_token(const uint4 *k, const uint4 *v, int 
             const bool is_v = i >= n;
             const int ii = is_v ? i - n : i, g = ii % kG;
             uint32_t scale;
-            const uint2 codes = quantise(x[j], is_v ? v_inv : k_inv, &scale);
+            const uint2 codes = quantise(x[j], is_v ? a.v_scale : a.k_scale, is_v ? a.v_inv : a.k_inv, &scale);
             uint8_t *tile = tiles + (long long)(ii / kG) * Tile::kBytes;
             put_codes<D>(tile, is_v, row, g, codes);
             tile[is_v ? Tile::v_scale(row, g) : Tile::k_scale(row, g)] = (uint8_t)scale;
@@ -173,60 +171,60 @@ __device__ __forceinline__ void write_token(const uint4 *k, const uint4 *v, int 
 
 // A CTA has 16 tokens, and the block that starts among them if a run of tokens
 // fills it: such blocks (prompts) are turned into whole tiles, other tokens (decode
-// rows, a prompt's ends) are written code by code.
+// rows, a prompt's ends) are written code by code. Every warp finds that out for
+// itself from the slots around. 32768 tokens of 8 heads of 128: see the table of
+// measurements beside the calls' description.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kv4_write_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const StoreArgs a) {
     using Tile = Kv4Tile<D>;
-    __shared__ int s_slot[48];
-    __shared__ uint32_t s_full;
     __shared__ __align__(16) uint8_t s_tile[kWarps][9 * D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = (int)blockIdx.x * PKV_BLOCK_SIZE;
     // this CTA's heads: where tokens are few, several CTAs share theirs
     const int per = (a.num_kv_heads + (int)gridDim.y - 1) / (int)gridDim.y;
     const int h0 = (int)blockIdx.y * per, heads = min(per, a.num_kv_heads - h0);
-    if (heads <= 0) return;
     pdl_launch_dependents();
     pdl_wait();
-    if (tid < 48) {
-        const int t = t0 - 15 + tid;
-        s_slot[tid] = t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : -1;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        bool full = false;
-        if (lane < 16) {
-            const int slot = s_slot[15 + lane], row = slot & 15;
-            full = slot >= 0 && slot / PKV_BLOCK_SIZE < a.num_blocks;
-            for (int i = 0; i < 16; ++i) full &= s_slot[15 + lane - row + i] == slot - row + i;
-        }
-        const uint32_t all = __ballot_sync(0xffffffffu, full);
-        if (lane == 0) s_full = all;
-    }
-    __syncthreads();
-    const uint32_t full = s_full;
-    const int mine = s_slot[15 + (lane & 15)];
-    const uint32_t begin = __ballot_sync(0xffffffffu, lane < 16 && (full >> lane & 1) && (mine & 15) == 0);
+    if (heads <= 0) return;
+    // slots of the 16 tokens before (lane 16 is the CTA's first token), and of the 16 behind
+    auto slot_of = [&](int t) { return t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : -1; };
+    const int one = slot_of(t0 - 16 + lane), two = slot_of(t0 + 16 + lane);
+    // bit i: the token at t0 - 16 + i has the slot after its predecessor's, in the same block
+    const int before1 = __shfl_up_sync(0xffffffffu, one, 1), last = __shfl_sync(0xffffffffu, one, 31);
+    const int before2 = __shfl_up_sync(0xffffffffu, two, 1);
+    const uint32_t run1 = __ballot_sync(0xffffffffu, lane > 0 && one > 0 && (one & 15) && one - 1 == before1);
+    const uint32_t run2 = __ballot_sync(0xffffffffu, two > 0 && (two & 15) && two - 1 == (lane ? before2 : last));
+    const uint64_t run = run1 | (uint64_t)run2 << 32;
+    // the CTA's tokens (lane 16 on) that belong to a whole block's run
+    const int row1 = one & 15;
+    const bool in_full = lane >= 16 && one >= 0 && one / PKV_BLOCK_SIZE < a.num_blocks && (run >> (lane - row1 + 1) & 0x7fff) == 0x7fff;
+    const uint32_t full = __ballot_sync(0xffffffffu, in_full) >> 16;
+    const uint32_t begin = __ballot_sync(0xffffffffu, in_full && row1 == 0) >> 16;
     if (begin) {  // at most one: a run of 16 has one token in row 0
         const int first = __ffs(begin) - 1;
-        uint8_t *tiles = a.pool + (long long)(s_slot[15 + first] / PKV_BLOCK_SIZE) * a.num_kv_heads * Tile::kBytes;
+        const int blk = __shfl_sync(0xffffffffu, one, 16 + first) / PKV_BLOCK_SIZE;
+        uint8_t *tiles = a.pool + (long long)blk * a.num_kv_heads * Tile::kBytes;
         for (int task = warp; task < 2 * heads; task += kWarps) {
             const int h = h0 + (task >> 1);
             uint8_t *to = tiles + (long long)h * Tile::kBytes;
-            if (task & 1) write_tile<D, true>(a.v + (t0 + first) * a.v_stride + h * (D / 8), a.v_stride, a.v_inv, to, s_tile[warp], lane);
-            else write_tile<D, false>(a.k + (t0 + first) * a.k_stride + h * (D / 8), a.k_stride, a.k_inv, to, s_tile[warp], lane);
+            if (task & 1)
+                write_tile<D, true>(a.v + (t0 + first) * a.v_stride + h * (D / 8), a.v_stride, a.v_scale, a.v_inv, to, s_tile[warp], lane);
+            else
+                write_tile<D, false>(a.k + (t0 + first) * a.k_stride + h * (D / 8), a.k_stride, a.k_scale, a.k_inv, to, s_tile[warp], lane);
         }
     }
-    const int slot = s_slot[15 + warp];
-    if (slot < 0 || (full >> warp & 1)) return;
-    const int blk = slot / PKV_BLOCK_SIZE, row = slot % PKV_BLOCK_SIZE;
-    if (blk >= a.num_blocks) {
-        if (lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
-        return;
+    for (int j = warp; j < 16; j += kWarps) {
+        const int slot = __shfl_sync(0xffffffffu, one, 16 + j);
+        if (slot < 0 || (full >> j & 1)) continue;
+        const int blk = slot / PKV_BLOCK_SIZE, row = slot % PKV_BLOCK_SIZE;
+        if (blk >= a.num_blocks) {
+            if (lane == 0) raise_status(a.status, PKV_DEV_BAD_SLOT);
+            continue;
+        }
+        const long long t = t0 + j;
+        uint8_t *tiles = a.pool + ((long long)blk * a.num_kv_heads + h0) * Tile::kBytes;
+        write_token<D>(a.k + t * a.k_stride + h0 * (D / 8), a.v + t * a.v_stride + h0 * (D / 8), heads, a, tiles, row, lane);
     }
-    const long long t = t0 + warp;
-    uint8_t *tiles = a.pool + ((long long)blk * a.num_kv_heads + h0) * Tile::kBytes;
-    write_token<D>(a.k + t * a.k_stride + h0 * (D / 8), a.v + t * a.v_stride + h0 * (D / 8), heads, a.k_inv, a.v_inv, tiles, row, lane);
 }
 
 struct LoadArgs {
@@ -299,13 +297,13 @@ int check_common(const void *pool, const pkv_cache_desc *desc, const int32_t *sl
     return PKV_OK;
 }
 
-// CTAs of 16 tokens, and of a part of the heads where those leave SMs without two.
-int grid_for(int num_tokens, int heads, dim3 *grid) {
+// CTAs of so many tokens, and of a part of the heads where those leave SMs without four.
+int grid_for(int num_tokens, int tokens, int heads, dim3 *grid) {
     int sms = 0;
     const int rc = device_sms(&sms);
     if (rc) return rc;
-    const unsigned x = ((unsigned)num_tokens + kWarps - 1) / kWarps;
-    *grid = dim3(x, std::min<unsigned>(heads, std::max(1u, 2u * sms / x)));
+    const unsigned x = ((unsigned)num_tokens + tokens - 1) / tokens;
+    *grid = dim3(x, std::min<unsigned>(heads, std::max(1u, 4u * sms / x)));
     return PKV_OK;
 }
 
@@ -336,10 +334,10 @@ extern "C" PKV_API int paged_kv4_write(const void *k, int64_t k_stride, const vo
         return PKV_E_DIMS;
     const StoreArgs a{static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), k_stride / 8, v_stride / 8,
                       slot_mapping, num_tokens, desc->num_kv_heads, desc->num_blocks,
-                      static_cast<uint8_t *>(kv4_cache), 1.0f / k_scale, 1.0f / v_scale, status};
+                      static_cast<uint8_t *>(kv4_cache), k_scale, v_scale, 1.0f / k_scale, 1.0f / v_scale, status};
     const auto kernel = desc->head_size == 128 ? kv4_write_kernel<128> : kv4_write_kernel<64>;
     dim3 grid;
-    const int rg = grid_for(num_tokens, desc->num_kv_heads, &grid);
+    const int rg = grid_for(num_tokens, PKV_BLOCK_SIZE, desc->num_kv_heads, &grid);
     if (rg) return rg;
     return launch_pdl(kernel, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
                    cudaSuccess
@@ -359,7 +357,7 @@ extern "C" PKV_API int paged_kv4_read(const void *kv4_cache, const pkv_cache_des
                      status};
     const auto kernel = desc->head_size == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>;
     dim3 grid;
-    const int rg = grid_for(num_tokens, desc->num_kv_heads, &grid);
+    const int rg = grid_for(num_tokens, kWarps, desc->num_kv_heads, &grid);
     if (rg) return rg;
     return launch_pdl(kernel, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
                    cudaSuccess

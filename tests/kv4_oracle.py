@@ -35,7 +35,7 @@ def quantise(x, by=1.0):
     with np.errstate(invalid="ignore"):
         q = g / SCALES[byte][..., None]
     code = np.where(np.isnan(q), 0, nearest(np.minimum(np.abs(np.nan_to_num(q, nan=0.0, posinf=9.0, neginf=-9.0)), 6.0), CODES))
-    code = code + 8 * np.signbit(g)
+    code = code + 8 * (g < 0)  # -0 is written as 0
     return code.reshape(y.shape), np.where(nan, 127, byte)
 
 
