@@ -41,12 +41,12 @@
 namespace pkv {
 namespace {
 
-// Warps of a CTA (one CTA an SM) and copies a warp has in flight, by the rows
-// of a tile.
+// Warps of a CTA (one CTA an SM), and copies of two blocks that a warp has in
+// flight, by the rows of a tile.
 template <int kMaxNt>
 constexpr int kWarps = kMaxNt == 4 ? 8 : 12;
 template <int D, int kMaxNt>
-constexpr int kStages = (D == 64 ? 2 : 1) * (kMaxNt == 1 ? 6 : 4);
+constexpr int kStages = (D == 64 ? 2 : 1) * (kMaxNt == 2 ? 2 : 3);
 
 // Counters of arrivals between calls, so that a workspace that nobody prepared is
 // noticed (every byte 0x5a).
@@ -66,7 +66,7 @@ struct Kv4Args {
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -82,28 +82,29 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
-// What a lane reads of a tile (lane 4 g + t).
+template <int D>
+constexpr int kQBytes = 4 * (D / 16) * 2 * 32 * 4;  // q's fragments of 32 rows
+
+// What a lane (4 g + t) reads of a tile: K of two tokens, V of two pairs of tokens.
 template <int D>
 struct Lane {
-    static constexpr int kW = D / 32;  // words of codes a lane has of a K token, and of a pair of V tokens
-    uint32_t k[2][kW], v[2][kW], ks, vs;
+    static constexpr int kW = D / 32;  // words of codes of each
 
-    __device__ __forceinline__ void load(uint32_t tile, int lane) {
+    static __device__ __forceinline__ void load_k(uint32_t tile, int lane, uint32_t (&k)[2][kW], uint32_t &scales) {
         if constexpr (D == 128) {
             lds(k[0], tile + 16 * lane);
             lds(k[1], tile + 4 * D + 16 * lane);
-            lds(v[0], tile + 8 * D + 16 * lane);
-            lds(v[1], tile + 12 * D + 16 * lane);
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ks) : "r"(tile + 16 * D + 4 * lane));
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vs) : "r"(tile + 17 * D + 4 * lane));
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(scales) : "r"(tile + 16 * D + 4 * lane));
         } else {
             lds(k[0], tile + 8 * lane);
             lds(k[1], tile + 4 * D + 8 * lane);
-            lds(v[0], tile + 8 * D + 8 * lane);
-            lds(v[1], tile + 12 * D + 8 * lane);
-            asm volatile("{\n\t.reg .b16 s;\n\tld.shared.b16 s, [%1];\n\tcvt.u32.u16 %0, s;\n\t}" : "=r"(ks) : "r"(tile + 16 * D + 2 * lane));
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vs) : "r"(tile + 17 * D + 16 * (lane >> 3) + 4 * (lane & 3)));
+            asm volatile("{\n\t.reg .b16 s;\n\tld.shared.b16 s, [%1];\n\tcvt.u32.u16 %0, s;\n\t}" : "=r"(scales) : "r"(tile + 16 * D + 2 * lane));
         }
+    }
+    static __device__ __forceinline__ void load_v(uint32_t tile, int lane, uint32_t (&v)[2][kW], uint32_t &scales) {
+        lds(v[0], tile + 8 * D + 4 * kW * lane);
+        lds(v[1], tile + 12 * D + 4 * kW * lane);
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(scales) : "r"(tile + 17 * D + (D == 128 ? 4 * lane : 16 * (lane >> 3) + 4 * (lane & 3))));
     }
     static __device__ __forceinline__ void lds(uint32_t (&w)[4], uint32_t at) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
@@ -113,14 +114,31 @@ struct Lane {
     }
 };
 
+// Where a pair of blocks lies among its item's rows.
+struct Span {
+    int key0;    // position of the first block's first key
+    int limit0;  // keys that the tile's first row sees
+    int end;     // keys that its last row sees
+    int row0, group;
+
+    // keys of block `blk` that row `row` of the tile sees (at most 16 count)
+    __device__ __forceinline__ int sees(int blk, int row) const {
+        return limit0 + (row0 + row) / group - row0 / group - key0 - 16 * blk;
+    }
+};
+
 // A whole warp's state for one item of up to 8 kNt rows. Of O^T a lane holds,
-// for rows 8 n + 2 t and 8 n + 2 t + 1, the D / 8 columns from D / 8 * g on.
-template <int D, int kNt, int kStg>
+// for rows 8 n + 2 t and 8 n + 2 t + 1, the D / 8 columns from D / 8 * g on. With
+// 32 rows q's fragments lie in shared memory: registers are full of O.
+template <int D, int kNt>
 struct Item {
     static constexpr int kK = D / 16;  // steps of 16 columns
+    static constexpr int kW = Lane<D>::kW;
+    static constexpr bool kQShared = kNt == 4;
     float o[kNt][kK][4];
     float2 m[kNt], l[kNt], mul[kNt];
-    uint32_t q[kNt][kK][2];
+    uint32_t q[kQShared ? 1 : kNt][kQShared ? 1 : kK][2];
+    uint32_t q_at;  // shared address, this lane's
 
     // q rows as fp16 fragments, each scaled by a power of two to lie in (-4, 4);
     // mul takes that back. Rows past `rows` are zero.
@@ -157,10 +175,16 @@ struct Item {
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t f[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    q[n][2 * i + j / 2][j & 1] =
-                        pack_f16x2(__uint_as_float(x[j] << 16) * down, __uint_as_float(x[j] & 0xffff0000u) * down);
+                for (int j = 0; j < 4; ++j) f[j] = pack_f16x2(__uint_as_float(x[j] << 16) * down, __uint_as_float(x[j] & 0xffff0000u) * down);
+                if constexpr (kQShared) {
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_at + 512 * (n * kW + i)), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3])
+                                 : "memory");
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) q[n][2 * i + j / 2][j & 1] = f[j];
+                }
             }
             const float f = row < rows ? up * a.scale_log2 : 0.0f;
             mul[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
@@ -182,12 +206,12 @@ struct Item {
         m = to;
         l *= *f;
     }
-    __device__ __forceinline__ void move_references(const float (&s)[kNt][4]) {
+    __device__ __forceinline__ void move_references(const float (&s)[2][kNt][4]) {
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
             float fx, fy;
-            move(m[n].x, l[n].x, mul[n].x, fmaxf(s[n][0], s[n][2]), &fx);
-            move(m[n].y, l[n].y, mul[n].y, fmaxf(s[n][1], s[n][3]), &fy);
+            move(m[n].x, l[n].x, mul[n].x, fmaxf(fmaxf(s[0][n][0], s[0][n][2]), fmaxf(s[1][n][0], s[1][n][2])), &fx);
+            move(m[n].y, l[n].y, mul[n].y, fmaxf(fmaxf(s[0][n][1], s[0][n][3]), fmaxf(s[1][n][1], s[1][n][3])), &fy);
 #pragma unroll
             for (int i = 0; i < kK; ++i) {
                 o[n][i][0] *= fx;
@@ -197,99 +221,146 @@ struct Item {
             }
         }
     }
-
-    // One block. key0: its first key's position; kMasked: rows end within it, row
-    // r (of the tile) at limit0 + (row0 + r) / group - first token.
+    // Scores to exponents of 2 against the references (0 where a row has none yet:
+    // it has seen no key, and all its scores are -inf); returns the largest.
     template <bool kMasked>
-    __device__ __forceinline__ void block(Lane<D> &x, bool first, int key0, int limit0, int row0, int group, int lane) {
-        const int g = lane >> 2, t = lane & 3;
-        float s[kNt][4];
-#pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[n][c] = 0.0f;
-        // K scales: tokens g and g + 8, one or two groups of this lane's quarter
-        __half2 sc[2][2];
-        {
-            if constexpr (D == 128) {
-                const __half2 a = kv4_scales(x.ks), b = kv4_scales(x.ks >> 16);
-                sc[0][0] = __low2half2(a);
-                sc[0][1] = __high2half2(a);
-                sc[1][0] = __low2half2(b);
-                sc[1][1] = __high2half2(b);
-            } else {
-                const __half2 a = kv4_scales(x.ks);
-                sc[0][0] = sc[0][1] = __low2half2(a);
-                sc[1][0] = sc[1][1] = __high2half2(a);
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < Lane<D>::kW; ++w) {
-            const int p = w * 2 / Lane<D>::kW;
-            {
-                const uint32_t f[4] = {as_u32(__hmul2(kv4_pair<0>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<0>(x.k[1][w]), sc[1][p])),
-                                       as_u32(__hmul2(kv4_pair<1>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<1>(x.k[1][w]), sc[1][p]))};
-#pragma unroll
-                for (int n = 0; n < kNt; ++n) mma_f16(s[n], f, q[n][2 * w][0], q[n][2 * w][1]);
-            }
-            {
-                const uint32_t f[4] = {as_u32(__hmul2(kv4_pair<2>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<2>(x.k[1][w]), sc[1][p])),
-                                       as_u32(__hmul2(kv4_pair<3>(x.k[0][w]), sc[0][p])), as_u32(__hmul2(kv4_pair<3>(x.k[1][w]), sc[1][p]))};
-#pragma unroll
-                for (int n = 0; n < kNt; ++n) mma_f16(s[n], f, q[n][2 * w + 1][0], q[n][2 * w + 1][1]);
-            }
-        }
-        if constexpr (kMasked) {
-#pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-                const int ra = row0 + 8 * n + 2 * t, first_tok = row0 / group;
-                const int la = limit0 + ra / group - first_tok - key0, lb = limit0 + (ra + 1) / group - first_tok - key0;
-                if (g >= la) s[n][0] = -INFINITY;
-                if (g >= lb) s[n][1] = -INFINITY;
-                if (g + 8 >= la) s[n][2] = -INFINITY;
-                if (g + 8 >= lb) s[n][3] = -INFINITY;
-            }
-            move_references(s);
-        } else {
-            float top = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-                const float2 a = fmul2(fadd2(make_float2(s[n][0], s[n][1]), make_float2(-m[n].x, -m[n].y)), mul[n]);
-                const float2 b = fmul2(fadd2(make_float2(s[n][2], s[n][3]), make_float2(-m[n].x, -m[n].y)), mul[n]);
-                top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
-            }
-            if (__any_sync(0xffffffffu, top > 10.0f) || first) move_references(s);
-        }
-        uint32_t p[kNt][2];
+    __device__ __forceinline__ float exponents(const float (&s)[2][kNt][4], float (&e)[2][kNt][4]) const {
+        float top = -INFINITY;
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
-            // a row that has seen no key yet has no reference: its scores are all -inf
             const float mx = kMasked && m[n].x == -INFINITY ? 0.0f : m[n].x, my = kMasked && m[n].y == -INFINITY ? 0.0f : m[n].y;
-            const float2 a = fmul2(fadd2(make_float2(s[n][0], s[n][1]), make_float2(-mx, -my)), mul[n]);
-            const float2 b = fmul2(fadd2(make_float2(s[n][2], s[n][3]), make_float2(-mx, -my)), mul[n]);
-            float e[4] = {fast_exp2(a.x), fast_exp2(a.y), fast_exp2(b.x), fast_exp2(b.y)};
-            if constexpr (kMasked) {  // a factor of 0 (a scale or q near the smallest value) times -inf is no number
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (s[n][c] == -INFINITY) e[c] = 0.0f;
+            for (int b = 0; b < 2; ++b) {
+                const float2 x = fmul2(fadd2(make_float2(s[b][n][0], s[b][n][1]), make_float2(-mx, -my)), mul[n]);
+                const float2 y = fmul2(fadd2(make_float2(s[b][n][2], s[b][n][3]), make_float2(-mx, -my)), mul[n]);
+                e[b][n][0] = x.x, e[b][n][1] = x.y, e[b][n][2] = y.x, e[b][n][3] = y.y;
+                if (!kMasked) top = fmax3(top, fmax3(x.x, x.y, y.x), y.y);
             }
-            l[n] = fadd2(l[n], fadd2(make_float2(e[0], e[1]), make_float2(e[2], e[3])));
-            p[n][0] = movmatrix_trans(pack_f16x2(e[0], e[1]));
-            p[n][1] = movmatrix_trans(pack_f16x2(e[2], e[3]));
         }
-        __half2 va = kv4_scales(x.vs), vb = kv4_scales(x.vs >> 16);  // tokens 2 t, 2 t + 1 and 8 on
+        return top;
+    }
+
+    // Two blocks at `tile` and behind it; between(): called when both are read.
+    // kMasked: some row does not see all of their keys.
+    template <bool kMasked, typename Between>
+    __device__ __forceinline__ void blocks(uint32_t tile, bool first, const Span &at, Between between, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        float s[2][kNt][4];
+        {
+            uint32_t k[2][2][kW], ks[2];
+            Lane<D>::load_k(tile, lane, k[0], ks[0]);
+            Lane<D>::load_k(tile + Kv4Tile<D>::kBytes, lane, k[1], ks[1]);
+            // scales: tokens g and g + 8, one or two groups of this lane's quarter
+            __half2 sc[2][2][2];
 #pragma unroll
-        for (int w = 0; w < Lane<D>::kW / 2; ++w) {
-            // low and high codes of two tokens side by side
-            constexpr int kH = Lane<D>::kW / 2;
-            const uint32_t a0 = x.v[0][w], a1 = x.v[0][w + kH], b0 = x.v[1][w], b1 = x.v[1][w + kH];
-            const uint32_t lo = 0x0f0f0f0fu;
-            const uint32_t ae = (a0 & lo) | ((a1 << 4) & ~lo), ao = ((a0 >> 4) & lo) | (a1 & ~lo);
-            const uint32_t be = (b0 & lo) | ((b1 << 4) & ~lo), bo = ((b0 >> 4) & lo) | (b1 & ~lo);
-            pv<0>(4 * w, ae, ao, be, bo, va, vb, p);
-            pv<1>(4 * w + 1, ae, ao, be, bo, va, vb, p);
-            pv<2>(4 * w + 2, ae, ao, be, bo, va, vb, p);
-            pv<3>(4 * w + 3, ae, ao, be, bo, va, vb, p);
+            for (int b = 0; b < 2; ++b) {
+                if constexpr (D == 128) {
+                    const __half2 x = kv4_scales(ks[b]), y = kv4_scales(ks[b] >> 16);
+                    sc[b][0][0] = __low2half2(x), sc[b][0][1] = __high2half2(x);
+                    sc[b][1][0] = __low2half2(y), sc[b][1][1] = __high2half2(y);
+                } else {
+                    const __half2 x = kv4_scales(ks[b]);
+                    sc[b][0][0] = sc[b][0][1] = __low2half2(x);
+                    sc[b][1][0] = sc[b][1][1] = __high2half2(x);
+                }
+#pragma unroll
+                for (int n = 0; n < kNt; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[b][n][c] = 0.0f;
+            }
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                const int p = w * 2 / kW;
+                uint32_t f[2][2][4];  // of each block: two steps
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t x = k[b][0][w], y = k[b][1][w];
+                    f[b][0][0] = as_u32(__hmul2(kv4_pair<0>(x), sc[b][0][p])), f[b][0][1] = as_u32(__hmul2(kv4_pair<0>(y), sc[b][1][p]));
+                    f[b][0][2] = as_u32(__hmul2(kv4_pair<1>(x), sc[b][0][p])), f[b][0][3] = as_u32(__hmul2(kv4_pair<1>(y), sc[b][1][p]));
+                    f[b][1][0] = as_u32(__hmul2(kv4_pair<2>(x), sc[b][0][p])), f[b][1][1] = as_u32(__hmul2(kv4_pair<2>(y), sc[b][1][p]));
+                    f[b][1][2] = as_u32(__hmul2(kv4_pair<3>(x), sc[b][0][p])), f[b][1][3] = as_u32(__hmul2(kv4_pair<3>(y), sc[b][1][p]));
+                }
+#pragma unroll
+                for (int n = 0; n < kNt; ++n) {
+                    uint32_t qf[4];
+                    if constexpr (kQShared) {
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(qf[0]), "=r"(qf[1]), "=r"(qf[2]), "=r"(qf[3])
+                                     : "r"(q_at + 512 * (n * kW + w)));
+                    } else {
+                        qf[0] = q[n][2 * w][0], qf[1] = q[n][2 * w][1], qf[2] = q[n][2 * w + 1][0], qf[3] = q[n][2 * w + 1][1];
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) mma_f16(s[b][n], f[b][0], qf[0], qf[1]);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) mma_f16(s[b][n], f[b][1], qf[2], qf[3]);
+                }
+            }
+        }
+        float e[2][kNt][4];
+        if constexpr (kMasked) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int n = 0; n < kNt; ++n) {
+                    const int x = at.sees(b, 8 * n + 2 * t), y = at.sees(b, 8 * n + 2 * t + 1);
+                    // never past the last row's keys: rows of padding would see more, and the
+                    // second block may be missing
+                    if (g >= min(x, at.end - at.key0 - 16 * b)) s[b][n][0] = -INFINITY;
+                    if (g >= min(y, at.end - at.key0 - 16 * b)) s[b][n][1] = -INFINITY;
+                    if (g + 8 >= min(x, at.end - at.key0 - 16 * b)) s[b][n][2] = -INFINITY;
+                    if (g + 8 >= min(y, at.end - at.key0 - 16 * b)) s[b][n][3] = -INFINITY;
+                }
+            move_references(s);
+            exponents<true>(s, e);
+        } else {
+            const float top = exponents<false>(s, e);
+            if (__any_sync(0xffffffffu, top > 10.0f) || first) {
+                move_references(s);
+                exponents<false>(s, e);
+            }
+        }
+        uint32_t p[2][kNt][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int n = 0; n < kNt; ++n) {
+                float x[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    x[c] = fast_exp2(e[b][n][c]);
+                    // a factor of 0 (a scale or q near the smallest value) times -inf is no number
+                    if (kMasked && s[b][n][c] == -INFINITY) x[c] = 0.0f;
+                }
+                l[n] = fadd2(l[n], fadd2(make_float2(x[0], x[1]), make_float2(x[2], x[3])));
+                p[b][n][0] = movmatrix_trans(pack_f16x2(x[0], x[1]));
+                p[b][n][1] = movmatrix_trans(pack_f16x2(x[2], x[3]));
+            }
+        uint32_t v[2][2][kW], vs[2];
+        Lane<D>::load_v(tile, lane, v[0], vs[0]);
+        Lane<D>::load_v(tile + Kv4Tile<D>::kBytes, lane, v[1], vs[1]);
+        __syncwarp();
+        between();
+        if constexpr (kMasked) {
+            guard(vs[0], 0, at, lane);
+            guard(vs[1], 1, at, lane);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const __half2 va = kv4_scales(vs[b]), vb = kv4_scales(vs[b] >> 16);  // tokens 2 t, 2 t + 1 and 8 on
+#pragma unroll
+            for (int w = 0; w < kW / 2; ++w) {
+                // low and high codes of two tokens side by side
+                constexpr int kH = kW / 2;
+                const uint32_t a0 = v[b][0][w], a1 = v[b][0][w + kH], b0 = v[b][1][w], b1 = v[b][1][w + kH];
+                const uint32_t lo = 0x0f0f0f0fu;
+                const uint32_t ae = (a0 & lo) | ((a1 << 4) & ~lo), ao = ((a0 >> 4) & lo) | (a1 & ~lo);
+                const uint32_t be = (b0 & lo) | ((b1 << 4) & ~lo), bo = ((b0 >> 4) & lo) | (b1 & ~lo);
+                pv<0>(4 * w, ae, ao, be, bo, va, vb, p[b]);
+                pv<1>(4 * w + 1, ae, ao, be, bo, va, vb, p[b]);
+                pv<2>(4 * w + 2, ae, ao, be, bo, va, vb, p[b]);
+                pv<3>(4 * w + 3, ae, ao, be, bo, va, vb, p[b]);
+            }
         }
     }
     template <int kB>
@@ -352,25 +423,23 @@ struct Item {
         }
     }
 
-    // V scales of tokens at or past `end` (of this block) become zero, and those
-    // that are no number too: the rows that see their token become NaN here,
-    // in this lane's columns, the others must not.
-    __device__ __forceinline__ void guard(Lane<D> &x, int end, int key0, int limit0, int row0, int group, int lane) {
-        const int t = lane & 3;
+    // V scales of tokens that no row sees become zero, and those that are no
+    // number too: the rows that see their token become NaN here, in this lane's
+    // columns, the others must not.
+    __device__ __forceinline__ void guard(uint32_t &vs, int blk, const Span &at, int lane) {
+        const int t = lane & 3, end = at.end - at.key0 - 16 * blk;
         uint32_t bad = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int tok = 8 * (i >> 1) + 2 * t + (i & 1);
-            const uint32_t byte = x.vs >> (8 * i) & 0x7fu;
-            if (tok >= end)
-                x.vs &= ~(0xffu << (8 * i));
-            else if (byte == 0x7fu)
+            if (tok >= end) {
+                vs &= ~(0xffu << (8 * i));
+            } else if ((vs >> (8 * i) & 0x7fu) == 0x7fu) {
+                vs &= ~(0xffu << (8 * i));
                 bad |= 1u << tok;
+            }
         }
         if (!__any_sync(0xffffffffu, bad != 0)) return;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if ((x.vs >> (8 * i) & 0x7fu) == 0x7fu) x.vs &= ~(0xffu << (8 * i));
         bad |= __shfl_xor_sync(0xffffffffu, bad, 1);  // the four lanes of one g: the same columns
         bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
         const float nan = __uint_as_float(0x7fffffffu);
@@ -378,7 +447,7 @@ struct Item {
         for (int n = 0; n < kNt; ++n) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int lim = limit0 + (row0 + 8 * n + 2 * t + c) / group - row0 / group - key0;
+                const int lim = at.sees(blk, 8 * n + 2 * t + c);
                 const uint32_t sees = lim >= 16 ? 0xffffu : lim <= 0 ? 0u : (1u << lim) - 1;
                 if (bad & sees)
 #pragma unroll
@@ -388,20 +457,37 @@ struct Item {
     }
 };
 
-// Everything a warp needs of its ring.
+// A warp's ring of pairs of tiles.
 template <int D, int kStg>
 struct Ring {
-    uint32_t buf, bar;  // shared addresses
-    uint32_t at;        // blocks taken so far
-    uint32_t issued;    // copies started so far
+    uint32_t buf, bar;              // shared addresses
+    uint32_t take, take_parity;     // the next pair to be read
+    uint32_t put;                   // the next one to be copied
+    uint32_t out;                   // pairs on their way
+    static constexpr uint32_t kPair = 2 * Kv4Tile<D>::kBytes;
 
-    __device__ __forceinline__ void start(const uint8_t *src, int lane) {
-        const uint32_t st = issued % kStg;
-        if (lane == 0) {
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar + 8 * st), "r"(Kv4Tile<D>::kBytes) : "memory");
-            bulk_copy(buf + st * Kv4Tile<D>::kBytes, src, Kv4Tile<D>::kBytes, bar + 8 * st);
+    __device__ __forceinline__ uint32_t tile() const { return buf + take * kPair; }
+    __device__ __forceinline__ uint32_t taking() const { return bar + 8 * take; }
+    __device__ __forceinline__ void taken() {
+        --out;
+        if (++take == kStg) {
+            take = 0;
+            take_parity ^= 1;
         }
-        ++issued;
+    }
+    // Two lanes start a copy each, or say that there is none.
+    __device__ __forceinline__ void start(int which, bool there, const uint8_t *src) {
+        const uint32_t b = bar + 8 * put;
+        if (which == 0 || which == 1) {
+            if (there) {
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(Kv4Tile<D>::kBytes) : "memory");
+                bulk_copy(buf + put * kPair + which * Kv4Tile<D>::kBytes, src, Kv4Tile<D>::kBytes, b);
+            } else {
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+            }
+        }
+        ++out;
+        if (++put == kStg) put = 0;
     }
 };
 
@@ -417,7 +503,8 @@ struct Team {
     int first, last;        // the item's shares
     bool begun, cut;        // it began in a share before this one, it ends in one behind
     Kv4Shares sh;
-    uint8_t *area;          // shared memory: a partial of each warp
+    float4 *area;           // a partial of each warp
+    uint32_t q;             // shared address of this warp's q fragments (32 rows)
     volatile int *abort;
     bool met;               // this warp has been at the CTA's barrier
 };
@@ -427,74 +514,67 @@ struct Kernel {
     static constexpr int kStg = kStages<D, kMaxNt>;
     static constexpr int kW = kWarps<kMaxNt>;
     static constexpr int kRows = 8 * kMaxNt;
-    static constexpr int kMinShare = 8 * 16 * 4;  // eight blocks of a decode token
-    static constexpr size_t kRing = (size_t)kW * kStg * Kv4Tile<D>::kBytes;
-    static constexpr int kArea = Item<D, kMaxNt, kStg>::kVecs * 512;    // bytes of a partial in shared memory
-    static constexpr int kPart = (Item<D, kMaxNt, kStg>::kVecs + kMaxNt) * 32;  // float4 of one in the workspace
-    static constexpr size_t kSmem = kRing + (size_t)kW * kArea;
+    static constexpr size_t kRing = (size_t)kW * kStg * 2 * Kv4Tile<D>::kBytes;
+    static constexpr int kArea = Item<D, kMaxNt>::kVecs * 32;             // float4 of a warp's partial
+    static constexpr int kPart = (Item<D, kMaxNt>::kVecs + kMaxNt) * 32;  // float4 of one for another CTA
+    // With 32 rows shared memory holds q's fragments, and the warps' partials lie
+    // in the workspace.
+    static constexpr bool kAreaShared = kMaxNt < 4;
+    static constexpr size_t kSmem = kRing + (size_t)kW * (kAreaShared ? kArea * 16 : kQBytes<D>);
 
     // Blocks [b0, b1) of an item; false: a wait gave up.
     template <int kNt>
     static __device__ bool run(const Kv4Args &a, Ring<D, kStg> &ring, const Where &w, const Kv4Tiling &tl, int b0, int b1,
                                Team &team, int lane) {
-        Item<D, kNt, kStg> it;
+        Item<D, kNt> it;
+        it.q_at = team.q + 16 * lane;
         const int row0 = w.i * kRows, rows = tl.rows;
         const int32_t *ids = a.table + (long long)w.r * a.max_blocks;
         const uint8_t *heads = a.pool + (long long)w.h * Kv4Tile<D>::kBytes;
         const long long block_bytes = (long long)a.num_kv_heads * Kv4Tile<D>::kBytes;
         int bits = 0;
-        // ids are looked up 32 at a time, the next 32 ahead
+        // ids are looked up 32 at a time, the next 32 ahead; a lane copies its own block
         int have = b0 + lane < b1 ? __ldg(ids + b0 + lane) : 0;
         int next = b0 + 32 + lane < b1 ? __ldg(ids + b0 + 32 + lane) : 0;
-        int base = b0;  // of `have`
-        int put = b0;   // next block to copy
+        int put = b0;  // next pair to copy
         auto start = [&]() {
-            if (put - base == 32) {
-                base += 32;
+            const int at = (put - b0) & 31;
+            if (at == 0 && put > b0) {
                 have = next;
-                next = base + 32 + lane < b1 ? __ldg(ids + base + 32 + lane) : 0;
+                next = put + 32 + lane < b1 ? __ldg(ids + put + 32 + lane) : 0;
             }
-            int id = __shfl_sync(0xffffffffu, have, put - base);
-            if (id < 0 || id >= a.num_blocks) {
-                bits = PKV_DEV_BAD_BLOCK;
-                id = 0;
-            }
-            ring.start(heads + id * block_bytes, lane);
-            ++put;
+            const bool bad = have < 0 || have >= a.num_blocks;
+            if (bad) bits = PKV_DEV_BAD_BLOCK;
+            ring.start(lane - at, put + lane - at < b1, heads + (bad ? 0 : have) * block_bytes);
+            put += 2;
         };
 #pragma unroll 1
         for (int i = 0; i < kStg && put < b1; ++i) start();
         it.load_q(a, w.q.q0, row0, rows, w.h, lane);
-        const int limit0 = w.q.len - w.q.n + row0 / a.group + 1;  // keys that the first row sees
-        const int plain = limit0 / 16;                            // blocks that every row sees whole
-        const int end = tl.keys;                                  // keys that the last row sees
+        if (Item<D, kNt>::kQShared) __syncwarp();
+        Span at{16 * b0, w.q.len - w.q.n + row0 / a.group + 1, tl.keys, row0, a.group};
 #pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const uint32_t st = ring.at % kStg;
-            if (!warp_wait(ring.bar + 8 * st, ring.at / kStg & 1, team.abort)) return false;
-            Lane<D> x;
-            x.load(ring.buf + st * Kv4Tile<D>::kBytes, lane);
-            ++ring.at;
-            __syncwarp();
-            if (put < b1) start();
-            if (b < plain) {
-                it.template block<false>(x, b == b0, 16 * b, 0, 0, 1, lane);
-            } else {
-                it.guard(x, end - 16 * b, 16 * b, limit0, row0, a.group, lane);
-                it.template block<true>(x, b == b0, 16 * b, limit0, row0, a.group, lane);
-            }
+        for (int b = b0; b < b1; b += 2, at.key0 += 32) {
+            if (!warp_wait(ring.taking(), ring.take_parity, team.abort)) return false;
+            const uint32_t tile = ring.tile();
+            ring.taken();
+            auto between = [&]() {
+                if (put < b1) start();
+            };
+            if (at.key0 + 32 <= at.limit0 && b + 1 < b1) it.template blocks<false>(tile, b == b0, at, between, lane);
+            else it.template blocks<true>(tile, b == b0, Span{at.key0, at.limit0, min(at.end, 16 * b1), row0, a.group}, between, lane);
         }
-        if (bits && lane == 0) raise_status(a.status, bits);
+        if (__any_sync(0xffffffffu, bits != 0) && lane == 0) raise_status(a.status, PKV_DEV_BAD_BLOCK);
         hand_over<kNt>(a, it, w, row0, rows, team, lane);
         return true;
     }
 
     // An item's end in this share: its output, or this share's part of it.
     template <int kNt>
-    static __device__ __forceinline__ void hand_over(const Kv4Args &a, Item<D, kNt, kStg> &it, const Where &w, int row0, int rows,
+    static __device__ __forceinline__ void hand_over(const Kv4Args &a, Item<D, kNt> &it, const Where &w, int row0, int rows,
                                                      Team &team, int lane) {
         if (team.begun && team.warp > 0) {  // for the first of its warps in this CTA
-            it.template store<false>(reinterpret_cast<float4 *>(team.area + team.warp * kArea), lane);
+            it.template store<false>(team.area + team.warp * kArea, lane);
             return;
         }
         const int base = team.cta * team.sh.per_cta;
@@ -504,7 +584,7 @@ struct Kernel {
             if (*team.abort) return;
             const int upto = min(team.last - base, team.shares - 1);
             for (int i = team.warp + 1; i <= upto; ++i)
-                it.template join<false>(reinterpret_cast<const float4 *>(team.area + i * kArea), false, lane);
+                it.template join<false>(team.area + i * kArea, false, lane);
         }
         if (team.first < base || team.last >= base + team.shares) {
             const int c0 = team.first / team.sh.per_cta, n = team.last / team.sh.per_cta - c0 + 1;
@@ -528,7 +608,7 @@ struct Kernel {
     }
 
     template <int kNt>
-    static __device__ __forceinline__ void output(const Kv4Args &a, Item<D, kNt, kStg> &it, const Where &w, int row0, int rows, int lane) {
+    static __device__ __forceinline__ void output(const Kv4Args &a, Item<D, kNt> &it, const Where &w, int row0, int rows, int lane) {
         constexpr int kC = D / 8;  // columns a lane holds
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -579,7 +659,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     __shared__ long long s_sum[kThreads], s_warp[K::kW];
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
-    for (int i = tid; i < K::kW * K::kStg; i += kThreads) mbar_init(s_bar + i, 1);
+    for (int i = tid; i < K::kW * K::kStg; i += kThreads) mbar_init(s_bar + i, 2);
     if (tid == 0) s_abort = 0;
     mbar_fence_init();
     pdl_launch_dependents();
@@ -614,17 +694,19 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     __syncthreads();
 
     Team team;
-    team.sh = kv4_shares(total, (int)gridDim.x, K::kW, K::kMinShare);
+    team.sh = kv4_shares(total, (int)gridDim.x, K::kW, kv4_least(K::kRows));
     team.warp = warp;
     team.cta = cta;
     team.shares = min(team.sh.per_cta, team.sh.count - cta * team.sh.per_cta);
-    team.area = s_mem + K::kRing;
+    team.area = K::kAreaShared ? reinterpret_cast<float4 *>(s_mem + K::kRing)
+                               : a.parts + (size_t)2 * gridDim.x * K::kPart + (size_t)cta * K::kW * K::kArea;
+    team.q = smem_u32(s_mem + K::kRing) + warp * kQBytes<D>;
     team.abort = &s_abort;
     team.met = false;
     if (team.shares <= 0) return;
     if (warp < team.shares) {
         const int share = cta * team.sh.per_cta + warp;
-        const long long from = team.sh.begin(share), to = team.sh.begin(share + 1);
+        const long long from = team.sh.begin(share);
         int none = 0;
         Where w;
         {
@@ -643,30 +725,28 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
             kv4_locate(w.q, a.num_kv_heads, from - first, &w.i, &w.h, &w.start);
             w.start += first;
         }
-        Ring<D, K::kStg> ring{smem_u32(s_mem) + (uint32_t)(warp * K::kStg * Kv4Tile<D>::kBytes), smem_u32(s_bar + warp * K::kStg), 0, 0};
+        Ring<D, K::kStg> ring{smem_u32(s_mem) + (uint32_t)warp * K::kStg * Ring<D, K::kStg>::kPair, smem_u32(s_bar + warp * K::kStg), 0, 0, 0, 0};
         while (true) {
             const Kv4Tiling tl = kv4_tile(w.q, w.i, a.group, K::kRows);
-            const long long cost = kv4_item_cost(w.q, w.i), stop = w.start + cost;
-            team.begun = w.start < from;
-            team.cut = stop > to;
-            team.first = team.begun ? team.sh.index(w.start) : share;
-            team.last = team.cut ? team.sh.index(stop - 1) : share;
-            const int b0 = team.begun ? kv4_block_at(from - w.start, cost, tl.blocks) : 0;
-            const int b1 = team.cut ? kv4_block_at(to - w.start, cost, tl.blocks) : tl.blocks;
-            bool ok;
-            if (kMaxNt == 1 || tl.rows <= 8) ok = K::template run<1>(a, ring, w, tl, b0, b1, team, lane);
-            else if (kMaxNt == 2 || tl.rows <= 16) ok = K::template run<kMaxNt >= 2 ? 2 : 1>(a, ring, w, tl, b0, b1, team, lane);
-            else ok = K::template run<kMaxNt>(a, ring, w, tl, b0, b1, team, lane);
-            if (!ok) {
-                // nothing may still be on its way into this SM's memory when the CTA ends
-                int never = 0;
-                for (; ring.at < ring.issued; ++ring.at)
-                    if (!warp_wait(ring.bar + 8 * (ring.at % K::kStg), ring.at / K::kStg & 1, &never)) break;
-                if (lane == 0) raise_status(a.status, PKV_DEV_TIMEOUT);
-                break;
+            const long long cost = kv4_item_cost(w.q, w.i);
+            const Kv4Piece p = kv4_piece(team.sh, share, w.start, cost, tl.blocks);
+            if (p.b0 < p.b1) {
+                team.begun = p.begun, team.cut = p.cut, team.first = p.first, team.last = p.last;
+                bool ok;
+                if (kMaxNt == 1 || tl.rows <= 8) ok = K::template run<1>(a, ring, w, tl, p.b0, p.b1, team, lane);
+                else if (kMaxNt == 2 || tl.rows <= 16) ok = K::template run<kMaxNt >= 2 ? 2 : 1>(a, ring, w, tl, p.b0, p.b1, team, lane);
+                else ok = K::template run<kMaxNt>(a, ring, w, tl, p.b0, p.b1, team, lane);
+                if (!ok) {
+                    // nothing may still be on its way into this SM's memory when the CTA ends
+                    int never = 0;
+                    for (; ring.out; ring.taken())
+                        if (!warp_wait(ring.taking(), ring.take_parity, &never)) break;
+                    if (lane == 0) raise_status(a.status, PKV_DEV_TIMEOUT);
+                    break;
+                }
             }
-            if (stop >= to) break;
-            w.start = stop;
+            if (!p.more) break;
+            w.start += cost;
             if (++w.h == a.num_kv_heads) {
                 w.h = 0;
                 if (++w.i == w.q.tiles) {
@@ -684,7 +764,8 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
 // Places in the workspace, for any batch and form.
 size_t parts_at(int sms) { return ((size_t)sms * sizeof(int) + 255) / 256 * 256; }
 size_t workspace_bytes(int sms, int head_size) {
-    return parts_at(sms) + (size_t)2 * sms * sizeof(float4) * (head_size == 128 ? Kernel<128, 4>::kPart : Kernel<64, 4>::kPart);
+    return parts_at(sms) + (size_t)sms * sizeof(float4) * (head_size == 128 ? 2 * Kernel<128, 4>::kPart + kWarps<4> * Kernel<128, 4>::kArea
+                                                                            : 2 * Kernel<64, 4>::kPart + kWarps<4> * Kernel<64, 4>::kArea);
 }
 
 std::mutex g_mu;

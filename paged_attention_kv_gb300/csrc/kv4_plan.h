@@ -85,11 +85,13 @@ PKV_HD Kv4Tiling kv4_tile(const Kv4Request &q, int i, int group, int rows) {
     return t;
 }
 
-// The block at which position `off` of an item of this cost lies: both shares
-// that meet there work it out alike, and it does not fall as off rises.
-PKV_HD int kv4_block_at(long long off, long long cost, int blocks) {
-    const int b = (int)((float)off / (float)cost * (float)blocks);
-    return b < blocks ? b : blocks;
+// The block before which an item is cut at its position `off`: an even one (a warp
+// takes two at a time), none and all of them included, so that no piece is
+// shorter than two. Both shares that meet there work it out alike, and it does
+// not fall as off rises.
+PKV_HD int kv4_cut(long long off, long long cost, int blocks) {
+    const int b = (int)((float)off / (float)cost * (float)blocks) & ~1;
+    return b + 2 > blocks ? blocks : b;
 }
 
 struct Kv4Shares {
@@ -100,6 +102,37 @@ struct Kv4Shares {
     // the share that a position lies in
     PKV_HD int index(long long pos) const { return kv4_quotient(pos, each); }
 };
+
+// Share k's piece [b0, b1) of the item that starts at `start`.
+struct Kv4Piece {
+    int b0, b1;
+    bool begun, cut, more;  // it begins in a share before, ends in one behind; the share goes on behind the item
+    int first, last;        // the shares that hold pieces of it
+};
+PKV_HD Kv4Piece kv4_piece(const Kv4Shares &sh, int k, long long start, long long cost, int blocks) {
+    const long long from = sh.begin(k), to = sh.begin(k + 1), stop = start + cost;
+    Kv4Piece p;
+    p.b0 = from > start ? kv4_cut(from - start, cost, blocks) : 0;
+    p.b1 = to < stop ? kv4_cut(to - start, cost, blocks) : blocks;
+    p.begun = p.b0 > 0;
+    p.cut = p.b1 < blocks;
+    p.more = stop < to;
+    p.first = p.last = k;
+    // a cut that moved to the item's start or end takes its share out (only one can:
+    // shares are longer than two blocks)
+    if (p.begun) {
+        p.first = sh.index(start);
+        if (kv4_cut(sh.begin(p.first + 1) - start, cost, blocks) == 0) ++p.first;
+    }
+    if (p.cut) {
+        p.last = sh.index(stop - 1);
+        if (kv4_cut(sh.begin(p.last) - start, cost, blocks) == blocks) --p.last;
+    }
+    return p;
+}
+
+// What a share has at least: four blocks of the rows of a tile.
+PKV_HD int kv4_least(int rows) { return 4 * 16 * kv4_weight(rows); }
 
 // At most ctas * warps shares of at least `least`, over as many CTAs as there are.
 PKV_HD Kv4Shares kv4_shares(long long total, int ctas, int warps, int least) {

@@ -14,10 +14,10 @@ PROGRAM = r"""
 #include <vector>
 #include "kv4_plan.h"
 using namespace pkv;
-// in: reqs group heads rows ctas warps least, then (n, len) of each. Walks every share as a warp of the kernel does.
+// in: reqs group heads rows ctas warps, then (n, len) of each. Walks every share as a warp of the kernel does.
 int main() {
-    int R, group, heads, rows, ctas, warps, least;
-    while (scanf("%d %d %d %d %d %d %d", &R, &group, &heads, &rows, &ctas, &warps, &least) == 7) {
+    int R, group, heads, rows, ctas, warps;
+    while (scanf("%d %d %d %d %d %d", &R, &group, &heads, &rows, &ctas, &warps) == 6) {
         std::vector<Kv4Request> q(R);
         std::vector<long long> first(R + 1, 0);
         int q0 = 0;
@@ -29,9 +29,9 @@ int main() {
             first[r + 1] = first[r] + kv4_cost(q[r], heads, q[r].tiles);
         }
         const long long total = first[R];
-        const Kv4Shares sh = kv4_shares(total, ctas, warps, least);
+        const Kv4Shares sh = kv4_shares(total, ctas, warps, kv4_least(rows));
         if (sh.per_cta > warps || (long long)sh.per_cta * ctas < sh.count) { printf("%d shares, %d a CTA\n", sh.count, sh.per_cta); return 1; }
-        // next block expected of each item, and partials seen / announced
+        // next block expected of each item, and its pieces: seen, told by the first, told by the others
         std::vector<std::vector<int>> next(R), seen(R), told(R);
         for (int r = 0; r < R; ++r) next[r].assign(q[r].tiles * heads, 0), seen[r].assign(q[r].tiles * heads, 0), told[r].assign(q[r].tiles * heads, -1);
         for (int k = 0; k < sh.count; ++k) {
@@ -39,7 +39,8 @@ int main() {
             if (!(from < to)) { printf("empty share %d\n", k); return 1; }
             int r = 0;
             while (first[r + 1] <= from) ++r;
-            int i, h, slots = 0;
+            int i, h, pieces = 0;
+            bool ended = false;
             long long start;
             kv4_locate(q[r], heads, from - first[r], &i, &h, &start);
             start += first[r];
@@ -47,19 +48,24 @@ int main() {
                 const Kv4Tiling tl = kv4_tile(q[r], i, group, rows);
                 const long long cost = kv4_item_cost(q[r], i), stop = start + cost;
                 if (!(start <= from || start < to) || stop <= from || tl.rows < 1 || tl.keys < 1 || tl.keys > q[r].len) { printf("bad item\n"); return 1; }
-                const int b0 = from > start ? kv4_block_at(from - start, cost, tl.blocks) : 0;
-                const int b1 = to < stop ? kv4_block_at(to - start, cost, tl.blocks) : tl.blocks;
-                int &n = next[r][i * heads + h];
-                if (b0 != n || b1 < b0 || b1 > tl.blocks) { printf("blocks %d..%d, %d next\n", b0, b1, n); return 1; }
-                n = b1;
-                const bool begun = start < from, cut = stop > to;
-                if (begun || cut) {
-                    seen[r][i * heads + h]++;
-                    if (begun && slots) { printf("a continued item after another\n"); return 1; }
-                }
-                ++slots;
-                if (!begun && cut) told[r][i * heads + h] = sh.index(stop - 1) - k + 1;
-                if (stop >= to) break;
+                const Kv4Piece p = kv4_piece(sh, k, start, cost, tl.blocks);
+                if (p.b0 < p.b1) {
+                    int &n = next[r][i * heads + h];
+                    if (p.b0 != n || p.b1 > tl.blocks) { printf("blocks %d..%d, %d next\n", p.b0, p.b1, n); return 1; }
+                    n = p.b1;
+                    if (p.begun != (p.b0 > 0) || p.cut != (p.b1 < tl.blocks) || ended || (p.begun && pieces)) { printf("order\n"); return 1; }
+                    if (p.begun || p.cut) {
+                        const int held = p.last - p.first + 1;
+                        int &m = told[r][i * heads + h], &at = seen[r][i * heads + h];
+                        if (m < 0) m = held;
+                        if (held != m || p.first + at != k || (p.cut && (tl.blocks < 4 || p.b1 - p.b0 < 2))) { printf("shares %d..%d, %d of %d seen by %d\n", p.first, p.last, at, m, k); return 1; }
+                        ++at;
+                    }
+                    ended = p.cut;
+                    ++pieces;
+                } else if (p.b0 > p.b1 || (p.begun && p.cut)) { printf("empty piece\n"); return 1; }
+                if (p.more != (stop < to)) { printf("more\n"); return 1; }
+                if (!p.more) break;
                 start = stop;
                 if (++h == heads) {
                     h = 0;
@@ -105,25 +111,24 @@ def walk(program, batches):
 
 def test_named_batches(program):
     counts = walk(program, [
-        ((8, 4, 8, 152, 12, 512), [(1, 17), (1, 40)]),
-        ((4, 8, 8, 152, 12, 512), [(1, 1)]),
-        ((4, 8, 32, 152, 8, 512), [(0, 0), (512, 512), (0, 5), (1, 2_000_000), (300, 301), (0, 0)]),
-        ((128, 1, 32, 152, 8, 512), [(3, 90)] * 40),
-        ((3, 5, 8, 152, 12, 512), [(7, 1000)] * 9),
-        ((4, 8, 8, 152, 12, 512), [(1, 3000)] * 256),
-        ((4, 8, 8, 152, 12, 512), []), ((4, 8, 8, 152, 12, 512), [(0, 0)] * 7)])
+        ((8, 4, 8, 152, 12), [(1, 17), (1, 40)]),
+        ((4, 8, 8, 152, 12), [(1, 1)]),
+        ((4, 8, 32, 152, 8), [(0, 0), (512, 512), (0, 5), (1, 2_000_000), (300, 301), (0, 0)]),
+        ((128, 1, 32, 152, 8), [(3, 90)] * 40),
+        ((3, 5, 8, 152, 12), [(7, 1000)] * 9),
+        ((4, 8, 8, 152, 12), [(1, 3000)] * 256),
+        ((4, 8, 8, 152, 12), []), ((4, 8, 8, 152, 12), [(0, 0)] * 7)])
     assert counts[-2:] == [0, 0] and counts[5] == 1824
 
 
 def test_random_batches(program):
     rng = random.Random(4)
     batches = []
-    for _ in range(400):
+    for _ in range(1500):
         rows = rng.choice((8, 16, 32))
         reqs = []
         for _ in range(rng.randint(1, 40)):
             n = rng.choice((0, 1, 1, rng.randint(1, 9), rng.randint(1, 400)))
             reqs.append((n, n + rng.choice((0, 0, rng.randint(0, 50), rng.randint(0, 5000)))))
-        batches.append(((rng.choice((1, 2, 3, 4, 5, 8, 16, 33, 128)), rng.randint(1, 8), rows, *rng.choice(((1, 1), (7, 1), (3, 5), (152, 8), (152, 12))),
-                         rng.choice((1, 64, 512, 4096))), reqs))
+        batches.append(((rng.choice((1, 2, 3, 4, 5, 8, 16, 33, 128)), rng.randint(1, 8), rows, *rng.choice(((1, 1), (7, 1), (3, 5), (152, 8), (152, 12)))), reqs))
     walk(program, batches)
