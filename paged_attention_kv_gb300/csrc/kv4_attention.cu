@@ -46,7 +46,7 @@ namespace {
 template <int kMaxNt>
 constexpr int kWarps = kMaxNt == 4 ? 8 : 12;
 template <int D, int kMaxNt>
-constexpr int kStages = (D == 64 ? 2 : 1) * (kMaxNt == 2 ? 2 : 3);
+constexpr int kStages = (D == 64 ? 2 : 1) * 3;
 
 // Counters of arrivals between calls, so that a workspace that nobody prepared is
 // noticed (every byte 0x5a).
@@ -82,8 +82,8 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
-template <int D>
-constexpr int kQBytes = 4 * (D / 16) * 2 * 32 * 4;  // q's fragments of 32 rows
+template <int D, int kNt>
+constexpr int kQBytes = kNt * (D / 16) * 2 * 32 * 4;  // q's fragments of 8 kNt rows
 
 // What a lane (4 g + t) reads of a tile: K of two tokens, V of two pairs of tokens.
 template <int D>
@@ -129,12 +129,12 @@ struct Span {
 
 // A whole warp's state for one item of up to 8 kNt rows. Of O^T a lane holds,
 // for rows 8 n + 2 t and 8 n + 2 t + 1, the D / 8 columns from D / 8 * g on. With
-// 32 rows q's fragments lie in shared memory: registers are full of O.
+// 16 rows or more q's fragments lie in shared memory: registers are full of O.
 template <int D, int kNt>
 struct Item {
     static constexpr int kK = D / 16;  // steps of 16 columns
     static constexpr int kW = Lane<D>::kW;
-    static constexpr bool kQShared = kNt == 4;
+    static constexpr bool kQShared = kNt >= 2;
     float o[kNt][kK][4];
     float2 m[kNt], l[kNt], mul[kNt];
     uint32_t q[kQShared ? 1 : kNt][kQShared ? 1 : kK][2];
@@ -240,12 +240,8 @@ struct Item {
         return top;
     }
 
-    // Two blocks at `tile` and behind it; between(): called when both are read.
-    // kMasked: some row does not see all of their keys.
-    template <bool kMasked, typename Between>
-    __device__ __forceinline__ void blocks(uint32_t tile, bool first, const Span &at, Between between, int lane) {
-        const int g = lane >> 2, t = lane & 3;
-        float s[2][kNt][4];
+    // Scores of the two blocks at `tile` and behind it.
+    __device__ __forceinline__ void scores(uint32_t tile, float (&s)[2][kNt][4], int lane) const {
         {
             uint32_t k[2][2][kW], ks[2];
             Lane<D>::load_k(tile, lane, k[0], ks[0]);
@@ -297,6 +293,13 @@ struct Item {
                 }
             }
         }
+    }
+
+    // Their probabilities, as fragments for the product with V. kMasked: some row
+    // does not see all of their keys.
+    template <bool kMasked>
+    __device__ __forceinline__ void probabilities(float (&s)[2][kNt][4], bool first, const Span &at, uint32_t (&p)[2][kNt][2], int lane) {
+        const int g = lane >> 2, t = lane & 3;
         float e[2][kNt][4];
         if constexpr (kMasked) {
 #pragma unroll
@@ -320,7 +323,6 @@ struct Item {
                 exponents<false>(s, e);
             }
         }
-        uint32_t p[2][kNt][2];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -336,12 +338,17 @@ struct Item {
                 p[b][n][0] = movmatrix_trans(pack_f16x2(x[0], x[1]));
                 p[b][n][1] = movmatrix_trans(pack_f16x2(x[2], x[3]));
             }
+    }
+
+    // O += V P; between(): called when the tiles are read.
+    template <typename Between>
+    __device__ __forceinline__ void values(uint32_t tile, bool masked, const Span &at, const uint32_t (&p)[2][kNt][2], Between between, int lane) {
         uint32_t v[2][2][kW], vs[2];
         Lane<D>::load_v(tile, lane, v[0], vs[0]);
         Lane<D>::load_v(tile + Kv4Tile<D>::kBytes, lane, v[1], vs[1]);
         __syncwarp();
         between();
-        if constexpr (kMasked) {
+        if (masked) {
             guard(vs[0], 0, at, lane);
             guard(vs[1], 1, at, lane);
         }
@@ -504,7 +511,7 @@ struct Team {
     bool begun, cut;        // it began in a share before this one, it ends in one behind
     Kv4Shares sh;
     float4 *area;           // a partial of each warp
-    uint32_t q;             // shared address of this warp's q fragments (32 rows)
+    uint32_t q;             // shared address of this warp's q fragments (16 rows or more)
     volatile int *abort;
     bool met;               // this warp has been at the CTA's barrier
 };
@@ -517,10 +524,10 @@ struct Kernel {
     static constexpr size_t kRing = (size_t)kW * kStg * 2 * Kv4Tile<D>::kBytes;
     static constexpr int kArea = Item<D, kMaxNt>::kVecs * 32;             // float4 of a warp's partial
     static constexpr int kPart = (Item<D, kMaxNt>::kVecs + kMaxNt) * 32;  // float4 of one for another CTA
-    // With 32 rows shared memory holds q's fragments, and the warps' partials lie
-    // in the workspace.
-    static constexpr bool kAreaShared = kMaxNt < 4;
-    static constexpr size_t kSmem = kRing + (size_t)kW * (kAreaShared ? kArea * 16 : kQBytes<D>);
+    // With 16 rows or more shared memory holds q's fragments, and the warps' partials
+    // lie in the workspace (12 times 16 rows of them, or 8 times 32).
+    static constexpr bool kAreaShared = kMaxNt == 1;
+    static constexpr size_t kSmem = kRing + (size_t)kW * (kAreaShared ? kArea * 16 : kQBytes<D, kMaxNt>);
 
     // Blocks [b0, b1) of an item; false: a wait gave up.
     template <int kNt>
@@ -552,17 +559,22 @@ struct Kernel {
         for (int i = 0; i < kStg && put < b1; ++i) start();
         it.load_q(a, w.q.q0, row0, rows, w.h, lane);
         if (Item<D, kNt>::kQShared) __syncwarp();
-        Span at{16 * b0, w.q.len - w.q.n + row0 / a.group + 1, tl.keys, row0, a.group};
+        Span at{16 * b0, w.q.len - w.q.n + row0 / a.group + 1, min(tl.keys, 16 * b1), row0, a.group};
+        auto between = [&]() {
+            if (put < b1) start();
+        };
 #pragma unroll 1
         for (int b = b0; b < b1; b += 2, at.key0 += 32) {
             if (!warp_wait(ring.taking(), ring.take_parity, team.abort)) return false;
             const uint32_t tile = ring.tile();
             ring.taken();
-            auto between = [&]() {
-                if (put < b1) start();
-            };
-            if (at.key0 + 32 <= at.limit0 && b + 1 < b1) it.template blocks<false>(tile, b == b0, at, between, lane);
-            else it.template blocks<true>(tile, b == b0, Span{at.key0, at.limit0, min(at.end, 16 * b1), row0, a.group}, between, lane);
+            const bool masked = at.key0 + 32 > at.limit0 || b + 1 >= b1;
+            float s[2][kNt][4];
+            uint32_t p[2][kNt][2];
+            it.scores(tile, s, lane);
+            if (masked) it.template probabilities<true>(s, b == b0, at, p, lane);
+            else it.template probabilities<false>(s, b == b0, at, p, lane);
+            it.values(tile, masked, at, p, between, lane);
         }
         if (__any_sync(0xffffffffu, bits != 0) && lane == 0) raise_status(a.status, PKV_DEV_BAD_BLOCK);
         hand_over<kNt>(a, it, w, row0, rows, team, lane);
@@ -700,7 +712,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     team.shares = min(team.sh.per_cta, team.sh.count - cta * team.sh.per_cta);
     team.area = K::kAreaShared ? reinterpret_cast<float4 *>(s_mem + K::kRing)
                                : a.parts + (size_t)2 * gridDim.x * K::kPart + (size_t)cta * K::kW * K::kArea;
-    team.q = smem_u32(s_mem + K::kRing) + warp * kQBytes<D>;
+    team.q = smem_u32(s_mem + K::kRing) + warp * kQBytes<D, kMaxNt>;
     team.abort = &s_abort;
     team.met = false;
     if (team.shares <= 0) return;

@@ -29,10 +29,10 @@ struct Kv4Tiling {
     int rows, keys, blocks;  // rows of the tile, keys its last row sees, blocks of those
 };
 
-// What a key costs with so many rows beside it, and what an item costs by itself
-// (start, end, partials), as a number of keys of weight 1.
+// What a key costs with so many rows beside it, and an item by itself (its start,
+// which is a chain of trips to memory, and its end): as much as so many keys.
 PKV_HD int kv4_weight(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 6 : 11; }
-constexpr int kKv4ItemCost = 128;
+constexpr int kKv4ItemKeys = 96;
 
 // x / y for a quotient below 2^20, without a division of 64 bits (which takes
 // longer than all the rest here).
@@ -48,10 +48,10 @@ PKV_HD Kv4Request kv4_request(int q0, int n, int len, int group, int rows) {
     const unsigned all = (unsigned)n * (unsigned)group;  // below 2^31
     q.tiles = (int)((all + (unsigned)rows - 1) / (unsigned)rows);
     if (q.tiles <= 1) {
-        q.c0 = (long long)kv4_weight((int)all) * len + kKv4ItemCost;
+        q.c0 = (long long)kv4_weight((int)all) * ((long long)len + kKv4ItemKeys);
     } else {
         const int step = kv4_weight(rows) * rows / group;  // keys more from tile to tile
-        q.c0 = (long long)kv4_weight(rows) * (len - n) + step + kKv4ItemCost;
+        q.c0 = (long long)kv4_weight(rows) * ((long long)len - n + kKv4ItemKeys) + step;
         q.c1 = step;
     }
     return q;
@@ -131,8 +131,10 @@ PKV_HD Kv4Piece kv4_piece(const Kv4Shares &sh, int k, long long start, long long
     return p;
 }
 
-// What a share has at least: four blocks of the rows of a tile.
-PKV_HD int kv4_least(int rows) { return 4 * 16 * kv4_weight(rows); }
+// What a share has at least: six blocks of the rows of a tile. An item that is cut
+// has four blocks or more, and costs kKv4ItemKeys / 16 = 6 more than those, so that
+// a share holds more than two of its blocks: see kv4_piece.
+PKV_HD int kv4_least(int rows) { return 6 * 16 * kv4_weight(rows); }
 
 // At most ctas * warps shares of at least `least`, over as many CTAs as there are.
 PKV_HD Kv4Shares kv4_shares(long long total, int ctas, int warps, int least) {
