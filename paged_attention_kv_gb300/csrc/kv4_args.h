@@ -1,0 +1,53 @@
+// What the two kernels of attention over the 4-bit pool share: kv4_attention.cu
+// (any rows, a warp an item) and kv4_chunk.cu (requests with many rows).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kv4_plan.h"
+#include "pagedkv.h"
+
+namespace pkv {
+
+// Counters between calls, so that a workspace that nobody prepared is noticed
+// (every byte 0x5a).
+constexpr int kKv4Nobody = 0x5a5a5a5a;
+
+struct Kv4Args {
+    const __nv_bfloat16 *q;
+    long long q_stride;
+    const uint8_t *pool;
+    const int32_t *table, *lens, *qsl;
+    int num_tokens, num_kv_heads, group, num_reqs, max_blocks, num_blocks;
+    float scale_log2, v_scale;
+    __nv_bfloat16 *out;
+    int *claimed;   // the workspace: items of kv4_chunk.cu taken so far;
+    int *arrived;   // of each CTA, the arrivals for the item that begins there and ends in another;
+    float4 *parts;  // and two partials: of the item that began before it, and of that one
+    int chunks;     // kv4_chunk.cu runs too
+    int32_t *status;
+};
+
+#ifdef __CUDACC__
+// Request r's description, and the status bits of one that is skipped.
+__device__ __forceinline__ Kv4Request kv4_request_of(const Kv4Args &a, int r, int rows, int *bits) {
+    const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), len = __ldg(a.lens + r);
+    int n = q1 - q0;
+    if (q0 < 0 || n < 0 || q1 > a.num_tokens) {
+        *bits |= PKV_DEV_BAD_QSL;
+        n = 0;
+    } else if (n > 0 && (len < n || len > (long long)a.max_blocks * PKV_BLOCK_SIZE)) {
+        *bits |= PKV_DEV_BAD_LEN;
+        n = 0;
+    }
+    return kv4_request(q0, n, len, a.group, rows);
+}
+#endif
+
+// Launches the chunk kernel in front of the other one.
+int kv4_chunk_launch(const Kv4Args &a, int head_size, int sms, cudaStream_t stream);
+
+}  // namespace pkv

@@ -31,6 +31,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "kv4_args.h"
 #include "kv4_format.cuh"
 #include "kv4_plan.h"
 #include "pagedkv.h"
@@ -47,23 +48,6 @@ template <int kMaxNt>
 constexpr int kWarps = kMaxNt == 4 ? 8 : 12;
 template <int D, int kMaxNt>
 constexpr int kStages = (D == 64 ? 2 : 1) * 3;
-
-// Counters of arrivals between calls, so that a workspace that nobody prepared is
-// noticed (every byte 0x5a).
-constexpr int kNobody = 0x5a5a5a5a;
-
-struct Kv4Args {
-    const __nv_bfloat16 *q;
-    long long q_stride;
-    const uint8_t *pool;
-    const int32_t *table, *lens, *qsl;
-    int num_tokens, num_kv_heads, group, num_reqs, max_blocks, num_blocks;
-    float scale_log2, v_scale;
-    __nv_bfloat16 *out;
-    int *arrived;   // the workspace: of each CTA, the arrivals for the item that begins there and ends in another,
-    float4 *parts;  // and two partials: of the item that began before it, and of that one
-    int32_t *status;
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
@@ -606,8 +590,8 @@ struct Kernel {
             int seen = 0;
             if (lane == 0) {
                 __threadfence();
-                seen = atomicAdd(a.arrived + c0, 1) - kNobody;
-                if (seen == n - 1) atomicExch(a.arrived + c0, kNobody);
+                seen = atomicAdd(a.arrived + c0, 1) - kKv4Nobody;
+                if (seen == n - 1) atomicExch(a.arrived + c0, kKv4Nobody);
                 if (seen < 0 || seen >= n) raise_status(a.status, PKV_DEV_BAD_WORKSPACE);
                 __threadfence();
             }
@@ -648,20 +632,6 @@ struct Kernel {
     }
 };
 
-// Request r's description, and the status bits of one that is skipped.
-__device__ __forceinline__ Kv4Request request_of(const Kv4Args &a, int r, int rows, int *bits) {
-    const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), len = __ldg(a.lens + r);
-    int n = q1 - q0;
-    if (q0 < 0 || n < 0 || q1 > a.num_tokens) {
-        *bits |= PKV_DEV_BAD_QSL;
-        n = 0;
-    } else if (n > 0 && (len < n || len > (long long)a.max_blocks * PKV_BLOCK_SIZE)) {
-        *bits |= PKV_DEV_BAD_LEN;
-        n = 0;
-    }
-    return kv4_request(q0, n, len, a.group, rows);
-}
-
 template <int D, int kMaxNt>
 __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(const Kv4Args a) {
     using K = Kernel<D, kMaxNt>;
@@ -669,7 +639,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     extern __shared__ __align__(128) uint8_t s_mem[];  // rings, then a partial of each warp
     __shared__ __align__(8) uint64_t s_bar[K::kW * K::kStg];
     __shared__ long long s_sum[kThreads], s_warp[K::kW];
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_most[K::kW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     for (int i = tid; i < K::kW * K::kStg; i += kThreads) mbar_init(s_bar + i, 2);
     if (tid == 0) s_abort = 0;
@@ -677,18 +647,54 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     pdl_launch_dependents();
     pdl_wait();
 
-    // The costs of all requests: `each` of them a thread, in order.
+    // The costs of all requests: `each` of them a thread, in order; of those that the
+    // chunk kernel may have, apart.
     const int each = (a.num_reqs + kThreads - 1) / kThreads;
-    long long sum = 0;
+    long long sum = 0, theirs = 0;
+    bool skip = false;  // they are the chunk kernel's
     {
-        int bits = 0;
+        int bits = 0, most = 0;
+        long long units = 0;
         if (cta == 0 && tid == 0 && (a.qsl[0] != 0 || a.qsl[a.num_reqs] != a.num_tokens)) bits |= PKV_DEV_BAD_QSL;
         for (int r = tid * each; r < min((tid + 1) * each, a.num_reqs); ++r) {
-            const Kv4Request q = request_of(a, r, K::kRows, &bits);
-            sum += kv4_cost(q, a.num_kv_heads, q.tiles);
+            const Kv4Request q = kv4_request_of(a, r, K::kRows, &bits);
+            const long long cost = kv4_cost(q, a.num_kv_heads, q.tiles);
+            if (kMaxNt == 4 && a.chunks && kv4_is_chunk(q, a.group)) {
+                theirs += cost;
+                units += kv4_chunk_units(kv4_request(q.q0, q.n, q.len, a.group, kKv4ChunkRows), a.num_kv_heads);
+                most = max(most, kv4_chunk_tiles(q.len));
+            } else {
+                sum += cost;
+            }
         }
         if (cta == 0 && bits) raise_status(a.status, bits);
+        if (kMaxNt == 4 && a.chunks) {
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                units += __shfl_xor_sync(0xffffffffu, units, d);
+                most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+            }
+            if (lane == 0) {
+                s_warp[warp] = units;
+                s_most[warp] = most;
+            }
+            __syncthreads();
+            units = most = 0;
+            for (int i = 0; i < K::kW; ++i) {
+                units += s_warp[i];
+                most = max(most, s_most[i]);
+            }
+            __syncthreads();
+            skip = kv4_use_chunks(units, most);
+        }
+        if (!skip) sum += theirs;
     }
+    auto request = [&](int r) {
+        int none = 0;
+        Kv4Request q = kv4_request_of(a, r, K::kRows, &none);
+        if (kMaxNt == 4 && skip && kv4_is_chunk(q, a.group)) q.tiles = 0;
+        return q;
+    };
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, sum, d);
@@ -719,7 +725,6 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     if (warp < team.shares) {
         const int share = cta * team.sh.per_cta + warp;
         const long long from = team.sh.begin(share);
-        int none = 0;
         Where w;
         {
             int lo = 0, hi = kThreads - 1;  // the first thread with s_sum > from
@@ -729,7 +734,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
             }
             long long first = lo ? s_sum[lo - 1] : 0;
             for (w.r = lo * each;; ++w.r) {  // of its requests, the one that `from` lies in
-                w.q = request_of(a, w.r, K::kRows, &none);
+                w.q = request(w.r);
                 const long long cost = kv4_cost(w.q, a.num_kv_heads, w.q.tiles);
                 if (from < first + cost) break;
                 first += cost;
@@ -764,7 +769,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
                 if (++w.i == w.q.tiles) {
                     w.i = 0;
                     do {
-                        w.q = request_of(a, ++w.r, K::kRows, &none);
+                        w.q = request(++w.r);
                     } while (w.q.tiles == 0);  // one follows: positions up to `to` belong to requests
                 }
             }
@@ -774,7 +779,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
 }
 
 // Places in the workspace, for any batch and form.
-size_t parts_at(int sms) { return ((size_t)sms * sizeof(int) + 255) / 256 * 256; }
+size_t parts_at(int sms) { return (((size_t)sms + 1) * sizeof(int) + 255) / 256 * 256; }
 size_t workspace_bytes(int sms, int head_size) {
     return parts_at(sms) + (size_t)sms * sizeof(float4) * (head_size == 128 ? 2 * Kernel<128, 4>::kPart + kWarps<4> * Kernel<128, 4>::kArea
                                                                             : 2 * Kernel<64, 4>::kPart + kWarps<4> * Kernel<64, 4>::kArea);
@@ -829,7 +834,7 @@ extern "C" PKV_API int paged_kv4_attention_init(const pkv_cache_desc *desc, void
     const int rs = device_sms(&sms);
     if (rs) return rs;
     if (workspace_size < workspace_bytes(sms, desc->head_size)) return PKV_E_WORKSPACE;
-    return cudaMemsetAsync(workspace, kNobody & 0xff, parts_at(sms), static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return cudaMemsetAsync(workspace, kKv4Nobody & 0xff, parts_at(sms), static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
 }
@@ -862,14 +867,19 @@ extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int3
     if (workspace_size < workspace_bytes(sms, desc->head_size)) return PKV_E_WORKSPACE;
     const float scale_log2 = scale * 1.4426950408889634f * k_scale;
     if (!std::isfinite(scale_log2)) return PKV_E_DIMS;
+    // rows that the longest request has of a kv head
+    const long long rows = (long long)(max_query_len ? max_query_len : num_tokens) * group;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Kv4Args a{static_cast<const __nv_bfloat16 *>(q), q_stride, static_cast<const uint8_t *>(kv4_cache), block_table,
                     seq_lens, query_start_loc, num_tokens, desc->num_kv_heads, group, num_reqs, max_blocks_per_req,
                     desc->num_blocks, scale_log2, v_scale, static_cast<__nv_bfloat16 *>(out),
-                    reinterpret_cast<int *>(ws), reinterpret_cast<float4 *>(ws + parts_at(sms)), status};
+                    reinterpret_cast<int *>(ws), reinterpret_cast<int *>(ws) + 1, reinterpret_cast<float4 *>(ws + parts_at(sms)),
+                    rows >= 64, status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // rows that the longest request has of a kv head
-    const long long rows = (long long)(max_query_len ? max_query_len : num_tokens) * group;
+    if (a.chunks) {
+        const int rl = kv4_chunk_launch(a, desc->head_size, sms, st);
+        if (rl) return rl;
+    }
     if (desc->head_size == 128)
         return rows <= 8 ? launch<128, 1>(a, sms, 0, st) : rows <= 16 ? launch<128, 2>(a, sms, 1, st) : launch<128, 4>(a, sms, 2, st);
     return rows <= 8 ? launch<64, 1>(a, sms, 0, st) : rows <= 16 ? launch<64, 2>(a, sms, 1, st) : launch<64, 4>(a, sms, 2, st);

@@ -94,6 +94,18 @@ PKV_HD int kv4_cut(long long off, long long cost, int blocks) {
     return b + 2 > blocks ? blocks : b;
 }
 
+// Requests of the chunk kernel: tiles of 128 rows, keys in tiles of 128.
+constexpr int kKv4ChunkRows = 128;
+PKV_HD bool kv4_is_chunk(const Kv4Request &q, int group) { return (long long)q.n * group >= 64; }
+PKV_HD int kv4_chunk_tiles(int keys) { return (int)(((unsigned)keys + 127) / 128); }
+// Its key tiles of all heads, about (q made with tiles of 128 rows).
+PKV_HD long long kv4_chunk_units(const Kv4Request &q, int heads) {
+    return (long long)q.tiles * heads * kv4_chunk_tiles(q.len - q.n / 2);
+}
+// An item of the chunk kernel is never cut: where the longest would take longer
+// than all of them cut into equal shares by the other kernel, that one has them.
+PKV_HD bool kv4_use_chunks(long long units, int longest) { return units > 0 && units >= 40LL * longest; }
+
 struct Kv4Shares {
     long long total, each;
     int count, per_cta;  // shares; of one CTA: CTA c has shares c * per_cta on
