@@ -94,60 +94,75 @@ struct Raw {
     // K: tokens g and g + 8 of the block, a quarter of the columns each, to rows of
     // 128 bytes (64 columns), 16-byte chunks swizzled. D 128: lanes of the upper
     // columns take their words in another order, or two lanes would meet in a bank.
-    __device__ __forceinline__ void put_k(uint8_t *to, int lane) const {
+    // `to`: this lane's place (k_place); the chunk's number is XOR-ed into it.
+    static __device__ __forceinline__ uint32_t k_place(int lane) {
         const int g = lane >> 2, t = lane & 3;
-        constexpr int kGrp = Smem<D>::kGrp;
+        return D == 128 ? (t >> 1) * 1024 + g * 128 + ((((t & 1) * 4 + (t & 2)) ^ g) << 4) : g * 128 + (((2 * t) ^ g) << 4);
+    }
+    __device__ __forceinline__ void put_k(uint32_t to, int lane) const {
+        const bool upper = lane & 2;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint8_t *row = to + h * kGrp + (D == 128 ? (t >> 1) * 1024 : 0) + g * 128;
             const __half2 sc = kv4_scales(D == 128 ? scales >> (16 * h) : scales);
+            const __half2 lo = __low2half2(sc), hi = __high2half2(sc);
 #pragma unroll
             for (int i = 0; i < kW; ++i) {
-                if constexpr (D == 128) {
-                    const uint32_t x = t & 2 ? w[h][i ^ 2] : w[h][i];
-                    const int word = t & 2 ? i ^ 2 : i;
-                    const __half2 s = word < 2 ? __low2half2(sc) : __high2half2(sc);
-                    *reinterpret_cast<uint4 *>(row + ((((t & 1) * 4 + word) ^ g) << 4)) = unpack8(x, s);
-                } else {
-                    *reinterpret_cast<uint4 *>(row + (((2 * t + i) ^ g) << 4)) = unpack8(w[h][i], h ? __high2half2(sc) : __low2half2(sc));
-                }
+                const uint32_t x = D == 128 && upper ? w[h][i ^ 2] : w[h][i];
+                const __half2 s = D == 128 ? ((i < 2) != upper ? lo : hi) : h ? hi : lo;
+                store((to + h * Smem<D>::kGrp) ^ (i << 4), unpack8(x, s));
             }
         }
     }
     // V: tokens 2 t and 2 t + 1 of each half block, an eighth of the columns. Tokens
     // at or past `end` become zero, and those whose scale is no number, which are noted.
-    __device__ __forceinline__ void put_v(uint8_t *to, int end, int key0, int *first_nan, int lane) {
+    static __device__ __forceinline__ uint32_t v_place(int lane) {
         const int g = lane >> 2, t = lane & 3;
-        constexpr int kGrp = Smem<D>::kGrp;
+        return D == 128 ? (g >> 2) * 1024 + 2 * t * 128 + ((((g & 3) * 2 + (g & 1)) ^ (2 * t)) << 4) : 2 * t * 128 + ((g ^ (2 * t)) << 4);
+    }
+    __device__ __forceinline__ void put_v(uint32_t to, int end, int key0, int *first_nan, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        // a byte is 0x7f or 0xff where adding 1 to its low seven bits reaches the eighth
+        if (end < 16 || (((scales & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tok = 8 * (i >> 1) + 2 * t + (i & 1);
-            const bool nan = (scales >> (8 * i) & 0x7fu) == 0x7fu;
-            if (nan && tok < end) atomicMin(first_nan + (D == 128 ? g : g >> 1), key0 + tok);
-            if (nan || tok >= end) scales &= ~(0xffu << (8 * i));
+            for (int i = 0; i < 4; ++i) {
+                const int tok = 8 * (i >> 1) + 2 * t + (i & 1);
+                const bool nan = (scales >> (8 * i) & 0x7fu) == 0x7fu;
+                if (nan && tok < end) atomicMin(first_nan + (D == 128 ? g : g >> 1), key0 + tok);
+                if (nan || tok >= end) scales &= ~(0xffu << (8 * i));
+            }
         }
+        const bool odd = g & 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const __half2 sc = kv4_scales(scales >> (16 * h));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = 2 * t + e;
                 const __half2 s = e ? __high2half2(sc) : __low2half2(sc);
+                const uint32_t line = to + h * Smem<D>::kGrp + e * 128;
                 if constexpr (D == 128) {
-                    uint8_t *line = to + h * kGrp + (g >> 2) * 1024 + row * 128;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t x = g & 1 ? w[h][2 * e + (i ^ 1)] : w[h][2 * e + i];
-                        const int word = g & 1 ? i ^ 1 : i;
-                        *reinterpret_cast<uint4 *>(line + ((((g & 3) * 2 + word) ^ row) << 4)) = unpack8(x, s);
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        store(line ^ ((i ^ e) << 4), unpack8(odd ? w[h][2 * e + (i ^ 1)] : w[h][2 * e + i], s));
                 } else {
-                    *reinterpret_cast<uint4 *>(to + h * kGrp + row * 128 + ((g ^ row) << 4)) = unpack8(w[h][e], s);
+                    store(line ^ (e << 4), unpack8(w[h][e], s));
                 }
             }
         }
     }
+    static __device__ __forceinline__ void store(uint32_t at, uint4 x) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+    }
 };
+
+// Barrier of two warps, and whether any of their threads says so.
+__device__ __forceinline__ bool pair_any(uint32_t id, bool mine) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\tbarrier.cta.red.or.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(any)
+                 : "r"(id), "r"((uint32_t)mine)
+                 : "memory");
+    return any != 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a) {
@@ -318,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             }
             if (tid < 8) s_nan[tid] = 0x7fffffff;
         }
-        uint8_t *k_to = smem + S::kK + warp * 2 * S::kGrp, *v_to = smem + S::kV + warp * 2 * S::kGrp;
+        const uint32_t k_to = k_s + warp * 2 * S::kGrp + Raw<D>::k_place(lane), v_to = v_s + warp * 2 * S::kGrp + Raw<D>::v_place(lane);
         rk.put_k(k_to, lane);
         rk.load(tile_of(1, id1), false, lane);
         fence_proxy_async_smem();
@@ -340,41 +355,39 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             }
             const int key0 = j * kKeys;
             rv.put_v(v_to, tl.keys - key0 - 16 * warp, key0 + 16 * warp, s_nan, lane);
-            rv.load(tile_of(j + 1, id1), true, lane);
-            id1 = id_of(j + 2);
             fence_proxy_async_smem();
-
             warp_wait(bar_s, phase, abort);
             tmem_fence_after_sync();
-            float s[64];
-            tmem_ld32(tm_row + part * 64, *reinterpret_cast<float(*)[32]>(s));
-            tmem_ld32(tm_row + part * 64 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
-            tmem_wait_ld_regs(*reinterpret_cast<float(*)[32]>(s));
-            tmem_wait_ld_regs(*reinterpret_cast<float(*)[32]>(s + 32));
+            const uint32_t s_at = tm_row + part * 64;
             const int mine = limit - key0 - part * 64;  // of these keys, the row sees so many
-            if (!__all_sync(0xffffffffu, mine >= 64)) {
+            const bool masked = !__all_sync(0xffffffffu, mine >= 64);
+            auto scores = [&](int c, float (&s)[32]) {  // 32 of them
+                tmem_ld32(s_at + 32 * c, s);
+                tmem_wait_ld_regs(s);
+                if (masked) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e >= mine) s[e] = -INFINITY;
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e >= mine) s[e] = -INFINITY;
+                }
+            };
+            // The reference becomes the row's largest score so far; O and l follow.
+            auto move = [&](bool all) {
+                float best = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    float s[32];
+                    scores(c, s);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top[e & 3] = fmax3(top[e & 3], s[2 * e], s[2 * e + 1]);
-            s_x[part * 128 + row] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            // both halves of these rows have their scores in registers now: P may go over them
-            tmem_fence_before_sync();
-            named_barrier_sync(1 + (warp & 3), 64);
-            tmem_fence_after_sync();
-            const float best = fmaxf(s_x[row], s_x[128 + row]);
-            // the reference moves when a score passes it by 2^10: p fits fp16 until then
-            const bool moves = j == 0 || (best - m) * mul > 10.0f;
-            if (__any_sync(0xffffffffu, moves)) {
-                const float to = moves ? fmaxf(m, best) : m;
+                    for (int e = 0; e < 16; ++e) best = fmax3(best, s[2 * e], s[2 * e + 1]);
+                }
+                s_x[part * 128 + row] = best;
+                named_barrier_sync(1 + (warp & 3), 64);
+                const float to = fmaxf(m, fmaxf(s_x[row], s_x[128 + row]));
                 const float f = m == to ? 1.0f : m == -INFINITY ? 0.0f : fast_exp2((m - to) * mul);
                 m = to;
                 l *= f;
-                if (j > 0) {
-#pragma unroll
+                if (all) {
+#pragma unroll 1
                     for (int c = 0; c < D / 64; ++c) {
                         float o[32];
                         const uint32_t at_o = tm_row + kColO + part * (D / 2) + 32 * c;
@@ -384,22 +397,41 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
                         for (int e = 0; e < 32; ++e) o[e] *= f;
                         tmem_st32(at_o, o);
                     }
+                    tmem_wait_st();
                 }
-            }
-            const float2 nm = make_float2(-m, -m), mm = make_float2(mul, mul);
-            float2 sum = make_float2(0.0f, 0.0f);
+                named_barrier_sync(1 + (warp & 3), 64);  // the maxima are read
+            };
+            if (j == 0) move(false);
+            uint32_t p[32];
+            float2 sum;
+            for (int round = 0;; ++round) {
+                const float2 nm = make_float2(-m, -m), mm = make_float2(mul, mul);
+                float top = -INFINITY;
+                sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t p[16];
+                for (int c = 0; c < 2; ++c) {
+                    float s[32];
+                    scores(c, s);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 x = fmul2(fadd2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), nm), mm);
-                    const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                    sum = fadd2(sum, y);
-                    p[e] = half_bits(__floats2half2_rn(y.x, y.y));
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = fmul2(fadd2(make_float2(s[2 * e], s[2 * e + 1]), nm), mm);
+                        top = fmax3(top, x.x, x.y);
+                        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        sum = fadd2(sum, y);
+                        p[16 * c + e] = half_bits(__floats2half2_rn(y.x, y.y));
+                    }
                 }
-                tmem_st16u(tm_row + part * 32 + 16 * c, p);
+                // the reference moves when a score passes it by 2^10: p fits fp16 until then.
+                // Behind this barrier both halves of these rows have read their scores, and
+                // P may go over them.
+                tmem_fence_before_sync();
+                const bool again = pair_any(1 + (warp & 3), top > 10.0f);
+                tmem_fence_after_sync();
+                if (!again || round) break;  // against the largest score none is past it
+                move(j > 0);
             }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_st16u(tm_row + part * 32 + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
             l += sum.x + sum.y;
             tmem_wait_st();
             tmem_fence_before_sync();
@@ -413,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
                 umma_commit_warp(bar_pv);
             }
             if (j + 1 < nt) {
+                rv.load(tile_of(j + 1, id1), true, lane);
+                id1 = id_of(j + 2);
                 rk.put_k(k_to, lane);
                 rk.load(tile_of(j + 2, id1), false, lane);
                 fence_proxy_async_smem();
