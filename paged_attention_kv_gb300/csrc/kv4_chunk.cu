@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
     using S = Smem<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long s_units[kThreads / 32];
-    __shared__ int s_items[kThreads], s_sum[kThreads / 32], s_most[kThreads / 32];
+    __shared__ int s_items[kThreads], s_len[kThreads], s_order[kThreads], s_sum[kThreads / 32], s_most[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_claim;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -187,19 +187,42 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
     pdl_launch_dependents();
     pdl_wait();
 
-    // Which requests are this kernel's, and how many items they have.
+    // Which requests are this kernel's, and how many items they have: `each` of them
+    // a thread, in order; up to a thread each, those with the longest contexts first,
+    // so that what runs last is short.
     const int each = (a.num_reqs + kThreads - 1) / kThreads;
     int items = 0, most = 0;
     long long units = 0;
+    auto take = [&](int r, int *have, int *bits) {
+        const Kv4Request q = kv4_request_of(a, r, kKv4ChunkRows, bits);
+        *have = kv4_is_chunk(q, a.group) ? q.tiles * a.num_kv_heads : 0;
+        return q;
+    };
     {
         int bits = 0;  // the other kernel reports them
         for (int r = tid * each; r < min((tid + 1) * each, a.num_reqs); ++r) {
-            const Kv4Request q = kv4_request_of(a, r, kKv4ChunkRows, &bits);
-            if (!kv4_is_chunk(q, a.group)) continue;
-            items += q.tiles * a.num_kv_heads;
+            int have;
+            const Kv4Request q = take(r, &have, &bits);
+            if (!have) continue;
+            items += have;
             units += kv4_chunk_units(q, a.num_kv_heads);
             most = max(most, kv4_chunk_tiles(q.len));
         }
+    }
+    s_len[tid] = items ? most : -1;
+    __syncthreads();
+    if (each == 1) {
+        int place = 0;
+        for (int i = 0; i < min(kThreads, a.num_reqs); ++i) place += s_len[i] > s_len[tid] || (s_len[i] == s_len[tid] && i < tid);
+        if (tid < a.num_reqs) {
+            s_order[place] = tid;
+            s_items[place] = items;
+        }
+        __syncthreads();
+        items = tid < a.num_reqs ? s_items[tid] : 0;
+        __syncthreads();
+    } else {
+        s_order[tid] = tid;
     }
     int sum = items;
 #pragma unroll
@@ -259,10 +282,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
                 const int mid = (lo + hi) >> 1;
                 if (s_items[mid] > item) hi = mid; else lo = mid + 1;
             }
-            int off = item - (lo ? s_items[lo - 1] : 0), none = 0;
-            for (r = lo * each;; ++r) {
-                q = kv4_request_of(a, r, kKv4ChunkRows, &none);
-                const int have = kv4_is_chunk(q, a.group) ? q.tiles * a.num_kv_heads : 0;
+            int off = item - (lo ? s_items[lo - 1] : 0), have, none = 0;
+            for (r = s_order[lo] * each;; ++r) {
+                q = take(r, &have, &none);
                 if (off < have) break;
                 off -= have;
             }
