@@ -375,43 +375,41 @@ struct Item {
             if (kMul) to[(kVecs + n) * 32 + lane] = make_float4(mul[n].x, mul[n].y, 0.0f, 0.0f);
         }
     }
-    // Joins a partial to this one; kGlobal: written by another SM, with mul,
-    // which `first` takes over with everything else.
     static __device__ __forceinline__ void factors(float m, float n, float mul, float *to, float *f, float *g) {
         *to = fmaxf(m, n);
         *f = m == *to ? 1.0f : m == -INFINITY ? 0.0f : fast_exp2((m - *to) * mul);
         *g = n == *to ? 1.0f : n == -INFINITY ? 0.0f : fast_exp2((n - *to) * mul);
     }
+    struct Loaded {
+        float4 o[kK], st;
+    };
+    // A partial's 8 rows n. kGlobal: written by another SM.
     template <bool kGlobal>
-    __device__ __forceinline__ void join(const float4 *from, bool first, int lane) {
+    static __device__ __forceinline__ void load(const float4 *from, int n, Loaded &x, int lane) {
         auto get = [&](int i) { return kGlobal ? __ldcg(from + i * 32 + lane) : from[i * 32 + lane]; };
 #pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-            float4 v[kK];
+        for (int i = 0; i < kK; ++i) x.o[i] = get(n * kK + i);
+        x.st = get(kNt * kK + n);
+    }
+    __device__ __forceinline__ void join(int n, const Loaded &x) {
+        float fx, fy, gx, gy;
+        factors(m[n].x, x.st.x, mul[n].x, &m[n].x, &fx, &gx);
+        factors(m[n].y, x.st.y, mul[n].y, &m[n].y, &fy, &gy);
+        l[n] = make_float2(l[n].x * fx + x.st.z * gx, l[n].y * fy + x.st.w * gy);
 #pragma unroll
-            for (int i = 0; i < kK; ++i) v[i] = get(n * kK + i);
-            const float4 st = get(kNt * kK + n);
-            float fx, fy, gx, gy;
-            if (kGlobal && first) {
-                const float4 x = get(kVecs + n);
-                mul[n] = make_float2(x.x, x.y);
-                m[n] = make_float2(st.x, st.y);
-                l[n] = make_float2(st.z, st.w);
-#pragma unroll
-                for (int i = 0; i < kK; ++i) o[n][i][0] = v[i].x, o[n][i][1] = v[i].y, o[n][i][2] = v[i].z, o[n][i][3] = v[i].w;
-                continue;
-            }
-            factors(m[n].x, st.x, mul[n].x, &m[n].x, &fx, &gx);
-            factors(m[n].y, st.y, mul[n].y, &m[n].y, &fy, &gy);
-            l[n] = make_float2(l[n].x * fx + st.z * gx, l[n].y * fy + st.w * gy);
-#pragma unroll
-            for (int i = 0; i < kK; ++i) {
-                o[n][i][0] = o[n][i][0] * fx + v[i].x * gx;
-                o[n][i][1] = o[n][i][1] * fy + v[i].y * gy;
-                o[n][i][2] = o[n][i][2] * fx + v[i].z * gx;
-                o[n][i][3] = o[n][i][3] * fy + v[i].w * gy;
-            }
+        for (int i = 0; i < kK; ++i) {
+            o[n][i][0] = o[n][i][0] * fx + x.o[i].x * gx;
+            o[n][i][1] = o[n][i][1] * fy + x.o[i].y * gy;
+            o[n][i][2] = o[n][i][2] * fx + x.o[i].z * gx;
+            o[n][i][3] = o[n][i][3] * fy + x.o[i].w * gy;
         }
+    }
+    __device__ __forceinline__ void become(int n, const Loaded &x, float4 scale) {
+        mul[n] = make_float2(scale.x, scale.y);
+        m[n] = make_float2(x.st.x, x.st.y);
+        l[n] = make_float2(x.st.z, x.st.w);
+#pragma unroll
+        for (int i = 0; i < kK; ++i) o[n][i][0] = x.o[i].x, o[n][i][1] = x.o[i].y, o[n][i][2] = x.o[i].z, o[n][i][3] = x.o[i].w;
     }
 
     // V scales of tokens that no row sees become zero, and those that are no
@@ -580,7 +578,12 @@ struct Kernel {
             if (*team.abort) return;
             const int upto = min(team.last - base, team.shares - 1);
             for (int i = team.warp + 1; i <= upto; ++i)
-                it.template join<false>(team.area + i * kArea, false, lane);
+#pragma unroll
+                for (int g = 0; g < kNt; ++g) {
+                    typename Item<D, kNt>::Loaded x;
+                    Item<D, kNt>::template load<false>(team.area + i * kArea, g, x, lane);
+                    it.join(g, x);
+                }
         }
         if (team.first < base || team.last >= base + team.shares) {
             const int c0 = team.first / team.sh.per_cta, n = team.last / team.sh.per_cta - c0 + 1;
@@ -589,16 +592,32 @@ struct Kernel {
             __syncwarp();
             int seen = 0;
             if (lane == 0) {
-                __threadfence();
-                seen = atomicAdd(a.arrived + c0, 1) - kKv4Nobody;
+                // releases this warp's partial, and takes the others' in
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(a.arrived + c0) : "memory");
+                seen -= kKv4Nobody;
                 if (seen == n - 1) atomicExch(a.arrived + c0, kKv4Nobody);
                 if (seen < 0 || seen >= n) raise_status(a.status, PKV_DEV_BAD_WORKSPACE);
-                __threadfence();
             }
             seen = __shfl_sync(0xffffffffu, seen, 0);
             if (seen != n - 1) return;
-            __syncwarp();  // the other lanes' loads behind lane 0's fence
-            for (int i = 0; i < n; ++i) it.template join<true>(part(c0 + i), i == 0, lane);
+            __syncwarp();
+            // a part's values are on their way while the one before is joined
+#pragma unroll
+            for (int g = 0; g < kNt; ++g) {
+                typename Item<D, kNt>::Loaded x[2];
+                Item<D, kNt>::template load<true>(part(c0), g, x[0], lane);
+                const float4 scale = __ldcg(part(c0) + (Item<D, kNt>::kVecs + g) * 32 + lane);
+                Item<D, kNt>::template load<true>(part(c0 + 1), g, x[1], lane);
+                it.become(g, x[0], scale);
+#pragma unroll 1
+                for (int i = 1; i < n; i += 2) {
+                    if (i + 1 < n) Item<D, kNt>::template load<true>(part(c0 + i + 1), g, x[0], lane);
+                    it.join(g, x[1]);
+                    if (i + 1 == n) break;
+                    if (i + 2 < n) Item<D, kNt>::template load<true>(part(c0 + i + 2), g, x[1], lane);
+                    it.join(g, x[0]);
+                }
+            }
         }
         output<kNt>(a, it, w, row0, rows, lane);
     }
