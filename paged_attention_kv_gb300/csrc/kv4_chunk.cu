@@ -37,8 +37,7 @@ constexpr uint32_t kTmemCols = 256, kColO = 128;  // S (P over it), O
 
 template <int D>
 struct Smem {
-    static constexpr int kHalf = 128 * 128;      // q: 128 rows x 64 columns
-    static constexpr int kGrp = (D / 64) * 1024;  // K, V: 8 keys, [D / 64][8][128 B]
+    static constexpr int kHalf = 128 * 128;         // q, K, V: 128 rows x 64 columns
     static constexpr int kTile = (D / 64) * kHalf;
     static constexpr int kQ = 0, kK = kTile, kV = 2 * kTile;
     static constexpr int kX = 3 * kTile;         // float [2][128]: the halves' maxima, at last their sums
@@ -51,6 +50,52 @@ struct Smem {
 
 constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
     return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// A value that all lanes hold, as the compiler can know it too.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+
+// Products and commits by one elected lane, four MMAs at a time, with operands that
+// stay in uniform registers: of a matrix descriptor (128-byte swizzle) only the low
+// word changes from one to the next, with the address (and the leading offset).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading) { return ((addr & 0x3FFFF) >> 4) | ((leading >> 4) << 16); }
+// Four steps of 16 of a product from shared memory: both operands' columns go on
+// 32 bytes a step.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t.reg .b32 a, b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+        "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\tmov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, 1;\n\t"
+        "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\tmov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, 1;\n\t"
+        "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\tmov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, 1;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
+}
+// Four steps of a product of P, in tensor memory, and V: 8 columns and 16 rows a step.
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t"
+        "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 db, {b, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, 1;\n\t"
+        "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\tmov.b64 db, {b, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, 1;\n\t"
+        "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\tmov.b64 db, {b, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, 1;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t half_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
@@ -97,7 +142,7 @@ struct Raw {
     // `to`: this lane's place (k_place); the chunk's number is XOR-ed into it.
     static __device__ __forceinline__ uint32_t k_place(int lane) {
         const int g = lane >> 2, t = lane & 3;
-        return D == 128 ? (t >> 1) * 1024 + g * 128 + ((((t & 1) * 4 + (t & 2)) ^ g) << 4) : g * 128 + (((2 * t) ^ g) << 4);
+        return D == 128 ? (t >> 1) * Smem<D>::kHalf + g * 128 + ((((t & 1) * 4 + (t & 2)) ^ g) << 4) : g * 128 + (((2 * t) ^ g) << 4);
     }
     __device__ __forceinline__ void put_k(uint32_t to, int lane) const {
         const bool upper = lane & 2;
@@ -109,7 +154,7 @@ struct Raw {
             for (int i = 0; i < kW; ++i) {
                 const uint32_t x = D == 128 && upper ? w[h][i ^ 2] : w[h][i];
                 const __half2 s = D == 128 ? ((i < 2) != upper ? lo : hi) : h ? hi : lo;
-                store((to + h * Smem<D>::kGrp) ^ (i << 4), unpack8(x, s));
+                store((to + h * 1024) ^ (i << 4), unpack8(x, s));
             }
         }
     }
@@ -117,7 +162,7 @@ struct Raw {
     // at or past `end` become zero, and those whose scale is no number, which are noted.
     static __device__ __forceinline__ uint32_t v_place(int lane) {
         const int g = lane >> 2, t = lane & 3;
-        return D == 128 ? (g >> 2) * 1024 + 2 * t * 128 + ((((g & 3) * 2 + (g & 1)) ^ (2 * t)) << 4) : 2 * t * 128 + ((g ^ (2 * t)) << 4);
+        return D == 128 ? (g >> 2) * Smem<D>::kHalf + 2 * t * 128 + ((((g & 3) * 2 + (g & 1)) ^ (2 * t)) << 4) : 2 * t * 128 + ((g ^ (2 * t)) << 4);
     }
     __device__ __forceinline__ void put_v(uint32_t to, int end, int key0, int *first_nan, int lane) {
         const int g = lane >> 2, t = lane & 3;
@@ -138,7 +183,7 @@ struct Raw {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const __half2 s = e ? __high2half2(sc) : __low2half2(sc);
-                const uint32_t line = to + h * Smem<D>::kGrp + e * 128;
+                const uint32_t line = to + h * 1024 + e * 128;
                 if constexpr (D == 128) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
@@ -248,31 +293,25 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         most = max(most, s_most[i]);
     }
     s_items[tid] = sum;
-    if (!kv4_use_chunks(units, most) || (int)blockIdx.x >= total) return;  // the items go by `total` claims and no more CTAs
+    total = (int)uniform((uint32_t)total);
+    // what steers this kernel is uniform for the compiler too: see mma_ss4
+    if (uniform(!kv4_use_chunks(units, most) || (int)blockIdx.x >= total)) return;  // the items go by `total` claims and no more CTAs
     const int ctas = min((int)gridDim.x, total);
     if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
-    const uint32_t tm = s_tmem;
+    const uint32_t tm = s_tmem, tmu = uniform(tm);
 
     constexpr uint32_t kIdS = idesc_f16(128, kKeys, 0), kIdPv = idesc_f16(128, D, 1);
     const uint32_t q_s = smem_u32(smem + S::kQ), k_s = smem_u32(smem + S::kK), v_s = smem_u32(smem + S::kV);
+    const uint32_t q_lo = desc_lo(q_s, 16), k_lo = desc_lo(k_s, 16), v_lo = desc_lo(v_s, S::kHalf);
     const int part = warp >> 2, row = (warp & 3) * 32 + lane;  // this thread's keys (of 64) and row in the softmax
     const uint32_t tm_row = tm + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t phase = 0;  // of both barriers: they complete once a key tile
     const long long block_bytes = (long long)a.num_kv_heads * Kv4Tile<D>::kBytes;
 
     for (int item = blockIdx.x; item < total;) {
-        // the next item is claimed now, and looked at when this one is done
-        if (tid == 0) {
-            const int seen = atomicAdd(a.claimed, 1) - kKv4Nobody;
-            // CTA b has item b without a claim; all claim until one is past the end, and the last of those
-            // leaves the counter as it was
-            if (seen == total - 1) atomicExch(a.claimed, kKv4Nobody);
-            if (seen < 0 || seen >= total) raise_status(a.status, PKV_DEV_BAD_WORKSPACE);
-            s_claim = seen < 0 || seen >= total ? total : ctas + seen;
-        }
         // the item: request, tile and head
         Kv4Request q;
         int r, i, h;
@@ -293,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             h = off % a.num_kv_heads;
         }
         const Kv4Tiling tl = kv4_tile(q, i, a.group, kKv4ChunkRows);
-        const int nt = (tl.keys + kKeys - 1) / kKeys;
+        const int nt = (int)uniform((uint32_t)kv4_chunk_tiles(tl.keys));
         const int row0 = i * kKv4ChunkRows;
         const int32_t *ids = a.table + (long long)r * a.max_blocks;
         const uint8_t *heads = a.pool + (long long)h * Kv4Tile<D>::kBytes;
@@ -309,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             return heads + id * block_bytes;
         };
         const int id0 = id_of(0);
-        int id1 = id_of(1);
+        int id1 = id_of(1), id2 = id_of(2);  // of the tiles that V and K are read of next
         Raw<D> rk, rv;
         const uint8_t *at = tile_of(0, id0);
         rk.load(at, false, lane);
@@ -341,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             int e = (int)(top >> 7);
             e = e == 255 ? 127 : min(max(e, 64), 253);
             const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
-            if (half == 0) s_mul[qr] = qr < tl.rows ? up * a.scale_log2 : 0.0f;
+            // never 0: masked scores times it have to stay -inf
+            if (half == 0) s_mul[qr] = qr < tl.rows ? fmaxf(up * a.scale_log2, 0x1p-126f) : 1.0f;
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
                 const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
@@ -355,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             }
             if (tid < 8) s_nan[tid] = 0x7fffffff;
         }
-        const uint32_t k_to = k_s + warp * 2 * S::kGrp + Raw<D>::k_place(lane), v_to = v_s + warp * 2 * S::kGrp + Raw<D>::v_place(lane);
+        const uint32_t k_to = k_s + warp * 2048 + Raw<D>::k_place(lane), v_to = v_s + warp * 2048 + Raw<D>::v_place(lane);
         rk.put_k(k_to, lane);
         rk.load(tile_of(1, id1), false, lane);
         fence_proxy_async_smem();
@@ -365,15 +405,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         const int limit = row < tl.rows ? q.len - q.n + rr / a.group + 1 : 1;
         const float mul = s_mul[row];
         float m = -INFINITY, l = 0.0f;
+        bool large = false;  // some row's reference is
 
         for (int j = 0; j < nt; ++j) {
             if (warp == 0) {
                 tmem_fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_warp(tm, umma_desc_sw128(q_s + (kk / 4) * S::kHalf + (kk % 4) * 32, 16, 1024),
-                                   umma_desc_sw128(k_s + (kk / 4) * 1024 + (kk % 4) * 32, 16, S::kGrp), kIdS, kk > 0 ? 1u : 0u);
-                umma_commit_warp(bar_s);
+                for (int c = 0; c < D / 64; ++c) mma_ss4(tmu, q_lo + c * (S::kHalf >> 4), k_lo + c * (S::kHalf >> 4), kIdS, c);
+                commit(smem_u32(bar_s));
             }
             const int key0 = j * kKeys;
             rv.put_v(v_to, tl.keys - key0 - 16 * warp, key0 + 16 * warp, s_nan, lane);
@@ -408,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
                 const float f = m == to ? 1.0f : m == -INFINITY ? 0.0f : fast_exp2((m - to) * mul);
                 m = to;
                 l *= f;
+                large = __any_sync(0xffffffffu, !(fabsf(m * mul) <= 1024.0f));
                 if (all) {
 #pragma unroll 1
                     for (int c = 0; c < D / 64; ++c) {
@@ -427,27 +467,36 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             uint32_t p[32];
             float2 sum;
             for (int round = 0;; ++round) {
-                const float2 nm = make_float2(-m, -m), mm = make_float2(mul, mul);
-                float top = -INFINITY;
+                const float2 mm = make_float2(mul, mul);
                 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float s[32];
                     scores(c, s);
+                    auto exps = [&](auto exponent) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x = fmul2(fadd2(make_float2(s[2 * e], s[2 * e + 1]), nm), mm);
-                        top = fmax3(top, x.x, x.y);
-                        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        sum = fadd2(sum, y);
-                        p[16 * c + e] = half_bits(__floats2half2_rn(y.x, y.y));
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = exponent(make_float2(s[2 * e], s[2 * e + 1]));
+                            const float2 z = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            sum = fadd2(sum, z);
+                            p[16 * c + e] = half_bits(__floats2half2_rn(z.x, z.y));
+                        }
+                    };
+                    // One rounding where the reference's own, mul * m, is small: at 2^10 it is
+                    // off by 2^-15, for a whole row and tile alike.
+                    if (!large) {
+                        const float2 nm = make_float2(-m * mul, -m * mul);
+                        exps([&](float2 x) { return ffma2(x, mm, nm); });
+                    } else {
+                        const float2 nm = make_float2(-m, -m);
+                        exps([&](float2 x) { return fmul2(fadd2(x, nm), mm); });
                     }
                 }
-                // the reference moves when a score passes it by 2^10: p fits fp16 until then.
-                // Behind this barrier both halves of these rows have read their scores, and
-                // P may go over them.
+                // The reference moves when the sum shows that a p may be large: none is
+                // above 2^12 until then, and fits fp16. Behind this barrier both halves of these rows have read their
+                // scores, and P may go over them.
                 tmem_fence_before_sync();
-                const bool again = pair_any(1 + (warp & 3), top > 10.0f);
+                const bool again = pair_any(1 + (warp & 3), !(sum.x + sum.y <= 4096.0f));
                 tmem_fence_after_sync();
                 if (!again || round) break;  // against the largest score none is past it
                 move(j > 0);
@@ -461,24 +510,30 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             if (warp == 0) {
                 tmem_fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    umma_bf16_tmem_a_warp(tm + kColO, tm + kk * 8, umma_desc_sw128(v_s + kk * 2 * S::kGrp, 1024, S::kGrp), kIdPv,
-                                          (j > 0 || kk > 0) ? 1u : 0u);
-                umma_commit_warp(bar_pv);
+                for (int c = 0; c < 2; ++c) mma_ts4(tmu + kColO, tmu + c * 32, v_lo + c * (8192 >> 4), kIdPv, c | j);
+                commit(smem_u32(bar_pv));
             }
             if (j + 1 < nt) {
                 rv.load(tile_of(j + 1, id1), true, lane);
-                id1 = id_of(j + 2);
                 rk.put_k(k_to, lane);
-                rk.load(tile_of(j + 2, id1), false, lane);
+                rk.load(tile_of(j + 2, id2), false, lane);
+                id1 = id2;
+                id2 = id_of(j + 3);
                 fence_proxy_async_smem();
+            } else if (tid == 0) {
+                // the next item: CTA b has item b without a claim, every item claims another, and
+                // the last of these claims leaves the counter as it was
+                const int seen = atomicAdd(a.claimed, 1) - kKv4Nobody;
+                if (seen == total - 1) atomicExch(a.claimed, kKv4Nobody);
+                if (seen < 0 || seen >= total) raise_status(a.status, PKV_DEV_BAD_WORKSPACE);
+                s_claim = seen < 0 || seen >= total ? total : ctas + seen;
             }
             warp_wait(bar_pv, phase, abort);
             phase ^= 1;
             __syncthreads();
-            if (*abort) break;
+            if (uniform(*abort)) break;
         }
-        if (*abort) break;
+        if (uniform(*abort)) break;
         tmem_fence_after_sync();
         s_x[part * 128 + row] = l;
         named_barrier_sync(1 + (warp & 3), 64);
@@ -507,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         }
         if (__any_sync(0xffffffffu, bits != 0) && lane == 0) raise_status(a.status, PKV_DEV_BAD_BLOCK);
         tmem_fence_before_sync();
-        item = s_claim;
+        item = (int)uniform((uint32_t)s_claim);
         __syncthreads();
         tmem_fence_after_sync();
     }
