@@ -500,8 +500,8 @@ int paged_kv4_write(const void *k, int64_t k_stride, const void *v, int64_t v_st
 
 /*
  * The values that the pool holds at the given slots, as bf16 (exactly):
- * k_out and v_out bf16 [num_tokens][num_kv_heads][head_size], one of them may be
- * NULL. Rows of negative slots are left as they were; those of slots at or beyond
+ * k_out and v_out bf16 [num_tokens][num_kv_heads][head_size], not the same memory,
+ * and one of them may be NULL. Rows of negative slots are left as they were; those of slots at or beyond
  * 16 * num_blocks too, and raise PKV_DEV_BAD_SLOT. The same slot may be named
  * several times.
  */
@@ -533,8 +533,8 @@ int paged_kv4_attention_init(const pkv_cache_desc *desc, void *workspace, size_t
  *             heads per kv head); a bound that is too small costs time and nothing else
  *  scale      greater than 0, at most 1e30
  *  out        bf16 [num_tokens][num_q_heads][head_size], no overlap with the
- *             inputs. Rows outside every request, and rows of requests with bad
- *             metadata, are left as they were.
+ *             inputs (out at q: PKV_E_DIMS). Rows outside every request, and rows of
+ *             requests with bad metadata, are left as they were.
  *  workspace  device scratch, 16-byte aligned, prepared by
  *             paged_kv4_attention_init (else PKV_DEV_BAD_WORKSPACE, and rows whose
  *             context several CTAs share may be left unwritten or wrong); calls that
@@ -542,8 +542,10 @@ int paged_kv4_attention_init(const pkv_cache_desc *desc, void *workspace, size_t
  *  status     optional device int32, PKV_DEV_* bits OR-ed in: a request whose
  *             bounds descend or leave [0, num_tokens] (PKV_DEV_BAD_QSL) or whose
  *             length is below its new tokens or past its table (PKV_DEV_BAD_LEN)
- *             is skipped; a block id outside the pool (PKV_DEV_BAD_BLOCK) gives
- *             that request's rows unspecified values, and no other's
+ *             is skipped (where such bounds leave requests with more new tokens than
+ *             there are, nothing is computed); a block id outside the pool
+ *             (PKV_DEV_BAD_BLOCK) gives that request's rows unspecified values, and
+ *             no other's
  *
  * Scores, sums and the output's sums are held in 32 bits; the probabilities are
  * rounded to fp16 (2^-11 of each, or 2^-25 of the largest where that is more) for

@@ -45,6 +45,23 @@ __device__ __forceinline__ Kv4Request kv4_request_of(const Kv4Args &a, int r, in
     }
     return kv4_request(q0, n, len, a.group, rows);
 }
+
+// Whether the requests (`each` of them a thread) have more new tokens than there
+// are: that takes bounds that descend somewhere, and their sums of items and costs
+// might not fit their types. All of the CTA's threads call it; s: one each.
+template <int kThreads>
+__device__ __forceinline__ bool kv4_overlap(const Kv4Args &a, int each, long long *s) {
+    long long n = 0;
+    int none = 0;
+    for (int r = threadIdx.x * each; r < min(((int)threadIdx.x + 1) * each, a.num_reqs); ++r) n += kv4_request_of(a, r, 8, &none).n;
+    s[threadIdx.x] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll 1
+    for (int i = 0; i < kThreads; ++i) n += s[i];
+    __syncthreads();
+    return n > a.num_tokens;
+}
 #endif
 
 // Launches the chunk kernel in front of the other one.

@@ -671,10 +671,10 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     const int each = (a.num_reqs + kThreads - 1) / kThreads;
     long long sum = 0, theirs = 0;
     bool skip = false;  // they are the chunk kernel's
+    int bits = 0;
     {
-        int bits = 0, most = 0;
+        int most = 0;
         long long units = 0;
-        if (cta == 0 && tid == 0 && (a.qsl[0] != 0 || a.qsl[a.num_reqs] != a.num_tokens)) bits |= PKV_DEV_BAD_QSL;
         for (int r = tid * each; r < min((tid + 1) * each, a.num_reqs); ++r) {
             const Kv4Request q = kv4_request_of(a, r, K::kRows, &bits);
             const long long cost = kv4_cost(q, a.num_kv_heads, q.tiles);
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
         if (lane >= d) sum += o;
     }
     if (lane == 31) s_warp[warp] = sum;
-    __syncthreads();
+    if (__syncthreads_or(bits & PKV_DEV_BAD_QSL) && kv4_overlap<kThreads>(a, each, s_sum)) return;
     long long total = 0;
 #pragma unroll
     for (int i = 0; i < K::kW; ++i) {
@@ -868,7 +868,7 @@ extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int3
     const int rc = check_cache_desc(*desc, /*attention=*/true);
     if (rc) return rc;
     if (num_tokens < 0 || num_reqs < 0 || max_blocks_per_req < 0 || max_query_len < 0) return PKV_E_DIMS;
-    if (max_blocks_per_req > INT32_MAX / PKV_BLOCK_SIZE) return PKV_E_DIMS;
+    if (max_blocks_per_req > INT32_MAX / PKV_BLOCK_SIZE || num_reqs > INT32_MAX - 65536) return PKV_E_DIMS;
     if (num_q_heads <= 0 || num_q_heads % desc->num_kv_heads) return PKV_E_GQA;
     const int group = num_q_heads / desc->num_kv_heads;
     if (group > 128 || (long long)num_tokens * group > INT32_MAX - 1024) return PKV_E_DIMS;
@@ -880,6 +880,7 @@ extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int3
     if (!aligned(q, 16) || !aligned(kv4_cache, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(status, 4))
         return PKV_E_ALIGN;
+    if (out == q) return PKV_E_DIMS;
     int sms = 0;
     const int rs = device_sms(&sms);
     if (rs) return rs;

@@ -44,7 +44,7 @@ struct Smem {
     static constexpr int kMul = kX + 2 * 128 * 4;
     static constexpr int kNan = kMul + 128 * 4;  // first key whose V is no number, by groups of 16 columns
     static constexpr int kBar = kNan + 8 * 4;
-    static constexpr int kBytes = kBar + 2 * 8;
+    static constexpr int kBytes = kBar + 3 * 8;
     static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -220,13 +220,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *s_x = reinterpret_cast<float *>(smem + S::kX), *s_mul = reinterpret_cast<float *>(smem + S::kMul);
     int *s_nan = reinterpret_cast<int *>(smem + S::kNan);
-    uint64_t *bar_s = reinterpret_cast<uint64_t *>(smem + S::kBar), *bar_pv = bar_s + 1;
+    uint64_t *bar_s = reinterpret_cast<uint64_t *>(smem + S::kBar), *bar_pv = bar_s + 1, *bar_end = bar_s + 2;
     volatile int *abort = &s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         s_abort = 0;
         mbar_init(bar_s, 1);
         mbar_init(bar_pv, 1);
+        mbar_init(bar_end, 1);
         mbar_fence_init();
     }
     pdl_launch_dependents();
@@ -236,26 +237,23 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
     // a thread, in order; up to a thread each, those with the longest contexts first,
     // so that what runs last is short.
     const int each = (a.num_reqs + kThreads - 1) / kThreads;
-    int items = 0, most = 0;
+    int items = 0, most = 0, bits = 0;  // the other kernel reports them
     long long units = 0;
     auto take = [&](int r, int *have, int *bits) {
         const Kv4Request q = kv4_request_of(a, r, kKv4ChunkRows, bits);
         *have = kv4_is_chunk(q, a.group) ? q.tiles * a.num_kv_heads : 0;
         return q;
     };
-    {
-        int bits = 0;  // the other kernel reports them
-        for (int r = tid * each; r < min((tid + 1) * each, a.num_reqs); ++r) {
-            int have;
-            const Kv4Request q = take(r, &have, &bits);
-            if (!have) continue;
-            items += have;
-            units += kv4_chunk_units(q, a.num_kv_heads);
-            most = max(most, kv4_chunk_tiles(q.len));
-        }
+    for (int r = tid * each; r < min((tid + 1) * each, a.num_reqs); ++r) {
+        int have;
+        const Kv4Request q = take(r, &have, &bits);
+        if (!have) continue;
+        items += have;
+        units += kv4_chunk_units(q, a.num_kv_heads);
+        most = max(most, kv4_chunk_tiles(q.len));
     }
     s_len[tid] = items ? most : -1;
-    __syncthreads();
+    if (__syncthreads_or(bits & PKV_DEV_BAD_QSL) && kv4_overlap<kThreads>(a, each, reinterpret_cast<long long *>(smem))) return;
     if (each == 1) {
         int place = 0;
         for (int i = 0; i < min(kThreads, a.num_reqs); ++i) place += s_len[i] > s_len[tid] || (s_len[i] == s_len[tid] && i < tid);
@@ -336,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         const int row0 = i * kKv4ChunkRows;
         const int32_t *ids = a.table + (long long)r * a.max_blocks;
         const uint8_t *heads = a.pool + (long long)h * Kv4Tile<D>::kBytes;
-        int bits = 0;
+        bits = 0;
         // this warp's block of key tile j
         auto id_of = [&](int j) { return j * 8 + warp < tl.blocks ? __ldg(ids + j * 8 + warp) : -1; };
         auto tile_of = [&](int j, int id) -> const uint8_t * {
@@ -566,9 +564,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         __syncthreads();
         tmem_fence_after_sync();
     }
-    if (*abort && tid == 0) raise_status(a.status, PKV_DEV_TIMEOUT);
+    if (warp == 0) {
+        // no product may still be on its way when the tensor memory is freed
+        commit(smem_u32(bar_end));
+        int never = 0;
+        if (!warp_wait(bar_end, 0, &never) || *abort)
+            if (lane == 0) raise_status(a.status, PKV_DEV_TIMEOUT);
+    }
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tm, kTmemCols);
+    if (warp == 0) {
+        tmem_fence_after_sync();
+        tmem_dealloc(tm, kTmemCols);
+    }
 }
 
 std::mutex g_mu;

@@ -290,7 +290,7 @@ int check_common(const void *pool, const pkv_cache_desc *desc, const int32_t *sl
     if (!desc) return PKV_E_NULL;
     const int rc = check_cache_desc(*desc, /*attention=*/true);
     if (rc) return rc;
-    if (num_tokens < 0 || !kv4_scale_ok(k_scale) || !kv4_scale_ok(v_scale)) return PKV_E_DIMS;
+    if (num_tokens < 0 || num_tokens > INT32_MAX - 65536 || !kv4_scale_ok(k_scale) || !kv4_scale_ok(v_scale)) return PKV_E_DIMS;
     if (num_tokens == 0) return PKV_OK;
     if (!pool || !slots) return PKV_E_NULL;
     if (!aligned(pool, 16) || !aligned(slots, 4) || !aligned(status, 4)) return PKV_E_ALIGN;
@@ -351,6 +351,7 @@ extern "C" PKV_API int paged_kv4_read(const void *kv4_cache, const pkv_cache_des
     const int rc = check_common(kv4_cache, desc, slot_mapping, num_tokens, status, k_scale, v_scale);
     if (rc || num_tokens == 0) return rc;
     if (!k_out && !v_out) return PKV_E_NULL;
+    if (k_out == v_out) return PKV_E_DIMS;
     if (!aligned(k_out, 16) || !aligned(v_out, 16)) return PKV_E_ALIGN;
     const LoadArgs a{static_cast<const uint8_t *>(kv4_cache), slot_mapping, num_tokens, desc->num_kv_heads,
                      desc->num_blocks, k_scale, v_scale, static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out),

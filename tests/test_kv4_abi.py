@@ -74,7 +74,8 @@ def test_scales_are_powers_of_two(call, name, s):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(t=-1), pkv.PKV_E_DIMS), (dict(t=0), pkv.PKV_OK), (dict(k=0), pkv.PKV_E_NULL), (dict(v=0), pkv.PKV_E_NULL),
+    (dict(t=-1), pkv.PKV_E_DIMS), (dict(t=2 ** 31 - 1), pkv.PKV_E_DIMS), (dict(t=0), pkv.PKV_OK), (dict(k=0), pkv.PKV_E_NULL),
+    (dict(v=0), pkv.PKV_E_NULL),
     (dict(slots=0), pkv.PKV_E_NULL), (dict(kv=0), pkv.PKV_E_NULL), (dict(k=0x1008), pkv.PKV_E_ALIGN),
     (dict(kv=0x4008), pkv.PKV_E_ALIGN), (dict(slots=0x3002), pkv.PKV_E_ALIGN), (dict(status=0x5001), pkv.PKV_E_ALIGN),
     (dict(ks=1020), pkv.PKV_E_DIMS), (dict(vs=1016), pkv.PKV_E_DIMS), (dict(ks=-1024), pkv.PKV_E_DIMS)])
@@ -85,7 +86,8 @@ def test_write(kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(t=-1), pkv.PKV_E_DIMS), (dict(t=0), pkv.PKV_OK), (dict(k=0, v=0), pkv.PKV_E_NULL),
     (dict(slots=0), pkv.PKV_E_NULL), (dict(kv=0), pkv.PKV_E_NULL), (dict(k=0x1008), pkv.PKV_E_ALIGN),
-    (dict(v=0x2004), pkv.PKV_E_ALIGN), (dict(status=0x5001), pkv.PKV_E_ALIGN)])
+    (dict(v=0x2004), pkv.PKV_E_ALIGN), (dict(status=0x5001), pkv.PKV_E_ALIGN), (dict(t=2 ** 31 - 1), pkv.PKV_E_DIMS),
+    (dict(v=0x1000), pkv.PKV_E_DIMS)])
 def test_read(kw, code):
     assert read(**kw) == code
 
@@ -99,10 +101,22 @@ def test_read(kw, code):
     (dict(qs=4092), pkv.PKV_E_DIMS), (dict(qs=4088), pkv.PKV_E_DIMS), (dict(t=0), pkv.PKV_OK), (dict(r=0), pkv.PKV_OK),
     (dict(q=0), pkv.PKV_E_NULL), (dict(kv=0), pkv.PKV_E_NULL), (dict(bt=0), pkv.PKV_E_NULL), (dict(sl=0), pkv.PKV_E_NULL),
     (dict(qsl=0), pkv.PKV_E_NULL), (dict(out=0), pkv.PKV_E_NULL), (dict(ws=0), pkv.PKV_E_NULL),
+    (dict(r=2 ** 31 - 1), pkv.PKV_E_DIMS), (dict(out=0x1000), pkv.PKV_E_DIMS),
     (dict(q=0x1008), pkv.PKV_E_ALIGN), (dict(kv=0x2004), pkv.PKV_E_ALIGN), (dict(out=0x6008), pkv.PKV_E_ALIGN),
     (dict(ws=0x10008), pkv.PKV_E_ALIGN), (dict(bt=0x3001), pkv.PKV_E_ALIGN), (dict(status=0x7002), pkv.PKV_E_ALIGN)])
 def test_attention(kw, code):
     assert attend(**kw) == code
+
+
+@pytest.mark.parametrize("pool,ws,code", [p[:1] + (0x1000,) + p[1:] for p in POOLS] +
+                         [({}, 0, pkv.PKV_E_NULL), ({}, 0x1008, pkv.PKV_E_ALIGN)])
+def test_workspace(pool, ws, code):
+    assert pkv.LIB.paged_kv4_attention_init(ctypes.byref(desc(**pool)), vp(ws), 1 << 40, None) == code
+    n = ctypes.c_size_t(0)
+    if pool:
+        assert pkv.LIB.paged_kv4_attention_workspace_bytes(ctypes.byref(desc(**pool)), ctypes.byref(n)) == code
+    assert pkv.LIB.paged_kv4_attention_workspace_bytes(None, ctypes.byref(n)) == pkv.PKV_E_NULL
+    assert pkv.LIB.paged_kv4_attention_init(None, vp(0x1000), 1 << 40, None) == pkv.PKV_E_NULL
 
 
 @pytest.mark.parametrize("kw,code", [
