@@ -66,6 +66,10 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
+// The factor that what was taken against reference m has against `to` (0 where it
+// saw no key; to may be -inf too then).
+__device__ __forceinline__ float against(float m, float to, float mul) { return fast_exp2((m - fmaxf(to, -3e38f)) * mul); }
+
 template <int D, int kNt>
 constexpr int kQBytes = kNt * (D / 16) * 2 * 32 * 4;  // q's fragments of 8 kNt rows
 
@@ -103,11 +107,12 @@ struct Span {
     int key0;    // position of the first block's first key
     int limit0;  // keys that the tile's first row sees
     int end;     // keys that its last row sees
-    int row0, group;
+    int row0, tok0, group;  // tok0: row0 / group
+    uint32_t inv;
 
     // keys of block `blk` that row `row` of the tile sees (at most 16 count)
     __device__ __forceinline__ int sees(int blk, int row) const {
-        return limit0 + (row0 + row) / group - row0 / group - key0 - 16 * blk;
+        return limit0 + kv4_over(row0 + row, group, inv) - tok0 - key0 - 16 * blk;
     }
 };
 
@@ -134,7 +139,7 @@ struct Item {
             uint4 w[D / 32];
             uint32_t top = 0;
             if (row < rows) {
-                const int rr = row0 + row, tok = rr / a.group;
+                const int rr = row0 + row, tok = kv4_over(rr, a.group, a.group_inv);
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     a.q + (long long)(token0 + tok) * a.q_stride + (long long)(head * a.group + rr - tok * a.group) * D) + t * (D / 32);
 #pragma unroll
@@ -170,7 +175,8 @@ struct Item {
                     for (int j = 0; j < 4; ++j) q[n][2 * i + j / 2][j & 1] = f[j];
                 }
             }
-            const float f = row < rows ? up * a.scale_log2 : 0.0f;
+            // never 0: masked scores times it have to stay -inf
+            const float f = row < rows ? fmaxf(up * a.scale_log2, 0x1p-126f) : 1.0f;
             mul[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
             m[n] = make_float2(-INFINITY, -INFINITY);
             l[n] = make_float2(0.0f, 0.0f);
@@ -186,7 +192,7 @@ struct Item {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float to = fmaxf(m, top);
-        *f = m == to ? 1.0f : m == -INFINITY ? 0.0f : fast_exp2((m - to) * mul);
+        *f = against(m, to, mul);
         m = to;
         l *= *f;
     }
@@ -313,11 +319,7 @@ struct Item {
             for (int n = 0; n < kNt; ++n) {
                 float x[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    x[c] = fast_exp2(e[b][n][c]);
-                    // a factor of 0 (a scale or q near the smallest value) times -inf is no number
-                    if (kMasked && s[b][n][c] == -INFINITY) x[c] = 0.0f;
-                }
+                for (int c = 0; c < 4; ++c) x[c] = fast_exp2(e[b][n][c]);
                 l[n] = fadd2(l[n], fadd2(make_float2(x[0], x[1]), make_float2(x[2], x[3])));
                 p[b][n][0] = movmatrix_trans(pack_f16x2(x[0], x[1]));
                 p[b][n][1] = movmatrix_trans(pack_f16x2(x[2], x[3]));
@@ -377,19 +379,16 @@ struct Item {
     }
     static __device__ __forceinline__ void factors(float m, float n, float mul, float *to, float *f, float *g) {
         *to = fmaxf(m, n);
-        *f = m == *to ? 1.0f : m == -INFINITY ? 0.0f : fast_exp2((m - *to) * mul);
-        *g = n == *to ? 1.0f : n == -INFINITY ? 0.0f : fast_exp2((n - *to) * mul);
+        *f = against(m, *to, mul);
+        *g = against(n, *to, mul);
     }
     struct Loaded {
         float4 o[kK], st;
     };
-    // A partial's 8 rows n. kGlobal: written by another SM.
-    template <bool kGlobal>
-    static __device__ __forceinline__ void load(const float4 *from, int n, Loaded &x, int lane) {
-        auto get = [&](int i) { return kGlobal ? __ldcg(from + i * 32 + lane) : from[i * 32 + lane]; };
+    static __device__ __forceinline__ void load(const float4 *from, int n, Loaded &x, int lane) {  // a partial's 8 rows n
 #pragma unroll
-        for (int i = 0; i < kK; ++i) x.o[i] = get(n * kK + i);
-        x.st = get(kNt * kK + n);
+        for (int i = 0; i < kK; ++i) x.o[i] = from[(n * kK + i) * 32 + lane];
+        x.st = from[(kNt * kK + n) * 32 + lane];
     }
     __device__ __forceinline__ void join(int n, const Loaded &x) {
         float fx, fy, gx, gy;
@@ -403,13 +402,6 @@ struct Item {
             o[n][i][2] = o[n][i][2] * fx + x.o[i].z * gx;
             o[n][i][3] = o[n][i][3] * fy + x.o[i].w * gy;
         }
-    }
-    __device__ __forceinline__ void become(int n, const Loaded &x, float4 scale) {
-        mul[n] = make_float2(scale.x, scale.y);
-        m[n] = make_float2(x.st.x, x.st.y);
-        l[n] = make_float2(x.st.z, x.st.w);
-#pragma unroll
-        for (int i = 0; i < kK; ++i) o[n][i][0] = x.o[i].x, o[n][i][1] = x.o[i].y, o[n][i][2] = x.o[i].z, o[n][i][3] = x.o[i].w;
     }
 
     // V scales of tokens that no row sees become zero, and those that are no
@@ -486,6 +478,21 @@ struct Where {
     long long start;  // the item's first position
 };
 
+// Of what another SM wrote. Volatile: such loads go out together, before their
+// values are used.
+__device__ __forceinline__ float4 far_load(const float4 *from) {
+    float4 x;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(from) : "memory");
+    return x;
+}
+
+// An item of which this CTA was the last to leave its part.
+struct Far {
+    int rows, nt;  // 0: none; the partials are of 8 nt rows
+    int row0, token0, head;
+    int first, last;  // the item's shares
+};
+
 // What an item's warps have in common, and this warp's place among the CTA's.
 struct Team {
     int warp, cta, shares;  // shares of this CTA, one a warp
@@ -496,6 +503,8 @@ struct Team {
     uint32_t q;             // shared address of this warp's q fragments (16 rows or more)
     volatile int *abort;
     bool met;               // this warp has been at the CTA's barrier
+    Far *far;               // of the CTA: the item begun before it, the one that goes on behind it
+    int *any_far;           // it has parts of such
 };
 
 template <int D, int kMaxNt>
@@ -541,7 +550,8 @@ struct Kernel {
         for (int i = 0; i < kStg && put < b1; ++i) start();
         it.load_q(a, w.q.q0, row0, rows, w.h, lane);
         if (Item<D, kNt>::kQShared) __syncwarp();
-        Span at{16 * b0, w.q.len - w.q.n + row0 / a.group + 1, min(tl.keys, 16 * b1), row0, a.group};
+        const int tok0 = kv4_over(row0, a.group, a.group_inv);
+        Span at{16 * b0, w.q.len - w.q.n + tok0 + 1, min(tl.keys, 16 * b1), row0, tok0, a.group, a.group_inv};
         auto between = [&]() {
             if (put < b1) start();
         };
@@ -572,6 +582,8 @@ struct Kernel {
             return;
         }
         const int base = team.cta * team.sh.per_cta;
+        const bool far = team.first < base || team.last >= base + team.shares;
+        if (far && lane == 0) *team.any_far = 1;
         if (team.cut) {
             team.met = true;
             __syncthreads();
@@ -581,45 +593,82 @@ struct Kernel {
 #pragma unroll
                 for (int g = 0; g < kNt; ++g) {
                     typename Item<D, kNt>::Loaded x;
-                    Item<D, kNt>::template load<false>(team.area + i * kArea, g, x, lane);
+                    Item<D, kNt>::load(team.area + i * kArea, g, x, lane);
                     it.join(g, x);
                 }
         }
-        if (team.first < base || team.last >= base + team.shares) {
+        if (far) {
             const int c0 = team.first / team.sh.per_cta, n = team.last / team.sh.per_cta - c0 + 1;
-            auto part = [&](int c) { return a.parts + ((size_t)2 * c + (c == c0)) * kPart; };
-            it.template store<true>(part(team.cta), lane);
+            it.template store<true>(a.parts + ((size_t)2 * team.cta + (team.cta == c0)) * kPart, lane);
             __syncwarp();
-            int seen = 0;
             if (lane == 0) {
+                int seen;
                 // releases this warp's partial, and takes the others' in
                 asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(a.arrived + c0) : "memory");
                 seen -= kKv4Nobody;
-                if (seen == n - 1) atomicExch(a.arrived + c0, kKv4Nobody);
+                if (seen == n - 1) {
+                    atomicExch(a.arrived + c0, kKv4Nobody);
+                    team.far[team.cta == c0] = Far{rows, kNt, row0, w.q.q0, w.h, team.first, team.last};
+                }
                 if (seen < 0 || seen >= n) raise_status(a.status, PKV_DEV_BAD_WORKSPACE);
             }
-            seen = __shfl_sync(0xffffffffu, seen, 0);
-            if (seen != n - 1) return;
-            __syncwarp();
-            // a part's values are on their way while the one before is joined
-#pragma unroll
-            for (int g = 0; g < kNt; ++g) {
-                typename Item<D, kNt>::Loaded x[2];
-                Item<D, kNt>::template load<true>(part(c0), g, x[0], lane);
-                const float4 scale = __ldcg(part(c0) + (Item<D, kNt>::kVecs + g) * 32 + lane);
-                Item<D, kNt>::template load<true>(part(c0 + 1), g, x[1], lane);
-                it.become(g, x[0], scale);
-#pragma unroll 1
-                for (int i = 1; i < n; i += 2) {
-                    if (i + 1 < n) Item<D, kNt>::template load<true>(part(c0 + i + 1), g, x[0], lane);
-                    it.join(g, x[1]);
-                    if (i + 1 == n) break;
-                    if (i + 2 < n) Item<D, kNt>::template load<true>(part(c0 + i + 2), g, x[1], lane);
-                    it.join(g, x[0]);
-                }
-            }
+            return;
         }
         output<kNt>(a, it, w, row0, rows, lane);
+    }
+
+    // The parts of an item that several CTAs left, by all warps of the last of them:
+    // one of the D / 16 steps of 8 rows at a time, kAhead parts on their way.
+    static __device__ __forceinline__ void join_far(const Kv4Args &a, const Far &j, int per_cta, int warp, int lane) {
+        constexpr int kK = D / 16, kAhead = 4;
+        const int g = lane >> 2, t = lane & 3;
+        const int c0 = j.first / per_cta, count = j.last / per_cta - c0 + 1;
+        const float4 *lead = a.parts + ((size_t)2 * c0 + 1) * kPart + lane;
+        auto part = [&](int c) { return lead + (c ? (size_t)(2 * c - 1) * kPart : 0); };
+#pragma unroll 1
+        for (int unit = warp; unit < j.nt * kK; unit += kW) {
+            const int n = unit / kK, at = (j.nt * kK + n) * 32;
+            const float4 mul = __ldcg(lead + at + 32 * j.nt);
+            float mx = -INFINITY, my = -INFINITY, lx = 0.0f, ly = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int k0 = 0; k0 < count; k0 += kAhead) {
+                float4 st[kAhead], x[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float4 *from = part(min(k0 + k, count - 1));
+                    st[k] = far_load(from + at);
+                    x[k] = far_load(from + unit * 32);
+                }
+                float tx = mx, ty = my;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) tx = fmaxf(tx, st[k].x), ty = fmaxf(ty, st[k].y);
+                const float fx = against(mx, tx, mul.x), fy = against(my, ty, mul.y);
+                mx = tx, my = ty;
+                lx *= fx, ly *= fy;
+                o = make_float4(o.x * fx, o.y * fy, o.z * fx, o.w * fy);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const bool live = k0 + k < count;
+                    const float gx = live ? against(st[k].x, tx, mul.x) : 0.0f, gy = live ? against(st[k].y, ty, mul.y) : 0.0f;
+                    lx += st[k].z * gx, ly += st[k].w * gy;
+                    o = make_float4(o.x + x[k].x * gx, o.y + x[k].y * gy, o.z + x[k].z * gx, o.w + x[k].w * gy);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = c ? ly : lx;
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const int row = 8 * n + 2 * t + c;
+                if (row >= j.rows) continue;
+                const float f = __fdividef(a.v_scale, l);
+                const int rr = j.row0 + row, tok = kv4_over(rr, a.group, a.group_inv);
+                *reinterpret_cast<uint32_t *>(a.out + ((long long)(j.token0 + tok) * a.num_kv_heads * a.group + j.head * a.group + rr - tok * a.group) * D +
+                                              D / 8 * g + 2 * (unit - n * kK)) = c ? pack_bf16x2(o.y * f, o.w * f) : pack_bf16x2(o.x * f, o.z * f);
+            }
+        }
     }
 
     template <int kNt>
@@ -636,8 +685,8 @@ struct Kernel {
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 const int row = 8 * n + 2 * t + c;
                 if (row >= rows) continue;
-                const float f = a.v_scale / l;
-                const int rr = row0 + row, tok = rr / a.group;
+                const float f = __fdividef(a.v_scale, l);
+                const int rr = row0 + row, tok = kv4_over(rr, a.group, a.group_inv);
                 uint4 *to = reinterpret_cast<uint4 *>(
                     a.out + ((long long)(w.q.q0 + tok) * a.num_kv_heads * a.group + w.h * a.group + rr - tok * a.group) * D + kC * g);
 #pragma unroll
@@ -658,10 +707,11 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     extern __shared__ __align__(128) uint8_t s_mem[];  // rings, then a partial of each warp
     __shared__ __align__(8) uint64_t s_bar[K::kW * K::kStg];
     __shared__ long long s_sum[kThreads], s_warp[K::kW];
-    __shared__ int s_abort, s_most[K::kW];
+    __shared__ int s_abort, s_most[K::kW], s_any_far;
+    __shared__ Far s_far[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     for (int i = tid; i < K::kW * K::kStg; i += kThreads) mbar_init(s_bar + i, 2);
-    if (tid == 0) s_abort = 0;
+    if (tid == 0) s_abort = s_any_far = s_far[0].rows = s_far[1].rows = 0;
     mbar_fence_init();
     pdl_launch_dependents();
     pdl_wait();
@@ -731,7 +781,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     __syncthreads();
 
     Team team;
-    team.sh = kv4_shares(total, (int)gridDim.x, K::kW, kv4_least(K::kRows));
+    team.sh = kv4_shares(total, (int)gridDim.x, K::kW, kv4_least(K::kRows), a.num_reqs, a.num_kv_heads);
     team.warp = warp;
     team.cta = cta;
     team.shares = min(team.sh.per_cta, team.sh.count - cta * team.sh.per_cta);
@@ -740,17 +790,18 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     team.q = smem_u32(s_mem + K::kRing) + warp * kQBytes<D, kMaxNt>;
     team.abort = &s_abort;
     team.met = false;
+    team.far = s_far;
+    team.any_far = &s_any_far;
     if (team.shares <= 0) return;
     if (warp < team.shares) {
         const int share = cta * team.sh.per_cta + warp;
         const long long from = team.sh.begin(share);
         Where w;
         {
-            int lo = 0, hi = kThreads - 1;  // the first thread with s_sum > from
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (s_sum[mid] > from) hi = mid; else lo = mid + 1;
-            }
+            // the first thread with s_sum > from: among the last of each kW of them, and before it
+            constexpr int kRun = kThreads / 32;
+            const int run = __ffs(__ballot_sync(0xffffffffu, s_sum[lane * kRun + kRun - 1] > from)) - 1;
+            const int lo = run * kRun + __ffs(__ballot_sync(0xffffffffu, s_sum[run * kRun + min(lane, kRun - 1)] > from)) - 1;
             long long first = lo ? s_sum[lo - 1] : 0;
             for (w.r = lo * each;; ++w.r) {  // of its requests, the one that `from` lies in
                 w.q = request(w.r);
@@ -795,6 +846,10 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
         }
     }
     if (!team.met) __syncthreads();
+    if (!s_any_far) return;
+    __syncthreads();
+    for (int k = 0; k < 2; ++k)
+        if (s_far[k].rows) K::join_far(a, s_far[k], team.sh.per_cta, warp, lane);
 }
 
 // Places in the workspace, for any batch and form.
@@ -892,7 +947,7 @@ extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int3
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Kv4Args a{static_cast<const __nv_bfloat16 *>(q), q_stride, static_cast<const uint8_t *>(kv4_cache), block_table,
                     seq_lens, query_start_loc, num_tokens, desc->num_kv_heads, group, num_reqs, max_blocks_per_req,
-                    desc->num_blocks, scale_log2, v_scale, static_cast<__nv_bfloat16 *>(out),
+                    desc->num_blocks, kv4_inverse(group), scale_log2, v_scale, static_cast<__nv_bfloat16 *>(out),
                     reinterpret_cast<int *>(ws), reinterpret_cast<int *>(ws) + 1, reinterpret_cast<float4 *>(ws + parts_at(sms)),
                     rows >= 64, status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);

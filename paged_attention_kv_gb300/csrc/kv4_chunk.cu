@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
 
         // q: two threads a row, fp16 scaled by a power of two to lie in (-4, 4)
         {
-            const int qr = tid >> 1, half = tid & 1, rr = row0 + qr, tok = rr / a.group;
+            const int qr = tid >> 1, half = tid & 1, rr = row0 + qr, tok = kv4_over(rr, a.group, a.group_inv);
             constexpr int kC = D / 16;  // 16-byte chunks of a thread
             uint4 x[kC];
             uint32_t top = 0;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         __syncthreads();
         // keys that this row sees (padding rows: one)
         const int rr = row0 + row;
-        const int limit = row < tl.rows ? q.len - q.n + rr / a.group + 1 : 1;
+        const int limit = row < tl.rows ? q.len - q.n + kv4_over(rr, a.group, a.group_inv) + 1 : 1;
         const float mul = s_mul[row];
         float m = -INFINITY, l = 0.0f;
         bool large = false;  // some row's reference is
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         s_x[part * 128 + row] = l;
         named_barrier_sync(1 + (warp & 3), 64);
         const float f = a.v_scale / (s_x[row] + s_x[128 + row]);
-        const int tok = rr / a.group;
+        const int tok = kv4_over(rr, a.group, a.group_inv);
         __nv_bfloat16 *out = a.out + ((long long)(q.q0 + tok) * a.num_kv_heads * a.group + h * a.group + rr - tok * a.group) * D + part * (D / 2);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {

@@ -34,13 +34,22 @@ struct Kv4Tiling {
 PKV_HD int kv4_weight(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 6 : 11; }
 constexpr int kKv4ItemKeys = 96;
 
-// x / y for a quotient below 2^20, without a division of 64 bits (which takes
-// longer than all the rest here).
+// About x / y (2^-21), in a few cycles on the device: every warp works its share out
+// before it can ask for any key.
+PKV_HD float kv4_ratio(float x, float y) {
+#ifdef __CUDA_ARCH__
+    return __fdividef(x, y);
+#else
+    return x / y;
+#endif
+}
+// x / y for a quotient below 2^19, without a division of 64 bits.
 PKV_HD int kv4_quotient(long long x, long long y) {
-    long long q = (long long)((float)x / (float)y);  // off by at most 1
-    if (q * y > x) --q;
-    if ((q + 1) * y <= x) ++q;
-    return (int)q;
+    int q = (int)kv4_ratio((float)x, (float)y);  // off by at most 1
+    const long long left = x - q * y;
+    if (left < 0) --q;
+    if (left >= y) ++q;
+    return q;
 }
 
 PKV_HD Kv4Request kv4_request(int q0, int n, int len, int group, int rows) {
@@ -80,17 +89,18 @@ PKV_HD Kv4Tiling kv4_tile(const Kv4Request &q, int i, int group, int rows) {
     const unsigned from = (unsigned)i * (unsigned)rows, left = (unsigned)q.n * (unsigned)group - from;
     Kv4Tiling t;
     t.rows = left < (unsigned)rows ? (int)left : rows;
-    t.keys = q.len - q.n + (int)((from + t.rows - 1) / (unsigned)group) + 1;
+    t.keys = q.tiles == 1 ? q.len : q.len - q.n + (int)((from + t.rows - 1) / (unsigned)group) + 1;
     t.blocks = (int)(((unsigned)t.keys + 15) / 16);
     return t;
 }
 
-// The block before which an item is cut at its position `off`: an even one (a warp
+// The block before which an item is cut at its position `off`, with so many blocks
+// a position: an even one (a warp
 // takes two at a time), none and all of them included, so that no piece is
 // shorter than two. Both shares that meet there work it out alike, and it does
 // not fall as off rises.
-PKV_HD int kv4_cut(long long off, long long cost, int blocks) {
-    const int b = (int)((float)off / (float)cost * (float)blocks) & ~1;
+PKV_HD int kv4_cut(long long off, float each, int blocks) {
+    const int b = (int)((float)off * each) & ~1;
     return b + 2 > blocks ? blocks : b;
 }
 
@@ -123,9 +133,10 @@ struct Kv4Piece {
 };
 PKV_HD Kv4Piece kv4_piece(const Kv4Shares &sh, int k, long long start, long long cost, int blocks) {
     const long long from = sh.begin(k), to = sh.begin(k + 1), stop = start + cost;
+    const float each = kv4_ratio((float)blocks, (float)cost);
     Kv4Piece p;
-    p.b0 = from > start ? kv4_cut(from - start, cost, blocks) : 0;
-    p.b1 = to < stop ? kv4_cut(to - start, cost, blocks) : blocks;
+    p.b0 = from > start ? kv4_cut(from - start, each, blocks) : 0;
+    p.b1 = to < stop ? kv4_cut(to - start, each, blocks) : blocks;
     p.begun = p.b0 > 0;
     p.cut = p.b1 < blocks;
     p.more = stop < to;
@@ -134,11 +145,11 @@ PKV_HD Kv4Piece kv4_piece(const Kv4Shares &sh, int k, long long start, long long
     // shares are longer than two blocks)
     if (p.begun) {
         p.first = sh.index(start);
-        if (kv4_cut(sh.begin(p.first + 1) - start, cost, blocks) == 0) ++p.first;
+        if (kv4_cut(sh.begin(p.first + 1) - start, each, blocks) == 0) ++p.first;
     }
     if (p.cut) {
         p.last = sh.index(stop - 1);
-        if (kv4_cut(sh.begin(p.last) - start, cost, blocks) == blocks) --p.last;
+        if (kv4_cut(sh.begin(p.last) - start, each, blocks) == blocks) --p.last;
     }
     return p;
 }
@@ -148,19 +159,29 @@ PKV_HD Kv4Piece kv4_piece(const Kv4Shares &sh, int k, long long start, long long
 // a share holds more than two of its blocks: see kv4_piece.
 PKV_HD int kv4_least(int rows) { return 6 * 16 * kv4_weight(rows); }
 
-// At most ctas * warps shares of at least `least`, over as many CTAs as there are.
-PKV_HD Kv4Shares kv4_shares(long long total, int ctas, int warps, int least) {
+// At most ctas * warps shares of at least `least`. Where that leaves warps idle, up to
+// six shares of an item (of the mean of `reqs` requests' kv heads) go into one CTA: it
+// joins them in 1 us, where parts of other CTAs take 3. The kv heads of a request alone
+// are of one length and get shares that end where they do.
+PKV_HD Kv4Shares kv4_shares(long long total, int ctas, int warps, int least, int reqs, int heads) {
     const int most = ctas * warps;
     Kv4Shares s;
     s.total = total;
-    if (total <= (long long)least * most) {
+    int together = 0;
+    if (total <= 0) {
         s.each = least;
+    } else if (total <= (long long)least * most) {
+        const float mean = kv4_ratio((float)total, (float)reqs * (float)heads);
+        const int k = (int)kv4_ratio(mean, (float)least);
+        s.each = reqs == 1 && k > 1 ? (total / heads + k - 1) / k : least;
+        together = k < 6 ? k : 6;
     } else {
-        s.each = (long long)((float)total / (float)most);
+        s.each = (long long)(kv4_ratio((float)total, (float)most) * 1.000001f) + 1;
         while (s.each * most < total) s.each += 1 + (s.each >> 22);
     }
     s.count = total <= 0 ? 0 : kv4_quotient(total - 1, s.each) + 1;
-    s.per_cta = (s.count + ctas - 1) / ctas;
+    s.per_cta = kv4_quotient(s.count + ctas - 1, ctas);
+    if (s.per_cta < together) s.per_cta = together < warps ? together : warps;
     return s;
 }
 

@@ -29,7 +29,7 @@ int main() {
             first[r + 1] = first[r] + kv4_cost(q[r], heads, q[r].tiles);
         }
         const long long total = first[R];
-        const Kv4Shares sh = kv4_shares(total, ctas, warps, kv4_least(rows));
+        const Kv4Shares sh = kv4_shares(total, ctas, warps, kv4_least(rows), R, heads);
         if (sh.per_cta > warps || (long long)sh.per_cta * ctas < sh.count) { printf("%d shares, %d a CTA\n", sh.count, sh.per_cta); return 1; }
         // next block expected of each item, and its pieces: seen, told by the first, told by the others
         std::vector<std::vector<int>> next(R), seen(R), told(R);
