@@ -129,25 +129,37 @@ struct Item {
     uint32_t q[kQShared ? 1 : kNt][kQShared ? 1 : kK][2];
     uint32_t q_at;  // shared address, this lane's
 
-    // q rows as fp16 fragments, each scaled by a power of two to lie in (-4, 4);
-    // mul takes that back. Rows past `rows` are zero.
-    __device__ __forceinline__ void load_q(const Kv4Args &a, int token0, int row0, int rows, int head, int lane) {
+    // q rows as they are; zero past `rows`. The loads go out before anything waits for
+    // the block ids.
+    using Rows = uint4[kNt][D / 32];
+    static __device__ __forceinline__ void read_q(const Kv4Args &a, int token0, int row0, int rows, int head, Rows &w, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
             const int row = 8 * n + g;
-            uint4 w[D / 32];
-            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) w[n][i] = make_uint4(0, 0, 0, 0);
             if (row < rows) {
                 const int rr = row0 + row, tok = kv4_over(rr, a.group, a.group_inv);
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     a.q + (long long)(token0 + tok) * a.q_stride + (long long)(head * a.group + rr - tok * a.group) * D) + t * (D / 32);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) w[i] = __ldg(src + i);
-            } else {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < D / 32; ++i)
+                    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[n][i].x), "=r"(w[n][i].y), "=r"(w[n][i].z), "=r"(w[n][i].w)
+                                 : "l"(src + i));
             }
+        }
+    }
+    // As fp16 fragments, each row scaled by a power of two to lie in (-4, 4); mul takes
+    // that back.
+    __device__ __forceinline__ void begin(const Kv4Args &a, int rows, const Rows &all, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+            const int row = 8 * n + g;
+            const uint4 (&w)[D / 32] = all[n];
+            uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const uint32_t mk = 0x7fff7fffu;
@@ -534,6 +546,8 @@ struct Kernel {
         // ids are looked up 32 at a time, the next 32 ahead; a lane copies its own block
         int have = b0 + lane < b1 ? __ldg(ids + b0 + lane) : 0;
         int next = b0 + 32 + lane < b1 ? __ldg(ids + b0 + 32 + lane) : 0;
+        typename Item<D, kNt>::Rows q_rows;
+        Item<D, kNt>::read_q(a, w.q.q0, row0, rows, w.h, q_rows, lane);
         int put = b0;  // next pair to copy
         auto start = [&]() {
             const int at = (put - b0) & 31;
@@ -548,7 +562,7 @@ struct Kernel {
         };
 #pragma unroll 1
         for (int i = 0; i < kStg && put < b1; ++i) start();
-        it.load_q(a, w.q.q0, row0, rows, w.h, lane);
+        it.begin(a, rows, q_rows, lane);
         if (Item<D, kNt>::kQShared) __syncwarp();
         const int tok0 = kv4_over(row0, a.group, a.group_inv);
         Span at{16 * b0, w.q.len - w.q.n + tok0 + 1, min(tl.keys, 16 * b1), row0, tok0, a.group, a.group_inv};
@@ -770,15 +784,15 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
         if (lane >= d) sum += o;
     }
     if (lane == 31) s_warp[warp] = sum;
-    if (__syncthreads_or(bits & PKV_DEV_BAD_QSL) && kv4_overlap<kThreads>(a, each, s_sum)) return;
+    s_sum[tid] = sum;  // of its warp's requests
+    if (__syncthreads_or(bits & PKV_DEV_BAD_QSL)) {
+        if (kv4_overlap<kThreads>(a, each, s_sum)) return;
+        s_sum[tid] = sum;
+        __syncthreads();
+    }
     long long total = 0;
 #pragma unroll
-    for (int i = 0; i < K::kW; ++i) {
-        if (i < warp) sum += s_warp[i];
-        total += s_warp[i];
-    }
-    s_sum[tid] = sum;
-    __syncthreads();
+    for (int i = 0; i < K::kW; ++i) total += s_warp[i];
 
     Team team;
     team.sh = kv4_shares(total, (int)gridDim.x, K::kW, kv4_least(K::kRows), a.num_reqs, a.num_kv_heads);
@@ -798,11 +812,18 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
         const long long from = team.sh.begin(share);
         Where w;
         {
-            // the first thread with s_sum > from: among the last of each kW of them, and before it
-            constexpr int kRun = kThreads / 32;
-            const int run = __ffs(__ballot_sync(0xffffffffu, s_sum[lane * kRun + kRun - 1] > from)) - 1;
-            const int lo = run * kRun + __ffs(__ballot_sync(0xffffffffu, s_sum[run * kRun + min(lane, kRun - 1)] > from)) - 1;
-            long long first = lo ? s_sum[lo - 1] : 0;
+            // the thread whose requests `from` lies in: its warp, then by a vote the lane
+            long long first = 0;
+            int run = 0;
+#pragma unroll
+            for (int i = 0; i < K::kW - 1; ++i)
+                if (first + s_warp[i] <= from && run == i) {
+                    first += s_warp[i];
+                    ++run;
+                }
+            const int in = __ffs(__ballot_sync(0xffffffffu, first + s_sum[run * 32 + lane] > from)) - 1;
+            if (in) first += s_sum[run * 32 + in - 1];
+            const int lo = run * 32 + in;
             for (w.r = lo * each;; ++w.r) {  // of its requests, the one that `from` lies in
                 w.q = request(w.r);
                 const long long cost = kv4_cost(w.q, a.num_kv_heads, w.q.tiles);
