@@ -30,8 +30,13 @@ struct Kv4Tiling {
 };
 
 // What a key costs with so many rows beside it, and an item by itself (its start,
-// which is a chain of trips to memory, and its end): as much as so many keys.
-PKV_HD int kv4_weight(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 6 : 11; }
+// which is a chain of trips to memory, and its end): as much as so many keys. 100
+// requests of 1 to 15 tokens and 500 to 2000 keys: 104.9 us, 109.5 with 11 in place
+// of 9, 113.5 with 7 and 12, 103.5 with one weight for all, which costs 256 requests
+// of 1 to 8 tokens 138.9 us against 130.1. Items at 48 keys instead of 96: two short
+// requests 6.7 us instead of 5.0, 128 requests of 4 tokens and 30 to 2000 keys 46.1
+// instead of 40.0; at 192 those take 41.5.
+PKV_HD int kv4_weight(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 6 : 9; }
 constexpr int kKv4ItemKeys = 96;
 
 // About x / y (2^-21), in a few cycles on the device: every warp works its share out
@@ -104,7 +109,8 @@ PKV_HD int kv4_cut(long long off, float each, int blocks) {
     return b + 2 > blocks ? blocks : b;
 }
 
-// Requests of the chunk kernel: tiles of 128 rows, keys in tiles of 128.
+// Requests of the chunk kernel: tiles of 128 rows, keys in tiles of 128. Half a tile
+// is worth it: 64 rows of 64 requests with 1000 keys take 61 us there, 110 here.
 constexpr int kKv4ChunkRows = 128;
 PKV_HD bool kv4_is_chunk(const Kv4Request &q, int group) { return (long long)q.n * group >= 64; }
 PKV_HD int kv4_chunk_tiles(int keys) { return (int)(((unsigned)keys + 127) / 128); }
@@ -112,9 +118,13 @@ PKV_HD int kv4_chunk_tiles(int keys) { return (int)(((unsigned)keys + 127) / 128
 PKV_HD long long kv4_chunk_units(const Kv4Request &q, int heads) {
     return (long long)q.tiles * heads * kv4_chunk_tiles(q.len - q.n / 2);
 }
-// An item of the chunk kernel is never cut: where the longest would take longer
-// than all of them cut into equal shares by the other kernel, that one has them.
-PKV_HD bool kv4_use_chunks(long long units, int longest) { return units > 0 && units >= 40LL * longest; }
+// An item of the chunk kernel is never cut: it takes about 7 us and 1.4 a key tile,
+// however few there are. The other kernel cuts them into equal shares: about 20 us and
+// 20 to 30 ns for each of all units. Measured (this kernel, the other; 8 heads of
+// 128): 1 request of 32 tokens and 1000 keys 21.7 and 35.3 us, 2000 keys about 34 and
+// 36.4, 4000 keys 58.8 and 40.9; 4 of them 59.7 and 60.6; 16 of 16 tokens and 4000 keys
+// 73 and 97; 1 of 512 tokens and 30000 keys 394 and 833.
+PKV_HD bool kv4_use_chunks(long long units, int longest) { return units > 0 && units + 400 >= 48LL * longest; }
 
 struct Kv4Shares {
     long long total, each;
@@ -156,7 +166,8 @@ PKV_HD Kv4Piece kv4_piece(const Kv4Shares &sh, int k, long long start, long long
 
 // What a share has at least: six blocks of the rows of a tile. An item that is cut
 // has four blocks or more, and costs kKv4ItemKeys / 16 = 6 more than those, so that
-// a share holds more than two of its blocks: see kv4_piece.
+// a share holds more than two of its blocks: see kv4_piece. (Ten blocks: two short
+// requests 6.6 us instead of 5.0, 8 of 500 to 2000 keys 14.4 instead of 12.7.)
 PKV_HD int kv4_least(int rows) { return 6 * 16 * kv4_weight(rows); }
 
 // At most ctas * warps shares of at least `least`. Where that leaves warps idle, up to

@@ -297,13 +297,19 @@ int check_common(const void *pool, const pkv_cache_desc *desc, const int32_t *sl
     return PKV_OK;
 }
 
-// CTAs of so many tokens, and of a part of the heads where those leave SMs without four.
-int grid_for(int num_tokens, int tokens, int heads, dim3 *grid) {
+// CTAs of so many tokens, and of a part of the heads where those leave SMs without
+// four; between 8 of them and half as many as SMs a part has the work of a warp at
+// least (32 groups of K and V). Written and read back, us, heads not shared / shared
+// as far as that / to the last one: 16 tokens of 8 heads of 128 6.9 / 4.2 / 4.1, 200
+// 7.1 / 4.8 / 5.4, 2240 15.5 / 11.3 / 11.2; 64 tokens of 4 heads of 64 4.1 / 4.1 / 3.9,
+// 512 4.3 / 4.3 / 5.7, 2240 of whole blocks 5.4 / 5.3 / 4.8.
+int grid_for(int num_tokens, int tokens, int heads, int head_size, dim3 *grid) {
     int sms = 0;
     const int rc = device_sms(&sms);
     if (rc) return rc;
     const unsigned x = ((unsigned)num_tokens + tokens - 1) / tokens;
-    *grid = dim3(x, std::min<unsigned>(heads, std::max(1u, 4u * sms / x)));
+    const unsigned most = x >= 8 && x < (unsigned)sms / 2 ? std::max(1, heads * head_size / 256) : heads;
+    *grid = dim3(x, std::min(most, std::max(1u, 4u * sms / x)));
     return PKV_OK;
 }
 
@@ -337,7 +343,7 @@ extern "C" PKV_API int paged_kv4_write(const void *k, int64_t k_stride, const vo
                       static_cast<uint8_t *>(kv4_cache), k_scale, v_scale, 1.0f / k_scale, 1.0f / v_scale, status};
     const auto kernel = desc->head_size == 128 ? kv4_write_kernel<128> : kv4_write_kernel<64>;
     dim3 grid;
-    const int rg = grid_for(num_tokens, PKV_BLOCK_SIZE, desc->num_kv_heads, &grid);
+    const int rg = grid_for(num_tokens, PKV_BLOCK_SIZE, desc->num_kv_heads, desc->head_size, &grid);
     if (rg) return rg;
     return launch_pdl(kernel, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
                    cudaSuccess
@@ -358,7 +364,7 @@ extern "C" PKV_API int paged_kv4_read(const void *kv4_cache, const pkv_cache_des
                      status};
     const auto kernel = desc->head_size == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>;
     dim3 grid;
-    const int rg = grid_for(num_tokens, kWarps, desc->num_kv_heads, &grid);
+    const int rg = grid_for(num_tokens, kWarps, desc->num_kv_heads, desc->head_size, &grid);
     if (rg) return rg;
     return launch_pdl(kernel, grid, dim3(kThreads), 0, static_cast<cudaStream_t>(stream), a) ==
                    cudaSuccess
