@@ -268,7 +268,6 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
     }
     if (rank == 0 && tid == 0 && list) *a.cursor = from + min(copies, a.num_free - from);
     if (bits) raise_status(a.status, bits);
-    __threadfence();
 }
 
 constexpr int kCopyThreads = 256;
