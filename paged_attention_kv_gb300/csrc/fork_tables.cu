@@ -13,7 +13,12 @@
 // list does not depend on the order of atomics.
 //
 // One cluster does it all, with a barrier between counting, claiming, giving
-// back and handing out. Rows with exactly one child change no count.
+// back and handing out. Rows with exactly one child change no count. A warp takes a
+// row, four entries a lane at a time; as many CTAs as rows have warps, up to 16 (64
+// beams with their copies 12.6 us, 14.7 in one CTA; a quarter of that many rows a CTA
+// is no faster). Bound by its five phases, each a trip to L2 and a barrier of the
+// cluster, 1.5 to 2 us together: 10.6 us for 64 rows, 13.5 for 384, of which the bytes
+// would take less than 1.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -280,7 +285,9 @@ struct CopyArgs {
     int32_t *status;
 };
 
-// A CTA copies one part of one block of one pool.
+// A CTA copies one part of one block of one pool, in parts of a pass each, four at
+// most: 64 beams 12.6 us against 13.7 with two, 384 samples (12 pools, 130 MB moved) 26.7
+// against 28.1 with eight smaller ones.
 __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
     constexpr int kUnroll = 4;
     pdl_launch_dependents();

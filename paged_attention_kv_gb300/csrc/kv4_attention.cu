@@ -3,26 +3,44 @@
 //
 // For a row (query token, head) with keys j = 0 .. p:
 //     out = sum_j softmax_j(scale q . K_j) V_j,  K_j = k_scale * codes * scales
-// A warp works alone. It takes an item's blocks of 16 keys one after another
-// through its own ring of bulk copies, turns the codes into fp16 fragments in
-// registers (exactly: six significant bits), and runs both products transposed,
-// S^T (16 keys x 8 rows) = K Q^T and O^T (D x 8 rows) += V^T P^T, on mma.sync
-// m16n8k16, so that the 4 to 8 rows of a decode token's head group fill the N
-// side and K and V are made once for up to four such groups of rows. An item is
-// (request, tile of 8 kMaxNt rows, kv head) and its cost a number of keys; all
-// items in a row are cut into equal shares, one a warp (kv4_plan.h), neighbouring
-// shares in one CTA. An item that lies in several shares leaves one partial
-// (m, l, O) a share, in the layout of the fragments: the first of its warps in a
-// CTA joins those of the CTA, through shared memory, and where it lies in several
-// CTAs, the last of them to arrive joins theirs, always in order, so that the
-// result does not depend on timing. Every CTA adds the requests' costs up itself:
-// one launch.
+// A warp works alone. It takes an item's blocks of 16 keys two at a time through
+// its own ring of bulk copies, turns the codes into fp16 fragments in registers
+// (exactly: six significant bits), and runs both products transposed, S^T (16
+// keys x 8 rows) = K Q^T and O^T (D x 8 rows) += V^T P^T, on mma.sync m16n8k16,
+// so that the 4 to 8 rows of a decode token's head group fill the N side and K
+// and V are made once for up to four such groups of rows. An item is (request,
+// tile of 8 kMaxNt rows, kv head) and its cost a number of keys; all items in a
+// row are cut into equal shares, one a warp (kv4_plan.h), neighbouring shares in
+// one CTA. An item that lies in several shares leaves one partial (m, l, O) a
+// share, in the layout of the fragments: the first of its warps in a CTA joins
+// those of the CTA, through shared memory, and where it lies in several CTAs,
+// all warps of the last of them to arrive join theirs, always in order, so that
+// the result does not depend on timing. Every CTA adds the requests' costs up
+// itself: one launch.
 //
 // Softmax: scores stay unscaled; a row's reference m is the largest score of its
-// first block, and moves only when a score passes it by 2^10 (p then still fits
-// fp16), so that a block costs one vote and no exchange between lanes. p is 2^x
-// in 32 bits, rounded to fp16 (2^-11 of each) for the product with V; sums are
+// first two blocks, and moves only when a score passes it by 2^10 (p then still
+// fits fp16), so that two blocks cost one vote and no exchange between lanes. p is
+// 2^x in 32 bits, rounded to fp16 (2^-11 of each) for the product with V; sums are
 // held in 32 bits.
+//
+// Bound by, and measured (us in a graph, one GB300; bytes over the copy bandwidth
+// of 6685 GB/s as the floor):
+//   256 decode requests of 512 to 4096 keys, 32 heads on 8 of 128: 95.3, floor 78.3.
+//     525 MB of DRAM reads, 6.0 TB/s while all warps work; 3 us of prologue and 5 of
+//     joins and ends. A step of a pair takes 57 % of the issue slots.
+//   the same with 4 tokens each: 136, floor 80. Three warps a scheduler, as many as
+//     registers allow, wait for one another's chains (48 % of the issue slots).
+//   64 decode requests of 128 to 2048 keys, 4 heads of 64: 12.7, floor 2.3: a chain of
+//     1.3 us for the sums of all costs, 1 for a warp's share, 1 to the first keys, 3
+//     of them, and joins. Two requests of 17 and 40 keys: 5.5. Instructions that run
+//     once come from L2 and are waited for, hence the votes,
+//     approximate quotients and few branches where each warp finds its share.
+//   3 requests of 30000 to 100000 keys: 34.2, floor 21.1.
+// Chosen against: one block at a time with 14 or 16 warps (16 rows 149 to 168 us against
+// 143 then; 8 rows 110 against 99), scores a pair ahead of the values (103 against 97:
+// registers), 8 rows with 16 warps of 128 registers (103 against 99), 32 rows with 10
+// warps (spills), pieces joined by all of a CTA's warps (64 requests 17.8 against 15.3).
 #include <cuda_runtime.h>
 
 #include <algorithm>

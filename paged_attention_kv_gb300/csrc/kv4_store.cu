@@ -5,6 +5,13 @@
 // Both roundings are exact, ties to even: A has 8 significant bits and a tie
 // between scales times 6 at most 7, so the 32-bit quotient never crosses one it
 // does not hit; the same holds for x against a tie between codes times s.
+//
+// Bound by, and measured (one GB300, tokens of 8 heads of 128, floor at 6685 GB/s):
+// 32768 tokens written in 34.5 us and read back in 33.3 (together 67.7 in a graph,
+// floor 45.8): 153 MB of DRAM traffic at 4.4 TB/s with 52 % of the issue slots for
+// the write, whose groups take about 9 instructions a value pair; the read is bound
+// by its conversions (73 % of the issue slots). 2240 tokens 7.7 us, floor 3.1; 64
+// tokens of 4 heads of 64 in 3.9: two launches and their first loads.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -60,7 +67,8 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 
 // A group as 16 codes and its scale byte. Quotients x / (s * by) are x * (1 / (s *
-// by)), the reciprocal to about 2^-23, corrected once by their remainder, which one
+// by)), the reciprocal to about 2^-23, corrected once by their remainder (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000", 1990), which one
 // fused operation gives exactly: what is left is off by 2^-46, so that a tie (x a
 // border between codes times s) comes out as that border itself, and everything
 // else is 2^-8 away from one. (The correction makes +0 of -0: code 0 for both.)
@@ -172,8 +180,10 @@ __device__ __forceinline__ void write_token(const uint4 *k, const uint4 *v, int 
 // A CTA has 16 tokens, and the block that starts among them if a run of tokens
 // fills it: such blocks (prompts) are turned into whole tiles, other tokens (decode
 // rows, a prompt's ends) are written code by code. Every warp finds that out for
-// itself from the slots around. 32768 tokens of 8 heads of 128: see the table of
-// measurements beside the calls' description.
+// itself from the slots around. Tiles go through shared memory because their codes
+// and scales have the lanes' order: stores of 16 bytes instead of 8 and 1 (32768
+// tokens written and read back 86 us against 92), found from registers instead of
+// by counting in shared memory (67.7 against 82.7).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const StoreArgs a) {
     using Tile = Kv4Tile<D>;
@@ -236,11 +246,45 @@ struct LoadArgs {
     int32_t *status;
 };
 
-// A warp per token: a lane per 8 columns, K's and V's side by side.
+// Of one token's K or V, what a lane reads: the same 8 columns of every so many
+// heads, whose places are a constant apart.
+template <int D>
+struct Part {
+    static constexpr int kC = D / 8, kStep = 32 / kC * Kv4Tile<D>::kBytes;  // 32 lanes have 32 / kC heads
+    const uint8_t *at, *at_scale;
+    float by;
+    uint4 *to;
+    uint32_t codes[2], byte[2];
+
+    __device__ __forceinline__ void load(int i0, int n) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (i0 + 32 * j >= n) break;
+            codes[j] = *reinterpret_cast<const uint32_t *>(at + j * kStep);
+            byte[j] = at_scale[j * kStep];
+        }
+        at += 2 * kStep;
+        at_scale += 2 * kStep;
+    }
+    __device__ __forceinline__ void store(int i0, int n) const {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (i0 + 32 * j >= n) break;
+            const float s = __low2float(kv4_scales(byte[j])) * by;
+            auto pair = [&](__half2 x) {
+                const float2 f = fmul2(__half22float2(x), make_float2(s, s));
+                return pack_bf16x2(f.x, f.y);
+            };
+            to[i0 + 32 * j] = make_uint4(pair(kv4_pair<0>(codes[j])), pair(kv4_pair<1>(codes[j])), pair(kv4_pair<2>(codes[j])), pair(kv4_pair<3>(codes[j])));
+        }
+    }
+};
+
+// A warp per token; two pieces of K and of V of a lane on their way at a time.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const LoadArgs a) {
     using Tile = Kv4Tile<D>;
-    constexpr int kC = D / 8, kAhead = 4;
+    constexpr int kC = D / 8;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
@@ -257,31 +301,15 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const LoadArgs a) {
     }
     const uint8_t *tiles = a.pool + ((long long)blk * a.num_kv_heads + h0) * Tile::kBytes;
     const long long at = (t * a.num_kv_heads + h0) * kC;
-    const int i1 = a.v ? 2 * n : n;
-    for (int i0 = (a.k ? 0 : n) + lane; i0 < i1; i0 += 32 * kAhead) {
-        uint32_t codes[kAhead], byte[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int i = min(i0 + 32 * j, i1 - 1);
-            const bool is_v = i >= n;
-            const int ii = is_v ? i - n : i, c = ii % kC;
-            const uint8_t *tile = tiles + (long long)(ii / kC) * Tile::kBytes;
-            codes[j] = *reinterpret_cast<const uint32_t *>(tile + (is_v ? Tile::v_code(row, c) : Tile::k_code(row, c)));
-            byte[j] = tile[is_v ? Tile::v_scale(row, c >> 1) : Tile::k_scale(row, c >> 1)];
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + 32 * j;
-            if (i >= i1) break;
-            const bool is_v = i >= n;
-            const float s = __low2float(kv4_scales(byte[j])) * (is_v ? a.v_scale : a.k_scale);
-            auto pair = [&](__half2 x) {
-                const float2 f = fmul2(__half22float2(x), make_float2(s, s));
-                return pack_bf16x2(f.x, f.y);
-            };
-            (is_v ? a.v : a.k)[at + (is_v ? i - n : i)] =
-                make_uint4(pair(kv4_pair<0>(codes[j])), pair(kv4_pair<1>(codes[j])), pair(kv4_pair<2>(codes[j])), pair(kv4_pair<3>(codes[j])));
-        }
+    const int c = lane % kC;
+    const uint8_t *tile = tiles + lane / kC * Tile::kBytes;
+    Part<D> k{tile + Tile::k_code(row, c), tile + Tile::k_scale(row, c >> 1), a.k_scale, a.k + at};
+    Part<D> v{tile + Tile::v_code(row, c), tile + Tile::v_scale(row, c >> 1), a.v_scale, a.v + at};
+    for (int i0 = lane; i0 < n; i0 += 64) {
+        if (a.k) k.load(i0, n);
+        if (a.v) v.load(i0, n);
+        if (a.k) k.store(i0, n);
+        if (a.v) v.store(i0, n);
     }
 }
 
