@@ -7,11 +7,12 @@
 // does not hit; the same holds for x against a tie between codes times s.
 //
 // Bound by, and measured (one GB300, tokens of 8 heads of 128, floor at 6685 GB/s):
-// 32768 tokens written in 34.5 us and read back in 33.3 (together 67.7 in a graph,
-// floor 45.8): 153 MB of DRAM traffic at 4.4 TB/s with 52 % of the issue slots for
-// the write, whose groups take about 9 instructions a value pair; the read is bound
-// by its conversions (73 % of the issue slots). 2240 tokens 7.7 us, floor 3.1; 64
-// tokens of 4 heads of 64 in 3.9: two launches and their first loads.
+// 32768 tokens written in 34.5 us and read back in 28.6 (together 63.7 in a graph,
+// floor 45.8). The write moves 153 MB of DRAM bytes at 4.4 TB/s with 53 % of the issue
+// slots and waits for its loads, of which 64 registers a thread hold two groups; the
+// read 111 MB (the rest of its output stays in L2), 45 % of the issue slots. 2240
+// tokens 7.3 us, floor 3.1; 64 tokens of 4 heads of 64 in 3.8: two launches and their
+// first loads.
 #include <cuda_runtime.h>
 
 #include <algorithm>
