@@ -37,7 +37,7 @@ constexpr int kThreads = 1024;
 constexpr int kMaxCtas = 16;
 constexpr int kMinCtas = 8;           // that a cluster has on every device
 constexpr int kFree = INT_MIN / 2;    // counts below this are claims: INT_MIN + entry
-constexpr int kMaxOwn = PKV_MAX_FORK_ROWS / kMinCtas;  // rows of a CTA
+static_assert(PKV_MAX_FORK_ROWS / kMinCtas <= kThreads, "a thread has one of its CTA's rows at most");
 
 struct ForkArgs {
     const int32_t *parents, *table, *lens;
@@ -47,8 +47,11 @@ struct ForkArgs {
     int32_t *cursor, *table_out, *lens_out, *copy_src, *copy_dst, *status;
 };
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Stores v to `at` (a shared address) of CTA `rank` of the cluster.
@@ -61,7 +64,7 @@ __device__ __forceinline__ void store_to(uint32_t at, uint32_t rank, int v) {
 __device__ __forceinline__ int seen(const int32_t *p) { return __ldcg(p); }
 
 __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a) {
-    __shared__ int s_children[PKV_MAX_FORK_ROWS], s_first[PKV_MAX_FORK_ROWS], s_dst[kMaxOwn];
+    __shared__ int s_children[PKV_MAX_FORK_ROWS], s_first[PKV_MAX_FORK_ROWS];
     __shared__ int s_warp[32], s_total[kMaxCtas];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, ctas = gridDim.x;  // the grid is one cluster
@@ -112,110 +115,41 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
     if (!list) bits |= PKV_DEV_BAD_PAGES;
     __syncthreads();
 
-    // this CTA's rows, one a warp at a time
-    const int per = (R + ctas - 1) / ctas, r0 = min(R, rank * per), r1 = min(R, r0 + per);
-    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
+    // this CTA's rows, one a warp at a time; of a warp's first row the first entries are
+    // read once, and their counts once in the two phases that see the same ones
+    const int per = (R + ctas - 1) / ctas, r0 = min(R, rank * per), r1 = min(R, r0 + per), own = r0 + warp;
+    int b_own[kU], v_own[kU];
+    auto entries = [&](int r, int e0, int held, int (&b)[kU]) {
+        if (r != own || e0) {
+            blocks(r, e0, held, b);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) b[u] = b_own[u];
+    };
+    auto counts = [&](const int (&b)[kU], int (&v)[kU]) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[u] = b[u] >= 0 ? seen(a.shares + b[u]) : 0;
+    };
+    int gone = 0;  // rows without children that hold a block, of this thread's
+    for (int r = tid; r < R; r += kThreads) gone |= s_children[r] == 0 && length(r) > 0;
+    for (int r = own; r < r1; r += kThreads / 32) {
         const int c = s_children[r];
         if (c == 1) continue;
         const int n = length(r), full = n / PKV_BLOCK_SIZE, held = c ? full : (n + 15) / PKV_BLOCK_SIZE;
+        if (r == own) blocks(r, 0, held, b_own);
         for (int e0 = 0; e0 < held; e0 += 32 * kU) {
             int b[kU];
-            blocks(r, e0, held, b);
+            entries(r, e0, held, b);
 #pragma unroll
             for (int u = 0; u < kU; ++u)
                 if (b[u] >= 0) atomicAdd(a.shares + b[u], c - 1);
         }
     }
-    cluster_sync();
-    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
-        if (s_children[r]) continue;
-        const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
-        for (int e0 = 0; e0 < held; e0 += 32 * kU) {
-            int b[kU], v[kU];
-            blocks(r, e0, held, b);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) v[u] = b[u] >= 0 ? seen(a.shares + b[u]) : 0;
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                if (v[u] == -1 || v[u] < kFree) atomicMin(a.shares + b[u], INT_MIN + (r * a.width + e0 + 32 * u + lane));
-                else if (v[u] < -1) bits |= PKV_DEV_BAD_PAGES;  // given up more often than held
-            }
-        }
-    }
-    cluster_sync();
-    // blocks that this CTA's rows give back
-    int mine = 0;
-    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
-        if (s_children[r]) continue;
-        const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
-        int got = 0;
-        for (int e0 = 0; e0 < held; e0 += 32 * kU) {
-            int b[kU];
-            blocks(r, e0, held, b);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) got += b[u] >= 0 && seen(a.shares + b[u]) == INT_MIN + (r * a.width + e0 + 32 * u + lane);
-        }
-        got = __reduce_add_sync(0xffffffffu, got);
-        if (lane == 0) s_first[r] = got;  // a row without children has no first one
-        mine += got;
-    }
-    if (lane == 0) s_warp[warp] = mine;
-    __syncthreads();
-    if (warp == 0) {
-        const int sum = __reduce_add_sync(0xffffffffu, s_warp[lane]);
-        if (lane < ctas) store_to(smem_u32(s_total + rank), lane, sum);
-    }
-    cluster_sync();
-    int before = 0, given = 0;
-    for (int i = 0; i < ctas; ++i) {
-        if (i < rank) before += s_total[i];
-        given += s_total[i];
-    }
-    if (!list) given = 0;
-    if (given > cur && list) bits |= PKV_DEV_BAD_PAGES;  // more than were ever taken
-    const int base = list ? cur - given : 0;             // where the first one goes
-    // every row's place: a sum over the CTA's rows before it (at most a thread each)
-    {
-        const int r = r0 + tid, n = r < r1 && !s_children[r] ? s_first[r] : 0;
-        int v = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, v, d);
-            if (lane >= d) v += o;
-        }
-        if (lane == 31) s_warp[warp] = v;
-        __syncthreads();
-        int sum = lane < warp ? s_warp[lane] : 0;
-        sum = __reduce_add_sync(0xffffffffu, sum);
-        if (r < r1 && !s_children[r]) s_first[r] = before + sum + v - n;
-    }
-    __syncthreads();
-    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
-        if (s_children[r]) continue;
-        const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
-        int at = base + s_first[r];
-        for (int e0 = 0; e0 < held; e0 += 32 * kU) {
-            int b[kU], v[kU];
-            blocks(r, e0, held, b);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) v[u] = b[u] >= 0 ? seen(a.shares + b[u]) : 0;
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const bool take = v[u] == INT_MIN + (r * a.width + e0 + 32 * u + lane);
-                const uint32_t all = __ballot_sync(0xffffffffu, take);
-                if (take) {
-                    const int to = at + __popc(all & ((1u << lane) - 1));
-                    if (list && to >= 0) a.free_blocks[to] = b[u];
-                }
-                if (take || (v[u] < 0 && v[u] >= kFree)) a.shares[b[u]] = 0;
-                at += __popc(all);
-            }
-        }
-    }
-    cluster_sync();
-    // the new rows; every CTA numbers the copies of all rows up to its own
-    const int from = max(base, 0);
-    int copies = 0;
+    cluster_arrive();
+    // Meanwhile the new rows, but for the copies' places: every CTA numbers the copies
+    // of all rows up to its own, of which a thread has one at most.
+    int copies = 0, my_row = -1, my_src = -1, my_copy = -1, my_last = 0;
     for (int c0 = 0; c0 < R; c0 += kThreads) {
         const int r = c0 + tid;
         const int p = r < R ? parent(r) : -1;
@@ -228,34 +162,22 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         const int sum = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
         const int sums = __reduce_add_sync(0xffffffffu, s_warp[lane]);
         if (r >= r0 && r < r1) {
-            const int k = from + copies + sum + __popc(all & ((1u << lane) - 1));
-            int src = -1, dst = -1;
+            my_row = r;
+            my_last = n / PKV_BLOCK_SIZE;
             if (copy) {
-                src = __ldg(a.table + (long long)p * a.width + n / PKV_BLOCK_SIZE);
-                if (src < 0 || src >= a.num_blocks) {
-                    src = -1;
+                my_copy = copies + sum + __popc(all & ((1u << lane) - 1));
+                my_src = __ldg(a.table + (long long)p * a.width + my_last);
+                if (my_src < 0 || my_src >= a.num_blocks) {
+                    my_src = -1;
                     bits |= PKV_DEV_BAD_BLOCK;
                 }
-                if (list && k < a.num_free) {
-                    dst = __ldcg(a.free_blocks + k);
-                    if (dst < 0 || dst >= a.num_blocks) {
-                        dst = -1;
-                        bits |= PKV_DEV_BAD_BLOCK;
-                    }
-                } else {
-                    bits |= PKV_DEV_NO_BLOCKS;
-                }
             }
-            s_dst[r - r0] = copy ? dst : INT_MIN;
             a.lens_out[r] = n;
-            a.copy_src[r] = dst < 0 ? -1 : src;
-            a.copy_dst[r] = src < 0 ? -1 : dst;
         }
         copies += sums;
     }
-    __syncthreads();
-    for (int r = r0 + warp; r < r1; r += kThreads / 32) {
-        const int p = parent(r), held = p >= 0 ? (length(p) + 15) / PKV_BLOCK_SIZE : 0, dst = s_dst[r - r0];
+    for (int r = own; r < r1; r += kThreads / 32) {
+        const int p = parent(r), held = p >= 0 ? (length(p) + 15) / PKV_BLOCK_SIZE : 0;
         const int32_t *line = a.table + (long long)max(p, 0) * a.width;
         int32_t *to = a.table_out + (long long)r * a.width;
         for (int e0 = 0; e0 < a.width; e0 += 32 * kU) {
@@ -264,12 +186,128 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
             for (int u = 0; u < kU; ++u) {
                 const int e = e0 + 32 * u + lane;
                 b[u] = e < held ? __ldg(line + e) : -1;
-                if (e == held - 1 && dst != INT_MIN) b[u] = dst;
             }
 #pragma unroll
             for (int u = 0; u < kU; ++u)
                 if (e0 + 32 * u + lane < a.width) to[e0 + 32 * u + lane] = b[u];
         }
+    }
+    cluster_wait();
+    int given = 0;  // blocks that go back
+    if (__syncthreads_or(gone)) {  // of all rows, so all CTAs agree
+        for (int r = own; r < r1; r += kThreads / 32) {
+            if (s_children[r]) continue;
+            const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
+            for (int e0 = 0; e0 < held; e0 += 32 * kU) {
+                int b[kU], v[kU];
+                entries(r, e0, held, b);
+                counts(b, v);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    if (v[u] == -1 || v[u] < kFree) atomicMin(a.shares + b[u], INT_MIN + (r * a.width + e0 + 32 * u + lane));
+                    else if (v[u] < -1) bits |= PKV_DEV_BAD_PAGES;  // given up more often than held
+                }
+            }
+        }
+        cluster_sync();
+        // blocks that this CTA's rows give back
+        int mine = 0;
+        for (int r = own; r < r1; r += kThreads / 32) {
+            if (s_children[r]) continue;
+            const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
+            int got = 0;
+            for (int e0 = 0; e0 < held; e0 += 32 * kU) {
+                int b[kU], v[kU];
+                entries(r, e0, held, b);
+                counts(b, v);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    got += v[u] == INT_MIN + (r * a.width + e0 + 32 * u + lane);
+                    if (r == own && e0 == 0) v_own[u] = v[u];
+                }
+            }
+            got = __reduce_add_sync(0xffffffffu, got);
+            if (lane == 0) s_first[r] = got;  // a row without children has no first one
+            mine += got;
+        }
+        if (lane == 0) s_warp[warp] = mine;
+        __syncthreads();
+        if (warp == 0) {
+            const int sum = __reduce_add_sync(0xffffffffu, s_warp[lane]);
+            if (lane < ctas) store_to(smem_u32(s_total + rank), lane, sum);
+        }
+        cluster_sync();
+        int before = 0;
+        for (int i = 0; i < ctas; ++i) {
+            if (i < rank) before += s_total[i];
+            given += s_total[i];
+        }
+        if (!list) given = 0;
+        if (given > cur && list) bits |= PKV_DEV_BAD_PAGES;  // more than were ever taken
+        const int base = list ? cur - given : 0;             // where the first one goes
+        // every row's place: a sum over the CTA's rows before it (at most a thread each)
+        {
+            const int r = r0 + tid, n = r < r1 && !s_children[r] ? s_first[r] : 0;
+            int v = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, v, d);
+                if (lane >= d) v += o;
+            }
+            if (lane == 31) s_warp[warp] = v;
+            __syncthreads();
+            int sum = lane < warp ? s_warp[lane] : 0;
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            if (r < r1 && !s_children[r]) s_first[r] = before + sum + v - n;
+        }
+        __syncthreads();
+        for (int r = own; r < r1; r += kThreads / 32) {
+            if (s_children[r]) continue;
+            const int held = (length(r) + 15) / PKV_BLOCK_SIZE;
+            int at = base + s_first[r];
+            for (int e0 = 0; e0 < held; e0 += 32 * kU) {
+                int b[kU], v[kU];
+                entries(r, e0, held, b);
+                if (r == own && e0 == 0) {
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) v[u] = v_own[u];
+                } else {
+                    counts(b, v);
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const bool take = v[u] == INT_MIN + (r * a.width + e0 + 32 * u + lane);
+                    const uint32_t all = __ballot_sync(0xffffffffu, take);
+                    if (take) {
+                        const int to = at + __popc(all & ((1u << lane) - 1));
+                        if (list && to >= 0) a.free_blocks[to] = b[u];
+                    }
+                    if (take || (v[u] < 0 && v[u] >= kFree)) a.shares[b[u]] = 0;
+                    at += __popc(all);
+                }
+            }
+        }
+        cluster_sync();
+    }
+    // the copies' places
+    const int from = list ? max(cur - given, 0) : 0;
+    if (my_row >= 0) {
+        int dst = -1;
+        if (my_copy >= 0) {
+            const int k = from + my_copy;
+            if (list && k < a.num_free) {
+                dst = __ldcg(a.free_blocks + k);
+                if (dst < 0 || dst >= a.num_blocks) {
+                    dst = -1;
+                    bits |= PKV_DEV_BAD_BLOCK;
+                }
+            } else {
+                bits |= PKV_DEV_NO_BLOCKS;
+            }
+            a.table_out[(long long)my_row * a.width + my_last] = dst;
+        }
+        a.copy_src[my_row] = dst < 0 ? -1 : my_src;
+        a.copy_dst[my_row] = my_src < 0 ? -1 : dst;
     }
     if (rank == 0 && tid == 0 && list) *a.cursor = from + min(copies, a.num_free - from);
     if (bits) raise_status(a.status, bits);
