@@ -26,7 +26,8 @@ struct Kv4Args {
     float scale_log2, v_scale;
     __nv_bfloat16 *out;
     int *claimed;   // the workspace: items of kv4_chunk.cu taken so far;
-    int *arrived;   // of each CTA, the arrivals for the item that begins there and ends in another;
+    int *arrived;   // of each CTA, the arrivals for the item that begins there and ends in another
+                    // (of each split item of kv4_chunk.cu, those of its parts);
     float4 *parts;  // and two partials: of the item that began before it, and of that one
     int chunks;     // kv4_chunk.cu runs too
     int32_t *status;
@@ -76,6 +77,10 @@ __device__ __forceinline__ bool kv4_overlap(const Kv4Args &a, int each, long lon
     return n > a.num_tokens;
 }
 #endif
+
+// The chunk kernel: CTAs an SM, and floats of a part of an item (O, then m and l).
+constexpr int kKv4ChunkCtas = 2;
+constexpr int kv4_chunk_part(int head_size) { return kKv4ChunkRows * (head_size + 2); }
 
 // Launches the chunk kernel in front of the other one.
 int kv4_chunk_launch(const Kv4Args &a, int head_size, int sms, cudaStream_t stream);

@@ -756,13 +756,15 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     int bits = 0;
     {
         int most = 0;
-        long long units = 0;
+        long long units = 0, items = 0;
         for (int r = tid * each; r < min((tid + 1) * each, a.num_reqs); ++r) {
             const Kv4Request q = kv4_request_of(a, r, K::kRows, &bits);
             const long long cost = kv4_cost(q, a.num_kv_heads, q.tiles);
             if (kMaxNt == 4 && a.chunks && kv4_is_chunk(q, a.group)) {
                 theirs += cost;
-                units += kv4_chunk_units(kv4_request(q.q0, q.n, q.len, a.group, kKv4ChunkRows), a.num_kv_heads);
+                const Kv4Request c = kv4_request(q.q0, q.n, q.len, a.group, kKv4ChunkRows);
+                units += kv4_chunk_units(c, a.num_kv_heads);
+                items += (long long)c.tiles * a.num_kv_heads;
                 most = max(most, kv4_chunk_tiles(q.len));
             } else {
                 sum += cost;
@@ -773,20 +775,23 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 units += __shfl_xor_sync(0xffffffffu, units, d);
+                items += __shfl_xor_sync(0xffffffffu, items, d);
                 most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
             }
             if (lane == 0) {
                 s_warp[warp] = units;
+                s_sum[warp] = items;
                 s_most[warp] = most;
             }
             __syncthreads();
-            units = most = 0;
+            units = items = most = 0;
             for (int i = 0; i < K::kW; ++i) {
                 units += s_warp[i];
+                items += s_sum[i];
                 most = max(most, s_most[i]);
             }
             __syncthreads();
-            skip = kv4_use_chunks(units, most);
+            skip = kv4_use_chunks(units, most, kv4_splits(items, gridDim.x));
         }
         if (!skip) sum += theirs;
     }
@@ -891,11 +896,13 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
         if (s_far[k].rows) K::join_far(a, s_far[k], team.sh.per_cta, warp, lane);
 }
 
-// Places in the workspace, for any batch and form.
+// Places in the workspace, for any batch and form (the chunk kernel has left its
+// parts before the other one begins).
 size_t parts_at(int sms) { return (((size_t)sms + 1) * sizeof(int) + 255) / 256 * 256; }
 size_t workspace_bytes(int sms, int head_size) {
-    return parts_at(sms) + (size_t)sms * sizeof(float4) * (head_size == 128 ? 2 * Kernel<128, 4>::kPart + kWarps<4> * Kernel<128, 4>::kArea
-                                                                            : 2 * Kernel<64, 4>::kPart + kWarps<4> * Kernel<64, 4>::kArea);
+    const size_t chunks = (size_t)kKv4ChunkCtas * sms * kv4_chunk_part(head_size) * sizeof(float);
+    return parts_at(sms) + std::max(chunks, (size_t)sms * sizeof(float4) * (head_size == 128 ? 2 * Kernel<128, 4>::kPart + kWarps<4> * Kernel<128, 4>::kArea
+                                                                            : 2 * Kernel<64, 4>::kPart + kWarps<4> * Kernel<64, 4>::kArea));
 }
 
 std::mutex g_mu;

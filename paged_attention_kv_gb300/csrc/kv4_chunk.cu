@@ -13,13 +13,16 @@
 // is filled by a second CTA on the same SM (100 KB of shared memory, 256 columns of
 // TMEM and 128 registers a thread each). Items are claimed one by one from a counter
 // in the workspace, those of the longest contexts first, so that what runs last is
-// short (158 us against 188 for what follows).
+// short (158 us against 188 for what follows). Where they are too few for the CTAs, an
+// item's keys are split (kv4_plan.h), and the last CTA to arrive adds its parts up, in
+// order, from fp32 O, m and l in the workspace (1 request of 512 tokens and 30000 keys
+// 393 -> 275 us, 4 of 64 and 4000 60 -> 42).
 //
 // A row's reference m moves only when the sum of a tile's p shows that one of them
 // may be past 2^12: no pass for the maximum but the first (188 against 293 us).
 //
 // Measured: chunks of 60 to 512 tokens of 16 requests with 600 to 4000 keys, 32 heads
-// on 8 of 128: 141 us, 750 TFLOP/s of the two products, floor 54.7 (1948 TFLOP/s). The
+// on 8 of 128: 142 us, 750 TFLOP/s of the two products, floor 54.7 (1948 TFLOP/s). The
 // tensor cores are busy 35 % of the time, the issue slots 47 %: a tile and CTA take
 // 1024 cycles of products, 512 of exponentials and about 570 instructions a warp (200
 // of them unpacking), and four warps a scheduler, as many as registers allow, do not
@@ -218,14 +221,45 @@ __device__ __forceinline__ bool pair_any(uint32_t id, bool mine) {
     return any != 0;
 }
 
+// Half a row of an item from its parts, `step` floats apart, in order. A call: inlined it
+// takes registers from the loop over keys (145 us instead of 142 where nothing is split).
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a) {
+__device__ __noinline__ void join_parts(const float *first, size_t step, int parts, float mul, float v_scale, int row, int half, __nv_bfloat16 *out) {
+    float2 ml[kKv4MaxSplits];
+#pragma unroll
+    for (int k = 0; k < kKv4MaxSplits; ++k)
+        ml[k] = k < parts ? __ldcg(reinterpret_cast<const float2 *>(first + k * step + kKv4ChunkRows * D) + row) : make_float2(-INFINITY, 0.0f);
+    float to = -INFINITY, all = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kKv4MaxSplits; ++k) to = fmaxf(to, ml[k].x);
+#pragma unroll
+    for (int k = 0; k < kKv4MaxSplits; ++k) {
+        ml[k].x = fast_exp2((ml[k].x - to) * mul);
+        all = fmaf(ml[k].x, ml[k].y, all);
+    }
+    const float f = __fdividef(v_scale, all);
+#pragma unroll 2
+    for (int c = 0; c < D / 8; ++c) {
+        const float *from = first + 4 * ((size_t)(half * (D / 8) + c) * kKv4ChunkRows + row);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), x[kKv4MaxSplits];
+#pragma unroll
+        for (int k = 0; k < kKv4MaxSplits; ++k)
+            if (k < parts) x[k] = __ldcg(reinterpret_cast<const float4 *>(from + k * step));
+#pragma unroll
+        for (int k = 0; k < kKv4MaxSplits; ++k)
+            if (k < parts) o = make_float4(fmaf(x[k].x, ml[k].x, o.x), fmaf(x[k].y, ml[k].x, o.y), fmaf(x[k].z, ml[k].x, o.z), fmaf(x[k].w, ml[k].x, o.w));
+        reinterpret_cast<uint2 *>(out)[c] = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kKv4ChunkCtas) kv4_chunk_kernel(const Kv4Args a) {
     using S = Smem<D>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long s_units[kThreads / 32];
     __shared__ int s_items[kThreads], s_len[kThreads], s_order[kThreads], s_sum[kThreads / 32], s_most[kThreads / 32];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_claim;
+    __shared__ int s_abort, s_claim, s_last;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *s_x = reinterpret_cast<float *>(smem + S::kX), *s_mul = reinterpret_cast<float *>(smem + S::kMul);
     int *s_nan = reinterpret_cast<int *>(smem + S::kNan);
@@ -301,8 +335,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
     }
     s_items[tid] = sum;
     total = (int)uniform((uint32_t)total);
+    // pieces: items, or as many parts of each; all of those run at once
+    const Kv4Splits sp = kv4_splits(total, (int)gridDim.x / kKv4ChunkCtas);
+    const int splits = (int)uniform((uint32_t)sp.count), pieces = total * splits;
     // what steers this kernel is uniform for the compiler too: see mma_ss4
-    if (uniform(!kv4_use_chunks(units, most) || (int)blockIdx.x >= total)) return;  // the items go by `total` claims and no more CTAs
+    if (uniform(!kv4_use_chunks(units, most, sp) || (int)blockIdx.x >= pieces)) return;  // the items go by `total` claims and no more CTAs
     const int ctas = min((int)gridDim.x, total);
     if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
     tmem_fence_before_sync();
@@ -318,7 +355,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
     uint32_t phase = 0;  // of both barriers: they complete once a key tile
     const long long block_bytes = (long long)a.num_kv_heads * Kv4Tile<D>::kBytes;
 
-    for (int item = blockIdx.x; item < total;) {
+    for (int piece = blockIdx.x; piece < pieces;) {
+        int split = 0, item = piece;
+        for (; item >= total; item -= total) ++split;
         // the item: request, tile and head
         Kv4Request q;
         int r, i, h;
@@ -340,6 +379,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         }
         const Kv4Tiling tl = kv4_tile(q, i, a.group, kKv4ChunkRows);
         const int nt = (int)uniform((uint32_t)kv4_chunk_tiles(tl.keys));
+        int parts = 1, j0 = 0, j1 = nt;  // of this item; this part's key tiles
+        if (splits > 1) {
+            parts = kv4_parts(nt, sp);
+            if (uniform(split >= parts)) break;
+            j0 = (int)uniform((uint32_t)kv4_part_begin(nt, parts, split));
+            j1 = (int)uniform((uint32_t)kv4_part_begin(nt, parts, split + 1));
+        }
         const int row0 = i * kKv4ChunkRows;
         const int32_t *ids = a.table + (long long)r * a.max_blocks;
         const uint8_t *heads = a.pool + (long long)h * Kv4Tile<D>::kBytes;
@@ -354,10 +400,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             }
             return heads + id * block_bytes;
         };
-        const int id0 = id_of(0);
-        int id1 = id_of(1), id2 = id_of(2);  // of the tiles that V and K are read of next
+        const int id0 = id_of(j0);
+        int id1 = id_of(j0 + 1), id2 = id_of(j0 + 2);  // of the tiles that V and K are read of next
         Raw<D> rk, rv;
-        const uint8_t *at = tile_of(0, id0);
+        const uint8_t *at = tile_of(j0, id0);
         rk.load(at, false, lane);
         rv.load(at, true, lane);
 
@@ -404,17 +450,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         }
         const uint32_t k_to = k_s + warp * 2048 + Raw<D>::k_place(lane), v_to = v_s + warp * 2048 + Raw<D>::v_place(lane);
         rk.put_k(k_to, lane);
-        rk.load(tile_of(1, id1), false, lane);
+        rk.load(tile_of(j0 + 1, id1), false, lane);
         fence_proxy_async_smem();
         __syncthreads();
-        // keys that this row sees (padding rows: one)
+        // keys that this row sees: some of any part, which is longer than a tile (padding
+        // rows: one)
         const int rr = row0 + row;
-        const int limit = row < tl.rows ? q.len - q.n + kv4_over(rr, a.group, a.group_inv) + 1 : 1;
+        const int limit = row < tl.rows ? q.len - q.n + kv4_over(rr, a.group, a.group_inv) + 1 : j0 * kKeys + 1;
         const float mul = s_mul[row];
         float m = -INFINITY, l = 0.0f;
         bool large = false;  // some row's reference is
 
-        for (int j = 0; j < nt; ++j) {
+        for (int j = j0; j < j1; ++j) {
             if (warp == 0) {
                 tmem_fence_after_sync();
 #pragma unroll
@@ -470,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
                 }
                 named_barrier_sync(1 + (warp & 3), 64);  // the maxima are read
             };
-            if (j == 0) move(false);
+            if (j == j0) move(false);
             uint32_t p[32];
             float2 sum;
             for (int round = 0;; ++round) {
@@ -506,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
                 const bool again = pair_any(1 + (warp & 3), !(sum.x + sum.y <= 4096.0f));
                 tmem_fence_after_sync();
                 if (!again || round) break;  // against the largest score none is past it
-                move(j > 0);
+                move(j > j0);
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) tmem_st16u(tm_row + part * 32 + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
@@ -517,16 +564,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
             if (warp == 0) {
                 tmem_fence_after_sync();
 #pragma unroll
-                for (int c = 0; c < 2; ++c) mma_ts4(tmu + kColO, tmu + c * 32, v_lo + c * (8192 >> 4), kIdPv, c | j);
+                for (int c = 0; c < 2; ++c) mma_ts4(tmu + kColO, tmu + c * 32, v_lo + c * (8192 >> 4), kIdPv, c | (j - j0));
                 commit(smem_u32(bar_pv));
             }
-            if (j + 1 < nt) {
+            if (j + 1 < j1) {
                 rv.load(tile_of(j + 1, id1), true, lane);
                 rk.put_k(k_to, lane);
                 rk.load(tile_of(j + 2, id2), false, lane);
                 id1 = id2;
                 id2 = id_of(j + 3);
                 fence_proxy_async_smem();
+            } else if (splits > 1) {
+                if (tid == 0) s_claim = pieces;
             } else if (tid == 0) {
                 // the next item: CTA b has item b without a claim, every item claims another, and
                 // the last of these claims leaves the counter as it was
@@ -544,7 +593,46 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         tmem_fence_after_sync();
         s_x[part * 128 + row] = l;
         named_barrier_sync(1 + (warp & 3), 64);
-        const float f = a.v_scale / (s_x[row] + s_x[128 + row]);
+        l = s_x[row] + s_x[128 + row];
+        if (parts > 1) {
+            // this part for the last of the item's to arrive, which adds them up in order
+            float *mine = reinterpret_cast<float *>(a.parts) + (size_t)piece * kv4_chunk_part(D);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                float o[32];
+                tmem_ld32(tm_row + kColO + part * (D / 2) + 32 * c, o);
+                tmem_wait_ld_regs(o);
+#pragma unroll
+                for (int gI = 0; gI < 2; ++gI)
+                    if (s_nan[part * (D / 32) + 2 * c + gI] < limit)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[16 * gI + e] = __uint_as_float(0x7fffffffu);
+                // rows next to each other: [4 columns][row]
+                float4 *to = reinterpret_cast<float4 *>(mine) + (part * (D / 8) + 8 * c) * kKv4ChunkRows + row;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) to[e * kKv4ChunkRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+            if (part == 0) reinterpret_cast<float2 *>(mine + kKv4ChunkRows * D)[row] = make_float2(m, l);
+            __syncthreads();
+            if (tid == 0) {
+                int seen;
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(seen) : "l"(a.arrived + item) : "memory");
+                seen -= kKv4Nobody;
+                if (seen == parts - 1) atomicExch(a.arrived + item, kKv4Nobody);
+                if (seen < 0 || seen >= parts) raise_status(a.status, PKV_DEV_BAD_WORKSPACE);
+                s_last = seen == parts - 1;
+            }
+            __syncthreads();
+            if (s_last && row < tl.rows) {
+                const int tok = kv4_over(rr, a.group, a.group_inv);
+                join_parts<D>(reinterpret_cast<const float *>(a.parts) + (size_t)item * kv4_chunk_part(D), (size_t)total * kv4_chunk_part(D), parts, mul,
+                              a.v_scale, row, part,
+                              a.out + ((long long)(q.q0 + tok) * a.num_kv_heads * a.group + h * a.group + rr - tok * a.group) * D + part * (D / 2));
+            }
+            if (__any_sync(0xffffffffu, bits != 0) && lane == 0) raise_status(a.status, PKV_DEV_BAD_BLOCK);
+            break;
+        }
+        const float f = a.v_scale / l;
         const int tok = kv4_over(rr, a.group, a.group_inv);
         __nv_bfloat16 *out = a.out + ((long long)(q.q0 + tok) * a.num_kv_heads * a.group + h * a.group + rr - tok * a.group) * D + part * (D / 2);
 #pragma unroll
@@ -569,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_chunk_kernel(const Kv4Args a)
         }
         if (__any_sync(0xffffffffu, bits != 0) && lane == 0) raise_status(a.status, PKV_DEV_BAD_BLOCK);
         tmem_fence_before_sync();
-        item = (int)uniform((uint32_t)s_claim);
+        piece = (int)uniform((uint32_t)s_claim);
         __syncthreads();
         tmem_fence_after_sync();
     }
@@ -602,7 +690,7 @@ int launch(const Kv4Args &a, int sms, cudaStream_t st) {
             g_ready[dev][D == 128] = true;
         }
     }
-    return launch_pdl(kv4_chunk_kernel<D>, dim3(2 * sms), dim3(kThreads), Smem<D>::kAlloc, st, a) == cudaSuccess ? PKV_OK : PKV_E_CUDA;
+    return launch_pdl(kv4_chunk_kernel<D>, dim3(kKv4ChunkCtas * sms), dim3(kThreads), Smem<D>::kAlloc, st, a) == cudaSuccess ? PKV_OK : PKV_E_CUDA;
 }
 
 }  // namespace

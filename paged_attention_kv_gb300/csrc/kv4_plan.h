@@ -118,13 +118,36 @@ PKV_HD int kv4_chunk_tiles(int keys) { return (int)(((unsigned)keys + 127) / 128
 PKV_HD long long kv4_chunk_units(const Kv4Request &q, int heads) {
     return (long long)q.tiles * heads * kv4_chunk_tiles(q.len - q.n / 2);
 }
-// An item of the chunk kernel is never cut: it takes about 7 us and 1.4 a key tile,
-// however few there are. The other kernel cuts them into equal shares: about 20 us and
-// 20 to 30 ns for each of all units. Measured (this kernel, the other; 8 heads of
-// 128): 1 request of 32 tokens and 1000 keys 21.7 and 35.3 us, 2000 keys about 34 and
-// 36.4, 4000 keys 58.8 and 40.9; 4 of them 59.7 and 60.6; 16 of 16 tokens and 4000 keys
-// 73 and 97; 1 of 512 tokens and 30000 keys 394 and 833.
-PKV_HD bool kv4_use_chunks(long long units, int longest) { return units > 0 && units + 400 >= 48LL * longest; }
+// Where the chunk kernel's items leave CTAs idle, each is split by keys into as many
+// parts as there are CTAs for it (two an SM), of four key tiles at least, of ten where
+// most items have an SM to themselves as it is. Split and not: 4 requests of 64 tokens
+// and 4000 keys (8 heads of 128) 42 and 60 us, 1 of 512 and 30000 279 and 394; 16 of 32
+// and 2000, whose parts would have eight, 43 and 40.
+struct Kv4Splits {
+    int count, least;  // parts of an item at most, key tiles of a part at least (4 or 10)
+};
+constexpr int kKv4MaxSplits = 8;
+PKV_HD Kv4Splits kv4_splits(long long items, int sms) {
+    if (items <= 0 || items > sms) return Kv4Splits{1, 4};
+    const int n = kv4_quotient(2 * sms, items);
+    return Kv4Splits{n < kKv4MaxSplits ? n : kKv4MaxSplits, n < 4 ? 10 : 4};
+}
+// In how many parts so many key tiles are, and where part s begins.
+PKV_HD int kv4_parts(int tiles, Kv4Splits sp) {
+    const int n = sp.least == 4 ? tiles / 4 : tiles / 10;
+    return n < 2 ? 1 : n < sp.count ? n : sp.count;
+}
+PKV_HD int kv4_part_begin(int tiles, int parts, int s) { return (int)((unsigned)(tiles * s) / (unsigned)parts); }  // 8 * 2^24 at most
+
+// Which kernel has them. The chunk kernel takes about 7 us and 1.4 to 1.7 a key tile of
+// the longest part. The other one cuts items into equal shares: about 20 us and 20 to
+// 30 ns for each of all units. Measured (this kernel, the other): 1 request of 32 tokens
+// and 1000 keys of 8 heads of 128 22.5 and 35 us, 16000 keys 46 and 61; 16 of 16 tokens
+// and 4000 keys 64 and 96; 1 of 512 tokens and 30000 keys 279 and 831; 1 of 64 tokens and
+// 60000 keys of 2 heads of 128 116 and 131.
+PKV_HD bool kv4_use_chunks(long long units, int longest, Kv4Splits sp) {
+    return units > 0 && (units + 400) * kv4_parts(longest, sp) >= 48LL * longest;
+}
 
 struct Kv4Shares {
     long long total, each;

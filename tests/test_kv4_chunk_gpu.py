@@ -33,6 +33,37 @@ def test_more_items_than_the_device_runs_at_once():
     b.check(outs[0])
 
 
+@pytest.mark.parametrize("hq,hkv,d,lens,new", [
+    (32, 8, 128, [3000], [64]), (8, 8, 64, [5000], [100]), (16, 2, 128, [9000, 700], [130, 64]), (4, 1, 64, [2000], [2000]),
+    (32, 4, 64, [1200, 40, 2500], [16, 1, 9]), (128, 1, 128, [1030], [1]), (12, 4, 128, [4000, 600, 90], [50, 40, 30])])
+def test_items_that_several_ctas_share(hq, hkv, d, lens, new):
+    b = Batch(sum(lens) + hq, hq, hkv, d, lens, new)
+    ws, st = pkv.alloc_kv4_workspace(b.pool), status()
+    before = ws[:70].clone()
+    call = pkv.prepare_kv4_attention(*b.tensors(), b.scale, max_query_len=max(new), workspace=ws, status=st)
+    want = call().clone()
+    b.check(want)
+    for _ in range(10):
+        call.outputs.zero_()
+        assert torch.equal(call(), want)
+    assert torch.equal(ws[:70], before) and pkv.pkv_read_status(st) == 0
+    pkv.paged_kv4_attention(*b.tensors(), b.scale, max_query_len=max(new), workspace=torch.zeros_like(ws), status=st)
+    assert pkv.pkv_read_status(st) & pkv.PKV_DEV_BAD_WORKSPACE
+
+
+def test_values_that_are_not_finite_in_one_part_of_an_item():
+    b = Batch(19, 8, 2, 128, [4000], [70])
+    clean = pkv.paged_kv4_attention(*b.tensors(), b.scale)
+    b.v[3950, 1, 40] = float("nan")  # position 3950: query 20 on, heads 4 to 7
+    b.k[2600, 0, 3] = float("nan")   # in the middle: all of heads 0 to 3
+    pkv.paged_kv4_write(b.k.to(DEV), b.v.to(DEV), i32(b.slots), b.pool)
+    out = pkv.paged_kv4_attention(*b.tensors(), b.scale)
+    assert torch.isnan(out[:, :4]).all() and torch.isnan(out[20:, 4:, 32:48]).all()
+    rest = out.clone()
+    rest[:, :4], rest[20:, 4:, 32:48] = clean[:, :4], clean[20:, 4:, 32:48]
+    assert torch.equal(rest, clean)
+
+
 def test_references_that_move_and_rows_of_any_size():
     b = Batch(4, 32, 8, 128, [600, 40], [150, 1])
     ramp = torch.linspace(0.01, 20, 600)[:, None, None]

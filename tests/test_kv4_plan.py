@@ -132,3 +132,31 @@ def test_random_batches(program):
             reqs.append((n, n + rng.choice((0, 0, rng.randint(0, 50), rng.randint(0, 5000)))))
         batches.append(((rng.choice((1, 2, 3, 4, 5, 8, 16, 33, 128)), rng.randint(1, 8), rows, *rng.choice(((1, 1), (7, 1), (3, 5), (152, 8), (152, 12)))), reqs))
     walk(program, batches)
+
+
+def test_parts_of_a_chunk_item(tmp_path):
+    """Every key tile in one part, four in each at least, and no more pieces than CTAs."""
+    (tmp_path / "parts.cpp").write_text(r"""
+#include <cstdio>
+#include "kv4_plan.h"
+using namespace pkv;
+int main() {
+    const int some[] = {1, 2, 5, 152};
+    for (int sms : some)
+        for (long long items = 0; items < 700; ++items) {
+            const Kv4Splits sp = kv4_splits(items, sms);
+            if (sp.count < 1 || sp.count > kKv4MaxSplits || (sp.count > 1 && (sp.count * items > 2 * sms || items > sms))) return 1;
+            for (int tiles = 1; tiles < 600; tiles += 1 + tiles / 50) {
+                const int parts = kv4_parts(tiles, sp);
+                if (parts < 1 || parts > sp.count || kv4_part_begin(tiles, parts, 0) != 0 || kv4_part_begin(tiles, parts, parts) != tiles) return 2;
+                for (int s = 0; parts > 1 && s < parts; ++s)
+                    if (kv4_part_begin(tiles, parts, s + 1) - kv4_part_begin(tiles, parts, s) < 4) return 3;
+            }
+        }
+    return kv4_splits(1LL << 40, 152).count == 1 && kv4_part_begin(1 << 24, 8, 8) == 1 << 24 ? 0 : 4;
+}
+""")
+    exe = str(tmp_path / "parts")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-I",
+                    os.path.join(REPO, "paged_attention_kv_gb300", "csrc"), str(tmp_path / "parts.cpp"), "-o", exe], check=True)
+    assert subprocess.run([exe]).returncode == 0
