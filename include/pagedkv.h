@@ -467,8 +467,8 @@ int pkv_prompt_attention(const void *q, int64_t q_stride, const void *k, int64_t
  * 448, badly). A group whose largest magnitude is A, after division by k_scale,
  * gets the scale A / 6 rounded to e4m3, at least 2^-9; a value the code nearest
  * to value / scale (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign; -0 becomes 0); both
- * round ties to even. Magnitudes past 2688, infinities too, become 2688; a group with a NaN
- * becomes NaN. The values that result are exact in bf16 and in fp16.
+ * round ties to even. Magnitudes past 2688, infinities too, become 2688; a group
+ * with a NaN becomes NaN. The values that result are exact in bf16 and in fp16.
  *
  * Bytes of a (block, kv head), D = head_size; a byte of codes holds an even
  * column in its low four bits and the next column above:
@@ -501,9 +501,9 @@ int paged_kv4_write(const void *k, int64_t k_stride, const void *v, int64_t v_st
 /*
  * The values that the pool holds at the given slots, as bf16 (exactly):
  * k_out and v_out bf16 [num_tokens][num_kv_heads][head_size], not the same memory,
- * and one of them may be NULL. Rows of negative slots are left as they were; those of slots at or beyond
- * 16 * num_blocks too, and raise PKV_DEV_BAD_SLOT. The same slot may be named
- * several times.
+ * and one of them may be NULL. Rows of negative slots are left as they were; those
+ * of slots at or beyond 16 * num_blocks too, and raise PKV_DEV_BAD_SLOT. The same
+ * slot may be named several times.
  */
 int paged_kv4_read(const void *kv4_cache, const pkv_cache_desc *desc, const int32_t *slot_mapping, int32_t num_tokens,
                    float k_scale, float v_scale, void *k_out, void *v_out, int32_t *status, void *stream);
@@ -547,11 +547,13 @@ int paged_kv4_attention_init(const pkv_cache_desc *desc, void *workspace, size_t
  *             (PKV_DEV_BAD_BLOCK) gives that request's rows unspecified values, and
  *             no other's
  *
- * Scores, sums and the output's sums are held in 32 bits; the probabilities are
- * rounded to fp16 (2^-11 of each, or 2^-25 of the largest where that is more) for
- * the product with V, and the output once more. Scores have to be finite in 32 bits. A value that is not finite reaches
- * the rows that may see its token and no other; tokens past a request's length
- * may hold anything. The result does not depend on timing. Nothing is read
+ * Scores, sums and the output's sums are held in 32 bits; q is held in fp16 (values
+ * below 2^-14 of their row's largest are off by 2^-25 of that at most, the others
+ * exact), the probabilities are rounded to fp16 (2^-11 of each, or 2^-25 of the
+ * largest where that is more) for the product with V, and the output once more.
+ * Scores have to be finite in 32 bits. A value that is not finite reaches the rows
+ * that may see its token and no other; tokens past a request's length may hold
+ * anything. The result does not depend on timing. Nothing is read
  * before every earlier kernel on the stream has completed. Make the first call
  * of each head size on a device before any capture.
  */

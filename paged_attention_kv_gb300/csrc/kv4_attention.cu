@@ -186,10 +186,9 @@ struct Item {
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // exponent of the largest value; a row that small is as good as
-            // zero below 2^-63, one that is not finite keeps its values
+            // exponent of the largest value; a row that is not finite keeps its values
             int e = (int)(top >> 7);
-            e = e == 255 ? 127 : min(max(e, 64), 253);
+            e = e == 255 ? 127 : min(max(e, 1), 253);
             const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
@@ -205,8 +204,8 @@ struct Item {
                     for (int j = 0; j < 4; ++j) q[n][2 * i + j / 2][j & 1] = f[j];
                 }
             }
-            // never 0: masked scores times it have to stay -inf
-            const float f = row < rows ? fmaxf(up * a.scale_log2, 0x1p-126f) : 1.0f;
+            // neither 0 nor infinite: masked scores times it have to stay -inf, and 0 has to stay 0
+            const float f = row < rows ? fminf(fmaxf(up * a.scale_log2, 0x1p-126f), 0x1p127f) : 1.0f;
             mul[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
             m[n] = make_float2(-INFINITY, -INFINITY);
             l[n] = make_float2(0.0f, 0.0f);

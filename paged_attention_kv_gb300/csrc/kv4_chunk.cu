@@ -431,10 +431,10 @@ __global__ void __launch_bounds__(kThreads, kKv4ChunkCtas) kv4_chunk_kernel(cons
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             // as in kv4_attention.cu
             int e = (int)(top >> 7);
-            e = e == 255 ? 127 : min(max(e, 64), 253);
+            e = e == 255 ? 127 : min(max(e, 1), 253);
             const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
-            // never 0: masked scores times it have to stay -inf
-            if (half == 0) s_mul[qr] = qr < tl.rows ? fmaxf(up * a.scale_log2, 0x1p-126f) : 1.0f;
+            // neither 0 nor infinite
+            if (half == 0) s_mul[qr] = qr < tl.rows ? fminf(fmaxf(up * a.scale_log2, 0x1p-126f), 0x1p127f) : 1.0f;
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
                 const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};

@@ -294,6 +294,24 @@ def test_requests_that_overlap_to_more_tokens_than_there_are(n):
     b.check(out)
 
 
+@pytest.mark.parametrize("new", [1, 3, 100])
+@pytest.mark.parametrize("by", [-115, -100, 100])
+def test_a_scale_far_from_q(new, by):
+    """Rows of very small or large q with a scale that brings their scores back."""
+    b = Batch(15, 16, 2, 128, [300, 140], [new, 1])
+    b.q *= 2.0 ** by
+    b.scale *= 2.0 ** -max(by, -100)
+    b.check(pkv.paged_kv4_attention(*b.tensors(), b.scale, max_query_len=new))
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_scores_of_zero_beside_a_factor_past_the_largest_value(new):
+    b = Batch(16, 16, 2, 128, [300, 140], [new, 1], spread=0.0)
+    b.q *= 2.0 ** 120
+    b.scale = 1e30
+    b.check(pkv.paged_kv4_attention(*b.tensors(), b.scale, max_query_len=new))
+
+
 def test_a_scale_near_the_smallest_value():
     """Scores times 2^-126 and less are 0: a mean over the keys that a row sees."""
     for new in (3, 100):
