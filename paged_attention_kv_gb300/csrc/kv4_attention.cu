@@ -44,6 +44,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -84,9 +85,11 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
-// The factor that what was taken against reference m has against `to` (0 where it
-// saw no key; to may be -inf too then).
-__device__ __forceinline__ float against(float m, float to, float mul) { return fast_exp2((m - fmaxf(to, -3e38f)) * mul); }
+// A row's reference before it sees any key: its sums are 0 then, whatever they are
+// multiplied by, and no score is below it.
+constexpr float kNoKey = -FLT_MAX;
+// The factor that what was taken against reference m has against `to`.
+__device__ __forceinline__ float against(float m, float to, float mul) { return fast_exp2((m - to) * mul); }
 
 template <int D, int kNt>
 constexpr int kQBytes = kNt * (D / 16) * 2 * 32 * 4;  // q's fragments of 8 kNt rows
@@ -128,10 +131,8 @@ struct Span {
     int row0, tok0, group;  // tok0: row0 / group
     uint32_t inv;
 
-    // keys of block `blk` that row `row` of the tile sees (at most 16 count)
-    __device__ __forceinline__ int sees(int blk, int row) const {
-        return limit0 + kv4_over(row0 + row, group, inv) - tok0 - key0 - 16 * blk;
-    }
+    // keys of the pair that row `row` of the tile sees (at most 32 count)
+    __device__ __forceinline__ int sees(int row) const { return limit0 + kv4_over(row0 + row, group, inv) - tok0 - key0; }
 };
 
 // A whole warp's state for one item of up to 8 kNt rows. Of O^T a lane holds,
@@ -207,7 +208,7 @@ struct Item {
             // neither 0 nor infinite: masked scores times it have to stay -inf, and 0 has to stay 0
             const float f = row < rows ? fminf(fmaxf(up * a.scale_log2, 0x1p-126f), 0x1p127f) : 1.0f;
             mul[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
-            m[n] = make_float2(-INFINITY, -INFINITY);
+            m[n] = make_float2(kNoKey, kNoKey);
             l[n] = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int i = 0; i < kK; ++i)
@@ -240,20 +241,17 @@ struct Item {
             }
         }
     }
-    // Scores to exponents of 2 against the references (0 where a row has none yet:
-    // it has seen no key, and all its scores are -inf); returns the largest.
-    template <bool kMasked>
+    // Scores to exponents of 2 against the references; returns the largest.
     __device__ __forceinline__ float exponents(const float (&s)[2][kNt][4], float (&e)[2][kNt][4]) const {
         float top = -INFINITY;
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
-            const float mx = kMasked && m[n].x == -INFINITY ? 0.0f : m[n].x, my = kMasked && m[n].y == -INFINITY ? 0.0f : m[n].y;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const float2 x = fmul2(fadd2(make_float2(s[b][n][0], s[b][n][1]), make_float2(-mx, -my)), mul[n]);
-                const float2 y = fmul2(fadd2(make_float2(s[b][n][2], s[b][n][3]), make_float2(-mx, -my)), mul[n]);
+                const float2 x = fmul2(fadd2(make_float2(s[b][n][0], s[b][n][1]), make_float2(-m[n].x, -m[n].y)), mul[n]);
+                const float2 y = fmul2(fadd2(make_float2(s[b][n][2], s[b][n][3]), make_float2(-m[n].x, -m[n].y)), mul[n]);
                 e[b][n][0] = x.x, e[b][n][1] = x.y, e[b][n][2] = y.x, e[b][n][3] = y.y;
-                if (!kMasked) top = fmax3(top, fmax3(x.x, x.y, y.x), y.y);
+                top = fmax3(top, fmax3(x.x, x.y, y.x), y.y);
             }
         }
         return top;
@@ -314,33 +312,31 @@ struct Item {
         }
     }
 
-    // Their probabilities, as fragments for the product with V. kMasked: some row
-    // does not see all of their keys.
-    template <bool kMasked>
-    __device__ __forceinline__ void probabilities(float (&s)[2][kNt][4], bool first, const Span &at, uint32_t (&p)[2][kNt][2], int lane) {
+    // Their probabilities, as fragments for the product with V. masked: some row does
+    // not see all of their keys. One copy of everything: what runs once an item comes
+    // from L2, and is waited for.
+    __device__ __forceinline__ void probabilities(float (&s)[2][kNt][4], bool masked, bool first, const Span &at, uint32_t (&p)[2][kNt][2], int lane) {
         const int g = lane >> 2, t = lane & 3;
         float e[2][kNt][4];
-        if constexpr (kMasked) {
+        if (masked) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int n = 0; n < kNt; ++n) {
+                // never past the last row's keys: rows of padding would see more, and the
+                // second block may be missing
+                const int end = at.end - at.key0, x = min(at.sees(8 * n + 2 * t), end), y = min(at.sees(8 * n + 2 * t + 1), end);
 #pragma unroll
-                for (int n = 0; n < kNt; ++n) {
-                    const int x = at.sees(b, 8 * n + 2 * t), y = at.sees(b, 8 * n + 2 * t + 1);
-                    // never past the last row's keys: rows of padding would see more, and the
-                    // second block may be missing
-                    if (g >= min(x, at.end - at.key0 - 16 * b)) s[b][n][0] = -INFINITY;
-                    if (g >= min(y, at.end - at.key0 - 16 * b)) s[b][n][1] = -INFINITY;
-                    if (g + 8 >= min(x, at.end - at.key0 - 16 * b)) s[b][n][2] = -INFINITY;
-                    if (g + 8 >= min(y, at.end - at.key0 - 16 * b)) s[b][n][3] = -INFINITY;
+                for (int b = 0; b < 2; ++b) {
+                    if (16 * b + g >= x) s[b][n][0] = -INFINITY;
+                    if (16 * b + g >= y) s[b][n][1] = -INFINITY;
+                    if (16 * b + g + 8 >= x) s[b][n][2] = -INFINITY;
+                    if (16 * b + g + 8 >= y) s[b][n][3] = -INFINITY;
                 }
-            move_references(s);
-            exponents<true>(s, e);
-        } else {
-            const float top = exponents<false>(s, e);
-            if (__any_sync(0xffffffffu, top > 10.0f) || first) {
-                move_references(s);
-                exponents<false>(s, e);
             }
+        }
+        const float top = exponents(s, e);
+        if (__any_sync(0xffffffffu, top > 10.0f) || first) {
+            move_references(s);
+            exponents(s, e);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -364,8 +360,13 @@ struct Item {
         __syncwarp();
         between();
         if (masked) {
-            guard(vs[0], 0, at, lane);
-            guard(vs[1], 1, at, lane);
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                uint32_t x = b ? vs[1] : vs[0];
+                guard(x, b, at, lane);
+                if (b) vs[1] = x;
+                else vs[0] = x;
+            }
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -394,16 +395,15 @@ struct Item {
         for (int n = 0; n < kNt; ++n) mma_f16(o[n][i], f, p[n][0], p[n][1]);
     }
 
-    // Partials, 32 lanes side by side: O, (m, l) of each 8 rows, and kMul: mul.
-    static constexpr int kVecs = kNt * (kK + 1);
-    template <bool kMul>
+    // A partial, 32 lanes side by side: O, then (m, l) and mul of each 8 rows.
+    static constexpr int kVecs = kNt * (kK + 2);
     __device__ __forceinline__ void store(float4 *to, int lane) const {
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
 #pragma unroll
             for (int i = 0; i < kK; ++i) to[(n * kK + i) * 32 + lane] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
             to[(kNt * kK + n) * 32 + lane] = make_float4(m[n].x, m[n].y, l[n].x, l[n].y);
-            if (kMul) to[(kVecs + n) * 32 + lane] = make_float4(mul[n].x, mul[n].y, 0.0f, 0.0f);
+            to[(kNt * (kK + 1) + n) * 32 + lane] = make_float4(mul[n].x, mul[n].y, 0.0f, 0.0f);
         }
     }
     static __device__ __forceinline__ void factors(float m, float n, float mul, float *to, float *f, float *g) {
@@ -457,7 +457,7 @@ struct Item {
         for (int n = 0; n < kNt; ++n) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int lim = at.sees(blk, 8 * n + 2 * t + c);
+                const int lim = at.sees(8 * n + 2 * t + c) - 16 * blk;
                 const uint32_t sees = lim >= 16 ? 0xffffu : lim <= 0 ? 0u : (1u << lim) - 1;
                 if (bad & sees)
 #pragma unroll
@@ -542,12 +542,11 @@ struct Kernel {
     static constexpr int kW = kWarps<kMaxNt>;
     static constexpr int kRows = 8 * kMaxNt;
     static constexpr size_t kRing = (size_t)kW * kStg * 2 * Kv4Tile<D>::kBytes;
-    static constexpr int kArea = Item<D, kMaxNt>::kVecs * 32;             // float4 of a warp's partial
-    static constexpr int kPart = (Item<D, kMaxNt>::kVecs + kMaxNt) * 32;  // float4 of one for another CTA
+    static constexpr int kPart = Item<D, kMaxNt>::kVecs * 32;  // float4 of a partial
     // With 16 rows or more shared memory holds q's fragments, and the warps' partials
     // lie in the workspace (12 times 16 rows of them, or 8 times 32).
     static constexpr bool kAreaShared = kMaxNt == 1;
-    static constexpr size_t kSmem = kRing + (size_t)kW * (kAreaShared ? kArea * 16 : kQBytes<D, kMaxNt>);
+    static constexpr size_t kSmem = kRing + (size_t)kW * (kAreaShared ? kPart * 16 : kQBytes<D, kMaxNt>);
 
     // Blocks [b0, b1) of an item; false: a wait gave up.
     template <int kNt>
@@ -595,8 +594,7 @@ struct Kernel {
             float s[2][kNt][4];
             uint32_t p[2][kNt][2];
             it.scores(tile, s, lane);
-            if (masked) it.template probabilities<true>(s, b == b0, at, p, lane);
-            else it.template probabilities<false>(s, b == b0, at, p, lane);
+            it.probabilities(s, masked, b == b0, at, p, lane);
             it.values(tile, masked, at, p, between, lane);
         }
         if (__any_sync(0xffffffffu, bits != 0) && lane == 0) raise_status(a.status, PKV_DEV_BAD_BLOCK);
@@ -608,14 +606,11 @@ struct Kernel {
     template <int kNt>
     static __device__ __forceinline__ void hand_over(const Kv4Args &a, Item<D, kNt> &it, const Where &w, int row0, int rows,
                                                      Team &team, int lane) {
-        if (team.begun && team.warp > 0) {  // for the first of its warps in this CTA
-            it.template store<false>(team.area + team.warp * kArea, lane);
-            return;
-        }
         const int base = team.cta * team.sh.per_cta;
+        const bool leads = !team.begun || team.warp == 0;  // it has the first of the item's pieces in this CTA
         const bool far = team.first < base || team.last >= base + team.shares;
-        if (far && lane == 0) *team.any_far = 1;
-        if (team.cut) {
+        if (leads && far && lane == 0) *team.any_far = 1;
+        if (leads && team.cut) {
             team.met = true;
             __syncthreads();
             if (*team.abort) return;
@@ -624,13 +619,14 @@ struct Kernel {
 #pragma unroll
                 for (int g = 0; g < kNt; ++g) {
                     typename Item<D, kNt>::Loaded x;
-                    Item<D, kNt>::load(team.area + i * kArea, g, x, lane);
+                    Item<D, kNt>::load(team.area + i * kPart, g, x, lane);
                     it.join(g, x);
                 }
         }
-        if (far) {
+        if (!leads || far) {  // for the first of its warps in this CTA; or for another CTA
             const int c0 = team.first / team.sh.per_cta, n = team.last / team.sh.per_cta - c0 + 1;
-            it.template store<true>(a.parts + ((size_t)2 * team.cta + (team.cta == c0)) * kPart, lane);
+            it.store(leads ? a.parts + ((size_t)2 * team.cta + (team.cta == c0)) * kPart : team.area + team.warp * kPart, lane);
+            if (!leads) return;
             __syncwarp();
             if (lane == 0) {
                 int seen;
@@ -822,7 +818,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     team.cta = cta;
     team.shares = min(team.sh.per_cta, team.sh.count - cta * team.sh.per_cta);
     team.area = K::kAreaShared ? reinterpret_cast<float4 *>(s_mem + K::kRing)
-                               : a.parts + (size_t)2 * gridDim.x * K::kPart + (size_t)cta * K::kW * K::kArea;
+                               : a.parts + (size_t)2 * gridDim.x * K::kPart + (size_t)cta * K::kW * K::kPart;
     team.q = smem_u32(s_mem + K::kRing) + warp * kQBytes<D, kMaxNt>;
     team.abort = &s_abort;
     team.met = false;
@@ -900,8 +896,8 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
 size_t parts_at(int sms) { return (((size_t)sms + 1) * sizeof(int) + 255) / 256 * 256; }
 size_t workspace_bytes(int sms, int head_size) {
     const size_t chunks = (size_t)kKv4ChunkCtas * sms * kv4_chunk_part(head_size) * sizeof(float);
-    return parts_at(sms) + std::max(chunks, (size_t)sms * sizeof(float4) * (head_size == 128 ? 2 * Kernel<128, 4>::kPart + kWarps<4> * Kernel<128, 4>::kArea
-                                                                            : 2 * Kernel<64, 4>::kPart + kWarps<4> * Kernel<64, 4>::kArea));
+    return parts_at(sms) + std::max(chunks, (size_t)sms * sizeof(float4) * (head_size == 128 ? 2 * Kernel<128, 4>::kPart + kWarps<4> * Kernel<128, 4>::kPart
+                                                                            : 2 * Kernel<64, 4>::kPart + kWarps<4> * Kernel<64, 4>::kPart));
 }
 
 std::mutex g_mu;
