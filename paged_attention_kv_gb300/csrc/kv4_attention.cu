@@ -26,17 +26,19 @@
 //
 // Bound by, and measured (us in a graph, one GB300; bytes over the copy bandwidth
 // of 6685 GB/s as the floor):
-//   256 decode requests of 512 to 4096 keys, 32 heads on 8 of 128: 95.3, floor 78.3.
-//     525 MB of DRAM reads, 6.0 TB/s while all warps work; 3 us of prologue and 5 of
-//     joins and ends. A step of a pair takes 57 % of the issue slots.
-//   the same with 4 tokens each: 136, floor 80. Three warps a scheduler, as many as
-//     registers allow, wait for one another's chains (48 % of the issue slots).
-//   64 decode requests of 128 to 2048 keys, 4 heads of 64: 12.7, floor 2.3: a chain of
+//   256 decode requests of 512 to 4096 keys, 32 heads on 8 of 128: 94.1, floor 78.3.
+//     525 MB of DRAM reads, 6.3 TB/s while all warps work (copies alone, without the
+//     products: 88 us in all); 10 us of prologue, items' starts, joins and ends. 57 % of
+//     the issue slots.
+//   the same with 4 tokens each: 133.5, floor 80. Three warps a scheduler, as many as
+//     registers allow, wait for one another's chains (48 % of the issue slots); 105 KB
+//     of code pass through the instruction cache, and items' starts and ends wait for it.
+//   64 decode requests of 128 to 2048 keys, 4 heads of 64: 12.8, floor 2.3: a chain of
 //     1.3 us for the sums of all costs, 1 for a warp's share, 1 to the first keys, 3
-//     of them, and joins. Two requests of 17 and 40 keys: 5.5. Instructions that run
+//     of them, and joins. Two requests of 17 and 40 keys: 5.3. Instructions that run
 //     once come from L2 and are waited for, hence the votes,
 //     approximate quotients and few branches where each warp finds its share.
-//   3 requests of 30000 to 100000 keys: 34.2, floor 21.1.
+//   3 requests of 30000 to 100000 keys: 34.1, floor 21.1.
 // Chosen against: one block at a time with 14 or 16 warps (16 rows 149 to 168 us against
 // 143 then; 8 rows 110 against 99), scores a pair ahead of the values (103 against 97:
 // registers), 8 rows with 16 warps of 128 registers (103 against 99), 32 rows with 10
@@ -887,6 +889,7 @@ __global__ void __launch_bounds__(32 * kWarps<kMaxNt>, 1) kv4_attention_kernel(c
     if (!team.met) __syncthreads();
     if (!s_any_far) return;
     __syncthreads();
+#pragma unroll 1
     for (int k = 0; k < 2; ++k)
         if (s_far[k].rows) K::join_far(a, s_far[k], team.sh.per_cta, warp, lane);
 }
