@@ -72,7 +72,8 @@ __device__ __forceinline__ float reciprocal(float x) {
 // "Computation of elementary functions on the IBM RISC System/6000", 1990), which one
 // fused operation gives exactly: what is left is off by 2^-46, so that a tie (x a
 // border between codes times s) comes out as that border itself, and everything
-// else is 2^-8 away from one. (The correction makes +0 of -0: code 0 for both.)
+// else is 2^-8 away from one. Quotients are 8 at most. (The correction makes +0 of -0:
+// code 0 for both.)
 __device__ __forceinline__ uint2 quantise(const Group &g, float by, float inv, uint32_t *scale) {
     const uint32_t top = max_bits(g);
     const float most = fminf(__uint_as_float(top << 16) * inv, 3e38f);
@@ -87,10 +88,14 @@ __device__ __forceinline__ uint2 quantise(const Group &g, float by, float inv, u
     float2 y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-    if (top == 0x7f80u) {  // an infinity has no remainder; the largest finite value becomes the same code
+    if (byte == 0x7e7e) {
+        // The largest scale (both halves hold it): values past its codes, infinite ones too,
+        // become 8 times it, which is the largest code with their sign. Further out the quotient
+        // would overflow where by is small, and its remainder be an infinity of the other sign.
+        const float bound = 8.0f * s * by;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            y[i] = make_float2(fminf(fmaxf(y[i].x, -3e38f), 3e38f), fminf(fmaxf(y[i].y, -3e38f), 3e38f));
+            y[i] = make_float2(fminf(fmaxf(y[i].x, -bound), bound), fminf(fmaxf(y[i].y, -bound), bound));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
