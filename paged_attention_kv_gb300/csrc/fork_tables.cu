@@ -154,7 +154,11 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         const int r = c0 + tid;
         const int p = r < R ? parent(r) : -1;
         const int n = p >= 0 ? length(p) : 0;
-        const bool copy = p >= 0 && n % PKV_BLOCK_SIZE && s_first[p] != r;
+        const int last = n / PKV_BLOCK_SIZE;
+        const bool part = n % PKV_BLOCK_SIZE && s_first[p] != r;
+        const int src = part ? __ldg(a.table + (long long)p * a.width + last) : -1;
+        const bool copy = src >= 0 && src < a.num_blocks;  // no block stays as it is, in all children
+        if (part && !copy) bits |= PKV_DEV_BAD_BLOCK;
         const uint32_t all = __ballot_sync(0xffffffffu, copy);
         __syncthreads();
         if (lane == 0) s_warp[warp] = __popc(all);
@@ -163,14 +167,10 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         const int sums = __reduce_add_sync(0xffffffffu, s_warp[lane]);
         if (r >= r0 && r < r1) {
             my_row = r;
-            my_last = n / PKV_BLOCK_SIZE;
+            my_last = last;
             if (copy) {
                 my_copy = copies + sum + __popc(all & ((1u << lane) - 1));
-                my_src = __ldg(a.table + (long long)p * a.width + my_last);
-                if (my_src < 0 || my_src >= a.num_blocks) {
-                    my_src = -1;
-                    bits |= PKV_DEV_BAD_BLOCK;
-                }
+                my_src = src;
             }
             a.lens_out[r] = n;
         }
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
             a.table_out[(long long)my_row * a.width + my_last] = dst;
         }
         a.copy_src[my_row] = dst < 0 ? -1 : my_src;
-        a.copy_dst[my_row] = my_src < 0 ? -1 : dst;
+        a.copy_dst[my_row] = dst;
     }
     if (rank == 0 && tid == 0 && list) *a.cursor = from + min(copies, a.num_free - from);
     if (bits) raise_status(a.status, bits);
