@@ -597,8 +597,9 @@ int paged_kv4_attention(const void *q, int64_t q_stride, int32_t num_tokens, int
  *
  * The last, partly filled block of a row must be its own. A parent that is no
  * row counts as -1 (PKV_DEV_BAD_PAGES); a length below 0 or past 16 *
- * max_blocks_per_req as 0 (PKV_DEV_BAD_LEN); entries outside [0, num_blocks) are
- * passed on and neither counted nor copied (PKV_DEV_BAD_BLOCK). A row for which the
+ * max_blocks_per_req as 0 (PKV_DEV_BAD_LEN); entries outside [0, num_blocks), of a
+ * row's first ceil(L / 16), are passed on and neither counted nor copied, and no block
+ * is taken for them (PKV_DEV_BAD_BLOCK, whatever becomes of the row). A row for which the
  * free list has no block gets entry -1 and no copy (PKV_DEV_NO_BLOCKS). A block
  * given up more often than held stays out of the free list, blocks that do not fit
  * before the cursor are lost, and a cursor outside [0, num_free] is left as it

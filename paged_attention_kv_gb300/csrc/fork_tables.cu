@@ -13,7 +13,8 @@
 // list does not depend on the order of atomics.
 //
 // One cluster does it all, with a barrier between counting, claiming, giving
-// back and handing out. Rows with exactly one child change no count. A warp takes a
+// back and handing out. Rows with exactly one child change no count; their entries are
+// looked at where the new row is written, as those of all rows with children. A warp takes a
 // row, four entries a lane at a time; as many CTAs as rows have warps, up to 16 (64
 // beams with their copies 12.6 us, 14.7 in one CTA, then; a quarter of that many rows a CTA
 // is no faster). Bound by its five phases, each a trip to L2 and a barrier of the
@@ -95,13 +96,14 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int e = e0 + 32 * u + lane;
-            b[u] = e < held ? __ldg(a.table + (long long)r * a.width + e) : INT_MIN;
+            b[u] = e < held ? __ldg(a.table + (long long)r * a.width + e) : -1;
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (b[u] != INT_MIN && (b[u] < 0 || b[u] >= a.num_blocks)) bits |= PKV_DEV_BAD_BLOCK;
-            if (b[u] < 0 || b[u] >= a.num_blocks) b[u] = -1;
-        }
+        for (int u = 0; u < kU; ++u)
+            if (b[u] < 0 || b[u] >= a.num_blocks) {
+                if (e0 + 32 * u + lane < held) bits |= PKV_DEV_BAD_BLOCK;
+                b[u] = -1;
+            }
     };
     for (int r = tid; r < R; r += kThreads) {
         const int p = parent(r);
@@ -158,7 +160,6 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
         const bool part = n % PKV_BLOCK_SIZE && s_first[p] != r;
         const int src = part ? __ldg(a.table + (long long)p * a.width + last) : -1;
         const bool copy = src >= 0 && src < a.num_blocks;  // no block stays as it is, in all children
-        if (part && !copy) bits |= PKV_DEV_BAD_BLOCK;
         const uint32_t all = __ballot_sync(0xffffffffu, copy);
         __syncthreads();
         if (lane == 0) s_warp[warp] = __popc(all);
@@ -188,8 +189,11 @@ __global__ void __launch_bounds__(kThreads) fork_tables_kernel(const ForkArgs a)
                 b[u] = e < held ? __ldg(line + e) : -1;
             }
 #pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (e0 + 32 * u + lane < a.width) to[e0 + 32 * u + lane] = b[u];
+            for (int u = 0; u < kU; ++u) {
+                const int e = e0 + 32 * u + lane;
+                if (e < held && (b[u] < 0 || b[u] >= a.num_blocks)) bits |= PKV_DEV_BAD_BLOCK;
+                if (e < a.width) to[e] = b[u];
+            }
         }
     }
     cluster_wait();

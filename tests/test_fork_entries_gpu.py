@@ -1,5 +1,5 @@
 """paged_fork_tables on tables with entries outside the pool: passed on, neither
-counted nor copied, and reported."""
+counted nor copied, and reported, in rows that end, go on once, or several times."""
 import numpy as np
 import pytest
 import torch
@@ -72,6 +72,42 @@ def test_the_partly_filled_entry_of_a_row_that_goes_on_twice(bad):
     # beside rows whose copies are made: those take the blocks that they would without it
     want = check([1, 2, 1, 2, 1, 2], table + [[-1] * 3] * 3, [20, 30, 40, 0, 0, 0], 20, free, 12)
     assert want[6] == [-1, -1, -1, 3, -1, 4]
+
+
+@pytest.mark.parametrize("rows", [33, 300, 1500])
+def test_bad_entries_among_many_rows(rows):
+    rng = np.random.default_rng(rows)
+    width = 5
+    lens = [int(x) for x in rng.integers(0, 16 * width + 1, rows)]
+    held = [-(-n // 16) for n in lens]
+    nb = sum(held) + rows + 10
+    perm = [int(x) for x in rng.permutation(nb)]
+    table, at = [], 0
+    for h in held:
+        table.append(perm[at:at + h] + [-1] * (width - h))
+        at += h
+    for r in rng.choice(rows, rows // 3, replace=False):
+        if held[r]:
+            e = held[r] - 1 if rng.random() < 0.6 else int(rng.integers(0, held[r]))
+            table[r][e] = int(rng.choice([-1, nb, -2 ** 31, 2 ** 31 - 1]))
+    parents = [-1 if rng.random() < 0.2 else int(rng.integers(0, rows)) for _ in range(rows)]
+    want = check(parents, table, lens, nb, perm, at)
+    assert want[7] and any(d >= 0 for d in want[6])
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("lens", [[20, 32, 40], [20, 30, 40]])
+@pytest.mark.parametrize("parents", [[0, 1, 2], [0, 1, 0], [2, 0, 1], [1, -1, -1]])
+def test_a_row_that_goes_on_once_is_looked_at_too(bad, lens, parents):
+    """Entry 1 is a whole block or the partly filled one; the row goes on unchanged."""
+    want = check(parents, [[3, 4, -1], [5, bad, -1], [7, 8, 9]], lens, 20, list(range(20)), 12)
+    assert want[7] and want[0][parents.index(1)] == [5, bad, -1]
+
+
+@pytest.mark.parametrize("bad", BAD)
+def test_a_row_that_ends(bad):
+    want = check([0, -1, 2], [[3, 4, -1], [5, bad, -1], [7, 8, 9]], [20, 32, 40], 20, list(range(20)), 12)
+    assert want[7] and want[4] == 11 and want[3][11] == 5
 
 
 def test_entries_behind_a_rows_length_are_not_looked_at():
