@@ -23,7 +23,7 @@ struct Kv4Args {
     const int32_t *table, *lens, *qsl;
     int num_tokens, num_kv_heads, group, num_reqs, max_blocks, num_blocks;
     uint32_t group_inv;  // see kv4_over
-    float scale_log2, v_scale;
+    float scale_log2, small, v_scale;  // scale * log2(e) * k_scale is scale_log2 times small, a power of two
     __nv_bfloat16 *out;
     int *claimed;   // the workspace: items of kv4_chunk.cu taken so far;
     int *arrived;   // of each CTA, the arrivals for the item that begins there and ends in another

@@ -208,7 +208,7 @@ struct Item {
                 }
             }
             // neither 0 nor infinite: masked scores times it have to stay -inf, and 0 has to stay 0
-            const float f = row < rows ? fminf(fmaxf(up * a.scale_log2, 0x1p-126f), 0x1p127f) : 1.0f;
+            const float f = row < rows ? fminf(fmaxf(up * a.small * a.scale_log2, 0x1p-126f), 0x1p127f) : 1.0f;
             mul[n] = make_float2(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
             m[n] = make_float2(kNoKey, kNoKey);
             l[n] = make_float2(0.0f, 0.0f);
@@ -984,14 +984,19 @@ extern "C" PKV_API int paged_kv4_attention(const void *q, int64_t q_stride, int3
     const int rs = device_sms(&sms);
     if (rs) return rs;
     if (workspace_size < workspace_bytes(sms, desc->head_size)) return PKV_E_WORKSPACE;
-    const float scale_log2 = scale * 1.4426950408889634f * k_scale;
+    // Below 2^-126 the product would keep few bits or none, but with q near the largest values
+    // there are scores of any size: 2^96 of it goes to q's powers of two then.
+    const double product = scale * 1.4426950408889634 * k_scale;
+    const bool tiny = product < 0x1p-126;
+    const float small = tiny ? 0x1p-96f : 1.0f;
+    const float scale_log2 = tiny ? (float)(product * 0x1p96) : scale * 1.4426950408889634f * k_scale;
     if (!std::isfinite(scale_log2)) return PKV_E_DIMS;
     // rows that the longest request has of a kv head
     const long long rows = (long long)(max_query_len ? max_query_len : num_tokens) * group;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Kv4Args a{static_cast<const __nv_bfloat16 *>(q), q_stride, static_cast<const uint8_t *>(kv4_cache), block_table,
                     seq_lens, query_start_loc, num_tokens, desc->num_kv_heads, group, num_reqs, max_blocks_per_req,
-                    desc->num_blocks, kv4_inverse(group), scale_log2, v_scale, static_cast<__nv_bfloat16 *>(out),
+                    desc->num_blocks, kv4_inverse(group), scale_log2, small, v_scale, static_cast<__nv_bfloat16 *>(out),
                     reinterpret_cast<int *>(ws), reinterpret_cast<int *>(ws) + 1, reinterpret_cast<float4 *>(ws + parts_at(sms)),
                     rows >= 64, status};
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kKv4ChunkCtas) kv4_chunk_kernel(cons
             e = e == 255 ? 127 : min(max(e, 1), 253);
             const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
             // neither 0 nor infinite
-            if (half == 0) s_mul[qr] = qr < tl.rows ? fminf(fmaxf(up * a.scale_log2, 0x1p-126f), 0x1p127f) : 1.0f;
+            if (half == 0) s_mul[qr] = qr < tl.rows ? fminf(fmaxf(up * a.small * a.scale_log2, 0x1p-126f), 0x1p127f) : 1.0f;
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
                 const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
