@@ -7,7 +7,7 @@
 // does not hit; the same holds for x against a tie between codes times s.
 //
 // Bound by, and measured (one GB300, tokens of 8 heads of 128, floor at 6685 GB/s):
-// 32768 tokens written in 34.5 us and read back in 28.6 (together 63.7 in a graph,
+// 32768 tokens written in 34 us and read back in 29 (together 63.4 in a graph,
 // floor 45.8). The write moves 153 MB of DRAM bytes at 4.4 TB/s with 53 % of the issue
 // slots and waits for its loads, of which 64 registers a thread hold two groups; the
 // read 111 MB (the rest of its output stays in L2), 45 % of the issue slots. 2240
